@@ -71,6 +71,7 @@ typedef enum { KVC_F16 = 0, KVC_F32 = 1 } kvc_dtype;
 #define KVC_DEVERR_SLOT 0x4u       /* an append slot >= num_blocks * block_size */
 #define KVC_DEVERR_TIMEOUT 0x8u    /* a bounded wait on a copy expired (the work was skipped) */
 #define KVC_DEVERR_SEQLENS 0x10u   /* cu_seqlens not non-decreasing / beyond total_tokens */
+#define KVC_DEVERR_TREE 0x20u      /* a drafted tree: size, parent, token or path out of range, or a row without mass */
 
 typedef struct {
     int num_layers;   /* L */
@@ -453,6 +454,155 @@ kvc_status paged_decode_attention_static_workspace(const void* q, const void* k_
                                                    const int32_t* context_lens, int B, int Hq, int Hkv, int head_dim,
                                                    int block_size, int max_context_len, float scale, void* out,
                                                    int out_dtype, int blocks_per_split, void* stream);
+
+/* ---- tree-drafted decoding --------------------------------------------
+ * One step verifies a tree of drafted tokens per sequence (several
+ * continuations at once; the speculative-decoding paragraph of "Tornar a
+ * inferência barata" (neuralialabs.com) verifies one chain of gamma proposed
+ * tokens in one pass over their positions; a chain is the tree in which every
+ * node has one child).  Node 0, the root, is the newest sampled token; every
+ * other node's parent has a smaller index; at most 64 nodes.  The nodes take
+ * the cache positions behind the history in index order: node t of sequence b
+ * is at position context_lens[b] - tree_len + t, whatever its depth, while its
+ * position for the rotation is (history length + depth).  A step is, per
+ * layer, kv_append_rope and paged_decode_tree_attention; then, once,
+ * draft_tree_verify on the target's probabilities and kv_tree_commit, after
+ * which the kept path is the end of an ordinary context. */
+
+/* Host helper: from parents [B][T] (parents[b][0] is not read; otherwise
+ * 0 <= parents[b][t] < t) and tree_lens [B] (NULL: T each) the masks [B][T]
+ * (bits of a node and its ancestors) and, if depths is not NULL, the depth of
+ * every node (root 0).  Entries behind a tree are set to 0 and not read.
+ * KVC_ERR_INVALID for a parent or a tree length out of range. */
+kvc_status kv_tree_masks(const int32_t* parents, const int32_t* tree_lens, int B, int T, uint64_t* masks,
+                         int32_t* depths);
+
+/* Host helper: rotation frequencies for kv_append_rope.  inv_freq[i] >= 0 is
+ * what the angle of pair i grows by per position, in radians (theta^(-2i /
+ * rot_dim) usually, scaled as a model wants); turns[i] is the same as a
+ * fraction of a full turn in units of 2^-64.  The kernel multiplies it by the
+ * position modulo one turn in integers, so the angle of any int32 position is
+ * as exact as the frequency's double.  KVC_ERR_INVALID for a negative or
+ * non-finite frequency. */
+kvc_status kv_rope_turns(const double* inv_freq, int n, uint64_t* turns);
+
+/* Query / key norm, position rotation and append in one pass over a step's
+ * (or a prompt's) projected rows; stands where kv_append does for models that
+ * rotate, and replaces the separate norm and rotation passes.
+ *   y_i = x_i * rsqrt(mean(x^2) + eps) * weight_i   per query / key head row
+ *   (y_a, y_b) = (y_a cos g - y_b sin g, y_b cos g + y_a sin g),
+ *   g = positions[t] * frequency, for the rot_dim / 2 pairs (a, b) of the first
+ *   rot_dim values of a row: (i, i + rot_dim / 2), or (2i, 2i + 1) when
+ *   interleaved; the other values and the value rows are not rotated.
+ *   q, k, v      device fp16 [n][Hq][D], [n][Hkv][D], [n][Hkv][D], the tokens
+ *                q_stride / k_stride / v_stride elements apart (multiples of 8,
+ *                at least heads * D): they may be parts of one projection
+ *   q_weight, k_weight  device fp16 [D], or NULL: those rows are not normed
+ *   turns        device uint64 [rot_dim / 2] (kv_rope_turns); positions device
+ *                int32 [n], any value; both unused at rot_dim 0.  rot_dim: a
+ *                multiple of 16 up to D
+ *   q_out        device fp16 [n][Hq][D]; may be q itself where q's stride is Hq * D
+ *   k_out, v_out device fp16 [n][Hkv][D] or NULL: the rows packed, for
+ *                prefill_attention or kv_append_fp8; may be k / v as q_out may be q
+ *   k_cache, v_cache  device fp16 [num_blocks][Hkv][bs][D] (one layer), with
+ *                slot_mapping device int64 [n] as in kv_append (negative =
+ *                skip, >= num_blocks * bs sets KVC_DEVERR_SLOT); all three NULL:
+ *                nothing is appended
+ * Arithmetic in fp32, one rounding to fp16 per value.  Value rows, and rows
+ * that are neither normed nor rotated, are copied bit for bit.  16-byte aligned
+ * pointers.  One kernel launch. */
+kvc_status kv_append_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                          int64_t v_stride, int n, int Hq, int Hkv, int head_dim, const void* q_weight,
+                          const void* k_weight, float eps, const uint64_t* turns, int rot_dim, int interleaved,
+                          const int32_t* positions, void* q_out, void* k_out, void* v_out, void* k_cache,
+                          void* v_cache, int num_blocks, int block_size, const int64_t* slot_mapping, void* stream);
+
+/* Attention of a tree of drafted tokens over the paged cache: node t's query
+ * attends to the history (positions 0 .. ctx - tree_len - 1) and to the tree's
+ * nodes j < tree_len with bit j of masks[b][t] set.
+ *   q            device fp16 [B][T][Hq][D]
+ *   context_lens device int32 [B], including the tree (tree_len <= ctx <=
+ *                min(max_blocks * bs, max_context_len))
+ *   masks        device uint64 [B][T] (kv_tree_masks, or any other bits; a row
+ *                that sees nothing, without history and bits, gives 0)
+ *   tree_lens    device int32 [B], 0 .. T, or NULL: T each.  Rows t >= tree_len
+ *                of out are left as they were
+ *   T            1 .. 64
+ *   out          device [B][T][Hq][D], out_dtype KVC_F16 or KVC_F32
+ *   workspace    device, 16-byte aligned, >= paged_decode_tree_plan's bytes; as
+ *                with the other decode calls, calls that share one must not
+ *                overlap in time
+ * Other arguments as in paged_decode_attention; the nodes' K/V must be in the
+ * cache already (kv_append_rope or kv_append).  What the cache holds past a
+ * context, and in nodes that a row does not see, cannot reach that row's
+ * output, infinities and NaN included.  With fp16 out the softmax weights
+ * multiply V in fp16 and the row sums add the same rounded weights (within
+ * 2^-11 relative, as in paged_decode_multi_attention); with fp32 out they keep
+ * ~22 bits.  A sequence whose lengths do not fit is flagged
+ * (KVC_DEVERR_CONTEXT) and its rows are zero; a block id out of range is
+ * flagged (KVC_DEVERR_BLOCK_ID) and the chunk of the context it lies in is
+ * left out.  One kernel launch, or two where the context is split (the plan's
+ * workspace is then not 0). */
+kvc_status paged_decode_tree_plan(int B, int Hq, int Hkv, int head_dim, int block_size, int max_context_len, int T,
+                                  size_t* workspace_bytes);
+kvc_status paged_decode_tree_attention(const void* q, const void* k_cache, const void* v_cache, int num_blocks,
+                                       const int32_t* block_table, int max_blocks, const int32_t* context_lens,
+                                       const uint64_t* masks, const int32_t* tree_lens, int T, int B, int Hq, int Hkv,
+                                       int head_dim, int block_size, int max_context_len, float scale, void* out,
+                                       int out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Which drafted tokens the target keeps, and the next token.  Starting at the
+ * root, a node's children x_1, x_2, ... (in index order) are tried against the
+ * target's row p_0 = p and the draft's row q_0 = q of the node: child x_k is
+ * kept if u_k q_k(x_k) < p_k(x_k) (probability min(1, p / q)), and the walk
+ * goes on from it; else p_{k+1} = max(0, p_k - q_k) divided by its sum.
+ * distinct 0: children were drawn independently, q_k = q.  distinct 1: they
+ * were drawn without replacement, q_{k+1} = q_k without x_k, divided by
+ * 1 - q_k(x_k) (a child tried after the draft's mass is spent is refused).  Where no
+ * child is kept, the next token is drawn from the last p_k: the smallest index
+ * whose running sum exceeds u_0 times the sum (from p itself if nothing of the
+ * residual is left).  The kept tokens and the next one are distributed as the
+ * target's own samples.
+ *   target_probs, draft_probs  device [B][T][V], prob_dtype KVC_F16 or KVC_F32
+ *                for both; row t of a sequence is the distribution behind node
+ *                t; rows p_stride / q_stride elements apart (>= V).  They are
+ *                read to 2^-53; NaN and negative values count as 0, values
+ *                above 1 as 1; a row's sum is about 1 (below 4096)
+ *   tokens, parents  device int32 [B][T] (entry 0 of a sequence is not read)
+ *   tree_lens    device int32 [B], 0 .. T, or NULL: T each
+ *   uniforms     device float [B][T] in [0, 1): u_t of node t's trial, u_0 of
+ *                the draw
+ *   path         device int32 [B][T]: the kept nodes, root first, then -1
+ *   path_len     device int32 [B] (1 .. tree_len; 0 for an empty tree)
+ *   next_token   device int32 [B] (-1 for an empty tree)
+ * V up to 2^24.  A node whose parent or token is out of range is flagged
+ * (KVC_DEVERR_TREE) and never kept; a row without any mass is flagged and
+ * gives next_token -1.  Sums are integers: results repeat bit for bit.  The
+ * inputs must not change while the call runs.  One kernel launch. */
+kvc_status draft_tree_verify(const void* target_probs, int64_t p_stride, const void* draft_probs, int64_t q_stride,
+                             int prob_dtype, const int32_t* tokens, const int32_t* parents, const int32_t* tree_lens,
+                             const float* uniforms, int B, int T, int V, int distinct, int32_t* path,
+                             int32_t* path_len, int32_t* next_token, void* stream);
+
+/* Move the kept nodes' cache rows (all layers, K and V of the handle's pools)
+ * to the end of their contexts, bit for bit: with base = context_lens[b] -
+ * tree_len, position base + i takes the row of position base + path[b][i] for
+ * i < path_len[b], and new_context_lens[b] = base + path_len[b].  The rows of
+ * the other nodes are left behind it and are overwritten by later appends.
+ *   block_table  device int32 [B][max_blocks], as the attention call had it; the
+ *                blocks of the tree are the sequence's own (not shared)
+ *   tree_lens    device int32 [B], or NULL: P each
+ *   path         device int32 [B][P], 0 = path[b][0] < path[b][1] < ... <
+ *                tree_len; path_len device int32 [B], 0 .. min(P, tree_len)
+ *   P            1 .. 64 (a tree of up to 64 nodes may be given a narrower path
+ *                with tree_lens)
+ *   new_context_lens  device int32 [B], not context_lens itself
+ * A sequence whose lengths (KVC_DEVERR_CONTEXT), path (KVC_DEVERR_TREE) or
+ * blocks (KVC_DEVERR_BLOCK_ID) do not fit is flagged and left as it was, with
+ * new_context_lens[b] = context_lens[b].  One kernel launch. */
+kvc_status kv_tree_commit(kvc_handle h, const int32_t* block_table, int max_blocks, const int32_t* context_lens,
+                          const int32_t* tree_lens, const int32_t* path, const int32_t* path_len, int P, int B,
+                          int32_t* new_context_lens, void* stream);
 
 /* Varlen packed prefill (xformers article parts 4-5): for every segment s
  * (rows cu_seqlens[s] .. cu_seqlens[s+1]-1) and query head h,

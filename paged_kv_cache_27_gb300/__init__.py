@@ -34,13 +34,15 @@ __all__ = [
     "paged_decode_multi_plan", "paged_decode_multi_attention", "kv_append_fp8", "paged_decode_attention_fp8",
     "kv_fp8_record_bytes",
     "prefill_attention", "prefill_attention_ex", "fp8_v_position", "DEVERR",
+    "kv_tree_masks", "kv_rope_turns", "kv_append_rope", "paged_decode_tree_plan", "paged_decode_tree_attention",
+    "draft_tree_verify", "kv_tree_commit",
 ]
 
 KVC_F16, KVC_F32 = 0, 1
 KVC_PREFILL_P_F16, KVC_PREFILL_P_SPLIT = 0, 1
 STATUS = {0: "KVC_OK", 1: "KVC_ERR_INVALID", 2: "KVC_ERR_OOM", 3: "KVC_ERR_CAPACITY", 4: "KVC_ERR_CUDA",
           5: "KVC_ERR_UNSUPPORTED"}
-DEVERR = {"BLOCK_ID": 0x1, "CONTEXT": 0x2, "SLOT": 0x4, "TIMEOUT": 0x8, "SEQLENS": 0x10}
+DEVERR = {"BLOCK_ID": 0x1, "CONTEXT": 0x2, "SLOT": 0x4, "TIMEOUT": 0x8, "SEQLENS": 0x10, "TREE": 0x20}
 
 
 class KvcError(RuntimeError):
@@ -127,6 +129,15 @@ def _load():
                                              P]),
         "paged_decode_cascade_attention": (I, [P, P, P, I, P, I, P, P, P, I, I, I, I, I, I, I, I, ctypes.c_float, P,
                                                I, P, SZ, P]),
+        "kv_tree_masks": (I, [P, P, I, I, P, P]),
+        "kv_rope_turns": (I, [P, I, P]),
+        "kv_append_rope": (I, [P, I64, P, I64, P, I64, I, I, I, I, P, P, ctypes.c_float, P, I, I, P, P, P, P, P, P, I,
+                               I, P, P]),
+        "paged_decode_tree_plan": (I, [I, I, I, I, I, I, I, PSZ]),
+        "paged_decode_tree_attention": (I, [P, P, P, I, P, I, P, P, P, I, I, I, I, I, I, I, ctypes.c_float, P, I, P,
+                                            SZ, P]),
+        "draft_tree_verify": (I, [P, I64, P, I64, I, P, P, P, P, I, I, I, I, P, P, P, P]),
+        "kv_tree_commit": (I, [P, P, I, P, P, P, P, I, I, P, P]),
         "prefill_attention": (I, [P, P, P, P, I, I, I, I, I, I, ctypes.c_float, I, P, I, P]),
         "prefill_attention_ex": (I, [P, P, P, P, I, I, I, I, I, I, ctypes.c_float, I, I, P, I, P]),
     }
@@ -701,3 +712,229 @@ def prefill_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seql
     P's fp16 high part and residual (KVC_PREFILL_P_SPLIT)."""
     prefill_attention_ex(q, k, v, cu_seqlens, max_seqlen, scale, causal,
                          KVC_PREFILL_P_SPLIT if precise else KVC_PREFILL_P_F16, out, stream)
+
+
+# ------------------------------------------------------------ tree-drafted decoding
+def kv_tree_masks(parents, tree_lens=None):
+    """Masks (int64 [B][T], the bits of a node and its ancestors) and depths (int32 [B][T]) of drafted trees from
+    their parents [B][T] (host arrays; a node's parent has a smaller index, node 0 is the root)."""
+    par = _host(parents, np.int32)
+    if par.ndim != 2:
+        raise ValueError("parents must be [B][T]")
+    B, T = par.shape
+    lens = None if tree_lens is None else _host(tree_lens, np.int32)
+    if lens is not None and lens.shape != (B,):
+        raise ValueError("tree_lens must have B entries")
+    masks, depths = np.zeros((B, T), np.int64), np.zeros((B, T), np.int32)
+    _check(_lib.kv_tree_masks(_np_ptr(par), None if lens is None else _np_ptr(lens), B, T, _np_ptr(masks),
+                              _np_ptr(depths)), "kv_tree_masks")
+    return masks, depths
+
+
+def kv_rope_turns(inv_freq) -> np.ndarray:
+    """Rotation frequencies (radians per position, one per pair) as fractions of a turn in units of 2^-64: the int64
+    bit patterns kv_append_rope takes (copy them to the device)."""
+    f = _host(inv_freq, np.float64)
+    if f.ndim != 1:
+        raise ValueError("inv_freq must be one-dimensional")
+    turns = np.zeros(f.size, np.int64)
+    _check(_lib.kv_rope_turns(_np_ptr(f), f.size, _np_ptr(turns)), "kv_rope_turns")
+    return turns
+
+
+def _same_device(*tensors) -> None:
+    """Every tensor given (None: left out) is on the current device, where the library's kernels run."""
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) > 1:
+        raise ValueError("tensors are on several devices: " + ", ".join(sorted(map(str, devices))))
+    for d in devices:
+        if d.type == "cuda" and d.index != torch.cuda.current_device():
+            raise ValueError(f"tensors are on {d}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _token_rows(t: torch.Tensor, name: str):
+    """Pointer and token stride of an [n][H][D] fp16 tensor whose heads are packed and whose tokens may be apart."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [n][H][D]")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.dtype != torch.float16:
+        raise TypeError(f"{name} must be torch.float16, got {t.dtype}")
+    n, H, D = t.shape
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return t.data_ptr(), (t.stride(0) if n > 1 else H * D)
+
+
+def kv_append_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: Optional[torch.Tensor],
+                   turns: Optional[torch.Tensor], q_out: torch.Tensor, k_cache: Optional[torch.Tensor] = None,
+                   v_cache: Optional[torch.Tensor] = None, slot_mapping: Optional[torch.Tensor] = None, *,
+                   q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                   eps: float = 1e-6, interleaved: bool = False, k_out: Optional[torch.Tensor] = None,
+                   v_out: Optional[torch.Tensor] = None, stream=None, prepare: bool = False):
+    """Norm and rotate query and key rows and append keys and values to the paged cache, in one pass.
+
+    q [n][Hq][D], k and v [n][Hkv][D] fp16 (the tokens may be apart, as parts of one projection's output); positions
+    int32 [n]; turns int64 [rot_dim / 2] (kv_rope_turns; None: no rotation); q_out [n][Hq][D]; k_cache / v_cache
+    [NB][Hkv][bs][D] (one layer) with slot_mapping int64 [n]; q_weight / k_weight fp16 [D] (None: no norm);
+    k_out / v_out [n][Hkv][D]: the rows packed.  prepare=True returns a PreparedCall instead of launching."""
+    qp, qs = _token_rows(q, "q")
+    kp, ks = _token_rows(k, "k")
+    vp, vs = _token_rows(v, "v")
+    n, Hq, D = q.shape
+    Hkv = k.shape[1]
+    if k.shape != (n, Hkv, D) or v.shape != k.shape or q_out.shape != q.shape:
+        raise ValueError("q, k, v and q_out do not match")
+    for t, nm in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is not None and t.shape != k.shape:
+            raise ValueError(f"{nm} must have k's shape")
+    for t, nm in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None and t.numel() != D:
+            raise ValueError(f"{nm} must have D entries")
+    rot = 0 if turns is None else 2 * turns.numel()
+    if rot and (positions is None or positions.numel() != n):
+        raise ValueError("positions must have n entries")
+    given = [t is not None for t in (k_cache, v_cache, slot_mapping)]
+    if any(given) != all(given):
+        raise ValueError("k_cache, v_cache and slot_mapping: all or none")
+    NB, bs = 0, 16
+    if k_cache is not None:
+        if k_cache.dim() != 4:
+            raise ValueError("k_cache must be [NB][Hkv][bs][D]")
+        NB, Hc, bs, Dc = k_cache.shape
+        if (Hc, Dc) != (Hkv, D) or v_cache.shape != k_cache.shape:
+            raise ValueError("cache shapes do not match k")
+        if slot_mapping.numel() != n:
+            raise ValueError("slot_mapping must have n entries")
+    if not rot:
+        positions = turns = None
+    keep = (q, k, v, positions, turns, q_out, k_cache, v_cache, slot_mapping, q_weight, k_weight, k_out, v_out)
+    _same_device(*keep)
+    f16 = torch.float16
+    args = (qp, qs, kp, ks, vp, vs, n, Hq, Hkv, D, _dptr(q_weight, f16, "q_weight"), _dptr(k_weight, f16, "k_weight"),
+            float(eps), _dptr(turns, torch.int64, "turns"), rot, int(bool(interleaved)),
+            _dptr(positions, torch.int32, "positions"), _dptr(q_out, f16, "q_out"), _dptr(k_out, f16, "k_out"),
+            _dptr(v_out, f16, "v_out"), _dptr(k_cache, f16, "k_cache"), _dptr(v_cache, f16, "v_cache"), NB, bs,
+            _dptr(slot_mapping, torch.int64, "slot_mapping"))
+    return _launch(_lib.kv_append_rope, args, "kv_append_rope", stream, prepare, keep)
+
+
+def paged_decode_tree_plan(B: int, Hq: int, Hkv: int, head_dim: int, max_context_len: int, T: int,
+                           block_size: int = 16) -> int:
+    """Workspace bytes of paged_decode_tree_attention for these sizes (trees of up to T nodes)."""
+    ws = ctypes.c_size_t()
+    _check(_lib.paged_decode_tree_plan(B, Hq, Hkv, head_dim, block_size, max_context_len, T, ctypes.byref(ws)),
+           "paged_decode_tree_plan")
+    return ws.value
+
+
+def paged_decode_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                block_table: torch.Tensor, context_lens: torch.Tensor, masks: torch.Tensor,
+                                scale: float, out: torch.Tensor, workspace: Optional[torch.Tensor],
+                                max_context_len: int, tree_lens: Optional[torch.Tensor] = None, stream=None,
+                                prepare: bool = False):
+    """Attention of drafted trees (the newest tree_lens[b] cached tokens of every sequence) over the paged cache.
+
+    q [B][T][Hq][D] fp16; masks int64 [B][T] (kv_tree_masks: bit j of a row = it sees node j; every row sees the
+    history); context_lens int32 [B], trees included; tree_lens int32 [B] (None: T nodes each; rows behind a tree are
+    left as they were); out like q, fp16 or fp32; workspace: paged_decode_tree_plan bytes.
+    prepare=True returns a PreparedCall instead of launching."""
+    B, T, Hq, D = q.shape
+    NB, Hkv, bs, Dk = k_cache.shape
+    if Dk != D or v_cache.shape != k_cache.shape:
+        raise ValueError("cache shapes do not match q")
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if block_table.dim() != 2 or block_table.shape[0] != B or context_lens.numel() != B:
+        raise ValueError("block_table / context_lens do not match B")
+    if masks.shape != (B, T) or (tree_lens is not None and tree_lens.numel() != B):
+        raise ValueError("masks must be [B][T] and tree_lens have B entries")
+    od = {torch.float16: KVC_F16, torch.float32: KVC_F32}.get(out.dtype)
+    if od is None:
+        raise TypeError("out must be float16 or float32")
+    keep = (q, k_cache, v_cache, block_table, context_lens, masks, tree_lens, out, workspace)
+    _same_device(*keep)
+    ws_ptr = _dptr(workspace, None, "workspace") if workspace is not None else None
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    args = (_dptr(q, torch.float16, "q"), _dptr(k_cache, torch.float16, "k_cache"),
+            _dptr(v_cache, torch.float16, "v_cache"), NB, _dptr(block_table, torch.int32, "block_table"),
+            block_table.shape[1], _dptr(context_lens, torch.int32, "context_lens"),
+            _dptr(masks, torch.int64, "masks"), _dptr(tree_lens, torch.int32, "tree_lens"), T, B, Hq, Hkv, D, bs,
+            int(max_context_len), float(scale), _dptr(out, None, "out"), od, ws_ptr, ws_bytes)
+    return _launch(_lib.paged_decode_tree_attention, args, "paged_decode_tree_attention", stream, prepare, keep)
+
+
+def _prob_rows(t: torch.Tensor, name: str):
+    """Pointer and row stride of a [B][T][V] tensor with contiguous rows at one distance from each other."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [B][T][V]")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.dtype not in (torch.float16, torch.float32):
+        raise TypeError(f"{name} must be float16 or float32")
+    B, T, V = t.shape
+    row = t.stride(1) if T > 1 else t.stride(0) if B > 1 else V
+    if (V > 1 and t.stride(2) != 1) or (B > 1 and T > 1 and t.stride(0) != T * row):
+        raise ValueError(f"{name}: rows must be contiguous and evenly spaced")
+    return t.data_ptr(), row
+
+
+def draft_tree_verify(target_probs: torch.Tensor, draft_probs: torch.Tensor, tokens: torch.Tensor,
+                      parents: torch.Tensor, uniforms: torch.Tensor, path: torch.Tensor, path_len: torch.Tensor,
+                      next_token: torch.Tensor, tree_lens: Optional[torch.Tensor] = None, distinct: bool = False,
+                      stream=None, prepare: bool = False):
+    """Which drafted tokens the target keeps (path int32 [B][T]: the kept nodes, root first, then -1; path_len int32
+    [B]) and the token after them (next_token int32 [B]).
+
+    target_probs / draft_probs [B][T][V] fp32 or fp16 (row t: the distribution behind node t); tokens / parents int32
+    [B][T]; uniforms fp32 [B][T] in [0, 1) (entry 0 draws the next token); tree_lens int32 [B] (None: T nodes each);
+    distinct: a node's children were drawn without replacement.  prepare=True returns a PreparedCall."""
+    pp, ps = _prob_rows(target_probs, "target_probs")
+    qp, qs = _prob_rows(draft_probs, "draft_probs")
+    B, T, V = target_probs.shape
+    if draft_probs.shape != target_probs.shape or draft_probs.dtype != target_probs.dtype:
+        raise ValueError("target_probs and draft_probs must agree in shape and type")
+    for t, nm in ((tokens, "tokens"), (parents, "parents"), (uniforms, "uniforms"), (path, "path")):
+        if t.shape != (B, T):
+            raise ValueError(f"{nm} must be [B][T]")
+    for t, nm in ((path_len, "path_len"), (next_token, "next_token"), (tree_lens, "tree_lens")):
+        if t is not None and t.numel() != B:
+            raise ValueError(f"{nm} must have B entries")
+    keep = (target_probs, draft_probs, tokens, parents, tree_lens, uniforms, path, path_len, next_token)
+    _same_device(*keep)
+    i32 = torch.int32
+    args = (pp, ps, qp, qs, KVC_F32 if target_probs.dtype == torch.float32 else KVC_F16, _dptr(tokens, i32, "tokens"),
+            _dptr(parents, i32, "parents"), _dptr(tree_lens, i32, "tree_lens"),
+            _dptr(uniforms, torch.float32, "uniforms"), B, T, V, int(bool(distinct)), _dptr(path, i32, "path"),
+            _dptr(path_len, i32, "path_len"), _dptr(next_token, i32, "next_token"))
+    return _launch(_lib.draft_tree_verify, args, "draft_tree_verify", stream, prepare, keep)
+
+
+def kv_tree_commit(h: int, block_table: torch.Tensor, context_lens: torch.Tensor, path: torch.Tensor,
+                   path_len: torch.Tensor, new_context_lens: torch.Tensor, tree_lens: Optional[torch.Tensor] = None,
+                   stream=None, prepare: bool = False):
+    """Move the kept nodes' cache rows (path int32 [B][P], path_len int32 [B]; all layers of the handle's pools) to
+    the end of their contexts and write the new context lengths (int32 [B], not context_lens itself).
+
+    block_table int32 [B][max_blocks] and context_lens int32 [B] (trees included) as the attention call had them;
+    tree_lens int32 [B] (None: P nodes each).  prepare=True returns a PreparedCall."""
+    if path.dim() != 2 or block_table.dim() != 2:
+        raise ValueError("path must be [B][P] and block_table [B][max_blocks]")
+    B, P = path.shape
+    if block_table.shape[0] != B:
+        raise ValueError("block_table does not match path")
+    for t, nm in ((context_lens, "context_lens"), (path_len, "path_len"), (new_context_lens, "new_context_lens"),
+                  (tree_lens, "tree_lens")):
+        if t is not None and t.numel() != B:
+            raise ValueError(f"{nm} must have B entries")
+    keep = (path, block_table, context_lens, tree_lens, path_len, new_context_lens)
+    _same_device(*keep)
+    i32 = torch.int32
+    args = (h, _dptr(block_table, i32, "block_table"), block_table.shape[1], _dptr(context_lens, i32, "context_lens"),
+            _dptr(tree_lens, i32, "tree_lens"), _dptr(path, i32, "path"), _dptr(path_len, i32, "path_len"), P, B,
+            _dptr(new_context_lens, i32, "new_context_lens"))
+    return _launch(_lib.kv_tree_commit, args, "kv_tree_commit", stream, prepare, keep)

@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -69,6 +70,17 @@ kvc_status copy_to_host(std::vector<T>& dst, const T* src, size_t n, cudaStream_
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) return cuda_fail(e, "checked mode copy");
     return KVC_OK;
+}
+
+// Checked mode reads device arrays into vectors; running out of host memory there is an error code like any other.
+template <typename F>
+kvc_status checked(F&& check) {
+    if (!g_checked.load()) return KVC_OK;
+    try {
+        return check();
+    } catch (...) {
+        return KVC_ERR_OOM;
+    }
 }
 
 }  // namespace
@@ -753,6 +765,338 @@ kvc_status paged_decode_multi_attention(const void* q, const void* k_cache, cons
     if (e != cudaSuccess) return cuda_fail(e, "device error word");
     e = kvc::launch_multi(a, q_len, as_stream(stream));
     if (e != cudaSuccess) return cuda_fail(e, "paged_decode_multi_attention launch");
+    return KVC_OK;
+}
+
+// ---- tree-drafted decoding ----------------------------------------------------
+kvc_status kv_tree_masks(const int32_t* parents, const int32_t* tree_lens, int B, int T, uint64_t* masks,
+                         int32_t* depths) {
+    if (B < 0 || T < 1) return fail(KVC_ERR_INVALID, "bad sizes");
+    if (T > kvc::kMaxTreeNodes) return fail(KVC_ERR_UNSUPPORTED, "trees of %d nodes not supported (%d)", T, kvc::kMaxTreeNodes);
+    if (B > 0 && (!parents || !masks)) return fail(KVC_ERR_INVALID, "null pointer");
+    for (int b = 0; b < B; ++b) {  // everything is checked before anything is written
+        const int len = tree_lens ? tree_lens[b] : T;
+        if (len < 0 || len > T) return fail(KVC_ERR_INVALID, "sequence %d: tree length %d outside [0, %d]", b, len, T);
+        for (int t = 1; t < len; ++t) {
+            const int32_t par = parents[static_cast<size_t>(b) * T + t];
+            if (par < 0 || par >= t) return fail(KVC_ERR_INVALID, "sequence %d: parent %d of node %d", b, par, t);
+        }
+    }
+    for (int b = 0; b < B; ++b) {
+        const size_t at = static_cast<size_t>(b) * T;
+        const int len = tree_lens ? tree_lens[b] : T;
+        for (int t = 0; t < T; ++t) {
+            const bool in = t < len, child = in && t > 0;
+            const size_t par = child ? at + parents[at + t] : at;
+            masks[at + t] = in ? (uint64_t(1) << t) | (child ? masks[par] : 0) : 0;
+            if (depths) depths[at + t] = child ? depths[par] + 1 : 0;
+        }
+    }
+    return KVC_OK;
+}
+
+kvc_status kv_rope_turns(const double* inv_freq, int n, uint64_t* turns) {
+    if (n < 0 || (n > 0 && (!inv_freq || !turns))) return fail(KVC_ERR_INVALID, "bad arguments");
+    for (int i = 0; i < n; ++i)
+        if (!(inv_freq[i] >= 0.0) || !std::isfinite(inv_freq[i]))
+            return fail(KVC_ERR_INVALID, "frequency %d is negative or not finite", i);
+    for (int i = 0; i < n; ++i) {
+        // whole turns drop out; the fraction times 2^64 is below 2^64 (its double is at most 1 - 2^-53)
+        double t = inv_freq[i] * 0.15915494309189535;  // 1 / (2 pi)
+        t -= std::floor(t);
+        turns[i] = static_cast<uint64_t>(std::nearbyint(std::ldexp(t, 64)));
+    }
+    return KVC_OK;
+}
+
+kvc_status kv_append_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                          int64_t v_stride, int n, int Hq, int Hkv, int head_dim, const void* q_weight,
+                          const void* k_weight, float eps, const uint64_t* turns, int rot_dim, int interleaved,
+                          const int32_t* positions, void* q_out, void* k_out, void* v_out, void* k_cache,
+                          void* v_cache, int num_blocks, int block_size, const int64_t* slot_mapping, void* stream) {
+    if (n < 0 || Hq < 1 || Hkv < 1) return fail(KVC_ERR_INVALID, "bad sizes");
+    if (Hq > 65535 || Hkv > 65535) return fail(KVC_ERR_UNSUPPORTED, "Hq and Hkv must be <= 65535");
+    if (head_dim != 64 && head_dim != 128) return fail(KVC_ERR_UNSUPPORTED, "head_dim %d not supported", head_dim);
+    if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 16)
+        return fail(KVC_ERR_UNSUPPORTED, "rot_dim %d is not a multiple of 16 up to head_dim", rot_dim);
+    if (interleaved != 0 && interleaved != 1) return fail(KVC_ERR_INVALID, "interleaved must be 0 or 1");
+    const bool cache = k_cache || v_cache || slot_mapping;
+    if (cache && block_size != kvc::kBlockSize) return fail(KVC_ERR_UNSUPPORTED, "block_size %d not supported", block_size);
+    if (n == 0) return KVC_OK;
+    if (!q || !k || !v || !q_out) return fail(KVC_ERR_INVALID, "null pointer");
+    if (rot_dim > 0 && (!turns || !positions)) return fail(KVC_ERR_INVALID, "rotation without turns or positions");
+    if (cache && (!k_cache || !v_cache || !slot_mapping))
+        return fail(KVC_ERR_INVALID, "k_cache, v_cache and slot_mapping: all or none");
+    if (cache && num_blocks < 1) return fail(KVC_ERR_INVALID, "num_blocks must be positive");
+    for (const void* ptr : {q, k, v, q_weight, k_weight, static_cast<const void*>(q_out), static_cast<const void*>(k_out),
+                            static_cast<const void*>(v_out), static_cast<const void*>(k_cache),
+                            static_cast<const void*>(v_cache)})
+        if (!aligned16(ptr)) return fail(KVC_ERR_INVALID, "device buffers must be 16-byte aligned");
+    const int64_t qrow = static_cast<int64_t>(Hq) * head_dim, krow = static_cast<int64_t>(Hkv) * head_dim;
+    if (q_stride % 8 || k_stride % 8 || v_stride % 8 || q_stride < qrow || k_stride < krow || v_stride < krow)
+        return fail(KVC_ERR_INVALID, "token strides must be multiples of 8 elements and hold a token's heads");
+    if ((q_out == q && q_stride != qrow) || (k_out == k && k_stride != krow) || (v_out == v && v_stride != krow))
+        return fail(KVC_ERR_INVALID, "in place only where the rows are packed");
+    if (cache) {
+        kvc_status st = checked([&]() -> kvc_status {
+            std::vector<int64_t> sl;
+            kvc_status e = copy_to_host(sl, slot_mapping, static_cast<size_t>(n), as_stream(stream));
+            if (e != KVC_OK) return e;
+            for (int t = 0; t < n; ++t)
+                if (sl[t] >= static_cast<int64_t>(num_blocks) * block_size)
+                    return fail(KVC_ERR_CAPACITY, "token %d: slot %lld beyond the pool", t, static_cast<long long>(sl[t]));
+            return KVC_OK;
+        });
+        if (st != KVC_OK) return st;
+    }
+    kvc::RopeArgs a;
+    a.q = static_cast<const __half*>(q);
+    a.k = static_cast<const __half*>(k);
+    a.v = static_cast<const __half*>(v);
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.n = n;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.D = head_dim;
+    a.q_weight = static_cast<const __half*>(q_weight);
+    a.k_weight = static_cast<const __half*>(k_weight);
+    a.eps = eps;
+    a.turns = turns;
+    a.rot_dim = rot_dim;
+    a.interleaved = interleaved;
+    a.positions = positions;
+    a.q_out = static_cast<__half*>(q_out);
+    a.k_out = static_cast<__half*>(k_out);
+    a.v_out = static_cast<__half*>(v_out);
+    a.k_cache = static_cast<__half*>(k_cache);
+    a.v_cache = static_cast<__half*>(v_cache);
+    a.num_blocks = num_blocks;
+    a.slots = slot_mapping;
+    cudaError_t e = kvc::device_error_word(&a.err);
+    if (e != cudaSuccess) return cuda_fail(e, "device error word");
+    e = kvc::launch_append_rope(a, as_stream(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "kv_append_rope launch");
+    return KVC_OK;
+}
+
+static kvc_status check_tree_shape(int B, int Hq, int Hkv, int head_dim, int block_size, int max_context_len, int T) {
+    kvc_status s = check_decode_shape(B, Hq, Hkv, head_dim, block_size, max_context_len);
+    if (s != KVC_OK) return s;
+    if (T < 1 || T > kvc::kMaxTreeNodes)
+        return fail(KVC_ERR_UNSUPPORTED, "trees of %d nodes not supported (1..%d)", T, kvc::kMaxTreeNodes);
+    return KVC_OK;
+}
+
+kvc_status paged_decode_tree_plan(int B, int Hq, int Hkv, int head_dim, int block_size, int max_context_len, int T,
+                                  size_t* workspace_bytes) {
+    kvc_status s = check_tree_shape(B, Hq, Hkv, head_dim, block_size, max_context_len, T);
+    if (s != KVC_OK) return s;
+    kvc::TreePlan plan;
+    cudaError_t e = kvc::tree_plan(B, Hq, Hkv, head_dim, max_context_len, T, &plan);
+    if (e != cudaSuccess) return cuda_fail(e, "tree plan");
+    if (workspace_bytes) *workspace_bytes = plan.workspace_bytes;
+    return KVC_OK;
+}
+
+kvc_status paged_decode_tree_attention(const void* q, const void* k_cache, const void* v_cache, int num_blocks,
+                                       const int32_t* block_table, int max_blocks, const int32_t* context_lens,
+                                       const uint64_t* masks, const int32_t* tree_lens, int T, int B, int Hq, int Hkv,
+                                       int head_dim, int block_size, int max_context_len, float scale, void* out,
+                                       int out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    kvc_status s = check_tree_shape(B, Hq, Hkv, head_dim, block_size, max_context_len, T);
+    if (s != KVC_OK || B == 0) return s;
+    if (!q || !k_cache || !v_cache || !block_table || !context_lens || !masks || !out)
+        return fail(KVC_ERR_INVALID, "null pointer");
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
+        return fail(KVC_ERR_INVALID, "q, caches and out must be 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(masks) & 7u) return fail(KVC_ERR_INVALID, "masks must be 8-byte aligned");
+    if (num_blocks < 1 || max_blocks < 1) return fail(KVC_ERR_INVALID, "num_blocks and max_blocks must be positive");
+    if (static_cast<int64_t>(num_blocks) * Hkv * block_size >= (int64_t(1) << 31))
+        return fail(KVC_ERR_UNSUPPORTED, "num_blocks * Hkv * block_size must be < 2^31");
+    if (static_cast<int64_t>(max_context_len) > static_cast<int64_t>(max_blocks) * block_size)
+        return fail(KVC_ERR_CAPACITY, "max_context_len %d beyond max_blocks * block_size", max_context_len);
+    if (out_dtype != KVC_F16 && out_dtype != KVC_F32) return fail(KVC_ERR_INVALID, "bad out_dtype");
+    if (!std::isfinite(scale)) return fail(KVC_ERR_INVALID, "scale is not finite");
+    s = checked([&]() -> kvc_status {
+        std::vector<int32_t> ctx, tree, table;
+        kvc_status e = copy_to_host(ctx, context_lens, static_cast<size_t>(B), as_stream(stream));
+        if (e == KVC_OK && tree_lens) e = copy_to_host(tree, tree_lens, static_cast<size_t>(B), as_stream(stream));
+        if (e == KVC_OK) e = copy_to_host(table, block_table, static_cast<size_t>(B) * max_blocks, as_stream(stream));
+        if (e != KVC_OK) return e;
+        for (int b = 0; b < B; ++b) {
+            const int32_t len = tree_lens ? tree[b] : T;
+            if (len < 0 || len > T) return fail(KVC_ERR_INVALID, "sequence %d: tree length %d outside [0, %d]", b, len, T);
+            if (ctx[b] < len || ctx[b] > max_context_len)
+                return fail(KVC_ERR_CAPACITY, "sequence %d: context length %d outside [%d, %d]", b, ctx[b], len, max_context_len);
+            for (int j = 0; j < (ctx[b] + block_size - 1) / block_size; ++j) {
+                const int32_t blk = table[static_cast<size_t>(b) * max_blocks + j];
+                if (blk < 0 || blk >= num_blocks)
+                    return fail(KVC_ERR_INVALID, "sequence %d: block-table entry %d = %d outside [0, %d)", b, j, blk, num_blocks);
+            }
+        }
+        return KVC_OK;
+    });
+    if (s != KVC_OK) return s;
+    kvc::TreePlan plan;
+    cudaError_t e = kvc::tree_plan(B, Hq, Hkv, head_dim, max_context_len, T, &plan);
+    if (e != cudaSuccess) return cuda_fail(e, "tree plan");
+    s = check_workspace(plan.workspace_bytes, workspace, workspace_bytes);
+    if (s != KVC_OK) return s;
+    kvc::TreeArgs a;
+    a.q = static_cast<const __half*>(q);
+    a.k_cache = static_cast<const __half*>(k_cache);
+    a.v_cache = static_cast<const __half*>(v_cache);
+    a.num_blocks = num_blocks;
+    a.block_table = block_table;
+    a.max_blocks = max_blocks;
+    a.context_lens = context_lens;
+    a.masks = masks;
+    a.tree_lens = tree_lens;
+    a.T = T;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.D = head_dim;
+    a.max_context_len = max_context_len;
+    a.scale = scale;
+    a.out = out;
+    a.out_f32 = out_dtype == KVC_F32;
+    a.workspace = workspace;
+    a.workspace_bytes = workspace_bytes;
+    e = kvc::device_error_word(&a.err);
+    if (e != cudaSuccess) return cuda_fail(e, "device error word");
+    e = kvc::launch_tree(a, as_stream(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "paged_decode_tree_attention launch");
+    return KVC_OK;
+}
+
+kvc_status draft_tree_verify(const void* target_probs, int64_t p_stride, const void* draft_probs, int64_t q_stride,
+                             int prob_dtype, const int32_t* tokens, const int32_t* parents, const int32_t* tree_lens,
+                             const float* uniforms, int B, int T, int V, int distinct, int32_t* path,
+                             int32_t* path_len, int32_t* next_token, void* stream) {
+    if (B < 0 || V < 1) return fail(KVC_ERR_INVALID, "bad sizes");
+    if (T < 1 || T > kvc::kMaxTreeNodes)
+        return fail(KVC_ERR_UNSUPPORTED, "trees of %d nodes not supported (1..%d)", T, kvc::kMaxTreeNodes);
+    if (B > 65535 || V > (1 << 24)) return fail(KVC_ERR_UNSUPPORTED, "B must be <= 65535 and V <= 2^24");
+    if (prob_dtype != KVC_F16 && prob_dtype != KVC_F32) return fail(KVC_ERR_INVALID, "bad prob_dtype");
+    if (distinct != 0 && distinct != 1) return fail(KVC_ERR_INVALID, "distinct must be 0 or 1");
+    if (p_stride < V || q_stride < V) return fail(KVC_ERR_INVALID, "row strides must be at least V");
+    if (B == 0) return KVC_OK;
+    if (!target_probs || !draft_probs || !tokens || !parents || !uniforms || !path || !path_len || !next_token)
+        return fail(KVC_ERR_INVALID, "null pointer");
+    const uintptr_t size = prob_dtype == KVC_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(target_probs) % size || reinterpret_cast<uintptr_t>(draft_probs) % size)
+        return fail(KVC_ERR_INVALID, "probabilities must be aligned to their type");
+    kvc_status s = checked([&]() -> kvc_status {
+        std::vector<int32_t> tok, par, len;
+        const size_t n = static_cast<size_t>(B) * T;
+        kvc_status e = copy_to_host(tok, tokens, n, as_stream(stream));
+        if (e == KVC_OK) e = copy_to_host(par, parents, n, as_stream(stream));
+        if (e == KVC_OK && tree_lens) e = copy_to_host(len, tree_lens, static_cast<size_t>(B), as_stream(stream));
+        if (e != KVC_OK) return e;
+        for (int b = 0; b < B; ++b) {
+            const int32_t nodes = tree_lens ? len[b] : T;
+            if (nodes < 0 || nodes > T) return fail(KVC_ERR_INVALID, "sequence %d: tree length %d outside [0, %d]", b, nodes, T);
+            for (int t = 1; t < nodes; ++t) {
+                const size_t at = static_cast<size_t>(b) * T + t;
+                if (par[at] < 0 || par[at] >= t) return fail(KVC_ERR_INVALID, "sequence %d: parent %d of node %d", b, par[at], t);
+                if (tok[at] < 0 || tok[at] >= V) return fail(KVC_ERR_INVALID, "sequence %d: token %d of node %d", b, tok[at], t);
+            }
+        }
+        return KVC_OK;
+    });
+    if (s != KVC_OK) return s;
+    kvc::VerifyArgs a;
+    a.p = target_probs;
+    a.q = draft_probs;
+    a.p_stride = p_stride;
+    a.q_stride = q_stride;
+    a.probs_f32 = prob_dtype == KVC_F32;
+    a.tokens = tokens;
+    a.parents = parents;
+    a.tree_lens = tree_lens;
+    a.uniforms = uniforms;
+    a.B = B;
+    a.T = T;
+    a.V = V;
+    a.distinct = distinct;
+    a.path = path;
+    a.path_len = path_len;
+    a.next_token = next_token;
+    cudaError_t e = kvc::device_error_word(&a.err);
+    if (e != cudaSuccess) return cuda_fail(e, "device error word");
+    e = kvc::launch_tree_verify(a, as_stream(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "draft_tree_verify launch");
+    return KVC_OK;
+}
+
+kvc_status kv_tree_commit(kvc_handle h, const int32_t* block_table, int max_blocks, const int32_t* context_lens,
+                          const int32_t* tree_lens, const int32_t* path, const int32_t* path_len, int P, int B,
+                          int32_t* new_context_lens, void* stream) {
+    if (!h) return fail(KVC_ERR_INVALID, "null handle");
+    if (!h->k_pool) return fail(KVC_ERR_INVALID, "host-only cache has no device pools");
+    if (B < 0 || max_blocks < 1) return fail(KVC_ERR_INVALID, "bad sizes");
+    if (P < 1 || P > kvc::kMaxTreeNodes)
+        return fail(KVC_ERR_UNSUPPORTED, "paths of %d nodes not supported (1..%d)", P, kvc::kMaxTreeNodes);
+    if (B > 65535) return fail(KVC_ERR_UNSUPPORTED, "B must be <= 65535");
+    if (B == 0) return KVC_OK;
+    if (!block_table || !context_lens || !path || !path_len || !new_context_lens) return fail(KVC_ERR_INVALID, "null pointer");
+    if (new_context_lens == context_lens) return fail(KVC_ERR_INVALID, "new_context_lens must not be context_lens");
+    kvc_status s = checked([&]() -> kvc_status {
+        std::vector<int32_t> ctx, tree, nodes, len, table;
+        kvc_status e = copy_to_host(ctx, context_lens, static_cast<size_t>(B), as_stream(stream));
+        if (e == KVC_OK && tree_lens) e = copy_to_host(tree, tree_lens, static_cast<size_t>(B), as_stream(stream));
+        if (e == KVC_OK) e = copy_to_host(nodes, path, static_cast<size_t>(B) * P, as_stream(stream));
+        if (e == KVC_OK) e = copy_to_host(len, path_len, static_cast<size_t>(B), as_stream(stream));
+        if (e == KVC_OK) e = copy_to_host(table, block_table, static_cast<size_t>(B) * max_blocks, as_stream(stream));
+        if (e != KVC_OK) return e;
+        for (int b = 0; b < B; ++b) {
+            const int32_t size = tree_lens ? tree[b] : P;
+            if (size < 0 || size > kvc::kMaxTreeNodes || ctx[b] < size ||
+                ctx[b] > static_cast<int64_t>(max_blocks) * kvc::kBlockSize)
+                return fail(KVC_ERR_CAPACITY, "sequence %d: context %d with a tree of %d", b, ctx[b], size);
+            if (len[b] < 0 || len[b] > P || len[b] > size)
+                return fail(KVC_ERR_INVALID, "sequence %d: path length %d", b, len[b]);
+            int32_t last = -1;
+            for (int i = 0; i < len[b]; ++i) {
+                const int32_t node = nodes[static_cast<size_t>(b) * P + i];
+                if (node <= last || node >= size || (i == 0 && node != 0))
+                    return fail(KVC_ERR_INVALID, "sequence %d: node %d at place %d of its path", b, node, i);
+                last = node;
+                if (node == i) continue;
+                const int32_t base = ctx[b] - size;
+                for (const int32_t pos : {base + i, base + node}) {
+                    const int32_t blk = table[static_cast<size_t>(b) * max_blocks + pos / kvc::kBlockSize];
+                    if (blk < 0 || blk >= h->cfg.num_blocks)
+                        return fail(KVC_ERR_INVALID, "sequence %d: block %d of position %d", b, blk, pos);
+                }
+            }
+        }
+        return KVC_OK;
+    });
+    if (s != KVC_OK) return s;
+    kvc::CommitArgs a;
+    a.k_pool = static_cast<__half*>(h->k_pool);
+    a.v_pool = static_cast<__half*>(h->v_pool);
+    a.L = h->cfg.num_layers;
+    a.num_blocks = h->cfg.num_blocks;
+    a.Hkv = h->cfg.num_kv_heads;
+    a.D = h->cfg.head_dim;
+    a.block_table = block_table;
+    a.max_blocks = max_blocks;
+    a.context_lens = context_lens;
+    a.tree_lens = tree_lens;
+    a.path = path;
+    a.path_len = path_len;
+    a.P = P;
+    a.B = B;
+    a.new_context_lens = new_context_lens;
+    cudaError_t e = kvc::device_error_word(&a.err);
+    if (e != cudaSuccess) return cuda_fail(e, "device error word");
+    e = kvc::launch_tree_commit(a, as_stream(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "kv_tree_commit launch");
     return KVC_OK;
 }
 

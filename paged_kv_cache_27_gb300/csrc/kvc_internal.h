@@ -135,6 +135,97 @@ void set_launch_overlap(int on);
 cudaError_t trace_read(void* host, int cap, int* n, int clear);
 int launch_overlap();
 
+// ---- tree-drafted decoding -----------------------------------------------------
+constexpr int kMaxTreeNodes = 64;  // a node's mask is one 64-bit word
+
+// query / key norm, position rotation and append (append_rope.cu)
+struct RopeArgs {
+    const __half* q;
+    const __half* k;
+    const __half* v;
+    int64_t q_stride, k_stride, v_stride;
+    int64_t n;
+    int Hq, Hkv, D;
+    const __half* q_weight;  // null: no norm of the query / key rows
+    const __half* k_weight;
+    float eps;
+    const uint64_t* turns;
+    int rot_dim, interleaved;
+    const int32_t* positions;
+    __half* q_out;
+    __half* k_out;  // null, or packed copies of the key / value rows
+    __half* v_out;
+    __half* k_cache;  // null with slots
+    __half* v_cache;
+    int num_blocks;
+    const int64_t* slots;
+    unsigned* err;
+};
+cudaError_t launch_append_rope(const RopeArgs& a, cudaStream_t stream);
+
+// attention of a tree of drafted tokens (tree_attention.cu)
+struct TreePlan {
+    int row_pairs;   // pairs of 128-row tiles per (sequence, KV head)
+    int chunk;       // key tiles of 128 per CTA
+    int max_chunks;  // chunks of the longest context; > 1: partial states and the combine kernel
+    size_t workspace_bytes;
+};
+cudaError_t tree_plan(int B, int Hq, int Hkv, int D, int max_context_len, int T, TreePlan* plan);
+struct TreeArgs {
+    const __half* q;
+    const __half* k_cache;
+    const __half* v_cache;
+    int num_blocks;
+    const int32_t* block_table;
+    int max_blocks;
+    const int32_t* context_lens;
+    const uint64_t* masks;
+    const int32_t* tree_lens;  // null: T nodes each
+    int T, B, Hq, Hkv, D, max_context_len;
+    float scale;
+    void* out;
+    int out_f32;
+    void* workspace;
+    size_t workspace_bytes;
+    unsigned* err;
+};
+cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream);
+
+// verification of drafted tokens (tree_verify.cu)
+struct VerifyArgs {
+    const void* p;
+    const void* q;
+    int64_t p_stride, q_stride;
+    int probs_f32;
+    const int32_t* tokens;
+    const int32_t* parents;
+    const int32_t* tree_lens;
+    const float* uniforms;
+    int B, T, V, distinct;
+    int32_t* path;
+    int32_t* path_len;
+    int32_t* next_token;
+    unsigned* err;
+};
+cudaError_t launch_tree_verify(const VerifyArgs& a, cudaStream_t stream);
+
+// the kept path's rows to the end of the context (tree_commit.cu)
+struct CommitArgs {
+    __half* k_pool;
+    __half* v_pool;
+    int L, num_blocks, Hkv, D;
+    const int32_t* block_table;
+    int max_blocks;
+    const int32_t* context_lens;
+    const int32_t* tree_lens;
+    const int32_t* path;
+    const int32_t* path_len;
+    int P, B;
+    int32_t* new_context_lens;
+    unsigned* err;
+};
+cudaError_t launch_tree_commit(const CommitArgs& a, cudaStream_t stream);
+
 // Records `msg` as the calling thread's last error (kvc_last_error_string) and returns `status`.
 int set_last_error(int status, const char* msg);
 

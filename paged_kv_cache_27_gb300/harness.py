@@ -11,10 +11,11 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (KvcConfig, kv_append, kv_block_alloc, kv_block_release, kv_block_share, kv_cache_create,
-               kv_cache_destroy, kv_copy_blocks, kvc_copy_async, kv_slot_mapping, kv_step_prepare,
-               paged_decode_append_attention, paged_decode_attention, paged_decode_plan, paged_decode_workspace_init,
-               prefill_attention)
+from . import (KvcConfig, draft_tree_verify, kv_append, kv_append_rope, kv_block_alloc, kv_block_release,
+               kv_block_share, kv_cache_create, kv_cache_destroy, kv_copy_blocks, kv_rope_turns, kv_tree_commit,
+               kv_tree_masks, kvc_copy_async, kv_slot_mapping, kv_step_prepare, paged_decode_append_attention,
+               paged_decode_attention, paged_decode_plan, paged_decode_tree_attention, paged_decode_tree_plan,
+               paged_decode_workspace_init, prefill_attention)
 
 F16_NAN = 0x7E00  # a quiet-NaN bit pattern used to poison cache slots nobody owns
 
@@ -223,6 +224,74 @@ def prefill_then_decode(wl, causal=True, device="cuda", out_dtype=torch.float32,
         return {"prefill_out": out, "decode_out": dec, "k_cache": k_pool[0], "v_cache": v_pool[0]}
     finally:
         kv_cache_destroy(h)
+
+
+class TreeSession:
+    """One step of tree-drafted decoding on a TreeWorkload: per layer kv_append_rope and paged_decode_tree_attention
+    over the drafted nodes, then draft_tree_verify and kv_tree_commit.
+
+    The step reads the sequences' lengths on the device only, and every call is prepared once, so it can be captured
+    into a graph.  After it, `context_lens` (lengths with the drafted tree) is superseded by `new_context_lens` (with the
+    kept path)."""
+
+    def __init__(self, wl, device="cuda", out_dtype=torch.float16):
+        self.wl, self.device = wl, device
+        B, T, L, Hq, Hkv, D = len(wl.hist), wl.T, wl.L, wl.Hq, wl.Hkv, wl.D
+        cfg = KvcConfig(num_layers=L, num_blocks=wl.NB, num_kv_heads=Hkv, head_dim=D, block_size=wl.bs)
+        self.k_pool, self.v_pool = _dev(wl.k_pool, device), _dev(wl.v_pool, device)
+        self.h = kv_cache_create(cfg, self.k_pool, self.v_pool)
+        self.block_table, self.tree_lens = _dev(wl.block_table, device), _dev(wl.tree_lens, device)
+        self.context_lens = _dev(wl.ctx, device)
+        self.max_ctx = int(wl.block_table.shape[1]) * wl.bs
+        masks, depths = kv_tree_masks(wl.parents, wl.tree_lens)
+        self.masks = _dev(masks, device)
+        self.positions = _dev((wl.hist[:, None] + depths).reshape(-1).astype(np.int32), device)
+        slots = kv_slot_mapping(wl.block_table, wl.hist, np.full(B, T, np.int32), wl.bs).reshape(B, T)
+        slots[np.arange(T)[None] >= wl.tree_lens[:, None]] = -1  # entries behind a tree are not appended
+        self.slots = _dev(slots.reshape(-1), device)
+        self.turns = _dev(kv_rope_turns(wl.inv_freq), device)
+        self.qkv = _dev(wl.qkv, device)
+        self.q_weight, self.k_weight = _dev(wl.q_weight, device), _dev(wl.k_weight, device)
+        self.tokens, self.parents = _dev(wl.tokens, device), _dev(wl.parents, device)
+        self.uniforms, self.p, self.q = _dev(wl.uniforms, device), _dev(wl.p, device), _dev(wl.q, device)
+        self.q_rot = torch.zeros((L, B, T, Hq, D), dtype=torch.float16, device=device)
+        self.out = torch.zeros((L, B, T, Hq, D), dtype=out_dtype, device=device)
+        ws = paged_decode_tree_plan(B, Hq, Hkv, D, self.max_ctx, T)
+        self.workspace = torch.empty(max(ws, 16), dtype=torch.uint8, device=device)
+        i32 = dict(dtype=torch.int32, device=device)
+        self.path, self.path_len = torch.zeros((B, T), **i32), torch.zeros(B, **i32)
+        self.next_token, self.new_context_lens = torch.zeros(B, **i32), torch.zeros(B, **i32)
+        self._calls = []
+        for layer in range(L):
+            q, k, v = (x.unflatten(1, (-1, D)) for x in self.qkv[layer].split((Hq * D, Hkv * D, Hkv * D), 1))
+            self._calls.append(kv_append_rope(
+                q, k, v, self.positions, self.turns, self.q_rot[layer].view(B * T, Hq, D), self.k_pool[layer],
+                self.v_pool[layer], self.slots, q_weight=self.q_weight[layer], k_weight=self.k_weight[layer],
+                eps=wl.eps, prepare=True))
+            self._calls.append(paged_decode_tree_attention(
+                self.q_rot[layer], self.k_pool[layer], self.v_pool[layer], self.block_table, self.context_lens,
+                self.masks, wl.scale, self.out[layer], self.workspace, self.max_ctx, tree_lens=self.tree_lens,
+                prepare=True))
+        self._calls.append(draft_tree_verify(self.p, self.q, self.tokens, self.parents, self.uniforms, self.path,
+                                             self.path_len, self.next_token, tree_lens=self.tree_lens, prepare=True))
+        self._calls.append(kv_tree_commit(self.h, self.block_table, self.context_lens, self.path, self.path_len,
+                                          self.new_context_lens, tree_lens=self.tree_lens, prepare=True))
+
+    def step(self, stream=None):
+        """The whole step on `stream` or the current one (asynchronous)."""
+        for call in self._calls:
+            call(stream)
+
+    def close(self):
+        if self.h:
+            kv_cache_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
 
 
 def _align16(n: int) -> int:

@@ -1,0 +1,196 @@
+"""Pins of the fp64 definitions of tree-drafted decoding (oracle/tree.py), and the library's host helpers (no GPU)."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+
+import oracle
+import paged_kv_cache_27_gb300 as kvc
+import workloads
+from oracle import tree
+
+
+def random_parents(rng, B, T):
+    par = np.full((B, T), -1, np.int32)
+    for t in range(1, T):
+        par[:, t] = rng.integers(0, t, B)
+    return par
+
+
+def test_chain_tree_is_the_causal_multi_token_decode():
+    wl = workloads.multi_token_decode(1, [5, 16, 40], 5, Hq=4, Hkv=2)
+    masks, depths = tree.tree_masks(np.tile(np.arange(-1, 4, dtype=np.int32), (3, 1)))
+    out, _ = tree.tree_attention(wl.q, wl.k_pool, wl.v_pool, wl.block_table, wl.ctx, masks, [5] * 3, wl.scale)
+    ref = oracle.decode_multi(wl.q, wl.k_pool, wl.v_pool, wl.block_table, wl.ctx, wl.scale)
+    assert np.abs(out - ref).max() < 1e-12
+    assert (depths == np.arange(5)).all()
+
+
+def test_rotation_depends_on_the_distance_alone():
+    rng = np.random.default_rng(2)
+    freq = 1e4 ** (-np.arange(0, 64, 2) / 64)
+    for inter in (False, True):
+        x, y = rng.standard_normal((2, 1, 1, 64))
+        dots = [float((tree.norm_rotate(x, None, 0, np.array([[p]]) * freq, inter)
+                       * tree.norm_rotate(y, None, 0, np.array([[p + 7]]) * freq, inter)).sum()) for p in (0, 3, 100)]
+        assert np.ptp(dots) < 1e-10
+        assert abs(dots[0] - float((x * tree.norm_rotate(y, None, 0, 7 * freq[None], inter)).sum())) < 1e-12
+    z = tree.norm_rotate(x, np.ones(64), 0.0, np.zeros((1, 0)), False)
+    assert abs((z * z).mean() - 1) < 1e-12
+
+
+@pytest.mark.parametrize("distinct", [False, True])
+def test_verification_emits_the_targets_distribution(distinct):
+    """Two drafted children of the root and the draw, over every combination of a grid of uniforms: the first token
+    that the step emits (a kept child's or the drawn one) is distributed as the target's row."""
+    V, n = 3, 60
+    p, q = np.array([0.2, 0.5, 0.3]), np.array([0.5, 0.3, 0.2])
+    rows = lambda r: np.stack([r] * 3)  # noqa: E731
+    grid = (np.arange(n) + 0.5) / n
+    mass = np.zeros(V)
+    for a in range(V):
+        for b in range(V):
+            if distinct and a == b:
+                continue
+            weight = q[a] * (q[b] / (1 - q[a]) if distinct else q[b])  # how often the draft gives these two
+            tokens, parents = [0, a, b], [-1, 0, 0]
+            for u1 in grid:
+                for u2 in grid:
+                    for u0 in grid[::6]:
+                        path, nxt = tree.verify(rows(p), rows(q), tokens, parents, [u0, u1, u2], distinct)
+                        emitted = tokens[path[1]] if len(path) > 1 else nxt
+                        mass[emitted] += weight / (n * n * len(grid[::6]))
+    # a kept or refused trial is off by at most one grid step per uniform
+    assert np.abs(mass - p).max() < 2.0 / n + 1.0 / len(grid[::6]) * 0.3, mass
+
+
+def test_commit_moves_the_path_and_nothing_else():
+    rng = np.random.default_rng(3)
+    pool = rng.standard_normal((2, 6, 2, 16, 4))
+    before = pool.copy()
+    table = np.array([[4, 1, 0]])
+    new = tree.commit([pool], table, [40], [9], [[0, 1, 4, 8]], [4])
+    rows = lambda a, n: tree.rows_of(a, table[0], n)  # noqa: E731
+    assert new[0] == 40 - 9 + 4
+    for lay in range(2):
+        old, got = rows(before[lay], 40), rows(pool[lay], 40)
+        assert (got[:33] == old[:33]).all()  # history and the root; node 1 stays
+        assert (got[33] == old[31 + 4]).all() and (got[34] == old[31 + 8]).all()
+        assert (got[35:] == old[35:]).all()
+    assert (pool[:, [2, 3, 5]] == before[:, [2, 3, 5]]).all()
+
+
+# ---------------------------------------------------------------- host helpers of the library
+@pytest.mark.parametrize("T", [1, 2, 7, 63, 64])
+def test_tree_masks_match_the_definition(T):
+    rng = np.random.default_rng(T)
+    par = random_parents(rng, 5, T)
+    lens = np.array([T, 0, 1, rng.integers(0, T + 1), T], np.int32)
+    for ln in (None, lens):
+        masks, depths = kvc.kv_tree_masks(par, ln)
+        ref_m, ref_d = tree.tree_masks(par, ln)
+        assert (masks.view(np.uint64) == ref_m).all() and (depths == ref_d).all()
+
+
+def test_tree_masks_refuse_bad_trees():
+    for par, lens, name in (([[-1, 1]], None, "INVALID"), ([[-1, -1]], None, "INVALID"), ([[-1, 0, 5]], None, "INVALID"),
+                            ([[-1, 0]], [3], "INVALID"), ([[-1, 0]], [-1], "INVALID"), ([[0] * 65], None, "UNSUPPORTED")):
+        with pytest.raises(kvc.KvcError) as e:
+            kvc.kv_tree_masks(np.array(par, np.int32), lens)
+        assert e.value.name == "KVC_ERR_" + name
+    kvc.kv_tree_masks(np.array([[7, 0, 99]], np.int32), [2])  # the root's parent and entries behind a tree: not read
+    assert kvc.kv_tree_masks(np.zeros((0, 4), np.int32))[0].shape == (0, 4)
+
+
+def test_rope_turns_keep_far_angles():
+    freq = 1e6 ** (-np.arange(0, 128, 2, dtype=np.float64) / 128)
+    turns = kvc.kv_rope_turns(freq).view(np.uint64)
+    for pos in (1, 4095, 131072, 2 ** 31 - 1):
+        for f, t in zip(freq.tolist(), turns.tolist()):
+            got = (pos * t % 2 ** 64) / 2 ** 64
+            want = math.fmod(pos * f, 2 * math.pi) / (2 * math.pi)
+            d = abs(got - want) % 1.0
+            # a few roundings (2^-53) of the angle in turns on both sides, and the integer's own: half a unit of
+            # 2^-64 turns per position
+            assert min(d, 1 - d) < 6 * 2.0 ** -53 * (pos * f / (2 * math.pi) + 1) + pos * 2.0 ** -65, (pos, f)
+    assert kvc.kv_rope_turns([0.0, 2 * math.pi]).view(np.uint64)[0] == 0
+    for bad in ([-1.0], [float("nan")], [float("inf")]):
+        with pytest.raises(kvc.KvcError):
+            kvc.kv_rope_turns(bad)
+
+
+# ---------------------------------------------------------------- refusals, before anything touches a device
+P = ctypes.c_void_p(4096)  # a non-null, aligned address that no refused call follows
+ODD = ctypes.c_void_p(4104)
+
+
+def refused(fn, args, status, text=""):
+    got = getattr(kvc._lib, fn)(*args)
+    assert kvc.STATUS[got] == "KVC_ERR_" + status, (kvc.STATUS[got], kvc._lib.kvc_last_error_string())
+    assert text in kvc._lib.kvc_last_error_string().decode()
+
+
+def test_append_rope_refusals():
+    base = dict(q=P, qs=256, k=P, ks=128, v=P, vs=128, n=2, Hq=4, Hkv=2, D=64, qw=None, kw=None, eps=1e-6, turns=P,
+                rot=64, inter=0, pos=P, qo=ctypes.c_void_p(8192), ko=None, vo=None, kc=P, vc=P, NB=4, bs=16, slots=P,
+                st=None)
+    for change, status in ((dict(n=-1), "INVALID"), (dict(Hq=0), "INVALID"), (dict(D=96), "UNSUPPORTED"),
+                           (dict(rot=24), "UNSUPPORTED"), (dict(rot=80), "UNSUPPORTED"), (dict(rot=-16), "UNSUPPORTED"),
+                           (dict(inter=2), "INVALID"), (dict(bs=32), "UNSUPPORTED"), (dict(q=None), "INVALID"),
+                           (dict(qo=None), "INVALID"), (dict(turns=None), "INVALID"), (dict(pos=None), "INVALID"),
+                           (dict(slots=None), "INVALID"), (dict(kc=None), "INVALID"), (dict(NB=0), "INVALID"),
+                           (dict(q=ODD), "INVALID"), (dict(kw=ODD), "INVALID"), (dict(vo=ODD), "INVALID"),
+                           (dict(qs=250), "INVALID"), (dict(qs=248), "INVALID"), (dict(ks=64), "INVALID"),
+                           (dict(qs=512, qo=P), "INVALID"), (dict(Hkv=70000), "UNSUPPORTED")):
+        refused("kv_append_rope", list({**base, **change}.values()), status)
+    assert kvc._lib.kv_append_rope(*{**base, "n": 0}.values()) == 0
+
+
+def test_tree_attention_refusals():
+    base = dict(q=P, k=P, v=P, NB=64, table=P, mb=8, ctx=P, masks=P, lens=None, T=4, B=2, Hq=4, Hkv=2, D=64, bs=16,
+                most=128, scale=0.125, out=P, od=0, ws=None, wb=0, st=None)
+    for change, status in ((dict(T=0), "UNSUPPORTED"), (dict(T=65), "UNSUPPORTED"), (dict(Hq=5), "INVALID"),
+                           (dict(Hq=130), "UNSUPPORTED"), (dict(D=80), "UNSUPPORTED"), (dict(bs=8), "UNSUPPORTED"),
+                           (dict(masks=None), "INVALID"), (dict(ctx=None), "INVALID"), (dict(out=ODD), "INVALID"),
+                           (dict(masks=ctypes.c_void_p(4100)), "INVALID"), (dict(most=129), "CAPACITY"),
+                           (dict(od=2), "INVALID"), (dict(NB=0), "INVALID"), (dict(NB=2 ** 26), "UNSUPPORTED"),
+                           (dict(scale=float("nan")), "INVALID"), (dict(B=-1), "INVALID"), (dict(B=70000), "UNSUPPORTED")):
+        refused("paged_decode_tree_attention", list({**base, **change}.values()), status)
+    assert kvc._lib.paged_decode_tree_attention(*{**base, "B": 0}.values()) == 0
+    with pytest.raises(kvc.KvcError):
+        kvc.paged_decode_tree_plan(1, 4, 2, 64, 100, 65)
+
+
+def test_verify_refusals():
+    base = dict(p=P, ps=100, q=P, qs=100, dt=1, tok=P, par=P, lens=None, u=P, B=2, T=4, V=100, distinct=0, path=P,
+                plen=P, nxt=P, st=None)
+    for change, status in ((dict(V=0), "INVALID"), (dict(T=0), "UNSUPPORTED"), (dict(T=65), "UNSUPPORTED"),
+                           (dict(ps=99), "INVALID"), (dict(qs=99), "INVALID"), (dict(dt=2), "INVALID"),
+                           (dict(distinct=2), "INVALID"), (dict(tok=None), "INVALID"), (dict(nxt=None), "INVALID"),
+                           (dict(p=ctypes.c_void_p(4098)), "INVALID"), (dict(B=-1), "INVALID"),
+                           (dict(V=2 ** 25, ps=2 ** 25, qs=2 ** 25), "UNSUPPORTED")):
+        refused("draft_tree_verify", list({**base, **change}.values()), status)
+    assert kvc._lib.draft_tree_verify(*{**base, "B": 0}.values()) == 0
+
+
+def test_commit_refusals():
+    h = kvc.kv_cache_create(kvc.KvcConfig(1, 4, 2, 64))
+    try:
+        out = ctypes.c_void_p(8192)
+        refused("kv_tree_commit", (None, P, 4, P, None, P, P, 4, 1, out, None), "INVALID", "null handle")
+        refused("kv_tree_commit", (h, P, 4, P, None, P, P, 4, 1, out, None), "INVALID", "host-only")
+    finally:
+        kvc.kv_cache_destroy(h)
+    hp = ctypes.c_void_p()
+    cfg = kvc.KvcConfig(1, 4, 2, 64)._c()
+    assert kvc._lib.kv_cache_create(ctypes.byref(cfg), P, P, ctypes.byref(hp)) == 0  # never followed below
+    base = dict(h=hp, table=P, mb=4, ctx=P, lens=None, path=P, plen=P, P=4, B=1, new=ctypes.c_void_p(8192), st=None)
+    try:
+        for change, status in ((dict(P=0), "UNSUPPORTED"), (dict(P=65), "UNSUPPORTED"), (dict(new=P), "INVALID"),
+                               (dict(path=None), "INVALID"), (dict(mb=0), "INVALID"), (dict(B=-1), "INVALID"),
+                               (dict(B=70000), "UNSUPPORTED")):
+            refused("kv_tree_commit", list({**base, **change}.values()), status)
+        assert kvc._lib.kv_tree_commit(*{**base, "B": 0}.values()) == 0
+    finally:
+        kvc.kv_cache_destroy(hp)

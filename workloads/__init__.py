@@ -364,3 +364,78 @@ def multi_token_decode(seed, ctx, T, Hq=14, Hkv=2, D=64, bs=16) -> MultiTokenWor
         name=f"multi_{seed}_T{T}", T=T, Hq=Hq, Hkv=Hkv, D=D, bs=bs, scale=1.0 / float(np.sqrt(D)), NB=NB,
         q=normal_f16(rng, (len(ctx), T, Hq, D)), k_pool=normal_f16(rng, (NB, Hkv, bs, D)),
         v_pool=normal_f16(rng, (NB, Hkv, bs, D)), block_table=table, ctx=ctx)
+
+
+@dataclass
+class TreeWorkload:
+    """One step of tree-drafted decoding: histories in a paged cache, a drafted tree per sequence, the projected rows
+    of its nodes for every layer, and the target's and the draft's probabilities behind every node."""
+
+    name: str
+    L: int
+    T: int
+    Hq: int
+    Hkv: int
+    D: int
+    bs: int
+    NB: int
+    V: int
+    scale: float
+    eps: float
+    hist: np.ndarray         # int32 [B] tokens before the tree
+    tree_lens: np.ndarray    # int32 [B]
+    block_table: np.ndarray  # int32 [B][max_blocks], -1 behind a sequence's blocks
+    parents: np.ndarray      # int32 [B][T]
+    tokens: np.ndarray       # int32 [B][T]
+    uniforms: np.ndarray     # float32 [B][T]
+    p: np.ndarray            # float32 [B][T][V]
+    q: np.ndarray
+    qkv: np.ndarray          # fp16 [L][B * T][(Hq + 2 Hkv) * D]
+    q_weight: np.ndarray     # fp16 [L][D]
+    k_weight: np.ndarray
+    inv_freq: np.ndarray     # float64 [D / 2]
+    k_pool: np.ndarray       # fp16 [L][NB][Hkv][bs][D], histories in place
+    v_pool: np.ndarray
+
+    @property
+    def ctx(self) -> np.ndarray:
+        return (self.hist + self.tree_lens).astype(np.int32)
+
+
+def tree_decode(seed, hist, tree_lens, T, L=1, Hq=14, Hkv=2, D=64, V=301, bs=16) -> TreeWorkload:
+    """Histories of `hist` tokens and trees of `tree_lens` nodes (at most T) on seeded-permuted blocks."""
+    rng = np.random.default_rng([48, seed])
+    hist, lens = np.array(hist, np.int32), np.array(tree_lens, np.int32)
+    B = len(hist)
+    nblk = [_ceil_div(int(h) + T, bs) for h in hist]
+    NB = sum(nblk) + 2
+    perm = rng.permutation(NB).astype(np.int32)
+    table = np.full((B, max(nblk)), -1, dtype=np.int32)
+    a = 0
+    for b, n in enumerate(nblk):
+        table[b, :n] = perm[a:a + n]
+        a += n
+    parents = np.full((B, T), -1, np.int32)
+    for t in range(1, T):
+        parents[:, t] = np.maximum(rng.integers(0, t, B), t // 2 - 1)
+
+    def rows():
+        x = np.exp(2.0 * rng.standard_normal((B, T, V)))
+        return (x / x.sum(-1, keepdims=True)).astype(np.float32)
+    p, d = rows(), rows()
+    q = 0.6 * p + 0.4 * d
+    q = (q / q.sum(-1, keepdims=True)).astype(np.float32)
+    tokens = np.zeros((B, T), np.int32)
+    for b in range(B):
+        for t in range(1, T):
+            c = np.cumsum(q[b, parents[b, t]].astype(np.float64))
+            tokens[b, t] = np.searchsorted(c, rng.random() * c[-1], side="right")
+    return TreeWorkload(
+        name=f"tree_{seed}_T{T}", L=L, T=T, Hq=Hq, Hkv=Hkv, D=D, bs=bs, NB=NB, V=V, scale=1.0 / float(np.sqrt(D)),
+        eps=1e-6, hist=hist, tree_lens=lens, block_table=table, parents=parents, tokens=tokens,
+        uniforms=rng.random((B, T), dtype=np.float32), p=p, q=q,
+        qkv=normal_f16(rng, (L, B * T, (Hq + 2 * Hkv) * D)),
+        q_weight=(1 + 0.2 * rng.standard_normal((L, D))).astype(np.float16),
+        k_weight=(1 + 0.2 * rng.standard_normal((L, D))).astype(np.float16),
+        inv_freq=1e4 ** (-np.arange(0, D, 2, dtype=np.float64) / D),
+        k_pool=normal_f16(rng, (L, NB, Hkv, bs, D)), v_pool=normal_f16(rng, (L, NB, Hkv, bs, D)))
