@@ -742,18 +742,51 @@ def kv_rope_turns(inv_freq) -> np.ndarray:
     return turns
 
 
+# the current device's index (the underscored form skips a wrapper, 0.1 µs a call)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _same_device(*tensors) -> None:
     """Every tensor given (None: left out) is on the current device, where the library's kernels run."""
     devices = {t.device for t in tensors if t is not None}
     if len(devices) > 1:
         raise ValueError("tensors are on several devices: " + ", ".join(sorted(map(str, devices))))
     for d in devices:
-        if d.type == "cuda" and d.index != torch.cuda.current_device():
-            raise ValueError(f"tensors are on {d}, the current device is cuda:{torch.cuda.current_device()}")
+        if d.type == "cuda" and d.index != _current_device():
+            raise ValueError(f"tensors are on {d}, the current device is cuda:{_current_device()}")
+
+
+def _ready(dev: int, dtype, *tensors) -> bool:
+    """Every tensor given is a contiguous CUDA tensor of the type on device dev: the test of a call's common case in one
+    go.  Where it fails, the call's own checks name what is wrong."""
+    for t in tensors:
+        if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+            return False
+    return True
+
+
+def _run(fn, args, name, stream, prepare, dev, keep):
+    """Launch fn(*args, stream) on `stream` or the current one of device dev, or return it as a PreparedCall."""
+    if prepare:
+        return PreparedCall(fn, args, name, dev, keep)
+    if stream is None and _raw_stream is not None:
+        st = _raw_stream(dev)
+    else:
+        st = _stream(stream, keep[0])
+    status = fn(*args, st)
+    if status:
+        _check(status, name)
+    return None
 
 
 def _token_rows(t: torch.Tensor, name: str):
     """Pointer and token stride of an [n][H][D] fp16 tensor whose heads are packed and whose tokens may be apart."""
+    if isinstance(t, torch.Tensor) and t.dtype is torch.float16 and t.is_cuda:
+        st = t.stride()
+        if len(st) == 3 and st[2] == 1:
+            n, H, D = t.shape
+            if st[1] == D:  # the common case; the checks below name the failure
+                return t.data_ptr(), (st[0] if n > 1 else H * D)
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != 3:
@@ -784,41 +817,53 @@ def kv_append_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions:
     kp, ks = _token_rows(k, "k")
     vp, vs = _token_rows(v, "v")
     n, Hq, D = q.shape
-    Hkv = k.shape[1]
-    if k.shape != (n, Hkv, D) or v.shape != k.shape or q_out.shape != q.shape:
+    kshape = k.shape
+    Hkv = kshape[1]
+    if kshape[0] != n or kshape[2] != D or v.shape != kshape or q_out.shape != q.shape:
         raise ValueError("q, k, v and q_out do not match")
     for t, nm in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is not None and t.shape != k.shape:
+        if t is not None and t.shape != kshape:
             raise ValueError(f"{nm} must have k's shape")
     for t, nm in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if t is not None and t.numel() != D:
             raise ValueError(f"{nm} must have D entries")
     rot = 0 if turns is None else 2 * turns.numel()
-    if rot and (positions is None or positions.numel() != n):
+    if not rot:
+        positions = turns = None
+    elif positions is None or positions.numel() != n:
         raise ValueError("positions must have n entries")
-    given = [t is not None for t in (k_cache, v_cache, slot_mapping)]
-    if any(given) != all(given):
-        raise ValueError("k_cache, v_cache and slot_mapping: all or none")
     NB, bs = 0, 16
-    if k_cache is not None:
+    if k_cache is not None and v_cache is not None and slot_mapping is not None:
         if k_cache.dim() != 4:
             raise ValueError("k_cache must be [NB][Hkv][bs][D]")
         NB, Hc, bs, Dc = k_cache.shape
-        if (Hc, Dc) != (Hkv, D) or v_cache.shape != k_cache.shape:
+        if Hc != Hkv or Dc != D or v_cache.shape != k_cache.shape:
             raise ValueError("cache shapes do not match k")
         if slot_mapping.numel() != n:
             raise ValueError("slot_mapping must have n entries")
-    if not rot:
-        positions = turns = None
+    elif k_cache is not None or v_cache is not None or slot_mapping is not None:
+        raise ValueError("k_cache, v_cache and slot_mapping: all or none")
     keep = (q, k, v, positions, turns, q_out, k_cache, v_cache, slot_mapping, q_weight, k_weight, k_out, v_out)
-    _same_device(*keep)
-    f16 = torch.float16
-    args = (qp, qs, kp, ks, vp, vs, n, Hq, Hkv, D, _dptr(q_weight, f16, "q_weight"), _dptr(k_weight, f16, "k_weight"),
-            float(eps), _dptr(turns, torch.int64, "turns"), rot, int(bool(interleaved)),
-            _dptr(positions, torch.int32, "positions"), _dptr(q_out, f16, "q_out"), _dptr(k_out, f16, "k_out"),
-            _dptr(v_out, f16, "v_out"), _dptr(k_cache, f16, "k_cache"), _dptr(v_cache, f16, "v_cache"), NB, bs,
-            _dptr(slot_mapping, torch.int64, "slot_mapping"))
-    return _launch(_lib.kv_append_rope, args, "kv_append_rope", stream, prepare, keep)
+    dev, f16 = q.get_device(), torch.float16
+    ready = dev == _current_device() == k.get_device() == v.get_device() and _ready(
+        dev, f16, *[t for t in (q_out, k_cache, v_cache, q_weight, k_weight, k_out, v_out) if t is not None]) and \
+        _ready(dev, torch.int64, *[t for t in (turns, slot_mapping) if t is not None]) and \
+        (positions is None or _ready(dev, torch.int32, positions))
+    if not ready:
+        _same_device(*keep)
+        for t, nm in ((q_weight, "q_weight"), (k_weight, "k_weight"), (q_out, "q_out"), (k_out, "k_out"),
+                      (v_out, "v_out"), (k_cache, "k_cache"), (v_cache, "v_cache")):
+            _dptr(t, f16, nm)
+        for t, nm in ((turns, "turns"), (slot_mapping, "slot_mapping")):
+            _dptr(t, torch.int64, nm)
+        _dptr(positions, torch.int32, "positions")
+    args = (qp, qs, kp, ks, vp, vs, n, Hq, Hkv, D, None if q_weight is None else q_weight.data_ptr(),
+            None if k_weight is None else k_weight.data_ptr(), float(eps), None if turns is None else turns.data_ptr(), rot,
+            1 if interleaved else 0, None if positions is None else positions.data_ptr(), q_out.data_ptr(),
+            None if k_out is None else k_out.data_ptr(), None if v_out is None else v_out.data_ptr(),
+            None if k_cache is None else k_cache.data_ptr(), None if v_cache is None else v_cache.data_ptr(), NB, bs,
+            None if slot_mapping is None else slot_mapping.data_ptr())
+    return _run(_lib.kv_append_rope, args, "kv_append_rope", stream, prepare, dev, keep)
 
 
 def paged_decode_tree_plan(B: int, Hq: int, Hkv: int, head_dim: int, max_context_len: int, T: int,
@@ -841,33 +886,46 @@ def paged_decode_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
     history); context_lens int32 [B], trees included; tree_lens int32 [B] (None: T nodes each; rows behind a tree are
     left as they were); out like q, fp16 or fp32; workspace: paged_decode_tree_plan bytes.
     prepare=True returns a PreparedCall instead of launching."""
-    B, T, Hq, D = q.shape
+    qshape = q.shape
+    B, T, Hq, D = qshape
     NB, Hkv, bs, Dk = k_cache.shape
     if Dk != D or v_cache.shape != k_cache.shape:
         raise ValueError("cache shapes do not match q")
-    if out.shape != q.shape:
+    if out.shape != qshape:
         raise ValueError("out must have q's shape")
     if block_table.dim() != 2 or block_table.shape[0] != B or context_lens.numel() != B:
         raise ValueError("block_table / context_lens do not match B")
     if masks.shape != (B, T) or (tree_lens is not None and tree_lens.numel() != B):
         raise ValueError("masks must be [B][T] and tree_lens have B entries")
-    od = {torch.float16: KVC_F16, torch.float32: KVC_F32}.get(out.dtype)
+    f16, i32, odt = torch.float16, torch.int32, out.dtype
+    od = KVC_F16 if odt is f16 else KVC_F32 if odt is torch.float32 else None
     if od is None:
         raise TypeError("out must be float16 or float32")
     keep = (q, k_cache, v_cache, block_table, context_lens, masks, tree_lens, out, workspace)
-    _same_device(*keep)
-    ws_ptr = _dptr(workspace, None, "workspace") if workspace is not None else None
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    args = (_dptr(q, torch.float16, "q"), _dptr(k_cache, torch.float16, "k_cache"),
-            _dptr(v_cache, torch.float16, "v_cache"), NB, _dptr(block_table, torch.int32, "block_table"),
-            block_table.shape[1], _dptr(context_lens, torch.int32, "context_lens"),
-            _dptr(masks, torch.int64, "masks"), _dptr(tree_lens, torch.int32, "tree_lens"), T, B, Hq, Hkv, D, bs,
-            int(max_context_len), float(scale), _dptr(out, None, "out"), od, ws_ptr, ws_bytes)
-    return _launch(_lib.paged_decode_tree_attention, args, "paged_decode_tree_attention", stream, prepare, keep)
+    dev = q.get_device()
+    if not (dev == _current_device() and _ready(dev, f16, q, k_cache, v_cache)
+            and _ready(dev, i32, block_table, context_lens) and _ready(dev, torch.int64, masks)
+            and _ready(dev, odt, out) and (tree_lens is None or _ready(dev, i32, tree_lens))
+            and (workspace is None or _ready(dev, workspace.dtype, workspace))):
+        _same_device(*keep)
+        for t, dt, nm in ((q, f16, "q"), (k_cache, f16, "k_cache"), (v_cache, f16, "v_cache"),
+                          (block_table, i32, "block_table"), (context_lens, i32, "context_lens"),
+                          (masks, torch.int64, "masks"), (tree_lens, i32, "tree_lens"), (out, None, "out"),
+                          (workspace, None, "workspace")):
+            _dptr(t, dt, nm)
+    args = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), NB, block_table.data_ptr(), block_table.shape[1],
+            context_lens.data_ptr(), masks.data_ptr(), None if tree_lens is None else tree_lens.data_ptr(), T, B, Hq,
+            Hkv, D, bs, int(max_context_len), float(scale), out.data_ptr(), od,
+            None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel() * workspace.element_size())
+    return _run(_lib.paged_decode_tree_attention, args, "paged_decode_tree_attention", stream, prepare, dev, keep)
 
 
 def _prob_rows(t: torch.Tensor, name: str):
     """Pointer and row stride of a [B][T][V] tensor with contiguous rows at one distance from each other."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in (torch.float32, torch.float16) and t.dim() == 3 \
+            and t.is_contiguous():
+        return t.data_ptr(), t.shape[2]  # the common case; the checks below name the failure
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != 3:
@@ -895,23 +953,29 @@ def draft_tree_verify(target_probs: torch.Tensor, draft_probs: torch.Tensor, tok
     distinct: a node's children were drawn without replacement.  prepare=True returns a PreparedCall."""
     pp, ps = _prob_rows(target_probs, "target_probs")
     qp, qs = _prob_rows(draft_probs, "draft_probs")
-    B, T, V = target_probs.shape
-    if draft_probs.shape != target_probs.shape or draft_probs.dtype != target_probs.dtype:
+    shape, pdt = target_probs.shape, target_probs.dtype
+    B, T, V = shape
+    if draft_probs.shape != shape or draft_probs.dtype is not pdt:
         raise ValueError("target_probs and draft_probs must agree in shape and type")
-    for t, nm in ((tokens, "tokens"), (parents, "parents"), (uniforms, "uniforms"), (path, "path")):
-        if t.shape != (B, T):
-            raise ValueError(f"{nm} must be [B][T]")
-    for t, nm in ((path_len, "path_len"), (next_token, "next_token"), (tree_lens, "tree_lens")):
-        if t is not None and t.numel() != B:
-            raise ValueError(f"{nm} must have B entries")
+    rows = tokens.shape
+    if rows != (B, T) or parents.shape != rows or uniforms.shape != rows or path.shape != rows:
+        raise ValueError("tokens, parents, uniforms and path must be [B][T]")
+    if path_len.numel() != B or next_token.numel() != B or (tree_lens is not None and tree_lens.numel() != B):
+        raise ValueError("path_len, next_token and tree_lens must have B entries")
     keep = (target_probs, draft_probs, tokens, parents, tree_lens, uniforms, path, path_len, next_token)
-    _same_device(*keep)
-    i32 = torch.int32
-    args = (pp, ps, qp, qs, KVC_F32 if target_probs.dtype == torch.float32 else KVC_F16, _dptr(tokens, i32, "tokens"),
-            _dptr(parents, i32, "parents"), _dptr(tree_lens, i32, "tree_lens"),
-            _dptr(uniforms, torch.float32, "uniforms"), B, T, V, int(bool(distinct)), _dptr(path, i32, "path"),
-            _dptr(path_len, i32, "path_len"), _dptr(next_token, i32, "next_token"))
-    return _launch(_lib.draft_tree_verify, args, "draft_tree_verify", stream, prepare, keep)
+    i32, dev = torch.int32, target_probs.get_device()
+    if not (dev == _current_device() == draft_probs.get_device()
+            and _ready(dev, i32, tokens, parents, path, path_len, next_token) and _ready(dev, torch.float32, uniforms)
+            and (tree_lens is None or _ready(dev, i32, tree_lens))):
+        _same_device(*keep)
+        for t, nm in ((tokens, "tokens"), (parents, "parents"), (tree_lens, "tree_lens"), (path, "path"),
+                      (path_len, "path_len"), (next_token, "next_token")):
+            _dptr(t, i32, nm)
+        _dptr(uniforms, torch.float32, "uniforms")
+    args = (pp, ps, qp, qs, KVC_F32 if pdt is torch.float32 else KVC_F16, tokens.data_ptr(), parents.data_ptr(),
+            None if tree_lens is None else tree_lens.data_ptr(), uniforms.data_ptr(), B, T, V, 1 if distinct else 0,
+            path.data_ptr(), path_len.data_ptr(), next_token.data_ptr())
+    return _run(_lib.draft_tree_verify, args, "draft_tree_verify", stream, prepare, dev, keep)
 
 
 def kv_tree_commit(h: int, block_table: torch.Tensor, context_lens: torch.Tensor, path: torch.Tensor,
@@ -925,16 +989,21 @@ def kv_tree_commit(h: int, block_table: torch.Tensor, context_lens: torch.Tensor
     if path.dim() != 2 or block_table.dim() != 2:
         raise ValueError("path must be [B][P] and block_table [B][max_blocks]")
     B, P = path.shape
-    if block_table.shape[0] != B:
+    nb, max_blocks = block_table.shape
+    if nb != B:
         raise ValueError("block_table does not match path")
-    for t, nm in ((context_lens, "context_lens"), (path_len, "path_len"), (new_context_lens, "new_context_lens"),
-                  (tree_lens, "tree_lens")):
-        if t is not None and t.numel() != B:
-            raise ValueError(f"{nm} must have B entries")
+    if context_lens.numel() != B or path_len.numel() != B or new_context_lens.numel() != B or (
+            tree_lens is not None and tree_lens.numel() != B):
+        raise ValueError("context_lens, path_len, new_context_lens and tree_lens must have B entries")
     keep = (path, block_table, context_lens, tree_lens, path_len, new_context_lens)
-    _same_device(*keep)
-    i32 = torch.int32
-    args = (h, _dptr(block_table, i32, "block_table"), block_table.shape[1], _dptr(context_lens, i32, "context_lens"),
-            _dptr(tree_lens, i32, "tree_lens"), _dptr(path, i32, "path"), _dptr(path_len, i32, "path_len"), P, B,
-            _dptr(new_context_lens, i32, "new_context_lens"))
-    return _launch(_lib.kv_tree_commit, args, "kv_tree_commit", stream, prepare, keep)
+    i32, dev = torch.int32, path.get_device()
+    if not (dev == _current_device() and _ready(dev, i32, path, block_table, context_lens, path_len, new_context_lens)
+            and (tree_lens is None or _ready(dev, i32, tree_lens))):
+        _same_device(*keep)
+        for t, nm in ((path, "path"), (block_table, "block_table"), (context_lens, "context_lens"),
+                      (tree_lens, "tree_lens"), (path_len, "path_len"), (new_context_lens, "new_context_lens")):
+            _dptr(t, i32, nm)
+    args = (h, block_table.data_ptr(), max_blocks, context_lens.data_ptr(),
+            None if tree_lens is None else tree_lens.data_ptr(), path.data_ptr(), path_len.data_ptr(), P, B,
+            new_context_lens.data_ptr())
+    return _run(_lib.kv_tree_commit, args, "kv_tree_commit", stream, prepare, dev, keep)

@@ -27,6 +27,12 @@
 namespace kvc {
 namespace rope {
 
+#ifndef KVC_ROPE_U
+#define KVC_ROPE_U 2
+#endif
+#ifndef KVC_ROPE_CTAS
+#define KVC_ROPE_CTAS 2
+#endif
 constexpr int kWarps = 8;
 
 struct Params {
@@ -64,7 +70,7 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32) kv_append_rope_kernel(const Params p) {
+__global__ void __launch_bounds__(kWarps * 32, KVC_ROPE_CTAS) kv_append_rope_kernel(const Params p) {
     constexpr int kLanes = D / 16;        // lanes of a row
     constexpr int kRows = 32 / kLanes;    // rows a warp handles at a time
     __shared__ float2 s_cs[kWarps][D / 2];  // (cos, sin) of the warp's token
@@ -121,7 +127,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv_append_rope_kernel(const Param
 
     const int total = p.Hq + 2 * p.Hkv;
     const int row_end = min(total, (static_cast<int>(w % p.split) + 1) * p.rows_per_warp);
-    constexpr int U = 2;  // iterations whose loads are in flight together
+    constexpr int U = KVC_ROPE_U;  // iterations whose loads are in flight together
     for (int rb = static_cast<int>(w % p.split) * p.rows_per_warp; rb < row_end; rb += U * kRows) {
         uint4 raw[U][2];
 #pragma unroll

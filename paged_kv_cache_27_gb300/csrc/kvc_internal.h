@@ -167,7 +167,8 @@ cudaError_t launch_append_rope(const RopeArgs& a, cudaStream_t stream);
 struct TreePlan {
     int row_pairs;   // pairs of 128-row tiles per (sequence, KV head)
     int chunk;       // key tiles of 128 per CTA
-    int max_chunks;  // chunks of the longest context; > 1: partial states and the combine kernel
+    int cluster;     // CTAs per cluster (they merge on chip)
+    int nclus;       // clusters along the longest context; > 1: partial states and the combine kernel
     size_t workspace_bytes;
 };
 cudaError_t tree_plan(int B, int Hq, int Hkv, int D, int max_context_len, int T, TreePlan* plan);

@@ -230,6 +230,16 @@ __device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, float4 v) {
                  "f"(v.w)
                  : "memory");
 }
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// every thread of every CTA of the cluster (whole warps): shared-memory writes before it are visible after it
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 // ---- programmatic dependent launch ------------------------------------------
 __device__ __forceinline__ void grid_dependency_wait() {

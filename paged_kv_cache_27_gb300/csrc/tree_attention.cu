@@ -39,8 +39,10 @@ constexpr int kKeys = 128;  // keys of a key tile
 constexpr int kPages = kKeys / kBlockSize;
 constexpr int kRowWarps = 8;
 constexpr int kMmaWarp = kRowWarps;
-constexpr int kLoadWarp = kRowWarps + 1;
-constexpr int kThreads = (kRowWarps + 2) * 32;
+constexpr int kLoadKWarp = kRowWarps + 1;
+constexpr int kLoadVWarp = kRowWarps + 2;
+constexpr int kThreads = (kRowWarps + 3) * 32;
+constexpr int kMaxTreeCluster = 8;
 constexpr uint64_t kWaitNs = 1000000000ull;
 // a scale of 0 is taken as this: the scores of fp16 rows (below 2^40) still vanish next to 1, and a masked score of
 // -inf times it stays -inf
@@ -54,15 +56,21 @@ struct Geom {
     static constexpr int kVStages = D == 64 ? 5 : 2;
     static constexpr int kChunkBytes = kRows * 128;  // 128 rows or keys x 64 dims
     static constexpr int kTileBytes = kChunks * kChunkBytes;
+    // Q_A, Q_B, V ring, K ring.  With one row tile Q_B's place is one more V stage (V is freed last: its product waits
+    // for the softmax).
     static constexpr int kQOff = 0;
-    static constexpr int kKOff = kQOff + 2 * kTileBytes;
-    static constexpr int kVOff = kKOff + kKStages * kTileBytes;
-    static constexpr int kBarOff = kVOff + kVStages * kTileBytes;
-    static constexpr int kSmemBytes = kBarOff + 256 + 1024;  // barriers, TMEM address, flags; alignment
+    static constexpr int kVOff = kQOff + 2 * kTileBytes;
+    static constexpr int kKOff = kVOff + kVStages * kTileBytes;
+    static constexpr int kBarOff = kKOff + kKStages * kTileBytes;
+    static constexpr int kMaxVStages = kVStages + 1;
+    static constexpr int kSmemBytes = kBarOff + 512 + 1024;  // barriers, TMEM address, flags; alignment
     static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
-    // the streams exchange half of their output columns in the K/V rings at the end
-    static constexpr int kXStride = D / 2 + 4;  // floats per exchanged row (padded: rows on distinct banks)
-    static_assert(2 * kRows * (kXStride + 2) * 4 <= kBarOff - kKOff, "exchange area");
+    // at the end the row threads leave their states in the idle V and K rings: per thread (max, sum), and a row of O,
+    // padded so that eight rows lie on distinct banks
+    static constexpr int kOStride = D + 4;  // floats
+    static constexpr int kStateOff = kVOff;
+    static constexpr int kMlOff = kStateOff + 2 * kRows * kOStride * 4;
+    static_assert(kMlOff + 2 * kRows * 8 <= kBarOff, "state area");
     // TMEM columns: S_A / P_A [0, 128), S_B / P_B [128, 256), O_A [256, 256 + D), O_B [256 + D, 256 + 2D)
     static constexpr int kTmemO = 2 * kKeys;
     static constexpr uint32_t kTmemCols = 512;
@@ -80,9 +88,10 @@ struct Params {
     float* part_acc;
     unsigned* err;
     int T, Hq, Hkv, G, max_blocks, num_blocks, max_ctx, out_f32;
-    int chunk;       // key tiles per CTA
-    int max_chunks;  // chunks of the longest context: stride of the partial states
-    int row_pairs;   // pairs of row tiles of the widest tree
+    int chunk;      // key tiles per CTA
+    int cluster;    // CTAs per cluster: consecutive chunks of one unit, merged in distributed shared memory
+    int nclus;      // clusters along the longest context: stride of the partial states
+    int row_pairs;  // pairs of row tiles of the widest tree
     int negate;      // scale < 0: the query rows change sign as they are loaded
     float scale_log2;  // |scale| * log2 e, at least kMinScaleLog2
 };
@@ -145,6 +154,25 @@ __device__ __forceinline__ uint32_t finite_halves(uint32_t w, bool& found) {
     return w;
 }
 
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
 // Sizes of sequence b; false where its lengths do not fit (tree_len and ctx stay as read).
 __device__ __forceinline__ bool lengths(const Params& p, int b, int& tree, int& ctx) {
     tree = p.tree_lens != nullptr ? p.tree_lens[b] : p.T;
@@ -159,16 +187,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
                                                                          const __grid_constant__ CUtensorMap tmV,
                                                                          const Params p) {
     using Geo = Geom<D>;
-    constexpr int KS = Geo::kKStages, VS = Geo::kVStages;
+    constexpr int KS = Geo::kKStages, MVS = Geo::kMaxVStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Geo::kBarOff);
     uint64_t* q_full = bars;                 // query rows in shared memory (one arrival per row warp)
     uint64_t* k_full = bars + 1;             // [KS] K tile landed
     uint64_t* k_empty = k_full + KS;         // [KS] S products of the stage's tile done
-    uint64_t* v_full = k_empty + KS;         // [VS] V tile landed
-    uint64_t* v_empty = v_full + VS;         // [VS] P V products of the stage's tile done
-    uint64_t* s_full = v_empty + VS;         // [2] S_X of the stream's tile in TMEM
+    uint64_t* v_full = k_empty + KS;         // [MVS] V tile landed
+    uint64_t* v_empty = v_full + MVS;        // [MVS] P V products of the stage's tile done
+    uint64_t* s_full = v_empty + MVS;        // [2] S_X of the stream's tile in TMEM
     uint64_t* p_full = s_full + 2;           // [2] P_X of the stream's tile in TMEM (4 arrivals)
     uint64_t* o_full = p_full + 2;           // [2] P_X V of the stream's tile done
     uint64_t* fin = o_full + 2;              // every MMA issued so far done
@@ -176,14 +204,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
     volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
     volatile int* s_bad_block = s_abort + 1;  // a block id out of range: the chunk is left out
     volatile int* s_bad_v = s_abort + 2;      // an infinity or NaN among the tree's V values
-    static_assert((1 + 2 * KS + 2 * VS + 7) * 8 + 16 <= 256, "barrier area");
+    static_assert((1 + 2 * KS + 2 * MVS + 7) * 8 + 16 <= 512, "barrier area");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int pair = static_cast<int>(blockIdx.x) % p.row_pairs, chunk = static_cast<int>(blockIdx.x) / p.row_pairs;
+    // blockIdx.x = (cluster along the context * row pairs + row pair) * CTAs per cluster + rank
+    const int rank = static_cast<int>(blockIdx.x) % p.cluster;
+    const int pair = static_cast<int>(blockIdx.x) / p.cluster % p.row_pairs;
+    const int clus = static_cast<int>(blockIdx.x) / p.cluster / p.row_pairs;
     const int hk = blockIdx.y, b = blockIdx.z;
     int tree, ctx;
     if (!lengths(p, b, tree, ctx)) {
-        if (chunk == 0 && pair == 0) {
+        if (blockIdx.x == 0) {
             if (threadIdx.x == 0) atomicOr(p.err, KVC_DEVERR_CONTEXT);
             const int rows = min(max(tree, 0), p.T);
             for (int e = threadIdx.x; e < rows * p.G * D; e += kThreads) {
@@ -195,39 +226,79 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
         return;
     }
     const int rows = tree * p.G, r0 = pair * 2 * kRows;
-    const int all_tiles = key_tiles(ctx), c0 = chunk * p.chunk;
-    if (r0 >= rows || c0 >= all_tiles) return;
-    const int n = min(p.chunk, all_tiles - c0);          // key tiles of this CTA
+    const int all_tiles = key_tiles(ctx), per_clus = p.chunk * p.cluster;
+    if (r0 >= rows || clus * per_clus >= all_tiles) return;  // the whole cluster
+    const int c0 = clus * per_clus + rank * p.chunk;
+    const int n = max(0, min(p.chunk, all_tiles - c0));  // key tiles of this CTA
     const bool two_rows = rows - r0 > kRows;             // two row tiles: they are the streams
     const int step = two_rows ? 1 : 2;                   // key tiles between two of a stream's
     const int hist = ctx - tree;                         // keys before the tree
     const int pages = (ctx + kBlockSize - 1) / kBlockSize;
-    const int nchunks = (all_tiles + p.chunk - 1) / p.chunk;
+    const bool whole = all_tiles <= per_clus;            // one cluster covers the context: no partial states
+    const uint32_t VS = two_rows ? Geo::kVStages : MVS;
 
     auto qs = [&](int x) { return smem + Geo::kQOff + x * Geo::kTileBytes; };
-    auto kst = [&](int st) { return smem + Geo::kKOff + st * Geo::kTileBytes; };
-    auto vst = [&](int st) { return smem + Geo::kVOff + st * Geo::kTileBytes; };
+    auto kst = [&](uint32_t st) { return smem + Geo::kKOff + st * Geo::kTileBytes; };
+    uint8_t* const vring = smem + (two_rows ? Geo::kVOff : Geo::kVOff - Geo::kTileBytes);
+    auto vst = [&](uint32_t st) { return vring + st * Geo::kTileBytes; };
 
-    if (threadIdx.x == 0) {
-        mbar_init(q_full, kRowWarps);
-        for (int i = 0; i < KS; ++i) {
-            mbar_init(&k_full[i], 1);
-            mbar_init(&k_empty[i], 1);
+    // Copies of key tile j: lane i of the calling warp takes block i.
+    const int32_t* const table_row = p.block_table + static_cast<int64_t>(b) * p.max_blocks;
+    auto block_of = [&](int j) {
+        const int page = (c0 + j) * kPages + lane;
+        return lane < kPages && page < pages ? table_row[page] : 0;
+    };
+    // a block id out of range is flagged and block 0 copied in its place; the chunk's values are then not used
+    auto checked_block = [&](int phys) {
+        if (phys >= 0 && phys < p.num_blocks) return phys;
+        atomicOr(p.err, KVC_DEVERR_BLOCK_ID);
+        *s_bad_block = 1;  // seen by the row warps behind this tile's barriers
+        return 0;
+    };
+    auto load = [&](uint8_t* tile, const CUtensorMap* map, uint64_t* bar, int j, int phys, uint64_t policy) {
+        const int np = min(kPages, pages - (c0 + j) * kPages);
+        if (lane == 0) mbar_arrive_expect_tx(bar, np * (kBlockSize * D * 2));
+        __syncwarp();
+        if (lane < np) {
+#pragma unroll
+            for (int c = 0; c < Geo::kChunks; ++c)
+                tma_load_2d(tile + c * Geo::kChunkBytes + lane * (kBlockSize * 128), map, bar, c * 64,
+                            (phys * p.Hkv + hk) * kBlockSize, policy);
         }
-        for (int i = 0; i < VS; ++i) {
-            mbar_init(&v_full[i], 1);
-            mbar_init(&v_empty[i], 1);
+    };
+    // one pair of row tiles reads its K and V once; several pairs meet them in L2
+    uint64_t policy = 0;
+    const int pre = min(n, Geo::kVStages);  // tiles whose copies start before the CTA's other preparations
+    if (warp == kLoadKWarp) {
+        if (lane == 0) {
+            mbar_init(q_full, kRowWarps);
+            for (int i = 0; i < KS; ++i) {
+                mbar_init(&k_full[i], 1);
+                mbar_init(&k_empty[i], 1);
+            }
+            for (int i = 0; i < MVS; ++i) {
+                mbar_init(&v_full[i], 1);
+                mbar_init(&v_empty[i], 1);
+            }
+            for (int x = 0; x < 2; ++x) {
+                mbar_init(&s_full[x], 1);
+                mbar_init(&p_full[x], 4);
+                mbar_init(&o_full[x], 1);
+            }
+            mbar_init(fin, 1);
+            *s_abort = 0;
+            *s_bad_block = 0;
+            *s_bad_v = 0;
+            fence_barrier_init();
         }
-        for (int x = 0; x < 2; ++x) {
-            mbar_init(&s_full[x], 1);
-            mbar_init(&p_full[x], 4);
-            mbar_init(&o_full[x], 1);
+        __syncwarp();
+        policy = p.row_pairs == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
+        static_assert(Geo::kVStages <= KS, "the first copies find every stage free");
+        for (int j = 0; j < pre; ++j) {
+            const int phys = checked_block(block_of(j));
+            load(kst(j), &tmK, &k_full[j], j, phys, policy);
+            load(vst(j), &tmV, &v_full[j], j, phys, policy);
         }
-        mbar_init(fin, 1);
-        *s_abort = 0;
-        *s_bad_block = 0;
-        *s_bad_v = 0;
-        fence_barrier_init();
     }
     if (warp == 0) {
         tmem_alloc(s_tmem, Geo::kTmemCols);
@@ -238,58 +309,34 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
 
-    if (warp == kLoadWarp) {
-        // ================= loads: lane i copies block i of every K and V tile =================
-        if (lane == 0) {
-            prefetch_tensormap(&tmK);
-            prefetch_tensormap(&tmV);
-        }
-        // one pair of row tiles reads its K and V once; several pairs meet them in L2
-        const uint64_t policy = p.row_pairs == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
-        const int32_t* row = p.block_table + static_cast<int64_t>(b) * p.max_blocks;
-        auto block_of = [&](int j) {
-            const int page = (c0 + j) * kPages + lane;
-            return lane < kPages && page < pages ? row[page] : -1;
-        };
-        auto load = [&](uint8_t* tile, const CUtensorMap* map, uint64_t* bar, int j, int phys) {
-            const int np = min(kPages, pages - (c0 + j) * kPages);
-            if (lane == 0) mbar_arrive_expect_tx(bar, np * (kBlockSize * D * 2));
-            __syncwarp();
-            if (lane < np) {
-#pragma unroll
-                for (int c = 0; c < Geo::kChunks; ++c)
-                    tma_load_2d(tile + c * Geo::kChunkBytes + lane * (kBlockSize * 128), map, bar, c * 64,
-                                (phys * p.Hkv + hk) * kBlockSize, policy);
-            }
-        };
-        int k_issued = 0, v_issued = 0, next = block_of(0);
+    if (warp == kLoadKWarp || warp == kLoadVWarp) {
+        // ================= copies: a warp for K and one for V, each as far ahead as its ring allows =================
+        const bool is_v = warp == kLoadVWarp;
+        if (is_v) policy = p.row_pairs == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
+        uint64_t* const full = is_v ? v_full : k_full;
+        uint64_t* const empty = is_v ? v_empty : k_empty;
+        const uint32_t stages = is_v ? VS : KS;
+        uint32_t st = static_cast<uint32_t>(pre) % stages, ph = static_cast<uint32_t>(pre) / stages;  // of tile j
+        int issued = pre;
         bool ok = true;
-        for (int j = 0; ok && j < n; ++j) {
-            int phys = next;
+        int next = pre < n ? block_of(pre) : 0;
+        for (int j = pre; j < n; ++j) {
+            const int phys = checked_block(next);
             if (j + 1 < n) next = block_of(j + 1);
-            if (lane < min(kPages, pages - (c0 + j) * kPages) && (phys < 0 || phys >= p.num_blocks)) {
-                atomicOr(p.err, KVC_DEVERR_BLOCK_ID);
-                *s_bad_block = 1;  // seen by the row warps behind this tile's barriers
-                phys = 0;          // a block of the pool, whose values are not used
+            if (ph > 0) ok = __all_sync(0xffffffffu, wait(&empty[st], (ph - 1) & 1, s_abort));
+            if (!ok) break;
+            load(is_v ? vst(st) : kst(st), is_v ? &tmV : &tmK, &full[st], j, phys, policy);
+            issued = j + 1;
+            if (++st == stages) {
+                st = 0;
+                ++ph;
             }
-            __syncwarp();
-            if (j >= KS) ok = __all_sync(0xffffffffu, wait(&k_empty[j % KS], ((j - KS) / KS) & 1, s_abort));
-            if (!ok) break;
-            load(kst(j % KS), &tmK, &k_full[j % KS], j, phys);
-            k_issued = j + 1;
-            if (j >= VS) ok = __all_sync(0xffffffffu, wait(&v_empty[j % VS], ((j - VS) / VS) & 1, s_abort));
-            if (!ok) break;
-            load(vst(j % VS), &tmV, &v_full[j % VS], j, phys);
-            v_issued = j + 1;
         }
-        // copies still in flight land before the shared memory is released (immediate unless aborted: the products
-        // consumed every tile)
-        if (lane == 0) {
-            for (int t = max(0, k_issued - KS); t < k_issued; ++t)
-                mbar_wait_bounded(&k_full[t % KS], (t / KS) & 1, kWaitNs / 8);
-            for (int t = max(0, v_issued - VS); t < v_issued; ++t)
-                mbar_wait_bounded(&v_full[t % VS], (t / VS) & 1, kWaitNs / 8);
-        }
+        // copies still in flight land before the shared memory is used otherwise or released (immediate unless
+        // aborted: the products consumed every tile)
+        if (lane == 0)
+            for (int t = max(0, issued - static_cast<int>(stages)); t < issued; ++t)
+                mbar_wait_bounded(&full[t % stages], (t / stages) & 1, kWaitNs / 8);
     } else if (warp == kMmaWarp) {
         // ================= tensor-core products (one thread) =================
         if (lane == 0) {
@@ -298,9 +345,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
             const uint64_t dQ = umma_smem_desc(smem_u32(qs(0)), 16, 1024);
             const uint64_t dK = umma_smem_desc(smem_u32(kst(0)), 16, 1024);
             // V as the MN-major B operand: 8-key groups 1024 bytes apart, 64-dim atoms one chunk apart
-            const uint64_t dV = umma_smem_desc(smem_u32(vst(0)), Geo::kChunkBytes, 1024);
+            const uint64_t dV = umma_smem_desc(smem_u32(vring), Geo::kChunkBytes, 1024);
             // S_X = Q_X K^T over D / 16 steps of 16 dims (with one row tile both streams use it)
-            auto mma_s = [&](int x, int st) {
+            auto mma_s = [&](int x, uint32_t st) {
                 const uint64_t a0 = dQ + static_cast<uint64_t>(two_rows ? x * (Geo::kTileBytes >> 4) : 0);
                 const uint64_t b0 = dK + static_cast<uint64_t>(st * (Geo::kTileBytes >> 4));
 #pragma unroll
@@ -312,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
                 umma_commit(&s_full[x]);
             };
             // O_X += P_X V: 8 steps of 16 keys, P from TMEM (fp16, or its high part and residual)
-            auto mma_pv = [&](int x, int st, bool first) {
+            auto mma_pv = [&](int x, uint32_t st, bool first) {
                 const uint64_t v0 = dV + static_cast<uint64_t>(st * (Geo::kTileBytes >> 4));
                 const uint32_t tP = tmem + x * kKeys, tO = tmem + Geo::kTmemO + x * D;
 #pragma unroll
@@ -323,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
                 }
                 umma_commit(&o_full[x]);
             };
-            bool ok = wait(q_full, 0, s_abort);
+            bool ok = n == 0 || wait(q_full, 0, s_abort);
             // the first tile of each stream: tile 0 for both, or tiles 0 and 1
             for (int x = 0; ok && x < 2; ++x) {
                 const int j = two_rows ? 0 : x;
@@ -333,8 +380,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
                 mma_s(x, j);
                 if (!two_rows || x == 1) umma_commit(&k_empty[j]);
             }
+            uint32_t vs = 0, vph = 0;                                                    // V stage and phase of tile j
+            uint32_t ks = static_cast<uint32_t>(step) % KS, kph = static_cast<uint32_t>(step) / KS;  // K: of tile j + step
             for (int j = 0; ok && j < n; ++j) {
-                if (!(ok = wait(&v_full[j % VS], (j / VS) & 1, s_abort))) break;
+                if (!(ok = wait(&v_full[vs], vph & 1, s_abort))) break;
                 const int jn = j + step;
                 const uint32_t it = static_cast<uint32_t>(two_rows ? j : j >> 1);  // the streams' tile count
                 // per stream of this tile: P_X V once P_X is in TMEM; then the stream's next S_X into the same
@@ -342,17 +391,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
                 for (int x = two_rows ? 0 : (j & 1), left = two_rows ? 2 : 1; ok && left > 0; ++x, --left) {
                     if (!(ok = wait(&p_full[x], it & 1, s_abort))) break;
                     tc_fence_after();
-                    mma_pv(x, j % VS, it == 0);
+                    mma_pv(x, vs, it == 0);
                     if (jn < n) {
-                        if (!(ok = wait(&k_full[jn % KS], (jn / KS) & 1, s_abort))) break;
+                        if (!(ok = wait(&k_full[ks], kph & 1, s_abort))) break;
                         if (!(ok = wait(&o_full[x], it & 1, s_abort))) break;
                         tc_fence_after();
-                        mma_s(x, jn % KS);
+                        mma_s(x, ks);
                     }
                 }
                 if (!ok) break;
-                umma_commit(&v_empty[j % VS]);
-                if (jn < n) umma_commit(&k_empty[jn % KS]);
+                umma_commit(&v_empty[vs]);
+                if (jn < n) umma_commit(&k_empty[ks]);
+                if (++vs == VS) {
+                    vs = 0;
+                    ++vph;
+                }
+                if (++ks == KS) {
+                    ks = 0;
+                    ++kph;
+                }
             }
             // every product issued is complete before the tensor memory is released
             umma_commit(fin);
@@ -392,6 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
         float m_used = -INFINITY, l = 0.f;
         bool ok = true;
         int it = 0;
+        uint32_t vs = two_rows ? 0u : static_cast<uint32_t>(x), vph = 0;  // V stage and phase of tile j
         for (int j = two_rows ? 0 : x; j < n; j += step, ++it) {
             // S_X complete also means the stream's previous P_X V complete: it was waited for before S_X was issued
             ok = __all_sync(0xffffffffu, wait(&s_full[x], it & 1, s_abort));
@@ -475,9 +533,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
                 // V rows past the context are zeroed, so that whatever they hold cannot reach an output through a
                 // zero weight; so are infinities and NaN among the tree's V rows, which not every row sees (the rows
                 // that do get them back at the end).  With two row tiles stream A does it: its product is first.
-                ok = __all_sync(0xffffffffu, wait(&v_full[j % VS], (j / VS) & 1, s_abort));
+                ok = __all_sync(0xffffffffu, wait(&v_full[vs], vph & 1, s_abort));
                 if (!ok) break;
-                uint8_t* vt = vst(j % VS);
+                uint8_t* vt = vst(vs);
                 const int from = max(hist - k0, 0), end = ctx - k0;
                 bool found = false;
                 for (int e = wq * 32 + lane; e < (kKeys - from) * 8 * Geo::kChunks; e += 128) {
@@ -503,124 +561,102 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[x]);
+            if ((vs += step) >= VS) {
+                vs -= VS;
+                ++vph;
+            }
         }
         if (ok && it > 0) ok = __all_sync(0xffffffffu, wait(&o_full[x], (it - 1) & 1, s_abort));
         tc_fence_after();
-        row_warps_sync();  // both streams done; their notes on bad blocks and values are complete
-        const bool drop = *s_bad_block != 0 || *s_abort != 0 || !ok;
-        if (drop) {
-            l = 0.f;
-            m_used = -INFINITY;
-        }
-        float w_own = 1.f;   // weights of this stream's and the other's state in the merged one
-        float w_other = 0.f;
-        int col0 = 0, cols = D;
-        float* xrow = nullptr;  // the other stream's half of this thread's row
-        if (!two_rows) {
-            // each stream keeps one half of the columns and hands the other half over, in the idle K/V rings
-            float* area = reinterpret_cast<float*>(smem + Geo::kKOff);
-            float2* ml = reinterpret_cast<float2*>(area + 2 * kRows * Geo::kXStride);
-            float* mine = area + ((1 - x) * kRows + row) * Geo::kXStride;
-            ml[x * kRows + row] = make_float2(m_used, l);
-            if (it > 0 && live_warp && !drop) {
-                const int give = (1 - x) * (D / 2);
+        row_warps_sync();  // both streams done: the rings are idle, the notes on bad blocks and values complete
+        // the thread's state into the state area: slot x * 128 + row
+        const bool drop = *s_bad_block != 0 || *s_abort != 0 || !ok || it == 0;
+        float2* ml = reinterpret_cast<float2*>(smem + Geo::kMlOff);
+        ml[x * kRows + row] = drop ? make_float2(-INFINITY, 0.f) : make_float2(m_used, l);
+        if (live_warp && !drop) {
+            float* mine = reinterpret_cast<float*>(smem + Geo::kStateOff) + (x * kRows + row) * Geo::kOStride;
 #pragma unroll 1
-                for (int c = 0; c < D / 2; c += 16) {
-                    float o[16];
-                    tmem_ld16(tO + give + c, o);
+            for (int c = 0; c < D; c += 32) {
+                float o[32];
+                tmem_ld32(tO + c, o);
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4)
-                        *reinterpret_cast<float4*>(mine + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-                }
-            }
-            row_warps_sync();
-            const float2 theirs = ml[(1 - x) * kRows + row];
-            const float M = fmaxf(m_used, theirs.x);
-            // a stream that saw no key (or no tile at all) holds l = 0 and adds nothing
-            w_own = l > 0.f ? (m_used == M ? 1.f : ex2(m_used - M)) : l != l ? 1.f : 0.f;
-            w_other = theirs.y > 0.f ? (theirs.x == M ? 1.f : ex2(theirs.x - M)) : theirs.y != theirs.y ? 1.f : 0.f;
-            l = (w_own != 0.f ? l * w_own : 0.f) + (w_other != 0.f ? theirs.y * w_other : 0.f);
-            m_used = M;
-            col0 = x * (D / 2);
-            cols = D / 2;
-            xrow = area + (x * kRows + row) * Geo::kXStride;
-        }
-        if (live_warp && !(*s_abort)) {
-            const bool whole = nchunks == 1;
-            const float inv = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
-            const int64_t orow = (static_cast<int64_t>(b) * p.T + rr / p.G) * p.Hq + hk * p.G + rr % p.G;
-            const int64_t prow = orow * p.max_chunks + chunk;
-            if (live && !whole && col0 == 0)
-                *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(m_used, l);
-            const bool bad_v = *s_bad_v != 0 && !drop;
-            // a state that holds nothing is left out, not multiplied by 0 (1 / l may be NaN or infinite)
-            const bool own = it > 0 && w_own != 0.f && l != 0.f, other = xrow != nullptr && w_other != 0.f;
-            const float f_own = w_own * inv, f_other = w_other * inv;
-#pragma unroll 1
-            for (int c = col0; c < col0 + cols; c += 16) {
-                float o[16];
-                if (it > 0) {
-                    tmem_ld16(tO + c, o);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = 0.f;
-                }
-                if (!live) continue;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = own ? o[i] * f_own : 0.f;
-                if (other) {
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 y = *reinterpret_cast<const float4*>(xrow + c - col0 + i);
-                        o[i] = fmaf(y.x, f_other, o[i]);
-                        o[i + 1] = fmaf(y.y, f_other, o[i + 1]);
-                        o[i + 2] = fmaf(y.z, f_other, o[i + 2]);
-                        o[i + 3] = fmaf(y.w, f_other, o[i + 3]);
-                    }
-                }
-                if (bad_v) {
-                    // infinities and NaN of the tree's V rows that this row sees, in this chunk's keys
-                    const int t0 = max(0, c0 * kKeys - hist), t1 = min(tree, (c0 + n) * kKeys - hist);
-                    for (int t = t0; t < t1; ++t) {
-                        if (!((mask >> t) & 1)) continue;
-                        const int pos = hist + t;
-                        const int64_t blk =
-                            p.block_table[static_cast<int64_t>(b) * p.max_blocks + pos / kBlockSize];
-                        const __half* v =
-                            p.v_cache + ((blk * p.Hkv + hk) * kBlockSize + pos % kBlockSize) * D + c;
-                        for (int i = 0; i < 16; ++i) {
-                            const float y = __half2float(v[i]);
-                            if (!(fabsf(y) < INFINITY)) o[i] += y;
-                        }
-                    }
-                }
-                if (!whole) {
-                    float4* dst = reinterpret_cast<float4*>(p.part_acc + prow * D + c);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                } else if (p.out_f32) {
-                    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + orow * D + c);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                } else {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<__half*>(p.out) + orow * D + c);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        dst[i] = make_uint4(pack_half2(o[8 * i], o[8 * i + 1]), pack_half2(o[8 * i + 2], o[8 * i + 3]),
-                                            pack_half2(o[8 * i + 4], o[8 * i + 5]),
-                                            pack_half2(o[8 * i + 6], o[8 * i + 7]));
-                }
+                for (int i = 0; i < 32; i += 4)
+                    *reinterpret_cast<float4*>(mine + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
             }
         }
     }
     // every TMEM access of the CTA is complete; the allocating warp frees it
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (warp == 0) {
         tc_fence_after();
         tmem_dealloc(tmem, Geo::kTmemCols);
+    }
+    if (*s_bad_block != 0) *s_bad_v = 0;  // the chunk is left out
+    if (p.cluster > 1) {
+        __syncwarp();
+        cluster_sync_all();  // every CTA's states are in its shared memory
+    } else {
+        __syncthreads();
+    }
+    // ================= the cluster's states merged: each CTA takes a share of the rows =================
+    {
+        constexpr int kCols = D / 4;  // a thread per four columns of a row
+        const int live_rows = min(two_rows ? 2 * kRows : kRows, rows - r0);
+        const int share = (live_rows + p.cluster - 1) / p.cluster;
+        const int ra = min(rank * share, live_rows), rb = min(ra + share, live_rows);
+        const int ncta = min(p.cluster, (all_tiles - clus * per_clus + p.chunk - 1) / p.chunk);  // CTAs with tiles
+        const uint32_t state0 = smem_u32(smem + Geo::kStateOff), ml0 = smem_u32(smem + Geo::kMlOff);
+        const uint32_t flag0 = smem_u32(const_cast<int*>(s_bad_v));
+        for (int e = threadIdx.x; e < (rb - ra) * kCols; e += kThreads) {
+            const int r = ra + e / kCols, c = e % kCols * 4, rr = r0 + r;
+            float m = -INFINITY, l = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            unsigned bad_v = 0;
+            for (int q = 0; q < ncta; ++q) {
+                const uint32_t st = cluster_addr(state0, q), mls = cluster_addr(ml0, q);
+                if (ld_cluster_u32(cluster_addr(flag0, q)) != 0) bad_v |= 1u << q;
+                for (int slot = r; slot < 2 * kRows; slot += two_rows ? 2 * kRows : kRows) {
+                    const float2 s = ld_cluster_f32x2(mls + slot * 8);
+                    if (s.y == 0.f) continue;  // the state holds nothing (and its O may be unwritten)
+                    const float4 a = ld_cluster_f32x4(st + (slot * Geo::kOStride + c) * 4);
+                    const float mn = fmaxf(m, s.x);
+                    const float f_old = m == mn ? 1.f : ex2(m - mn), f_new = s.x == mn ? 1.f : ex2(s.x - mn);
+                    o = fma4(f_new, a, scale4(o, f_old));
+                    l = l * f_old + s.y * f_new;
+                    m = mn;
+                }
+            }
+            const int64_t orow = (static_cast<int64_t>(b) * p.T + rr / p.G) * p.Hq + hk * p.G + rr % p.G;
+            if (whole) o = scale4(o, l > 0.f || l != l ? 1.f / l : 0.f);
+            if (bad_v != 0) {
+                // infinities and NaN of the tree's V rows that this row sees, in the noted CTAs' keys
+                const uint64_t mask = p.masks[static_cast<int64_t>(b) * p.T + rr / p.G];
+                for (int t = 0; t < tree; ++t) {
+                    const int pos = hist + t, q = pos / kKeys / p.chunk - clus * p.cluster;
+                    if (!((mask >> t) & 1) || q < 0 || q >= ncta || !((bad_v >> q) & 1u)) continue;
+                    const int64_t blk = table_row[pos / kBlockSize];
+                    const __half* v = p.v_cache + ((blk * p.Hkv + hk) * kBlockSize + pos % kBlockSize) * D + c;
+                    const float y[4] = {__half2float(v[0]), __half2float(v[1]), __half2float(v[2]), __half2float(v[3])};
+                    if (!(fabsf(y[0]) < INFINITY)) o.x += y[0];
+                    if (!(fabsf(y[1]) < INFINITY)) o.y += y[1];
+                    if (!(fabsf(y[2]) < INFINITY)) o.z += y[2];
+                    if (!(fabsf(y[3]) < INFINITY)) o.w += y[3];
+                }
+            }
+            if (whole) {
+                store_out4(p.out, p.out_f32, orow * D + c, o);
+            } else {
+                const int64_t prow = orow * p.nclus + clus;
+                if (c == 0) *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(m, l);
+                *reinterpret_cast<float4*>(p.part_acc + prow * D + c) = o;
+            }
+        }
+    }
+    if (p.cluster > 1) {
+        __syncwarp();
+        cluster_sync_all();  // no CTA leaves while another reads its shared memory
     }
 }
 
@@ -639,18 +675,18 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
     const int b = static_cast<int>(bt / p.T), t = static_cast<int>(bt % p.T);
     int tree, ctx;
     if (!lengths(p, b, tree, ctx) || t >= tree) return;
-    const int nchunks = (key_tiles(ctx) + p.chunk - 1) / p.chunk;
-    if (nchunks <= 1) return;  // the attention kernel wrote the row
+    const int per_clus = p.chunk * p.cluster, nclus = (key_tiles(ctx) + per_clus - 1) / per_clus;
+    if (nclus <= 1) return;  // the attention kernel wrote the row
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int s = 0; s < nchunks; ++s) {
-        const int64_t at = row * p.max_chunks + s;
+    for (int s = 0; s < nclus; ++s) {
+        const int64_t at = row * p.nclus + s;
         const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
         const float4 a = *reinterpret_cast<const float4*>(p.part_acc + at * D + c);
-        if (ml.y == 0.f) continue;  // the row saw none of the chunk's keys
+        if (ml.y == 0.f) continue;  // the row saw none of the part's keys
         const float mn = fmaxf(m, ml.x);
-        const float f_old = m == mn ? 1.f : m == -INFINITY ? 0.f : ex2(m - mn), f_new = ml.x == mn ? 1.f : ex2(ml.x - mn);
+        const float f_old = m == mn ? 1.f : ex2(m - mn), f_new = ml.x == mn ? 1.f : ex2(ml.x - mn);
         o = fma4(f_new, a, scale4(o, f_old));
         l = l * f_old + ml.y * f_new;
         m = mn;
@@ -659,6 +695,58 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
 }
 
 }  // namespace tree
+
+constexpr int kTreeSplitCluster = 4;  // CTAs per cluster where a context needs several clusters
+constexpr int kTreeCtaCost = 8;       // in half key tiles
+constexpr int kTreeCombineCost = 6;
+
+template <int D, bool kSplitP>
+static cudaError_t tree_setup() {
+    static std::once_flag once;
+    static cudaError_t err = cudaSuccess;
+    std::call_once(once, [] {
+        err = cudaFuncSetAttribute(tree::paged_decode_tree_kernel<D, kSplitP>,
+                                   cudaFuncAttributeMaxDynamicSharedMemorySize, tree::Geom<D>::kSmemBytes);
+    });
+    return err;
+}
+
+// Clusters of cs CTAs (one per SM) that the device holds at a time; the SMs of a GPC that no whole cluster fills stay
+// idle.  Asked once per device and size.
+static int resident_clusters(int D, int cs, int sms) {
+    static std::atomic<int> cache[128][2][tree::kMaxTreeCluster + 1];
+    if (cs == 1) return sms;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return sms / cs;
+    std::atomic<int>& slot = cache[dev][D == 128][cs];
+    int n = slot.load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = cs;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(cs);
+    cfg.blockDim = dim3(tree::kThreads);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cudaError_t e;
+    if (D == 64) {
+        cfg.dynamicSmemBytes = tree::Geom<64>::kSmemBytes;
+        e = tree_setup<64, false>();
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, tree::paged_decode_tree_kernel<64, false>, &cfg);
+    } else {
+        cfg.dynamicSmemBytes = tree::Geom<128>::kSmemBytes;
+        e = tree_setup<128, false>();
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, tree::paged_decode_tree_kernel<128, false>, &cfg);
+    }
+    if (e != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        n = std::max(1, sms / cs);
+    }
+    slot.store(n, std::memory_order_relaxed);
+    return n;
+}
 
 cudaError_t tree_plan(int B, int Hq, int Hkv, int D, int max_ctx, int T, TreePlan* plan) {
     const int sms = sm_count();
@@ -669,45 +757,42 @@ cudaError_t tree_plan(int B, int Hq, int Hkv, int D, int max_ctx, int T, TreePla
     plan->row_pairs = (row_tiles + 1) / 2;
     const int tiles = std::max(1, (max_ctx + tree::kKeys - 1) / tree::kKeys);
     const int64_t units = std::max<int64_t>(1, static_cast<int64_t>(B) * Hkv * plan->row_pairs);
-    // The number of chunks with the shortest run, counted in key tiles: waves of CTAs (one per SM) times the tiles of
-    // a chunk plus the start and end of a CTA (about four tiles' time); several chunks also pay for their states and
-    // the combine launch (about three).
-    int best = 1;
+    // The split of the context with the shortest run, counted in key tiles: waves of clusters times the tiles of a CTA
+    // plus the start and end of a CTA; merging in a cluster costs little, partial states and the combine launch more.
     int64_t best_cost = INT64_MAX;
-    for (int nc = 1; nc <= std::min(tiles, 64); ++nc) {
+    for (int nc = 1; nc <= std::min(tiles, 128); ++nc) {
         const int chunk = (tiles + nc - 1) / nc;
-        const int used = (tiles + chunk - 1) / chunk;
-        if (used != nc) continue;
-        const int64_t waves = (units * nc + sms - 1) / sms;
-        const int64_t cost = waves * (chunk + 4) + (nc > 1 ? 3 + nc / 8 : 0);
+        if ((tiles + chunk - 1) / chunk != nc) continue;
+#ifdef KVC_TREE_NC
+        if (nc != KVC_TREE_NC) continue;
+#endif
+        const int cs = std::min(nc, nc <= tree::kMaxTreeCluster ? tree::kMaxTreeCluster : kTreeSplitCluster);
+        const int nclus = (nc + cs - 1) / cs;
+        const int64_t resident = resident_clusters(D, cs, sms);
+        const int64_t waves = (units * nclus + resident - 1) / resident;
+        const int64_t cost = waves * (2 * chunk + kTreeCtaCost) + (nc > 1 ? 1 + cs / 2 : 0) + (nclus > 1 ? kTreeCombineCost + nclus / 4 : 0);
         if (cost < best_cost) {
             best_cost = cost;
-            best = nc;
+            plan->chunk = chunk;
+            plan->cluster = cs;
+            plan->nclus = nclus;
         }
     }
-    plan->chunk = (tiles + best - 1) / best;
-    plan->max_chunks = (tiles + plan->chunk - 1) / plan->chunk;
-    plan->workspace_bytes =
-        plan->max_chunks > 1 ? partials_bytes(static_cast<size_t>(B) * T * Hq * plan->max_chunks, D) : 0;
+    plan->workspace_bytes = plan->nclus > 1 ? partials_bytes(static_cast<size_t>(B) * T * Hq * plan->nclus, D) : 0;
     return cudaSuccess;
 }
 
 template <int D, bool kSplitP>
 static cudaError_t launch_tree_d(const TreeArgs& a, const TreePlan& plan, cudaStream_t stream) {
     using Geo = tree::Geom<D>;
-    static std::once_flag attr_once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(attr_once, [] {
-        attr_err = cudaFuncSetAttribute(tree::paged_decode_tree_kernel<D, kSplitP>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize, Geo::kSmemBytes);
-    });
-    if (attr_err != cudaSuccess) return attr_err;
+    cudaError_t e = tree_setup<D, kSplitP>();
+    if (e != cudaSuccess) return e;
     const int64_t rows = static_cast<int64_t>(a.num_blocks) * a.Hkv * kBlockSize;
     CUtensorMap tmK, tmV;
-    cudaError_t e = make_tile_map(&tmK, a.k_cache, D, rows);
+    e = make_tile_map(&tmK, a.k_cache, D, rows);
     if (e == cudaSuccess) e = make_tile_map(&tmV, a.v_cache, D, rows);
     if (e != cudaSuccess) return e;
-    const size_t nrow = static_cast<size_t>(a.B) * a.T * a.Hq * plan.max_chunks;
+    const size_t nrow = static_cast<size_t>(a.B) * a.T * a.Hq * plan.nclus;
     tree::Params p;
     p.q = a.q;
     p.block_table = a.block_table;
@@ -717,7 +802,7 @@ static cudaError_t launch_tree_d(const TreeArgs& a, const TreePlan& plan, cudaSt
     p.v_cache = a.v_cache;
     p.out = a.out;
     p.part_ml = static_cast<float*>(a.workspace);
-    p.part_acc = plan.max_chunks > 1 ? partials_acc(p.part_ml, nrow) : nullptr;
+    p.part_acc = plan.nclus > 1 ? partials_acc(p.part_ml, nrow) : nullptr;
     p.err = a.err;
     p.T = a.T;
     p.Hq = a.Hq;
@@ -728,14 +813,15 @@ static cudaError_t launch_tree_d(const TreeArgs& a, const TreePlan& plan, cudaSt
     p.max_ctx = a.max_context_len;
     p.out_f32 = a.out_f32;
     p.chunk = plan.chunk;
-    p.max_chunks = plan.max_chunks;
+    p.cluster = plan.cluster;
+    p.nclus = plan.nclus;
     p.row_pairs = plan.row_pairs;
     p.negate = a.scale < 0.f;
     p.scale_log2 = std::max(std::fabs(a.scale) * kLog2e, tree::kMinScaleLog2);
-    const dim3 grid(static_cast<unsigned>(plan.row_pairs * plan.max_chunks), a.Hkv, a.B);
+    const dim3 grid(static_cast<unsigned>(plan.row_pairs * plan.nclus * plan.cluster), a.Hkv, a.B);
     e = launch(tree::paged_decode_tree_kernel<D, kSplitP>, grid, dim3(tree::kThreads), Geo::kSmemBytes, stream, false,
-               1u, tmK, tmV, p);
-    if (e != cudaSuccess || plan.max_chunks == 1) return e;
+               static_cast<unsigned>(plan.cluster), tmK, tmV, p);
+    if (e != cudaSuccess || plan.nclus == 1) return e;
     const int64_t nrows = static_cast<int64_t>(a.B) * a.T * a.Hq;
     constexpr int per_cta = tree::kCombineWarps * 128 / D;
     return launch(tree::tree_combine_kernel<D>, dim3(static_cast<unsigned>((nrows + per_cta - 1) / per_cta)),

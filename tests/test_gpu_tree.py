@@ -211,6 +211,8 @@ TREES = [
     ([5000, 2500], [8, 1], 8, 14, 2, 64, False),
     ([0, 0], [0, 0], 5, 4, 4, 64, False),
     ([30, 31, 32], [2, 2, 2], 2, 8, 8, 128, False),
+    ([30000, 9000, 0], [5, 5, 5], 5, 2, 1, 64, False),    # several clusters of chunks, and their combine
+    ([20000, 3], [33, 40], 40, 8, 1, 128, True),          # the same with two row tiles
 ]
 
 
@@ -302,7 +304,7 @@ def test_tree_attention_flags_bad_inputs(kvc):
 
 
 def test_tree_attention_argument_checks(kvc, monkeypatch):
-    w = Tree(24, [3000], [4], 4, 4, 2, 64)
+    w = Tree(24, [30000], [4], 4, 4, 2, 64)
     w.run(kvc)
     d = w.d
     args = [d["q"], d["k"], d["v"], d["table"], d["ctx"], d["masks"], w.scale, w.out, w.ws, w.max_ctx]
@@ -319,16 +321,16 @@ def test_tree_attention_argument_checks(kvc, monkeypatch):
         with pytest.raises(kvc.KvcError) as e:
             call(8, ws)
         assert e.value.name == "KVC_ERR_INVALID"
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(kvc, "_current_device", lambda: 1)
     with pytest.raises(ValueError, match="current device"):
         call(0, d["q"])
 
 
 def test_tree_attention_captured_on_another_stream(kvc):
     """A captured call follows the lengths, masks and queries it finds at replay; two graphs share a workspace."""
-    w, x = Tree(25, [3000, 50], [9, 20], 20, 14, 2, 64), Tree(26, [10, 10], [20, 3], 20, 14, 2, 64)
+    w, x = Tree(25, [30000, 50], [9, 20], 20, 14, 2, 64), Tree(26, [10, 10], [20, 3], 20, 14, 2, 64)
     x.table, x.k, x.v, x.max_ctx = w.table, w.k, w.v, w.max_ctx
-    x.ctx = np.array([3005, 60], np.int32)  # inside what the pool holds
+    x.ctx = np.array([30005, 60], np.int32)  # inside what the pool holds
     assert kvc.paged_decode_tree_plan(2, 14, 2, 64, w.max_ctx, 20) > 0
     ref = []
     for t in (w, x):
