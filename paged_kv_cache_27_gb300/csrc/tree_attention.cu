@@ -22,8 +22,9 @@
 // output they are an fp16 high part plus residual (two products), ~22 bits.
 // The context is cut into chunks where (sequence, KV head, row tile pair) units are fewer than SMs; a chunk's state
 // (max, sum, O) goes through the workspace to the combine kernel below.
-// Lane 0 of warp 8 issues the products, warp 9 the copies (lane i the block i of a tile).  Every wait is bounded.
+// Every wait is bounded.
 #include <algorithm>
+#include <type_traits>
 
 #include "../../include/kvc.h"
 #include "decode_common.cuh"
@@ -36,13 +37,16 @@ namespace tree {
 
 constexpr int kRows = 128;  // rows of a row tile
 constexpr int kKeys = 128;  // keys of a key tile
+constexpr int kHalf = 64;   // keys of one step of a stream
 constexpr int kPages = kKeys / kBlockSize;
 constexpr int kRowWarps = 8;
-constexpr int kMmaWarp = kRowWarps;
-constexpr int kLoadKWarp = kRowWarps + 1;
-constexpr int kLoadVWarp = kRowWarps + 2;
-constexpr int kThreads = (kRowWarps + 3) * 32;
+constexpr int kSWarp = kRowWarps;        // S products of stream A, of stream B
+constexpr int kPvWarp = kRowWarps + 2;   // P V products of stream A, of stream B
+constexpr int kLoadKWarp = kRowWarps + 4;
+constexpr int kLoadVWarp = kRowWarps + 5;
+constexpr int kThreads = (kRowWarps + 6) * 32;
 constexpr int kMaxTreeCluster = 8;
+constexpr int kMaxStates = 2 * kMaxTreeCluster;  // states of a row in a cluster
 constexpr uint64_t kWaitNs = 1000000000ull;
 // a scale of 0 is taken as this: the scores of fp16 rows (below 2^40) still vanish next to 1, and a masked score of
 // -inf times it stays -inf
@@ -70,9 +74,11 @@ struct Geom {
     static constexpr int kOStride = D + 4;  // floats
     static constexpr int kStateOff = kVOff;
     static constexpr int kMlOff = kStateOff + 2 * kRows * kOStride * 4;
-    static_assert(kMlOff + 2 * kRows * 8 <= kBarOff, "state area");
-    // TMEM columns: S_A / P_A [0, 128), S_B / P_B [128, 256), O_A [256, 256 + D), O_B [256 + D, 256 + 2D)
-    static constexpr int kTmemO = 2 * kKeys;
+    static constexpr int kWeightOff = kMlOff + 2 * kRows * 8;  // the states' weights of the rows this CTA merges
+    // (rows / CTAs, rounded up, times states: at most 2 * 128 and one more row's)
+    static_assert(kWeightOff + (2 * kRows + kMaxStates) * 8 <= kBarOff, "state area");
+    // TMEM columns: two buffers of S / P per stream, A [0, 128) and B [128, 256), O_A [256, 256 + D), O_B [256 + D, 256 + 2D)
+    static constexpr int kTmemO = 4 * kHalf;
     static constexpr uint32_t kTmemCols = 512;
 };
 
@@ -92,6 +98,7 @@ struct Params {
     int cluster;    // CTAs per cluster: consecutive chunks of one unit, merged in distributed shared memory
     int nclus;      // clusters along the longest context: stride of the partial states
     int row_pairs;  // pairs of row tiles of the widest tree
+    uint32_t g_magic;  // ceil(2^18 / G): row * g_magic >> 18 = row / G for rows below 4096
     int negate;      // scale < 0: the query rows change sign as they are loaded
     float scale_log2;  // |scale| * log2 e, at least kMinScaleLog2
 };
@@ -138,6 +145,27 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
         }
     }
 }
+// The same for a whole warp whose waits sit between two products: it polls instead of sleeping.
+__device__ __forceinline__ bool wait_poll(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t i = 1;; ++i) {
+        if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+        if ((i & 255u) == 0u) {
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
+            if (__any_sync(0xffffffffu, global_timer_ns() - t0 > kWaitNs)) {
+                *abort_flag = 1;
+                return false;
+            }
+        }
+    }
+}
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id, int threads) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
 __device__ __forceinline__ void row_warps_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kRowWarps * 32) : "memory"); }
 
 // an infinity or NaN among the 8 fp16 values of a chunk
@@ -173,10 +201,7 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
     return v;
 }
 
-// Sizes of sequence b; false where its lengths do not fit (tree_len and ctx stay as read).
-__device__ __forceinline__ bool lengths(const Params& p, int b, int& tree, int& ctx) {
-    tree = p.tree_lens != nullptr ? p.tree_lens[b] : p.T;
-    ctx = p.context_lens[b];
+__device__ __forceinline__ bool lengths_fit(const Params& p, int tree, int ctx) {
     return tree >= 0 && tree <= p.T && ctx >= tree && ctx <= p.max_ctx &&
            ctx <= static_cast<int64_t>(p.max_blocks) * kBlockSize;
 }
@@ -196,28 +221,60 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
     uint64_t* k_empty = k_full + KS;         // [KS] S products of the stage's tile done
     uint64_t* v_full = k_empty + KS;         // [MVS] V tile landed
     uint64_t* v_empty = v_full + MVS;        // [MVS] P V products of the stage's tile done
-    uint64_t* s_full = v_empty + MVS;        // [2] S_X of the stream's tile in TMEM
-    uint64_t* p_full = s_full + 2;           // [2] P_X of the stream's tile in TMEM (4 arrivals)
-    uint64_t* o_full = p_full + 2;           // [2] P_X V of the stream's tile done
-    uint64_t* fin = o_full + 2;              // every MMA issued so far done
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(fin + 1);
+    uint64_t* s_full = v_empty + MVS;        // [2][2] S of stream x's buffer i in TMEM (index 2 x + i)
+    uint64_t* p_full = s_full + 4;           // [2][2] P of the buffer in TMEM (4 arrivals)
+    uint64_t* o_full = p_full + 4;           // [2][2] P V of the buffer done
+    uint64_t* fin = o_full + 4;              // [4] every product that a product warp issued is done
+    uint64_t* v_land = fin + 4;              // [2] the V tiles that reach into the tree landed (then mended)
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(v_land + 2);
     volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
     volatile int* s_bad_block = s_abort + 1;  // a block id out of range: the chunk is left out
     volatile int* s_bad_v = s_abort + 2;      // an infinity or NaN among the tree's V values
-    static_assert((1 + 2 * KS + 2 * MVS + 7) * 8 + 16 <= 512, "barrier area");
+    volatile int* s_bad_of = s_abort + 3;     // bit q: CTA q of the cluster has noted such values
+    static_assert((1 + 2 * KS + 2 * MVS + 18) * 8 + 20 <= 512, "barrier area");
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (the shuffle tells the compiler that the warp index is the same in all lanes: the product warp's descriptors and
+    // counters then live in uniform registers, as its instructions want them)
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     // blockIdx.x = (cluster along the context * row pairs + row pair) * CTAs per cluster + rank
     const int rank = static_cast<int>(blockIdx.x) % p.cluster;
     const int pair = static_cast<int>(blockIdx.x) / p.cluster % p.row_pairs;
     const int clus = static_cast<int>(blockIdx.x) / p.cluster / p.row_pairs;
     const int hk = blockIdx.y, b = blockIdx.z;
-    int tree, ctx;
-    if (!lengths(p, b, tree, ctx)) {
+    const int r0 = pair * 2 * kRows;
+    const int per_clus = p.chunk * p.cluster, c0 = clus * per_clus + rank * p.chunk;
+    auto node_of = [&](int rr) { return static_cast<int>(static_cast<uint32_t>(rr) * p.g_magic >> 18); };  // rr / G
+
+    // Loads that do not depend on the lengths go out together with them: the block ids of the first four key tiles
+    // (entries past the context are not used) and the query rows (rows past the tree are not used).
+    const int32_t* const table_row = p.block_table + static_cast<int64_t>(b) * p.max_blocks;
+    auto block_ids = [&](int j) {  // of tiles j .. j + 3, eight lanes each
+        const int page = (c0 + j) * kPages + lane;
+        return page < p.max_blocks ? table_row[page] : 0;
+    };
+    const int tree = p.tree_lens != nullptr ? p.tree_lens[b] : p.T, ctx = p.context_lens[b];
+    int ids = 0;
+    constexpr int kQLoads = D / 8;  // 16-byte chunks of two row tiles per row thread
+    constexpr int kQStep = kRowWarps * 32 / (D / 8);
+    uint4 qv[kQLoads];
+    if (warp < kRowWarps) {
+#pragma unroll
+        for (int i = 0; i < kQLoads; ++i) {
+            const int rr = r0 + threadIdx.x / (D / 8) + i * kQStep, t = node_of(rr);
+            qv[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (rr < p.T * p.G)
+                qv[i] = *reinterpret_cast<const uint4*>(
+                    p.q + ((static_cast<int64_t>(b) * p.T + t) * p.Hq + hk * p.G + rr - t * p.G) * D +
+                    threadIdx.x % (D / 8) * 8);
+        }
+    } else if (warp >= kLoadKWarp) {
+        ids = block_ids(0);
+    }
+    if (!lengths_fit(p, tree, ctx)) {
         if (blockIdx.x == 0) {
             if (threadIdx.x == 0) atomicOr(p.err, KVC_DEVERR_CONTEXT);
-            const int rows = min(max(tree, 0), p.T);
-            for (int e = threadIdx.x; e < rows * p.G * D; e += kThreads) {
+            const int rows = min(max(tree, 0), p.T) * p.G;
+            for (int e = threadIdx.x; e < rows * D; e += kThreads) {
                 const int r = e / D;
                 store_out(p.out, p.out_f32,
                           ((static_cast<int64_t>(b) * p.T + r / p.G) * p.Hq + hk * p.G + r % p.G) * D + e % D, 0.f);
@@ -225,214 +282,251 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
         }
         return;
     }
-    const int rows = tree * p.G, r0 = pair * 2 * kRows;
-    const int all_tiles = key_tiles(ctx), per_clus = p.chunk * p.cluster;
+    const int rows = tree * p.G, all_tiles = key_tiles(ctx);
     if (r0 >= rows || clus * per_clus >= all_tiles) return;  // the whole cluster
-    const int c0 = clus * per_clus + rank * p.chunk;
     const int n = max(0, min(p.chunk, all_tiles - c0));  // key tiles of this CTA
     const bool two_rows = rows - r0 > kRows;             // two row tiles: they are the streams
-    const int step = two_rows ? 1 : 2;                   // key tiles between two of a stream's
+    const int units = two_rows ? 2 * n : n;              // 64-key steps of each stream
     const int hist = ctx - tree;                         // keys before the tree
     const int pages = (ctx + kBlockSize - 1) / kBlockSize;
     const bool whole = all_tiles <= per_clus;            // one cluster covers the context: no partial states
     const uint32_t VS = two_rows ? Geo::kVStages : MVS;
+    // unit u of stream x: key tile and half of the tile
+    auto tile_of = [&](int u) { return two_rows ? u >> 1 : u; };
+    auto half_of = [&](int u, int x) { return two_rows ? u & 1 : x; };
 
     auto qs = [&](int x) { return smem + Geo::kQOff + x * Geo::kTileBytes; };
     auto kst = [&](uint32_t st) { return smem + Geo::kKOff + st * Geo::kTileBytes; };
     uint8_t* const vring = smem + (two_rows ? Geo::kVOff : Geo::kVOff - Geo::kTileBytes);
     auto vst = [&](uint32_t st) { return vring + st * Geo::kTileBytes; };
 
-    // Copies of key tile j: lane i of the calling warp takes block i.
-    const int32_t* const table_row = p.block_table + static_cast<int64_t>(b) * p.max_blocks;
-    auto block_of = [&](int j) {
-        const int page = (c0 + j) * kPages + lane;
-        return lane < kPages && page < pages ? table_row[page] : 0;
-    };
-    // a block id out of range is flagged and block 0 copied in its place; the chunk's values are then not used
-    auto checked_block = [&](int phys) {
-        if (phys >= 0 && phys < p.num_blocks) return phys;
-        atomicOr(p.err, KVC_DEVERR_BLOCK_ID);
-        *s_bad_block = 1;  // seen by the row warps behind this tile's barriers
-        return 0;
-    };
-    auto load = [&](uint8_t* tile, const CUtensorMap* map, uint64_t* bar, int j, int phys, uint64_t policy) {
-        const int np = min(kPages, pages - (c0 + j) * kPages);
-        if (lane == 0) mbar_arrive_expect_tx(bar, np * (kBlockSize * D * 2));
-        __syncwarp();
-        if (lane < np) {
-#pragma unroll
-            for (int c = 0; c < Geo::kChunks; ++c)
-                tma_load_2d(tile + c * Geo::kChunkBytes + lane * (kBlockSize * 128), map, bar, c * 64,
-                            (phys * p.Hkv + hk) * kBlockSize, policy);
-        }
-    };
-    // one pair of row tiles reads its K and V once; several pairs meet them in L2
-    uint64_t policy = 0;
-    const int pre = min(n, Geo::kVStages);  // tiles whose copies start before the CTA's other preparations
-    if (warp == kLoadKWarp) {
-        if (lane == 0) {
+    // The copy warps start as soon as the barriers are there; the others also need the tensor memory.
+    uint32_t tmem = 0;
+    if (warp >= kLoadKWarp) {
+        if (warp == kLoadKWarp && lane == 0) {
             mbar_init(q_full, kRowWarps);
             for (int i = 0; i < KS; ++i) {
                 mbar_init(&k_full[i], 1);
-                mbar_init(&k_empty[i], 1);
+                mbar_init(&k_empty[i], 2);  // both streams' products
             }
             for (int i = 0; i < MVS; ++i) {
                 mbar_init(&v_full[i], 1);
-                mbar_init(&v_empty[i], 1);
+                mbar_init(&v_empty[i], 2);
             }
-            for (int x = 0; x < 2; ++x) {
-                mbar_init(&s_full[x], 1);
-                mbar_init(&p_full[x], 4);
-                mbar_init(&o_full[x], 1);
+            for (int i = 0; i < 4; ++i) {
+                mbar_init(&s_full[i], 1);
+                mbar_init(&p_full[i], 4);
+                mbar_init(&o_full[i], 1);
+                mbar_init(&fin[i], 1);
             }
-            mbar_init(fin, 1);
+            mbar_init(&v_land[0], 1);
+            mbar_init(&v_land[1], 1);
             *s_abort = 0;
             *s_bad_block = 0;
             *s_bad_v = 0;
+            *s_bad_of = 0;
             fence_barrier_init();
         }
         __syncwarp();
-        policy = p.row_pairs == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
-        static_assert(Geo::kVStages <= KS, "the first copies find every stage free");
-        for (int j = 0; j < pre; ++j) {
-            const int phys = checked_block(block_of(j));
-            load(kst(j), &tmK, &k_full[j], j, phys, policy);
-            load(vst(j), &tmV, &v_full[j], j, phys, policy);
+        bar_sync(2, 64);  // the two copy warps
+        bar_arrive(3, kThreads);
+    } else {
+        if (warp == 0) {
+            tmem_alloc(s_tmem, Geo::kTmemCols);
+            tmem_relinquish();
+            tc_fence_before();
         }
+        bar_sync(3, kThreads);
+        tc_fence_after();
+        tmem = *s_tmem;
     }
-    if (warp == 0) {
-        tmem_alloc(s_tmem, Geo::kTmemCols);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *s_tmem;
 
-    if (warp == kLoadKWarp || warp == kLoadVWarp) {
-        // ================= copies: a warp for K and one for V, each as far ahead as its ring allows =================
+    if (warp >= kLoadKWarp) {
+        // ====== copies: a warp for K and one for V, each as far ahead as its ring allows; lane i copies block i ======
         const bool is_v = warp == kLoadVWarp;
-        if (is_v) policy = p.row_pairs == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
+        // one pair of row tiles reads its K and V once; several pairs meet them in L2
+        const uint64_t policy = p.row_pairs == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
         uint64_t* const full = is_v ? v_full : k_full;
         uint64_t* const empty = is_v ? v_empty : k_empty;
+        const CUtensorMap* const map = is_v ? &tmV : &tmK;
         const uint32_t stages = is_v ? VS : KS;
-        uint32_t st = static_cast<uint32_t>(pre) % stages, ph = static_cast<uint32_t>(pre) / stages;  // of tile j
-        int issued = pre;
+        const int mend0 = min(n, max(0, hist / kKeys - c0));  // first tile that reaches into the tree; at most two do
+        uint32_t st = 0, ph = 0;  // stage and use of tile j
+        int issued = 0, ids_next = 0;
         bool ok = true;
-        int next = pre < n ? block_of(pre) : 0;
-        for (int j = pre; j < n; ++j) {
-            const int phys = checked_block(next);
-            if (j + 1 < n) next = block_of(j + 1);
+        for (int j = 0; j < n; ++j) {
+            if ((j & 3) == 0) {
+                if (j > 0) ids = ids_next;
+                if (j + 4 < n) ids_next = block_ids(j + 4);
+            }
+            const int np = min(kPages, pages - (c0 + j) * kPages);
+            int phys = __shfl_sync(0xffffffffu, ids, (j & 3) * kPages + (lane & (kPages - 1)));
+            if (lane < np && (phys < 0 || phys >= p.num_blocks)) {
+                // flagged, and block 0 copied in its place; the chunk's values are then not used
+                atomicOr(p.err, KVC_DEVERR_BLOCK_ID);
+                *s_bad_block = 1;  // seen by the row warps behind this tile's barriers
+                phys = 0;
+            }
             if (ph > 0) ok = __all_sync(0xffffffffu, wait(&empty[st], (ph - 1) & 1, s_abort));
             if (!ok) break;
-            load(is_v ? vst(st) : kst(st), is_v ? &tmV : &tmK, &full[st], j, phys, policy);
+            // V tiles that reach into the tree are mended before the products may read them
+            const bool mend = is_v && (c0 + j + 1) * kKeys > hist;
+            uint64_t* const bar = mend ? &v_land[j - mend0] : &full[st];
+            if (lane == 0) mbar_arrive_expect_tx(bar, np * (kBlockSize * D * 2));
+            __syncwarp();
+            if (lane < np) {
+                uint8_t* tile = is_v ? vst(st) : kst(st);
+#pragma unroll
+                for (int c = 0; c < Geo::kChunks; ++c)
+                    tma_load_2d(tile + c * Geo::kChunkBytes + lane * (kBlockSize * 128), map, bar, c * 64,
+                                (phys * p.Hkv + hk) * kBlockSize, policy);
+            }
             issued = j + 1;
             if (++st == stages) {
                 st = 0;
                 ++ph;
             }
         }
-        // copies still in flight land before the shared memory is used otherwise or released (immediate unless
-        // aborted: the products consumed every tile)
-        if (lane == 0)
-            for (int t = max(0, issued - static_cast<int>(stages)); t < issued; ++t)
-                mbar_wait_bounded(&full[t % stages], (t / stages) & 1, kWaitNs / 8);
-    } else if (warp == kMmaWarp) {
-        // ================= tensor-core products (one thread) =================
-        if (lane == 0) {
-            constexpr uint32_t idS = umma_idesc_f16(kRows, kKeys, 0, 0);
-            constexpr uint32_t idPV = umma_idesc_f16(kRows, D, 0, 1);
-            const uint64_t dQ = umma_smem_desc(smem_u32(qs(0)), 16, 1024);
-            const uint64_t dK = umma_smem_desc(smem_u32(kst(0)), 16, 1024);
-            // V as the MN-major B operand: 8-key groups 1024 bytes apart, 64-dim atoms one chunk apart
-            const uint64_t dV = umma_smem_desc(smem_u32(vring), Geo::kChunkBytes, 1024);
-            // S_X = Q_X K^T over D / 16 steps of 16 dims (with one row tile both streams use it)
-            auto mma_s = [&](int x, uint32_t st) {
-                const uint64_t a0 = dQ + static_cast<uint64_t>(two_rows ? x * (Geo::kTileBytes >> 4) : 0);
-                const uint64_t b0 = dK + static_cast<uint64_t>(st * (Geo::kTileBytes >> 4));
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const int c = ks >> 2, kk = ks & 3;
-                    umma_f16_ss(tmem + x * kKeys, a0 + ((c * Geo::kChunkBytes + kk * 32) >> 4),
-                                b0 + ((c * Geo::kChunkBytes + kk * 32) >> 4), idS, ks > 0);
-                }
-                umma_commit(&s_full[x]);
-            };
-            // O_X += P_X V: 8 steps of 16 keys, P from TMEM (fp16, or its high part and residual)
-            auto mma_pv = [&](int x, uint32_t st, bool first) {
-                const uint64_t v0 = dV + static_cast<uint64_t>(st * (Geo::kTileBytes >> 4));
-                const uint32_t tP = tmem + x * kKeys, tO = tmem + Geo::kTmemO + x * D;
-#pragma unroll
-                for (int kk = 0; kk < kKeys / 16; ++kk) {
-                    const uint64_t bd = v0 + ((kk * 2048) >> 4);
-                    umma_f16_ts(tO, tP + kk * 8, bd, idPV, (!first || kk > 0) ? 1u : 0u);
-                    if constexpr (kSplitP) umma_f16_ts(tO, tP + 64 + kk * 8, bd, idPV, 1u);
-                }
-                umma_commit(&o_full[x]);
-            };
-            bool ok = n == 0 || wait(q_full, 0, s_abort);
-            // the first tile of each stream: tile 0 for both, or tiles 0 and 1
-            for (int x = 0; ok && x < 2; ++x) {
-                const int j = two_rows ? 0 : x;
-                if (j >= n) break;
-                if (!(ok = wait(&k_full[j], 0, s_abort))) break;
-                tc_fence_after();
-                mma_s(x, j);
-                if (!two_rows || x == 1) umma_commit(&k_empty[j]);
+        if (!is_v) {
+            // copies still in flight land before the shared memory is used otherwise or released (immediate unless
+            // aborted: the products consumed every tile)
+            if (lane == 0)
+                for (int t = max(0, issued - KS); t < issued; ++t)
+                    mbar_wait_bounded(&k_full[t % KS], (t / KS) & 1, kWaitNs / 8);
+        } else {
+            if (lane == 0) {
+                for (int t = max(0, issued - static_cast<int>(VS)); t < min(issued, mend0); ++t)
+                    mbar_wait_bounded(&v_full[t % VS], (t / VS) & 1, kWaitNs / 8);
+                for (int t = mend0; t < issued; ++t) mbar_wait_bounded(&v_land[t - mend0], 0, kWaitNs / 8);
             }
-            uint32_t vs = 0, vph = 0;                                                    // V stage and phase of tile j
-            uint32_t ks = static_cast<uint32_t>(step) % KS, kph = static_cast<uint32_t>(step) / KS;  // K: of tile j + step
-            for (int j = 0; ok && j < n; ++j) {
-                if (!(ok = wait(&v_full[vs], vph & 1, s_abort))) break;
-                const int jn = j + step;
-                const uint32_t it = static_cast<uint32_t>(two_rows ? j : j >> 1);  // the streams' tile count
-                // per stream of this tile: P_X V once P_X is in TMEM; then the stream's next S_X into the same
-                // columns once that product has read P_X
-                for (int x = two_rows ? 0 : (j & 1), left = two_rows ? 2 : 1; ok && left > 0; ++x, --left) {
-                    if (!(ok = wait(&p_full[x], it & 1, s_abort))) break;
-                    tc_fence_after();
-                    mma_pv(x, vs, it == 0);
-                    if (jn < n) {
-                        if (!(ok = wait(&k_full[ks], kph & 1, s_abort))) break;
-                        if (!(ok = wait(&o_full[x], it & 1, s_abort))) break;
-                        tc_fence_after();
-                        mma_s(x, ks);
+            __syncwarp();
+        }
+        // V rows past the context are zeroed, so that whatever they hold cannot reach an output through a zero weight;
+        // so are infinities and NaN among the tree's V rows, which not every row sees (the rows that do get them back
+        // at the end).  Both copy warps work on it, the K warp's copies being done.
+        for (int t = mend0; t < n; ++t) {
+            if (ok) ok = __all_sync(0xffffffffu, wait(&v_land[t - mend0], 0, s_abort));
+            if (ok) {
+                uint8_t* vt = vst(t % VS);
+                const int k0 = (c0 + t) * kKeys, from = max(hist - k0, 0), end = ctx - k0;
+                bool found = false;
+                constexpr int U = 4;
+                for (int e0 = (warp - kLoadKWarp) * 32 + lane; e0 < (kKeys - from) * 8 * Geo::kChunks; e0 += 64 * U) {
+                    uint4 v[U];
+                    uint4* at[U];
+#pragma unroll
+                    for (int i = 0; i < U; ++i) {
+                        const int e = e0 + i * 64, r = from + e / (8 * Geo::kChunks), rest = e % (8 * Geo::kChunks);
+                        at[i] = reinterpret_cast<uint4*>(vt + (rest / 8) * Geo::kChunkBytes + sw128(r, rest % 8));
+                        if (r >= kKeys) at[i] = nullptr;
+                        v[i] = make_uint4(0u, 0u, 0u, 0u);
+                        if (r < min(end, kKeys)) v[i] = *at[i];
+                    }
+#pragma unroll
+                    for (int i = 0; i < U; ++i) {
+                        if (at[i] == nullptr) continue;
+                        bool bad = false;
+                        *at[i] = make_uint4(finite_halves(v[i].x, bad), finite_halves(v[i].y, bad),
+                                            finite_halves(v[i].z, bad), finite_halves(v[i].w, bad));
+                        found = found || bad;
                     }
                 }
+                if (found) *s_bad_v = 1;
+                fence_proxy_async_smem();  // visible to the tensor cores (async proxy)
+            }
+            __syncwarp();
+            bar_sync(2, 64);
+            if (is_v && lane == 0) mbar_arrive(&v_full[t % VS]);
+        }
+    } else if (warp >= kSWarp) {
+        // ====== tensor-core products: a warp per stream for S and one for P V.  A warp waits as one, its elected lane
+        // issues.  (One warp for all of them was bound by its own instruction stream: every wait is about 200 clocks
+        // and every product about 40.) ======
+        const int x = (warp - kSWarp) & 1;
+        bool ok = true;
+        uint32_t st = 0, ph = 0;  // stage and use of the unit's tile
+        if (warp < kPvWarp) {
+            // S of unit u = Q K^T over D / 16 steps of 16 dims (with one row tile both streams use Q_A), once the P of
+            // unit u - 2 in the same buffer is consumed
+            constexpr uint32_t idS = umma_idesc_f16(kRows, kHalf, 0, 0);
+            const uint64_t dQ = umma_smem_desc(smem_u32(qs(two_rows ? x : 0)), 16, 1024);
+            const uint64_t dK = umma_smem_desc(smem_u32(kst(0)), 16, 1024);
+            if (n > 0) ok = wait_poll(q_full, 0, s_abort);
+            for (int u = 0; ok && u < units; ++u) {
+                const int buf = 2 * x + (u & 1);
+                const bool last = !two_rows || (u & 1);  // the tile's last unit
+                ok = wait_poll(&k_full[st], ph & 1, s_abort);
+                if (ok && u >= 2) ok = wait_poll(&o_full[buf], ((u - 2) >> 1) & 1, s_abort);
                 if (!ok) break;
-                umma_commit(&v_empty[vs]);
-                if (jn < n) umma_commit(&k_empty[ks]);
-                if (++vs == VS) {
-                    vs = 0;
-                    ++vph;
+                tc_fence_after();
+                const uint64_t b0 = dK + static_cast<uint64_t>((st * Geo::kTileBytes + half_of(u, x) * kHalf * 128) >> 4);
+                const uint32_t tS = tmem + buf * kHalf;
+                if (elect_one()) {
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        const int c = i >> 2, kk = i & 3;
+                        umma_f16_ss(tS, dQ + ((c * Geo::kChunkBytes + kk * 32) >> 4),
+                                    b0 + ((c * Geo::kChunkBytes + kk * 32) >> 4), idS, i > 0);
+                    }
+                    umma_commit(&s_full[buf]);
+                    if (last) umma_commit(&k_empty[st]);
                 }
-                if (++ks == KS) {
-                    ks = 0;
-                    ++kph;
+                __syncwarp();
+                if (last && ++st == KS) {
+                    st = 0;
+                    ++ph;
                 }
             }
-            // every product issued is complete before the tensor memory is released
-            umma_commit(fin);
-            mbar_wait_bounded(fin, 0, kWaitNs);
-            if (!ok) atomicOr(p.err, KVC_DEVERR_TIMEOUT);
+        } else {
+            // O_X += P V of unit u: 4 steps of 16 keys, P from TMEM (fp16, or its high part and residual); V as the
+            // MN-major B operand: 8-key groups 1024 bytes apart, 64-dim atoms one chunk apart
+            constexpr uint32_t idPV = umma_idesc_f16(kRows, D, 0, 1);
+            const uint64_t dV = umma_smem_desc(smem_u32(vring), Geo::kChunkBytes, 1024);
+            const uint32_t tO = tmem + Geo::kTmemO + x * D;
+            for (int u = 0; u < units; ++u) {
+                const int buf = 2 * x + (u & 1);
+                const bool last = !two_rows || (u & 1);
+                ok = wait_poll(&v_full[st], ph & 1, s_abort) && wait_poll(&p_full[buf], (u >> 1) & 1, s_abort);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t v0 = dV + static_cast<uint64_t>((st * Geo::kTileBytes + half_of(u, x) * kHalf * 128) >> 4);
+                const uint32_t tP = tmem + buf * kHalf;
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < kHalf / 16; ++kk) {
+                        const uint64_t bd = v0 + ((kk * 2048) >> 4);
+                        umma_f16_ts(tO, tP + kk * 8, bd, idPV, (u > 0 || kk > 0) ? 1u : 0u);
+                        if constexpr (kSplitP) umma_f16_ts(tO, tP + kHalf / 2 + kk * 8, bd, idPV, 1u);
+                    }
+                    umma_commit(&o_full[buf]);
+                    if (last) umma_commit(&v_empty[st]);
+                }
+                __syncwarp();
+                if (last && ++st == VS) {
+                    st = 0;
+                    ++ph;
+                }
+            }
         }
+        // every product issued is complete before the tensor memory is released
+        if (elect_one()) umma_commit(&fin[warp - kSWarp]);
+        __syncwarp();
+        mbar_wait_bounded(&fin[warp - kSWarp], 0, kWaitNs);
+        if (!ok && lane == 0) atomicOr(p.err, KVC_DEVERR_TIMEOUT);
     } else {
-        // ================= row warps: query rows, softmax, output; thread = query row = TMEM lane =================
+        // ================= row warps: query rows, softmax; thread = query row = TMEM lane =================
         const int x = warp / 4, wq = warp & 3;
         const int row = wq * 32 + lane;
         {
-            const int nrows = two_rows ? 2 * kRows : kRows;
             const uint32_t flip = p.negate ? 0x80008000u : 0u;
-            for (int e = threadIdx.x; e < nrows * (D / 8); e += kRowWarps * 32) {
-                const int r = e / (D / 8), c = e % (D / 8), rr = r0 + r;
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (rr < rows) {
-                    const int64_t at =
-                        ((static_cast<int64_t>(b) * p.T + rr / p.G) * p.Hq + hk * p.G + rr % p.G) * D + c * 8;
-                    v = *reinterpret_cast<const uint4*>(p.q + at);
-                    v = make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
+            const int c = threadIdx.x % (D / 8);
+#pragma unroll
+            for (int i = 0; i < kQLoads; ++i) {
+                const int r = threadIdx.x / (D / 8) + i * kQStep;
+                if (i < kQLoads / 2 || two_rows) {
+                    const uint4 v = make_uint4(qv[i].x ^ flip, qv[i].y ^ flip, qv[i].z ^ flip, qv[i].w ^ flip);
+                    *reinterpret_cast<uint4*>(qs(r / kRows) + (c / 8) * Geo::kChunkBytes + sw128(r % kRows, c % 8)) = v;
                 }
-                *reinterpret_cast<uint4*>(qs(r / kRows) + (c / 8) * Geo::kChunkBytes + sw128(r % kRows, c % 8)) = v;
             }
             fence_proxy_async_smem();  // visible to the tensor cores (async proxy)
             __syncwarp();
@@ -442,71 +536,69 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
         const bool live = rr < rows;
         const bool live_warp = __any_sync(0xffffffffu, live);
         const uint64_t tree_bits = tree >= 64 ? ~0ull : (1ull << tree) - 1;
-        const uint64_t mask = live ? p.masks[static_cast<int64_t>(b) * p.T + rr / p.G] & tree_bits : 0;
+        const uint64_t mask = live ? p.masks[static_cast<int64_t>(b) * p.T + node_of(rr)] & tree_bits : 0;
         const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
-        const uint32_t tS = tmem + x * kKeys + lane_base, tO = tmem + Geo::kTmemO + x * D + lane_base;
+        const uint32_t tO = tmem + Geo::kTmemO + x * D + lane_base;
         const float sl2 = p.scale_log2;
+        const uint64_t sc2 = pack_f32x2(sl2, sl2);
         float m_used = -INFINITY, l = 0.f;
         bool ok = true;
-        int it = 0;
-        uint32_t vs = two_rows ? 0u : static_cast<uint32_t>(x), vph = 0;  // V stage and phase of tile j
-        for (int j = two_rows ? 0 : x; j < n; j += step, ++it) {
-            // S_X complete also means the stream's previous P_X V complete: it was waited for before S_X was issued
-            ok = __all_sync(0xffffffffu, wait(&s_full[x], it & 1, s_abort));
+        for (int u = 0; u < units; ++u) {
+            const int buf = 2 * x + (u & 1);
+            const uint32_t tS = tmem + buf * kHalf + lane_base;
+            ok = __all_sync(0xffffffffu, wait(&s_full[buf], (u >> 1) & 1, s_abort));
             if (!ok) break;
             tc_fence_after();
-            const int k0 = (c0 + j) * kKeys;
-            const bool masked = k0 + kKeys > hist;  // the tile reaches into the tree or past the context
+            const int k0 = (c0 + tile_of(u)) * kKeys + half_of(u, x) * kHalf;  // the unit's first key
+            const bool masked = k0 + kHalf > hist;  // it reaches into the tree or past the context
             if (live_warp) {
-                float s[kKeys];
-                tmem_ld64(tS, reinterpret_cast<float(&)[64]>(s[0]));
-                tmem_ld64(tS + 64, reinterpret_cast<float(&)[64]>(s[64]));
+                float s[kHalf];
+                tmem_ld64(tS, s);
                 if (masked) {
-                    // per 64 keys: bit i of w = key i is seen; history keys all, tree keys by the row's mask
+                    // bit i of w = key i is seen: history keys all, tree keys by the row's mask
+                    const int d = hist - k0;  // history keys from here on, below 64
+                    const uint64_t w = (d > 0 ? (1ull << d) - 1 : 0ull) |
+                                       (d >= 0 ? mask << d : d > -64 ? mask >> -d : 0ull);
+                    const uint32_t w0 = static_cast<uint32_t>(w), w1 = static_cast<uint32_t>(w >> 32);
 #pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        const int d = hist - (k0 + hh * 64);  // history keys from here on
-                        const uint64_t old = d >= 64 ? ~0ull : d > 0 ? (1ull << d) - 1 : 0ull;
-                        const uint64_t tr = d >= 64 ? 0ull : d >= 0 ? mask << d : d > -64 ? mask >> -d : 0ull;
-                        const uint64_t w = old | tr;
-                        const uint32_t w0 = static_cast<uint32_t>(w), w1 = static_cast<uint32_t>(w >> 32);
-#pragma unroll
-                        for (int c = 0; c < 64; ++c)
-                            if (!(((c < 32 ? w0 : w1) >> (c & 31)) & 1u)) s[hh * 64 + c] = -INFINITY;
-                    }
+                    for (int c = 0; c < kHalf; ++c)
+                        if (!(((c < 32 ? w0 : w1) >> (c & 31)) & 1u)) s[c] = -INFINITY;
                 }
                 float e[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) e[i] = max3f(s[i], s[4 + i], s[8 + i]);
 #pragma unroll
-                for (int c = 12; c + 8 <= kKeys; c += 8)
+                for (int c = 12; c + 8 <= kHalf; c += 8)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) e[i] = max3f(e[i], s[c + i], s[c + 4 + i]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) e[i] = fmaxf(e[i], s[kKeys - 4 + i]);
-                const float ext = fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3]));
-                const float mx = ext * sl2;  // -inf: nothing seen
+                for (int i = 0; i < 4; ++i) e[i] = fmaxf(e[i], s[kHalf - 4 + i]);
+                const float mx = max3f(e[0], e[1], fmaxf(e[2], e[3])) * sl2;  // -inf: nothing seen
                 float alpha = 1.f;
                 if (mx > m_used + kRescaleLog2) {  // includes the first finite max (m_used = -inf)
                     alpha = m_used == -INFINITY ? 0.f : ex2(m_used - mx);
                     m_used = mx;
                 }
-                // O_X is idle here: the stream's previous product is complete, the next one not issued
-                if (it > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                if (u > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    // rescale O_X, which idles once the stream's previous product is complete (this unit's P is not
+                    // there yet)
+                    ok = __all_sync(0xffffffffu, wait(&o_full[buf ^ 1], ((u - 1) >> 1) & 1, s_abort));
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 16) {
-                        float o[16];
-                        tmem_ld16(tO + c, o);
+                    for (int c = 0; c < D; c += 32) {
+                        float o[32];
+                        tmem_ld32(tO + c, o);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] *= alpha;
-                        tmem_st16f(tO + c, o);
+                        for (int i = 0; i < 32; ++i) o[i] *= alpha;
+                        tmem_st32(tO + c, o);
                     }
                 }
                 const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
                 float ls[4] = {0.f, 0.f, 0.f, 0.f};
-                const uint64_t sc2 = pack_f32x2(sl2, sl2), nm2 = pack_f32x2(neg_m, neg_m);
+                const uint64_t nm2 = pack_f32x2(neg_m, neg_m);
 #pragma unroll
-                for (int hh = 0; hh < 4; ++hh) {  // 32 keys at a time
+                for (int hh = 0; hh < 2; ++hh) {  // 32 keys at a time
                     uint32_t hv[16], lv[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
@@ -525,62 +617,31 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
                         }
                     }
                     tmem_st16(tS + hh * 16, hv);
-                    if constexpr (kSplitP) tmem_st16(tS + 64 + hh * 16, lv);
+                    if constexpr (kSplitP) tmem_st16(tS + kHalf / 2 + hh * 16, lv);
                 }
                 l = l * alpha + ((ls[0] + ls[1]) + (ls[2] + ls[3]));
-            }
-            if (masked && (!two_rows || x == 0)) {
-                // V rows past the context are zeroed, so that whatever they hold cannot reach an output through a
-                // zero weight; so are infinities and NaN among the tree's V rows, which not every row sees (the rows
-                // that do get them back at the end).  With two row tiles stream A does it: its product is first.
-                ok = __all_sync(0xffffffffu, wait(&v_full[vs], vph & 1, s_abort));
-                if (!ok) break;
-                uint8_t* vt = vst(vs);
-                const int from = max(hist - k0, 0), end = ctx - k0;
-                bool found = false;
-                for (int e = wq * 32 + lane; e < (kKeys - from) * 8 * Geo::kChunks; e += 128) {
-                    const int r = from + e / (8 * Geo::kChunks), rest = e % (8 * Geo::kChunks);
-                    uint4* at = reinterpret_cast<uint4*>(vt + (rest / 8) * Geo::kChunkBytes + sw128(r, rest % 8));
-                    if (r >= end) {
-                        *at = make_uint4(0u, 0u, 0u, 0u);
-                    } else {
-                        uint4 v = *at;
-                        bool bad = false;
-                        v = make_uint4(finite_halves(v.x, bad), finite_halves(v.y, bad), finite_halves(v.z, bad),
-                                       finite_halves(v.w, bad));
-                        if (bad) {
-                            *at = v;
-                            found = true;
-                        }
-                    }
-                }
-                if (found) *s_bad_v = 1;
-                fence_proxy_async_smem();  // visible to the tensor cores (async proxy)
             }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[x]);
-            if ((vs += step) >= VS) {
-                vs -= VS;
-                ++vph;
-            }
+            if (lane == 0) mbar_arrive(&p_full[buf]);
         }
-        if (ok && it > 0) ok = __all_sync(0xffffffffu, wait(&o_full[x], (it - 1) & 1, s_abort));
+        if (ok && units > 0)
+            ok = __all_sync(0xffffffffu, wait(&o_full[2 * x + ((units - 1) & 1)], ((units - 1) >> 1) & 1, s_abort));
         tc_fence_after();
         row_warps_sync();  // both streams done: the rings are idle, the notes on bad blocks and values complete
         // the thread's state into the state area: slot x * 128 + row
-        const bool drop = *s_bad_block != 0 || *s_abort != 0 || !ok || it == 0;
+        const bool drop = *s_bad_block != 0 || *s_abort != 0 || !ok || units == 0;
         float2* ml = reinterpret_cast<float2*>(smem + Geo::kMlOff);
         ml[x * kRows + row] = drop ? make_float2(-INFINITY, 0.f) : make_float2(m_used, l);
         if (live_warp && !drop) {
             float* mine = reinterpret_cast<float*>(smem + Geo::kStateOff) + (x * kRows + row) * Geo::kOStride;
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                float o[32];
-                tmem_ld32(tO + c, o);
 #pragma unroll
-                for (int i = 0; i < 32; i += 4)
+            for (int c = 0; c < D; c += 64) {
+                float o[64];
+                tmem_ld64(tO + c, o);
+#pragma unroll
+                for (int i = 0; i < 64; i += 4)
                     *reinterpret_cast<float4*>(mine + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
             }
         }
@@ -601,59 +662,108 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
         __syncthreads();
     }
     // ================= the cluster's states merged: each CTA takes a share of the rows =================
+    const int live_rows = min(two_rows ? 2 * kRows : kRows, rows - r0);
+    const int share = (live_rows + p.cluster - 1) / p.cluster;
+    const int ra = min(rank * share, live_rows), nr = min(share, live_rows - ra);
+    const int ncta = min(p.cluster, (all_tiles - clus * per_clus + p.chunk - 1) / p.chunk);  // CTAs with tiles
+    const int sh = two_rows ? 0 : 1, nst = ncta << sh;  // states of a row: one or two in each CTA
+    auto out_row = [&](int rr) {
+        const int t = node_of(rr);
+        return (static_cast<int64_t>(b) * p.T + t) * p.Hq + hk * p.G + rr - t * p.G;
+    };
+    // weights of a row's states, s_w[row][state] = (weight, sum): a group of `group` lanes takes a row, a lane a state
+    float2* const s_w = reinterpret_cast<float2*>(smem + Geo::kWeightOff);
     {
-        constexpr int kCols = D / 4;  // a thread per four columns of a row
-        const int live_rows = min(two_rows ? 2 * kRows : kRows, rows - r0);
-        const int share = (live_rows + p.cluster - 1) / p.cluster;
-        const int ra = min(rank * share, live_rows), rb = min(ra + share, live_rows);
-        const int ncta = min(p.cluster, (all_tiles - clus * per_clus + p.chunk - 1) / p.chunk);  // CTAs with tiles
-        const uint32_t state0 = smem_u32(smem + Geo::kStateOff), ml0 = smem_u32(smem + Geo::kMlOff);
-        const uint32_t flag0 = smem_u32(const_cast<int*>(s_bad_v));
-        for (int e = threadIdx.x; e < (rb - ra) * kCols; e += kThreads) {
-            const int r = ra + e / kCols, c = e % kCols * 4, rr = r0 + r;
-            float m = -INFINITY, l = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            unsigned bad_v = 0;
-            for (int q = 0; q < ncta; ++q) {
-                const uint32_t st = cluster_addr(state0, q), mls = cluster_addr(ml0, q);
-                if (ld_cluster_u32(cluster_addr(flag0, q)) != 0) bad_v |= 1u << q;
-                for (int slot = r; slot < 2 * kRows; slot += two_rows ? 2 * kRows : kRows) {
-                    const float2 s = ld_cluster_f32x2(mls + slot * 8);
-                    if (s.y == 0.f) continue;  // the state holds nothing (and its O may be unwritten)
-                    const float4 a = ld_cluster_f32x4(st + (slot * Geo::kOStride + c) * 4);
-                    const float mn = fmaxf(m, s.x);
-                    const float f_old = m == mn ? 1.f : ex2(m - mn), f_new = s.x == mn ? 1.f : ex2(s.x - mn);
-                    o = fma4(f_new, a, scale4(o, f_old));
-                    l = l * f_old + s.y * f_new;
-                    m = mn;
-                }
-            }
-            const int64_t orow = (static_cast<int64_t>(b) * p.T + rr / p.G) * p.Hq + hk * p.G + rr % p.G;
-            if (whole) o = scale4(o, l > 0.f || l != l ? 1.f / l : 0.f);
-            if (bad_v != 0) {
-                // infinities and NaN of the tree's V rows that this row sees, in the noted CTAs' keys
-                const uint64_t mask = p.masks[static_cast<int64_t>(b) * p.T + rr / p.G];
-                for (int t = 0; t < tree; ++t) {
-                    const int pos = hist + t, q = pos / kKeys / p.chunk - clus * p.cluster;
-                    if (!((mask >> t) & 1) || q < 0 || q >= ncta || !((bad_v >> q) & 1u)) continue;
-                    const int64_t blk = table_row[pos / kBlockSize];
-                    const __half* v = p.v_cache + ((blk * p.Hkv + hk) * kBlockSize + pos % kBlockSize) * D + c;
-                    const float y[4] = {__half2float(v[0]), __half2float(v[1]), __half2float(v[2]), __half2float(v[3])};
-                    if (!(fabsf(y[0]) < INFINITY)) o.x += y[0];
-                    if (!(fabsf(y[1]) < INFINITY)) o.y += y[1];
-                    if (!(fabsf(y[2]) < INFINITY)) o.z += y[2];
-                    if (!(fabsf(y[3]) < INFINITY)) o.w += y[3];
-                }
-            }
-            if (whole) {
-                store_out4(p.out, p.out_f32, orow * D + c, o);
-            } else {
-                const int64_t prow = orow * p.nclus + clus;
-                if (c == 0) *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(m, l);
-                *reinterpret_cast<float4*>(p.part_acc + prow * D + c) = o;
+        const uint32_t ml0 = smem_u32(smem + Geo::kMlOff), flag0 = smem_u32(const_cast<int*>(s_bad_v));
+        int group = 1;
+        while (group < nst) group *= 2;
+        const int s = threadIdx.x & (group - 1), q = s >> sh;
+        for (int rbase = 0; rbase < nr; rbase += kThreads / group) {  // (group divides 32: whole warps)
+            const int r = rbase + threadIdx.x / group;
+            float2 st = make_float2(-INFINITY, 0.f);
+            if (r < nr && s < nst) st = ld_cluster_f32x2(cluster_addr(ml0, q) + (ra + r + (s - (q << sh)) * kRows) * 8);
+            float m = st.y != 0.f ? st.x : -INFINITY;  // a state with sum 0 holds nothing
+            for (int off = group / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+            const float w = st.y == 0.f ? 0.f : st.x == m ? 1.f : ex2(st.x - m);
+            float l = st.y != 0.f ? st.y * w : 0.f;
+            for (int off = group / 2; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+            const float inv = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
+            if (r < nr && s < nst) {
+                s_w[r * nst + s] = make_float2(w * inv, st.y);
+                if (!whole && s == 0)
+                    *reinterpret_cast<float2*>(p.part_ml + (out_row(r0 + ra + r) * p.nclus + clus) * 2) = make_float2(m, l);
             }
         }
+        if (threadIdx.x < ncta && ld_cluster_u32(cluster_addr(flag0, threadIdx.x)) != 0)
+            atomicOr(const_cast<int*>(s_bad_of), 1 << threadIdx.x);
     }
+    __syncthreads();
+    const uint32_t bad_of = static_cast<uint32_t>(*s_bad_of);
+    // output rows: a thread per four columns; U items of S states are read at a time
+    auto merge_rows = [&](auto u_items, auto s_states) {
+        constexpr int U = decltype(u_items)::value, S = decltype(s_states)::value;
+        constexpr int kCols = D / 4;
+        const uint32_t state0 = smem_u32(smem + Geo::kStateOff);
+        for (int e0 = threadIdx.x; e0 < nr * kCols; e0 += U * kThreads) {
+            float4 o[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int s0 = 0; s0 < nst; s0 += S) {
+                float4 a[U][S];
+#pragma unroll
+                for (int j = 0; j < S; ++j) {
+                    const int s = min(s0 + j, nst - 1), q = s >> sh;
+                    const uint32_t base = cluster_addr(state0, q) + (ra + (s - (q << sh)) * kRows) * (Geo::kOStride * 4);
+#pragma unroll
+                    for (int i = 0; i < U; ++i) {
+                        const int e = min(e0 + i * kThreads, nr * kCols - 1);
+                        a[i][j] = ld_cluster_f32x4(base + (e / kCols * Geo::kOStride + e % kCols * 4) * 4);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    const int r = min(e0 + i * kThreads, nr * kCols - 1) / kCols;
+#pragma unroll
+                    for (int j = 0; j < S; ++j) {
+                        if (s0 + j >= nst) continue;
+                        const float2 w = s_w[r * nst + s0 + j];
+                        if (w.y != 0.f) o[i] = fma4(w.x, a[i][j], o[i]);  // (O of a state that holds nothing: unwritten)
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int e = e0 + i * kThreads;
+                if (e >= nr * kCols) break;
+                const int rr = r0 + ra + e / kCols, c = e % kCols * 4;
+                const int64_t orow = out_row(rr);
+                if (bad_of != 0) {
+                    // infinities and NaN of the tree's V rows that this row sees, in the noted CTAs' keys
+                    const uint64_t mask = p.masks[static_cast<int64_t>(b) * p.T + node_of(rr)];
+                    for (int t = 0; t < tree; ++t) {
+                        const int pos = hist + t, q = pos / kKeys / p.chunk - clus * p.cluster;
+                        if (!((mask >> t) & 1) || q < 0 || q >= ncta || !((bad_of >> q) & 1u)) continue;
+                        const int64_t blk = table_row[pos / kBlockSize];
+                        const __half* v = p.v_cache + ((blk * p.Hkv + hk) * kBlockSize + pos % kBlockSize) * D + c;
+                        const float y[4] = {__half2float(v[0]), __half2float(v[1]), __half2float(v[2]),
+                                            __half2float(v[3])};
+                        if (!(fabsf(y[0]) < INFINITY)) o[i].x += y[0];
+                        if (!(fabsf(y[1]) < INFINITY)) o[i].y += y[1];
+                        if (!(fabsf(y[2]) < INFINITY)) o[i].z += y[2];
+                        if (!(fabsf(y[3]) < INFINITY)) o[i].w += y[3];
+                    }
+                }
+                if (whole)
+                    store_out4(p.out, p.out_f32, orow * D + c, o[i]);
+                else
+                    *reinterpret_cast<float4*>(p.part_acc + (orow * p.nclus + clus) * D + c) = o[i];
+            }
+        }
+    };
+    if (nst <= 2)
+        merge_rows(std::integral_constant<int, 4>(), std::integral_constant<int, 2>());
+    else
+        merge_rows(std::integral_constant<int, 1>(), std::integral_constant<int, 8>());
     if (p.cluster > 1) {
         __syncwarp();
         cluster_sync_all();  // no CTA leaves while another reads its shared memory
@@ -673,8 +783,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
     const int c = (lane % kLanes) * 4;
     const int64_t bt = row / p.Hq;
     const int b = static_cast<int>(bt / p.T), t = static_cast<int>(bt % p.T);
-    int tree, ctx;
-    if (!lengths(p, b, tree, ctx) || t >= tree) return;
+    const int tree = p.tree_lens != nullptr ? p.tree_lens[b] : p.T, ctx = p.context_lens[b];
+    if (!lengths_fit(p, tree, ctx) || t >= tree) return;
     const int per_clus = p.chunk * p.cluster, nclus = (key_tiles(ctx) + per_clus - 1) / per_clus;
     if (nclus <= 1) return;  // the attention kernel wrote the row
     float m = -INFINITY, l = 0.f;
@@ -808,6 +918,7 @@ static cudaError_t launch_tree_d(const TreeArgs& a, const TreePlan& plan, cudaSt
     p.Hq = a.Hq;
     p.Hkv = a.Hkv;
     p.G = a.Hq / a.Hkv;
+    p.g_magic = ((1u << 18) + p.G - 1) / p.G;
     p.max_blocks = a.max_blocks;
     p.num_blocks = a.num_blocks;
     p.max_ctx = a.max_context_len;
