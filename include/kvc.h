@@ -566,8 +566,8 @@ kvc_status paged_decode_tree_attention(const void* q, const void* k_cache, const
  *   target_probs, draft_probs  device [B][T][V], prob_dtype KVC_F16 or KVC_F32
  *                for both; row t of a sequence is the distribution behind node
  *                t; rows p_stride / q_stride elements apart (>= V).  They are
- *                read to 2^-53; NaN and negative values count as 0, values
- *                above 1 as 1; a row's sum is about 1 (below 4096)
+ *                read to 2^-46; NaN and negative values count as 0, values
+ *                above 1 as 1; a row's sum is about 1 (below 2^19)
  *   tokens, parents  device int32 [B][T] (entry 0 of a sequence is not read)
  *   tree_lens    device int32 [B], 0 .. T, or NULL: T each
  *   uniforms     device float [B][T] in [0, 1): u_t of node t's trial, u_0 of

@@ -17,11 +17,12 @@
 // lane (chunks l and l + rot_dim / 16, or 2 l and 2 l + 1): no exchange between lanes but the sum of squares.  A warp
 // takes kRows = 512 / D rows at a time and keeps one token's cosines and sines in registers for all its heads; they
 // are computed once per warp (rot_dim / 2 angles over 32 lanes) and handed out through shared memory.
-#include <atomic>
+#include <type_traits>
 
 #include "../../include/kvc.h"
 #include "decode_common.cuh"
 #include "kvc_internal.h"
+#include "f32x2.cuh"
 #include "ptx.cuh"
 
 namespace kvc {
@@ -31,9 +32,10 @@ namespace rope {
 #define KVC_ROPE_U 2
 #endif
 #ifndef KVC_ROPE_CTAS
-#define KVC_ROPE_CTAS 2
+#define KVC_ROPE_CTAS 3
 #endif
 constexpr int kWarps = 8;
+constexpr int U = KVC_ROPE_U;  // passes whose loads are in flight together
 
 struct Params {
     const __half* q;
@@ -52,21 +54,36 @@ struct Params {
     const int64_t* slots;
     unsigned* err;
     int64_t n;
-    int Hq, Hkv, num_blocks, rot, interleaved, split, rows_per_warp;
+    int Hq, Hkv, num_blocks, rot, interleaved, split, passes_per_warp;
     float eps;
 };
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
+// eight fp16 values as four packed pairs of fp32, and back (one rounding each)
+__device__ __forceinline__ void unpack8(const uint4& u, uint64_t (&f)[4]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 t = unpack_half2(w[i]);
-        f[2 * i] = t.x;
-        f[2 * i + 1] = t.y;
+        f[i] = pack_f32x2(t.x, t.y);
     }
 }
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-    return make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]), pack_half2(f[4], f[5]), pack_half2(f[6], f[7]));
+__device__ __forceinline__ uint32_t pack2(uint64_t v) {
+    float a, b;
+    unpack_f32x2(v, a, b);
+    return pack_half2(a, b);
+}
+__device__ __forceinline__ uint4 pack8(const uint64_t (&f)[4]) {
+    return make_uint4(pack2(f[0]), pack2(f[1]), pack2(f[2]), pack2(f[3]));
+}
+__device__ __forceinline__ uint64_t neg_f32x2(uint64_t v) { return v ^ 0x8000000080000000ull; }
+// (a, b) turned by the angle whose cosine and sine are half `hi` of c and s
+__device__ __forceinline__ uint64_t rotate_pair(uint64_t v, uint64_t c, uint64_t s, int hi) {
+    float a, b, c0, c1, s0, s1;
+    unpack_f32x2(v, a, b);
+    unpack_f32x2(c, c0, c1);
+    unpack_f32x2(s, s0, s1);
+    const float cc = hi ? c1 : c0, ss = hi ? s1 : s0;
+    return pack_f32x2(fmaf(a, cc, -(b * ss)), fmaf(b, cc, a * ss));
 }
 
 template <int D>
@@ -104,14 +121,14 @@ __global__ void __launch_bounds__(kWarps * 32, KVC_ROPE_CTAS) kv_append_rope_ker
         c1 = r0 ? l + hc : 2 * l + 1;
     }
     // cosines and sines of the lane's 8 pairs
-    float cs[8], sn[8];
+    uint64_t cs[4], sn[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int a = p.interleaved ? (i < 4 ? c0 * 4 + i : c1 * 4 + i - 4) : c0 * 8 + i;
-        const bool on = p.interleaved ? (i < 4 ? r0 : r1) : r0;
-        const float2 x = on ? s_cs[warp][a] : make_float2(1.f, 0.f);
-        cs[i] = x.x;
-        sn[i] = x.y;
+    for (int i = 0; i < 4; ++i) {
+        const int a = p.interleaved ? (i < 2 ? c0 * 4 + 2 * i : c1 * 4 + 2 * i - 4) : c0 * 8 + 2 * i;
+        const bool on = p.interleaved ? (i < 2 ? r0 : r1) : r0;
+        const float2 x = on ? s_cs[warp][a] : make_float2(1.f, 0.f), y = on ? s_cs[warp][a + 1] : make_float2(1.f, 0.f);
+        cs[i] = pack_f32x2(x.x, y.x);
+        sn[i] = pack_f32x2(x.y, y.y);
     }
 
     // the token's cache slot
@@ -125,85 +142,93 @@ __global__ void __launch_bounds__(kWarps * 32, KVC_ROPE_CTAS) kv_append_rope_ker
         }
     }
 
-    const int total = p.Hq + 2 * p.Hkv;
-    const int row_end = min(total, (static_cast<int>(w % p.split) + 1) * p.rows_per_warp);
-    constexpr int U = KVC_ROPE_U;  // iterations whose loads are in flight together
-    for (int rb = static_cast<int>(w % p.split) * p.rows_per_warp; rb < row_end; rb += U * kRows) {
-        uint4 raw[U][2];
+    // The warp's share of the passes: query rows, key rows, value rows, kRows heads at a time.
+    const int pass0 = static_cast<int>(w % p.split) * p.passes_per_warp, pass1 = pass0 + p.passes_per_warp;
+    const int pq = (p.Hq + kRows - 1) / kRows, pk = (p.Hkv + kRows - 1) / kRows;
+    const auto rows = [&](auto kind, int first, int last) {  // passes [first, last) of one kind of rows
+        constexpr int kKind = decltype(kind)::value;  // 0 query, 1 key, 2 value
+        if (first >= last) return;
+        const int H = kKind == 0 ? p.Hq : p.Hkv;
+        const __half* src = (kKind == 0 ? p.q + t * p.q_stride : kKind == 1 ? p.k + t * p.k_stride : p.v + t * p.v_stride);
+        __half* const packed = kKind == 0 ? p.q_out : kKind == 1 ? p.k_out : p.v_out;
+        __half* const cache = kKind == 1 ? p.k_cache : p.v_cache;
+        const __half* const wt = kKind == 0 ? p.qw : p.kw;
+        uint4 w0 = make_uint4(0u, 0u, 0u, 0u), w1 = w0;
+        if (kKind < 2 && wt != nullptr) {
+            w0 = *reinterpret_cast<const uint4*>(wt + c0 * 8);
+            w1 = *reinterpret_cast<const uint4*>(wt + c1 * 8);
+        }
+        for (int pass = first; pass < last; pass += U) {
+            uint4 raw[U][2];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int r = rb + u * kRows + rsub;
-            raw[u][0] = raw[u][1] = make_uint4(0u, 0u, 0u, 0u);
-            if (r < row_end) {
-                const __half* src = r < p.Hq ? p.q + t * p.q_stride + r * D
-                                    : r < p.Hq + p.Hkv ? p.k + t * p.k_stride + (r - p.Hq) * D
-                                                       : p.v + t * p.v_stride + (r - p.Hq - p.Hkv) * D;
-                raw[u][0] = *reinterpret_cast<const uint4*>(src + c0 * 8);
-                raw[u][1] = *reinterpret_cast<const uint4*>(src + c1 * 8);
+            for (int u = 0; u < U; ++u) {
+                const int h = (pass + u) * kRows + rsub;
+                raw[u][0] = raw[u][1] = make_uint4(0u, 0u, 0u, 0u);
+                if (pass + u < last && h < H) {
+                    raw[u][0] = *reinterpret_cast<const uint4*>(src + h * D + c0 * 8);
+                    raw[u][1] = *reinterpret_cast<const uint4*>(src + h * D + c1 * 8);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (pass + u >= last) break;
+                const int h = (pass + u) * kRows + rsub;
+                uint4 o0 = raw[u][0], o1 = raw[u][1];
+                if constexpr (kKind < 2) {
+                    uint64_t x[4], y[4];  // pairs of neighbouring values
+                    unpack8(o0, x);
+                    unpack8(o1, y);
+                    if (wt != nullptr) {
+                        uint64_t s2 = 0;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) s2 = fma_f32x2(x[i], x[i], fma_f32x2(y[i], y[i], s2));
+                        float sa, sb;
+                        unpack_f32x2(s2, sa, sb);
+                        float ss = sa + sb;
+#pragma unroll
+                        for (int off = kLanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+                        const float inv = rsqrtf(ss * (1.f / D) + p.eps);
+                        const uint64_t inv2 = pack_f32x2(inv, inv);
+                        uint64_t wx[4], wy[4];
+                        unpack8(w0, wx);
+                        unpack8(w1, wy);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            x[i] = mul_f32x2(mul_f32x2(x[i], inv2), wx[i]);
+                            y[i] = mul_f32x2(mul_f32x2(y[i], inv2), wy[i]);
+                        }
+                    }
+                    if (p.interleaved) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            x[i] = rotate_pair(x[i], cs[i / 2], sn[i / 2], i & 1);
+                            y[i] = rotate_pair(y[i], cs[2 + i / 2], sn[2 + i / 2], i & 1);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint64_t a = x[i], b = y[i];
+                            x[i] = fma_f32x2(a, cs[i], neg_f32x2(mul_f32x2(b, sn[i])));
+                            y[i] = fma_f32x2(b, cs[i], mul_f32x2(a, sn[i]));
+                        }
+                    }
+                    // without a norm, dims that are not rotated keep their bits
+                    if (wt != nullptr || r0) o0 = pack8(x);
+                    if (wt != nullptr || r1) o1 = pack8(y);
+                }
+                if (h >= H) continue;
+                auto put = [&](__half* row) {
+                    *reinterpret_cast<uint4*>(row + c0 * 8) = o0;
+                    *reinterpret_cast<uint4*>(row + c1 * 8) = o1;
+                };
+                if (kKind == 0 || packed != nullptr) put(packed + (t * H + h) * D);
+                if (kKind > 0 && dst >= 0) put(cache + dst + static_cast<int64_t>(h) * kBlockSize * D);
             }
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int r = rb + u * kRows + rsub;
-            const bool is_v = r >= p.Hq + p.Hkv, is_q = r < p.Hq;
-            uint4 o0 = raw[u][0], o1 = raw[u][1];
-            float x[8], y[8];
-            unpack8(o0, x);
-            unpack8(o1, y);
-            const __half* wt = is_q ? p.qw : p.kw;
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
-#pragma unroll
-            for (int off = kLanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-            if (!is_v) {
-                if (wt != nullptr) {
-                    const float inv = rsqrtf(ss * (1.f / D) + p.eps);
-                    float wx[8], wy[8];
-                    unpack8(__ldg(reinterpret_cast<const uint4*>(wt + c0 * 8)), wx);
-                    unpack8(__ldg(reinterpret_cast<const uint4*>(wt + c1 * 8)), wy);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        x[i] *= inv * wx[i];
-                        y[i] *= inv * wy[i];
-                    }
-                }
-                if (p.interleaved) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float a = x[2 * i], b = x[2 * i + 1], e = y[2 * i], f = y[2 * i + 1];
-                        x[2 * i] = a * cs[i] - b * sn[i];
-                        x[2 * i + 1] = b * cs[i] + a * sn[i];
-                        y[2 * i] = e * cs[4 + i] - f * sn[4 + i];
-                        y[2 * i + 1] = f * cs[4 + i] + e * sn[4 + i];
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float a = x[i], b = y[i];
-                        x[i] = a * cs[i] - b * sn[i];
-                        y[i] = b * cs[i] + a * sn[i];
-                    }
-                }
-                // without a norm, dims that are not rotated keep their bits
-                if (wt != nullptr || r0) o0 = pack8(x);
-                if (wt != nullptr || r1) o1 = pack8(y);
-            }
-            if (r >= row_end) continue;
-            auto put = [&](__half* row) {
-                *reinterpret_cast<uint4*>(row + c0 * 8) = o0;
-                *reinterpret_cast<uint4*>(row + c1 * 8) = o1;
-            };
-            if (is_q) {
-                put(p.q_out + (t * p.Hq + r) * D);
-            } else {
-                const int h = is_v ? r - p.Hq - p.Hkv : r - p.Hq;
-                __half* packed = is_v ? p.v_out : p.k_out;
-                if (packed != nullptr) put(packed + (t * p.Hkv + h) * D);
-                if (dst >= 0) put((is_v ? p.v_cache : p.k_cache) + dst + static_cast<int64_t>(h) * kBlockSize * D);
-            }
-        }
-    }
+    };
+    rows(std::integral_constant<int, 0>(), pass0, min(pass1, pq));
+    rows(std::integral_constant<int, 1>(), max(pass0 - pq, 0), min(pass1 - pq, pk));
+    rows(std::integral_constant<int, 2>(), max(pass0 - pq - pk, 0), min(pass1 - pq - pk, pk));
 }
 
 }  // namespace rope
@@ -237,16 +262,15 @@ cudaError_t launch_append_rope(const RopeArgs& a, cudaStream_t stream) {
     p.rot = a.rot_dim;
     p.interleaved = a.interleaved;
     p.eps = a.eps;
-    const int rows = a.Hq + 2 * a.Hkv, per_pass = 512 / a.D;
     // Warps per token: few tokens spread their heads over the GPU's SMs (one pass of rows per warp at least), many
     // keep a token in one warp, which computes its cosines and sines once.
+    const int per_pass = 512 / a.D;
+    const int passes = (a.Hq + per_pass - 1) / per_pass + 2 * ((a.Hkv + per_pass - 1) / per_pass);
     const int64_t want = static_cast<int64_t>(sms) * rope::kWarps;
-    const int passes = (rows + per_pass - 1) / per_pass;
     int split = static_cast<int>(std::min<int64_t>(passes, std::max<int64_t>(1, want / a.n)));
-    const int passes_each = (passes + split - 1) / split;
-    split = (passes + passes_each - 1) / passes_each;
+    p.passes_per_warp = (passes + split - 1) / split;
+    split = (passes + p.passes_per_warp - 1) / p.passes_per_warp;
     p.split = split;
-    p.rows_per_warp = passes_each * per_pass;
     const int64_t blocks = (a.n * split + rope::kWarps - 1) / rope::kWarps;
     if (blocks > 2147483647LL) return cudaErrorInvalidConfiguration;
     const dim3 grid(static_cast<unsigned>(blocks)), block(rope::kWarps * 32);

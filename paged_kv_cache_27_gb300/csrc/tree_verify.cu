@@ -15,12 +15,16 @@
 // and a refused token stays at zero: it was refused where p_k(x) <= q_k(x), and a only grows.
 //
 // Sums.  Which token a draw hits is a comparison of running sums, so they are kept in 64-bit integers, in units of
-// 2^-52: p is read to 2^-53, a q is formed as a product of two floats' sum with q (48 bits of a) with its rounding
-// error carried along.  Integer sums do not depend on their order, so results repeat bit for bit for every grid.
+// 2^-45.  A weight p - a q is formed in fp32 with every rounding error carried along (a as the sum of two floats, the
+// product's error by fma, the difference's by the two-term difference), and split exactly into a multiple of 2^-23 and a
+// remainder that is rounded to 2^-45, both by adding a constant whose last bit has that value: the sums are integer
+// additions of the results' bits.  (Conversions of floats to 64-bit integers run at the FP64 unit's rate: a pass over
+// 64 x 128,257 entries took 30 us with them.)  Integer sums do not depend on their order, so results repeat bit for bit
+// for every grid.
 //
 // Layout.  One thread-block cluster per sequence; its CTAs share the vocabulary in slices (a warp a part of a slice)
 // and exchange their sums through distributed shared memory, and all of them follow the same decisions on the same
-// numbers (the tree's, read by rank 0 once; the sums).  The kernel is bound by the two rows it reads per pass.
+// numbers (the tree's, gathered by rank 0 for all; the sums).
 #include <atomic>
 
 #include "../../include/kvc.h"
@@ -31,11 +35,15 @@
 namespace kvc {
 namespace verify {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+#ifndef KVC_VERIFY_U
+#define KVC_VERIFY_U 2
+#endif
+#ifndef KVC_VERIFY_WIDE
+#define KVC_VERIFY_WIDE 2
+#endif
 constexpr int kMaxClusterV = 8;
-constexpr float kUnit = 0x1p52f;  // probabilities are counted in 2^-52; a row's sum has room up to 4096
-constexpr double kUnitInv = 0x1p-52;
+constexpr int kUnitBits = 45;  // weights are counted in 2^-45; a row's sum has room up to 2^19
+constexpr double kUnit = 0x1p-45;
 
 struct Params {
     const void* p;
@@ -52,14 +60,6 @@ struct Params {
     int T, V, distinct, slice;  // slice: vocabulary entries per CTA
 };
 
-struct Tree {  // rank 0's copy is read by the other CTAs
-    int32_t token[kMaxTreeNodes];
-    int32_t parent[kMaxTreeNodes];
-    float u[kMaxTreeNodes];
-    float p[kMaxTreeNodes];  // target and draft probability of the node's token at its parent
-    float q[kMaxTreeNodes];
-};
-
 __device__ __forceinline__ void st_cluster_u64(uint32_t addr, uint64_t v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
@@ -69,13 +69,34 @@ __device__ __forceinline__ float prob(float x) { return __saturatef(x); }
 __device__ __forceinline__ float load_prob(const float* row, int i) { return prob(__ldg(row + i)); }
 __device__ __forceinline__ float load_prob(const __half* row, int i) { return prob(__half2float(__ldg(row + i))); }
 
-// (p - a q)^+ in units of 2^-52, a = ah + al
-__device__ __forceinline__ uint64_t weight(float p, float q, float ah, float al) {
-    const float h = ah * q;
-    if (!(h < 2.f)) return 0;  // p <= 1
-    const float e = fmaf(al, q, fmaf(ah, q, -h));  // a q = h + e
-    const int64_t w = __float2ll_rn(p * kUnit) - __float2ll_rn(h * kUnit) - __float2ll_rn(e * kUnit);
-    return w > 0 ? static_cast<uint64_t>(w) : 0;
+// (p - a q)^+ <= 1, a = ah + al, as a multiple of 2^-23 (in the bits of the first, above those of 1) and a remainder,
+// at most about 2^-24, in units of 2^-45 (in the bits of the second, above those of kFine)
+constexpr float kCoarse = 1.f;            // one ulp is 2^-23 up to 2
+constexpr float kFine = 1.5f * 0x1p-22f;  // one ulp is 2^-45 within 2^-23 on both sides
+struct Split {
+    float coarse, fine;
+};
+__device__ __forceinline__ Split split_weight(float p, float q, float ah, float al) {
+    const float h = __fmul_rn(ah, q);
+    const float e = __fmaf_rn(al, q, __fmaf_rn(ah, q, -h));  // a q = h + e
+    // p - h = r + d exactly
+    float r = __fsub_rn(p, h);
+    const float b = __fsub_rn(r, p);
+    const float d = __fsub_rn(__fsub_rn(p, __fsub_rn(r, b)), __fadd_rn(h, b));
+    float c = __fsub_rn(d, e);
+    // r > e decides the sign: where r and e are of one size, r is exact
+    const bool positive = r > e && h < 2.f;  // (an h of 2 or more, or a product of infinity, leaves nothing: p <= 1)
+    r = positive ? r : 0.f;
+    c = positive ? c : 0.f;
+    Split s;
+    s.coarse = __fadd_rn(r, kCoarse);
+    s.fine = __fadd_rn(__fadd_rn(__fsub_rn(r, __fsub_rn(s.coarse, kCoarse)), c), kFine);
+    return s;
+}
+__device__ __forceinline__ int coarse_units(const Split& s) { return __float_as_int(s.coarse) - __float_as_int(kCoarse); }
+__device__ __forceinline__ int fine_units(const Split& s) { return __float_as_int(s.fine) - __float_as_int(kFine); }
+__device__ __forceinline__ uint64_t units(int64_t coarse, int64_t fine) {
+    return static_cast<uint64_t>(coarse * (1 << (kUnitBits - 23)) + fine);
 }
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
@@ -84,77 +105,147 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
     return v;
 }
 
-// this lane's share of the weights of entries [b, e): entries b + lane, b + lane + 32, ...
-template <typename T>
-__device__ __forceinline__ uint64_t lane_weights(const T* __restrict__ p, const T* __restrict__ q, int b, int e, float ah,
-                                                 float al) {
-    constexpr int U = 8;
-    const int lane = threadIdx.x & 31;
+// sums of weights in the two parts' units, brought together every few weights
+struct LaneSum {
     uint64_t sum = 0;
+    int coarse = 0, fine = 0;  // of at most 32 weights: up to 2^28 and 2^27
+    __device__ __forceinline__ void add(float p, float q, float ah, float al) {
+        const Split w = split_weight(p, q, ah, al);
+        coarse += coarse_units(w);
+        fine += fine_units(w);
+    }
+    __device__ __forceinline__ void flush() {
+        sum += units(coarse, fine);
+        coarse = fine = 0;
+    }
+};
+// this lane's share of the weights of entries [b, e), one at a time: entries b + lane, b + lane + 32, ...
+template <typename T>
+__device__ __forceinline__ void add_entries(LaneSum& acc, const T* __restrict__ p, const T* __restrict__ q, int b, int e,
+                                            float ah, float al) {
+    constexpr int U = 8;
     const bool use_q = ah != 0.f;
-    for (int i0 = b; i0 < e; i0 += 32 * U) {
+    for (int i0 = b + (threadIdx.x & 31); i0 < e; i0 += 32 * U) {
         float pv[U], qv[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int i = i0 + u * 32 + lane;
+            const int i = i0 + u * 32;
             pv[u] = i < e ? load_prob(p, i) : 0.f;
             qv[u] = i < e && use_q ? load_prob(q, i) : 0.f;
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) sum += weight(pv[u], qv[u], ah, al);
+        for (int u = 0; u < U; ++u) acc.add(pv[u], qv[u], ah, al);
+        acc.flush();
     }
-    return sum;
+}
+template <typename T>
+__device__ __forceinline__ void unpack16(const uint4& v, float (&x)[16 / sizeof(T)]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            x[i] = prob(__uint_as_float(w[i]));
+        } else {
+            const float2 f = unpack_half2(w[i]);
+            x[2 * i] = prob(f.x);
+            x[2 * i + 1] = prob(f.y);
+        }
+    }
+}
+// this lane's share of the weights of entries [b, e).  Rows of one alignment (a vocabulary of any size, but one stride
+// and 16-byte aligned tensors) are read 16 bytes at a time between their first and last few entries: 64 sequences x
+// 128,257 entries 78.3 -> KVC_VEC us.
+template <typename T>
+__device__ __forceinline__ uint64_t lane_weights(const T* __restrict__ p, const T* __restrict__ q, int b, int e, float ah,
+                                                 float al) {
+    LaneSum acc;
+    if ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15u) {
+        add_entries(acc, p, q, b, e, ah, al);
+        return acc.sum;
+    }
+    constexpr int V = 16 / sizeof(T), U = KVC_VERIFY_U;
+    const int a = min(e, b + static_cast<int>((0 - reinterpret_cast<uintptr_t>(p + b)) & 15u) / static_cast<int>(sizeof(T)));
+    const int nv = (e - a) / V, lane = threadIdx.x & 31;
+    const uint4* pv = reinterpret_cast<const uint4*>(p + a);
+    const uint4* qv = reinterpret_cast<const uint4*>(q + a);
+    const bool use_q = ah != 0.f;
+    add_entries(acc, p, q, b, a, ah, al);
+    for (int i0 = lane; i0 < nv; i0 += 32 * U) {
+        uint4 x[U], y[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * 32;
+            x[u] = y[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (i < nv) x[u] = __ldg(pv + i);
+            if (i < nv && use_q) y[u] = __ldg(qv + i);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float fx[V], fy[V];
+            unpack16<T>(x[u], fx);
+            unpack16<T>(y[u], fy);
+#pragma unroll
+            for (int k = 0; k < V; ++k) acc.add(fx[k], fy[k], ah, al);
+        }
+        acc.flush();
+    }
+    add_entries(acc, p, q, a + nv * V, e, ah, al);
+    return acc.sum;
 }
 
-template <typename T>
+template <typename T, int kThreads>
 __global__ void __launch_bounds__(kThreads) draft_tree_verify_kernel(const Params p) {
-    __shared__ Tree s_tree;
-    __shared__ uint64_t s_tot[2][kMaxClusterV];  // the CTAs' sums of a pass, by pass parity
+    constexpr int kWarps = kThreads / 32;
+    __shared__ float4 s_tree[kMaxTreeNodes];        // a node's (parent, u, p, q): p and q of its token at its parent
+    __shared__ uint64_t s_tot[2][kMaxClusterV];     // the CTAs' sums of a pass, by pass parity
     __shared__ uint64_t s_warp[kWarps], s_part[kWarps];
     __shared__ float s_a[2];
     __shared__ int s_cmd, s_node;  // warp 0's decision: 1 = pass over node s_node's rows with a, 0 = draw
     __shared__ int s_path[kMaxTreeNodes];
     const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = static_cast<int>(blockIdx.x), cs = static_cast<int>(gridDim.x);  // one cluster spans x
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA runs
     int n_nodes = p.tree_lens != nullptr ? p.tree_lens[b] : p.T;
+    const T* const prow = static_cast<const T*>(p.p) + static_cast<int64_t>(b) * p.T * p.p_stride;
+    const T* const qrow = static_cast<const T*>(p.q) + static_cast<int64_t>(b) * p.T * p.q_stride;
+    // rank 0 gathers the tree for the whole cluster (decisions must not differ between its CTAs), a thread a node and
+    // one or more CTAs to tell
+    float4 mine = make_float4(__int_as_float(-2), 0.f, 0.f, 0.f);  // a node that no walk reaches
+    if (rank == 0) {
+        const int t = tid & (kMaxTreeNodes - 1);
+        const bool in = t < p.T;
+        const int64_t at = static_cast<int64_t>(b) * p.T + t;
+        const int par = in && t > 0 ? p.parents[at] : -1, tok = in && t > 0 ? p.tokens[at] : 0;
+        const float u = in ? p.uniforms[at] : 0.f;
+        if (t < n_nodes) {
+            mine.y = u;
+            if (t > 0) {
+                if (par < 0 || par >= t || tok < 0 || tok >= p.V) {
+                    if (tid == t) atomicOr(p.err, KVC_DEVERR_TREE);
+                } else {
+                    mine.x = __int_as_float(par);
+                    mine.z = load_prob(prow + par * p.p_stride, tok);
+                    mine.w = load_prob(qrow + par * p.q_stride, tok);
+                }
+            }
+        }
+    }
     if (n_nodes < 0 || n_nodes > p.T) {
         if (rank == 0 && tid == 0) atomicOr(p.err, KVC_DEVERR_TREE);
         n_nodes = 0;
     }
-    const T* const prow = static_cast<const T*>(p.p) + static_cast<int64_t>(b) * p.T * p.p_stride;
-    const T* const qrow = static_cast<const T*>(p.q) + static_cast<int64_t>(b) * p.T * p.q_stride;
-    if (rank == 0 && tid < kMaxTreeNodes) {
-        const int64_t at = static_cast<int64_t>(b) * p.T + tid;
-        int par = -2, tok = 0;  // a node that no walk reaches
-        float u = 0.f, pc = 0.f, qc = 0.f;
-        if (tid < n_nodes) {
-            u = p.uniforms[at];
-            if (tid > 0) {
-                par = p.parents[at];
-                tok = p.tokens[at];
-                if (par < 0 || par >= tid || tok < 0 || tok >= p.V) {
-                    atomicOr(p.err, KVC_DEVERR_TREE);
-                    par = -2;
-                } else {
-                    pc = load_prob(prow + par * p.p_stride, tok);
-                    qc = load_prob(qrow + par * p.q_stride, tok);
-                }
-            }
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA of the cluster runs
+    if (rank == 0) {
+        const uint32_t dst = smem_u32(&s_tree[tid & (kMaxTreeNodes - 1)]);
+        for (int r = tid / kMaxTreeNodes; r < cs; r += kThreads / kMaxTreeNodes) {
+            uint32_t remote;
+            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(dst), "r"(r));
+            st_cluster_f32x4(remote, mine);
         }
-        s_tree.token[tid] = tok;
-        s_tree.parent[tid] = par;
-        s_tree.u[tid] = u;
-        s_tree.p[tid] = pc;
-        s_tree.q[tid] = qc;
     }
     cluster_sync_all();
-    if (rank != 0 && n_nodes > 0) {  // (rank 0 stays until the first pass's barrier; without nodes it leaves at once)
-        const uint32_t src = map_to_rank(&s_tree, 0);
-        for (int i = tid; i < static_cast<int>(sizeof(Tree) / 4); i += kThreads)
-            reinterpret_cast<uint32_t*>(&s_tree)[i] = ld_cluster_u32(src + 4 * i);
-    }
+    const auto parent_of = [&](int t) { return __float_as_int(s_tree[t].x); };
     if (tid == 0) s_path[0] = 0;
-    __syncthreads();
 
     const int v0 = min(rank * p.slice, p.V), v1 = min(v0 + p.slice, p.V);
     const int wsz = ((v1 - v0 + kWarps - 1) / kWarps + 31) / 32 * 32;  // entries per warp
@@ -172,17 +263,18 @@ __global__ void __launch_bounds__(kThreads) draft_tree_verify_kernel(const Param
             int cmd = -1;
             while (cmd < 0) {
                 // the next child of cur behind `last`
-                const unsigned lo = __ballot_sync(0xffffffffu, lane > last && s_tree.parent[lane] == cur);
-                const unsigned hi = __ballot_sync(0xffffffffu, lane + 32 > last && s_tree.parent[lane + 32] == cur);
+                const unsigned lo = __ballot_sync(0xffffffffu, lane > last && parent_of(lane) == cur);
+                const unsigned hi = __ballot_sync(0xffffffffu, lane + 32 > last && parent_of(lane + 32) == cur);
                 if ((lo | hi) == 0) {
                     cmd = summed ? 0 : 1;  // draw, from the sums there are or after a pass
                     break;
                 }
                 const int c = lo ? __ffs(lo) - 1 : 31 + __ffs(hi);
                 last = c;
-                const double pc = s_tree.p[c], qc = s_tree.q[c];
+                const float4 child = s_tree[c];
+                const double pc = child.z, qc = child.w;
                 const double left = fmax(pc - a * qc, 0.0);
-                if (R > 0.0 && static_cast<double>(s_tree.u[c]) * qc * S < left * R) {
+                if (R > 0.0 && static_cast<double>(child.y) * qc * S < left * R) {
                     if (lane == 0) s_path[len] = c;
                     ++len;
                     cur = c;
@@ -223,7 +315,7 @@ __global__ void __launch_bounds__(kThreads) draft_tree_verify_kernel(const Param
             cluster_sync_all();
             total = 0;
             for (int r = 0; r < cs; ++r) total += s_tot[parity][r];
-            S = static_cast<double>(total) * kUnitInv;
+            S = static_cast<double>(total) * kUnit;
             summed = true;
             parity ^= 1;
             continue;
@@ -245,7 +337,7 @@ __global__ void __launch_bounds__(kThreads) draft_tree_verify_kernel(const Param
             }
             break;
         }
-        const double x = fmin(fmax(static_cast<double>(s_tree.u[0]), 0.0), 1.0) * static_cast<double>(total);
+        const double x = fmin(fmax(static_cast<double>(s_tree[0].y), 0.0), 1.0) * static_cast<double>(total);
         uint64_t th = static_cast<uint64_t>(x);
         if (th >= total) th = total - 1;
         int owner = 0;
@@ -266,7 +358,11 @@ __global__ void __launch_bounds__(kThreads) draft_tree_verify_kernel(const Param
         int found = -1;
         for (int i0 = pb; i0 < pe && found < 0; i0 += 32) {
             const int i = i0 + lane;
-            uint64_t incl = i < pe ? weight(load_prob(pr, i), ah != 0.f ? load_prob(qr, i) : 0.f, ah, al) : 0;
+            uint64_t incl = 0;
+            if (i < pe) {
+                const Split w = split_weight(load_prob(pr, i), ah != 0.f ? load_prob(qr, i) : 0.f, ah, al);
+                incl = units(coarse_units(w), fine_units(w));
+            }
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const uint64_t below = __shfl_up_sync(0xffffffffu, incl, o);
@@ -294,9 +390,12 @@ __global__ void __launch_bounds__(kThreads) draft_tree_verify_kernel(const Param
 }  // namespace verify
 
 template <typename T>
-static cudaError_t launch_verify_t(const verify::Params& p, int B, int cs, cudaStream_t stream) {
-    return launch(verify::draft_tree_verify_kernel<T>, dim3(cs, B), dim3(verify::kThreads), 0, stream, false,
-                  static_cast<unsigned>(cs), p);
+static cudaError_t launch_verify_t(const verify::Params& p, int B, int cs, bool wide, cudaStream_t stream) {
+    const dim3 grid(cs, B);
+    return wide ? launch(verify::draft_tree_verify_kernel<T, 512>, grid, dim3(512), 0, stream, false,
+                         static_cast<unsigned>(cs), p)
+                : launch(verify::draft_tree_verify_kernel<T, 256>, grid, dim3(256), 0, stream, false,
+                         static_cast<unsigned>(cs), p);
 }
 
 cudaError_t launch_tree_verify(const VerifyArgs& a, cudaStream_t stream) {
@@ -317,11 +416,16 @@ cudaError_t launch_tree_verify(const VerifyArgs& a, cudaStream_t stream) {
     p.T = a.T;
     p.V = a.V;
     p.distinct = a.distinct;
-    // CTAs per sequence: a warp should have a few loads in flight per lane before it is worth another CTA's share
+    // CTAs per sequence: a thread should have two entries before it is worth another CTA's share.  512 threads a CTA
+    // while all sequences' CTAs are resident with them (two per SM), else 256.
+    const int sms = sm_count();
+    if (sms <= 0) return cudaErrorNoDevice;
     int cs = 1;
-    while (cs < verify::kMaxClusterV && a.V > cs * verify::kThreads * 2) cs *= 2;
+    while (cs < verify::kMaxClusterV && a.V > cs * 1024) cs *= 2;
     p.slice = (a.V + cs - 1) / cs;
-    return a.probs_f32 ? launch_verify_t<float>(p, a.B, cs, stream) : launch_verify_t<__half>(p, a.B, cs, stream);
+    const bool wide = static_cast<int64_t>(a.B) * cs <= KVC_VERIFY_WIDE * sms;
+    return a.probs_f32 ? launch_verify_t<float>(p, a.B, cs, wide, stream)
+                       : launch_verify_t<__half>(p, a.B, cs, wide, stream);
 }
 
 }  // namespace kvc
