@@ -29,6 +29,7 @@
 
 #include "../../include/kvc.h"
 #include "decode_common.cuh"
+#include "f32x2.cuh"
 #include "kvc_internal.h"
 #include "ptx.cuh"
 
@@ -43,7 +44,6 @@ namespace verify {
 #endif
 constexpr int kMaxClusterV = 8;
 constexpr int kUnitBits = 45;  // weights are counted in 2^-45; a row's sum has room up to 2^19
-constexpr double kUnit = 0x1p-45;
 
 struct Params {
     const void* p;
@@ -96,7 +96,7 @@ __device__ __forceinline__ Split split_weight(float p, float q, float ah, float 
 __device__ __forceinline__ int coarse_units(const Split& s) { return __float_as_int(s.coarse) - __float_as_int(kCoarse); }
 __device__ __forceinline__ int fine_units(const Split& s) { return __float_as_int(s.fine) - __float_as_int(kFine); }
 __device__ __forceinline__ uint64_t units(int64_t coarse, int64_t fine) {
-    return static_cast<uint64_t>(coarse * (1 << (kUnitBits - 23)) + fine);
+    return static_cast<uint64_t>(coarse * (int64_t(1) << (kUnitBits - 23)) + fine);
 }
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
@@ -105,62 +105,99 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
     return v;
 }
 
+__device__ __forceinline__ uint64_t sub_f32x2(uint64_t a, uint64_t b) {
+    return fma_f32x2(b, pack_f32x2(-1.f, -1.f), a);  // one rounding of a - b
+}
+// What the entries of a pass are weighed with: nothing (a = 0, the target's row itself), a = 1 (after a node's first
+// refusal, always), any a.  The same numbers come out of each, for less work: of a pair 14, 25 and 29 instructions.
+enum { kPlain = 0, kOne = 1, kAny = 2 };
+struct Factor {
+    uint64_t ah, al, neg_ah;  // a = ah + al, twice each
+    float h, l;
+    int mode;
+};
 // sums of weights in the two parts' units, brought together every few weights
+template <int kMode>
 struct LaneSum {
     uint64_t sum = 0;
-    int coarse = 0, fine = 0;  // of at most 32 weights: up to 2^28 and 2^27
-    __device__ __forceinline__ void add(float p, float q, float ah, float al) {
-        const Split w = split_weight(p, q, ah, al);
-        coarse += coarse_units(w);
-        fine += fine_units(w);
+    uint32_t coarse = 0, fine = 0;  // bits, modulo 2^32, of at most 32 weights (whose parts' sums stay below 2^29)
+    uint32_t pairs = 0;
+    // the weights of two entries, as split_weight gives them one by one
+    __device__ __forceinline__ void add(uint64_t p, uint64_t q, const Factor& f) {
+        uint64_t r = p, c = 0;
+        if constexpr (kMode != kPlain) {
+            const uint64_t nh = kMode == kOne ? q ^ 0x8000000080000000ull : mul_f32x2(f.neg_ah, q);  // -h
+            r = add_f32x2(p, nh);
+            const uint64_t b = sub_f32x2(r, p);
+            c = add_f32x2(sub_f32x2(p, sub_f32x2(r, b)), sub_f32x2(nh, b));
+            float r0, r1, c0, c1, e0 = 0.f, e1 = 0.f, n0 = 0.f, n1 = 0.f;
+            if constexpr (kMode == kAny) {
+                const uint64_t e = fma_f32x2(f.al, q, fma_f32x2(f.ah, q, nh));
+                c = sub_f32x2(c, e);
+                unpack_f32x2(e, e0, e1);
+                unpack_f32x2(nh, n0, n1);
+            }
+            unpack_f32x2(r, r0, r1);
+            unpack_f32x2(c, c0, c1);
+            const bool p0 = r0 > e0 && n0 > -2.f, p1 = r1 > e1 && n1 > -2.f;
+            r = pack_f32x2(p0 ? r0 : 0.f, p1 ? r1 : 0.f);
+            c = pack_f32x2(p0 ? c0 : 0.f, p1 ? c1 : 0.f);
+        }
+        const uint64_t one = pack_f32x2(kCoarse, kCoarse);
+        const uint64_t co = add_f32x2(r, one);
+        uint64_t rest = sub_f32x2(r, sub_f32x2(co, one));
+        if constexpr (kMode != kPlain) rest = add_f32x2(rest, c);
+        const uint64_t fi = add_f32x2(rest, pack_f32x2(kFine, kFine));
+        coarse += static_cast<uint32_t>(co) + static_cast<uint32_t>(co >> 32);
+        fine += static_cast<uint32_t>(fi) + static_cast<uint32_t>(fi >> 32);
+        ++pairs;
     }
     __device__ __forceinline__ void flush() {
-        sum += units(coarse, fine);
-        coarse = fine = 0;
+        sum += units(static_cast<int>(coarse - 2 * pairs * __float_as_uint(kCoarse)),
+                     static_cast<int>(fine - 2 * pairs * __float_as_uint(kFine)));
+        coarse = fine = pairs = 0;
     }
 };
 // this lane's share of the weights of entries [b, e), one at a time: entries b + lane, b + lane + 32, ...
-template <typename T>
-__device__ __forceinline__ void add_entries(LaneSum& acc, const T* __restrict__ p, const T* __restrict__ q, int b, int e,
-                                            float ah, float al) {
+template <int kMode, typename T>
+__device__ __forceinline__ void add_entries(LaneSum<kMode>& acc, const T* __restrict__ p, const T* __restrict__ q, int b,
+                                            int e, const Factor& f) {
     constexpr int U = 8;
-    const bool use_q = ah != 0.f;
     for (int i0 = b + (threadIdx.x & 31); i0 < e; i0 += 32 * U) {
         float pv[U], qv[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int i = i0 + u * 32;
             pv[u] = i < e ? load_prob(p, i) : 0.f;
-            qv[u] = i < e && use_q ? load_prob(q, i) : 0.f;
+            qv[u] = kMode != kPlain && i < e ? load_prob(q, i) : 0.f;
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) acc.add(pv[u], qv[u], ah, al);
+        for (int u = 0; u < U; u += 2) acc.add(pack_f32x2(pv[u], pv[u + 1]), pack_f32x2(qv[u], qv[u + 1]), f);
         acc.flush();
     }
 }
 template <typename T>
-__device__ __forceinline__ void unpack16(const uint4& v, float (&x)[16 / sizeof(T)]) {
+__device__ __forceinline__ void unpack16(const uint4& v, uint64_t (&x)[8 / sizeof(T)]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (sizeof(T) == 4) {
+        x[0] = pack_f32x2(prob(__uint_as_float(w[0])), prob(__uint_as_float(w[1])));
+        x[1] = pack_f32x2(prob(__uint_as_float(w[2])), prob(__uint_as_float(w[3])));
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (sizeof(T) == 4) {
-            x[i] = prob(__uint_as_float(w[i]));
-        } else {
+        for (int i = 0; i < 4; ++i) {
             const float2 f = unpack_half2(w[i]);
-            x[2 * i] = prob(f.x);
-            x[2 * i + 1] = prob(f.y);
+            x[i] = pack_f32x2(prob(f.x), prob(f.y));
         }
     }
 }
 // this lane's share of the weights of entries [b, e).  Rows of one alignment (a vocabulary of any size, but one stride
-// and 16-byte aligned tensors) are read 16 bytes at a time between their first and last few entries: 64 sequences x
-// 128,257 entries 78.3 -> KVC_VEC us.
-template <typename T>
-__device__ __forceinline__ uint64_t lane_weights(const T* __restrict__ p, const T* __restrict__ q, int b, int e, float ah,
-                                                 float al) {
-    LaneSum acc;
-    if ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15u) {
-        add_entries(acc, p, q, b, e, ah, al);
+// and 16-byte aligned tensors) are read 16 bytes at a time between their first and last few entries.
+template <int kMode, typename T>
+__device__ __forceinline__ uint64_t lane_weights(const T* __restrict__ p, const T* __restrict__ q, int b, int e,
+                                                 const Factor& f) {
+    LaneSum<kMode> acc;
+    if (kMode != kPlain && (reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15u) {
+        add_entries(acc, p, q, b, e, f);
         return acc.sum;
     }
     constexpr int V = 16 / sizeof(T), U = KVC_VERIFY_U;
@@ -168,29 +205,82 @@ __device__ __forceinline__ uint64_t lane_weights(const T* __restrict__ p, const 
     const int nv = (e - a) / V, lane = threadIdx.x & 31;
     const uint4* pv = reinterpret_cast<const uint4*>(p + a);
     const uint4* qv = reinterpret_cast<const uint4*>(q + a);
-    const bool use_q = ah != 0.f;
-    add_entries(acc, p, q, b, a, ah, al);
+    add_entries(acc, p, q, b, a, f);
     for (int i0 = lane; i0 < nv; i0 += 32 * U) {
         uint4 x[U], y[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int i = i0 + u * 32;
             x[u] = y[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (i < nv) x[u] = __ldg(pv + i);
-            if (i < nv && use_q) y[u] = __ldg(qv + i);
+            if (i < nv) {
+                x[u] = __ldg(pv + i);
+                if constexpr (kMode != kPlain) y[u] = __ldg(qv + i);
+            }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            float fx[V], fy[V];
+            uint64_t fx[V / 2], fy[V / 2];
             unpack16<T>(x[u], fx);
             unpack16<T>(y[u], fy);
 #pragma unroll
-            for (int k = 0; k < V; ++k) acc.add(fx[k], fy[k], ah, al);
+            for (int k = 0; k < V / 2; ++k) acc.add(fx[k], fy[k], f);
         }
         acc.flush();
     }
-    add_entries(acc, p, q, a + nv * V, e, ah, al);
+    add_entries(acc, p, q, a + nv * V, e, f);
     return acc.sum;
+}
+template <typename T>
+__device__ __forceinline__ uint64_t lane_weights(const T* p, const T* q, int b, int e, const Factor& f) {
+    return f.mode == kPlain ? lane_weights<kPlain, T>(p, q, b, e, f)
+           : f.mode == kOne ? lane_weights<kOne, T>(p, q, b, e, f)
+                            : lane_weights<kAny, T>(p, q, b, e, f);
+}
+
+// Sums of two floats, ~48 bits: the walk's scalars (the FP64 unit is slow: a trial took 0.6 us on it).
+struct Two {
+    float h, l;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Two two_prod(float a, float b) {
+    const float s = __fmul_rn(a, b);
+    return {s, __fmaf_rn(a, b, -s)};
+}
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+    Two s = two_sum(a.h, b.h);
+    const Two t = two_sum(a.l, b.l);
+    s = two_sum(s.h, __fadd_rn(s.l, t.h));
+    return two_sum(s.h, __fadd_rn(s.l, t.l));
+}
+__device__ __forceinline__ Two operator-(Two a) { return {-a.h, -a.l}; }
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+    const Two p = two_prod(a.h, b.h);
+    return two_sum(p.h, __fadd_rn(p.l, __fmaf_rn(a.h, b.l, __fmul_rn(a.l, b.h))));
+}
+__device__ __forceinline__ Two operator/(Two a, Two b) {
+    const float q0 = __fdiv_rn(a.h, b.h);
+    const Two r = a + -(b * Two{q0, 0.f});
+    return two_sum(q0, __fdiv_rn(__fadd_rn(r.h, r.l), b.h));
+}
+__device__ __forceinline__ bool positive(Two a) { return a.h > 0.f || (a.h == 0.f && a.l > 0.f); }
+// a sum of weights as a number (exact below 2^48 units)
+__device__ __forceinline__ Two from_units(uint64_t n) {
+    return two_sum(__fmul_rn(static_cast<float>(static_cast<uint32_t>(min(n >> 24, uint64_t(0xFFFFFFFFu)))), 0x1p-21f),
+                   __fmul_rn(static_cast<float>(static_cast<uint32_t>(n) & 0xFFFFFFu), 0x1p-45f));
+}
+// floor(u n) for 0 <= u <= 1
+__device__ __forceinline__ uint64_t scaled(float u, uint64_t n) {
+    u = __saturatef(u);
+    if (u >= 1.f) return n;
+    const uint32_t bits = __float_as_uint(u);
+    const uint64_t m = bits & 0x7FFFFFu;
+    const int e = static_cast<int>(bits >> 23) - 86;  // u = (2^23 + m) 2^(e - 64)
+    if (e + 86 == 0) return 0;                        // below 2^-126
+    const uint64_t frac = e >= 0 ? (m | 0x800000u) << e : e > -24 ? (m | 0x800000u) >> -e : 0;
+    return __umul64hi(frac, n);
 }
 
 template <typename T, int kThreads>
@@ -253,7 +343,8 @@ __global__ void __launch_bounds__(kThreads) draft_tree_verify_kernel(const Param
 
     // the walk's state, kept by warp 0
     int cur = 0, len = n_nodes > 0 ? 1 : 0, last = 0;
-    double a = 0.0, S = 1.0, R = 1.0;
+    const Two zero{0.f, 0.f}, one{1.f, 0.f};
+    Two a = zero, S = one, R = one;
     bool summed = false;  // s_tot holds the sums of (cur, a)
     int parity = 0;
     uint64_t total = 0;
@@ -272,40 +363,47 @@ __global__ void __launch_bounds__(kThreads) draft_tree_verify_kernel(const Param
                 const int c = lo ? __ffs(lo) - 1 : 31 + __ffs(hi);
                 last = c;
                 const float4 child = s_tree[c];
-                const double pc = child.z, qc = child.w;
-                const double left = fmax(pc - a * qc, 0.0);
-                if (R > 0.0 && static_cast<double>(child.y) * qc * S < left * R) {
+                const Two uq = two_prod(child.y, child.w);
+                // u q S < (p - a q)^+ R; at a node's first child u q < p
+                const Two left = Two{child.z, 0.f} + -(a * Two{child.w, 0.f});
+                if (positive(R) && positive(left) && positive(left * R + -(uq * S))) {
                     if (lane == 0) s_path[len] = c;
                     ++len;
                     cur = c;
-                    a = 0.0;
-                    S = R = 1.0;
+                    a = zero;
+                    S = R = one;
                     summed = false;
                 } else {
-                    if (R > 0.0) {
-                        const double a_new = a + S / R;
-                        if (a_new != a) {
-                            a = a_new;
+                    if (positive(R)) {
+                        const Two next = a + (p.distinct ? S / R : S);
+                        if (next.h != a.h || next.l != a.l) {
+                            a = next;
                             cmd = 1;
                         }
                     }
-                    if (p.distinct) R -= qc;
+                    if (p.distinct) R = R + Two{-child.w, 0.f};
                 }
             }
             if (lane == 0) {
                 s_cmd = cmd;
                 s_node = cur;
-                s_a[0] = static_cast<float>(a);
-                s_a[1] = static_cast<float>(a - static_cast<double>(static_cast<float>(a)));
+                s_a[0] = a.h;
+                s_a[1] = a.l;
             }
         }
         __syncthreads();
         const int cmd = s_cmd, node = s_node;
-        const float ah = s_a[0], al = s_a[1];
+        Factor f;
+        f.h = s_a[0];
+        f.l = s_a[1];
+        f.ah = pack_f32x2(f.h, f.h);
+        f.al = pack_f32x2(f.l, f.l);
+        f.neg_ah = pack_f32x2(-f.h, -f.h);
+        f.mode = f.h == 0.f ? kPlain : f.h == 1.f && f.l == 0.f ? kOne : kAny;
         const T* const pr = prow + node * p.p_stride;
         const T* const qr = qrow + node * p.q_stride;
         if (cmd == 1) {
-            const uint64_t ws = warp_sum(lane_weights(pr, qr, w0, w1, ah, al));
+            const uint64_t ws = warp_sum(lane_weights(pr, qr, w0, w1, f));
             if (lane == 0) s_warp[warp] = ws;
             __syncthreads();
             if (warp == 0) {
@@ -315,7 +413,7 @@ __global__ void __launch_bounds__(kThreads) draft_tree_verify_kernel(const Param
             cluster_sync_all();
             total = 0;
             for (int r = 0; r < cs; ++r) total += s_tot[parity][r];
-            S = static_cast<double>(total) * kUnit;
+            S = from_units(total);
             summed = true;
             parity ^= 1;
             continue;
@@ -323,9 +421,9 @@ __global__ void __launch_bounds__(kThreads) draft_tree_verify_kernel(const Param
         // draw: the first entry whose running weight exceeds u * total
         const uint64_t* tot = s_tot[parity ^ 1];
         if (total == 0) {
-            if (ah != 0.f) {  // nothing of the residual is left: the target's own row
-                a = 0.0;
-                S = 1.0;
+            if (f.mode != kPlain) {  // nothing of the residual is left: the target's own row
+                a = zero;
+                S = one;
                 summed = false;
                 last = kMaxTreeNodes;  // no further child is tried
                 __syncthreads();
@@ -337,8 +435,7 @@ __global__ void __launch_bounds__(kThreads) draft_tree_verify_kernel(const Param
             }
             break;
         }
-        const double x = fmin(fmax(static_cast<double>(s_tree[0].y), 0.0), 1.0) * static_cast<double>(total);
-        uint64_t th = static_cast<uint64_t>(x);
+        uint64_t th = scaled(s_tree[0].y, total);
         if (th >= total) th = total - 1;
         int owner = 0;
         while (owner < cs - 1 && th >= tot[owner]) th -= tot[owner++];
@@ -349,7 +446,7 @@ __global__ void __launch_bounds__(kThreads) draft_tree_verify_kernel(const Param
         const int sb = min(v0 + sw * wsz, v1), se = min(sb + wsz, v1);
         const int psz = ((se - sb + kWarps - 1) / kWarps + 31) / 32 * 32;
         const int pb = min(sb + warp * psz, se), pe = min(pb + psz, se);
-        const uint64_t ps = warp_sum(lane_weights(pr, qr, pb, pe, ah, al));
+        const uint64_t ps = warp_sum(lane_weights(pr, qr, pb, pe, f));
         if (lane == 0) s_part[warp] = ps;
         __syncthreads();
         int pw = 0;
@@ -360,7 +457,7 @@ __global__ void __launch_bounds__(kThreads) draft_tree_verify_kernel(const Param
             const int i = i0 + lane;
             uint64_t incl = 0;
             if (i < pe) {
-                const Split w = split_weight(load_prob(pr, i), ah != 0.f ? load_prob(qr, i) : 0.f, ah, al);
+                const Split w = split_weight(load_prob(pr, i), f.mode != kPlain ? load_prob(qr, i) : 0.f, f.h, f.l);
                 incl = units(coarse_units(w), fine_units(w));
             }
 #pragma unroll
