@@ -742,6 +742,7 @@ def kv_rope_turns(inv_freq) -> np.ndarray:
     return turns
 
 
+_F16, _F32, _I32, _I64 = torch.float16, torch.float32, torch.int32, torch.int64
 # the current device's index (the underscored form skips a wrapper, 0.1 µs a call)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
@@ -757,10 +758,10 @@ def _same_device(*tensors) -> None:
 
 
 def _ready(dev: int, dtype, *tensors) -> bool:
-    """Every tensor given is a contiguous CUDA tensor of the type on device dev: the test of a call's common case in one
-    go.  Where it fails, the call's own checks name what is wrong."""
+    """Every tensor given (None: left out) is a contiguous CUDA tensor of the type on device dev: the test of a call's
+    common case in one go.  Where it fails, the call's own checks name what is wrong."""
     for t in tensors:
-        if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        if t is not None and (t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous()):
             return False
     return True
 
@@ -779,18 +780,10 @@ def _run(fn, args, name, stream, prepare, dev, keep):
     return None
 
 
-def _token_rows(t: torch.Tensor, name: str):
-    """Pointer and token stride of an [n][H][D] fp16 tensor whose heads are packed and whose tokens may be apart."""
-    if isinstance(t, torch.Tensor) and t.dtype is torch.float16 and t.is_cuda:
-        st = t.stride()
-        if len(st) == 3 and st[2] == 1:
-            n, H, D = t.shape
-            if st[1] == D:  # the common case; the checks below name the failure
-                return t.data_ptr(), (st[0] if n > 1 else H * D)
+def _token_stride(t: torch.Tensor, name: str) -> int:
+    """Token stride of an [n][H][D] fp16 tensor whose heads are packed and whose tokens may be apart."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [n][H][D]")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
     if t.dtype != torch.float16:
@@ -798,7 +791,7 @@ def _token_rows(t: torch.Tensor, name: str):
     n, H, D = t.shape
     if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    return t.data_ptr(), (t.stride(0) if n > 1 else H * D)
+    return t.stride(0) if n > 1 else H * D
 
 
 def kv_append_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: Optional[torch.Tensor],
@@ -813,51 +806,55 @@ def kv_append_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions:
     int32 [n]; turns int64 [rot_dim / 2] (kv_rope_turns; None: no rotation); q_out [n][Hq][D]; k_cache / v_cache
     [NB][Hkv][bs][D] (one layer) with slot_mapping int64 [n]; q_weight / k_weight fp16 [D] (None: no norm);
     k_out / v_out [n][Hkv][D]: the rows packed.  prepare=True returns a PreparedCall instead of launching."""
-    qp, qs = _token_rows(q, "q")
-    kp, ks = _token_rows(k, "k")
-    vp, vs = _token_rows(v, "v")
-    n, Hq, D = q.shape
-    kshape = k.shape
-    Hkv = kshape[1]
-    if kshape[0] != n or kshape[2] != D or v.shape != kshape or q_out.shape != q.shape:
+    qshape, kshape, rot, NB, bs = q.shape, k.shape, 0, 0, 16
+    if len(qshape) != 3 or len(kshape) != 3:
+        raise ValueError("q, k and v must be [n][H][D]")
+    n, Hq, D = qshape
+    kn, Hkv, kd = kshape
+    if kn != n or kd != D or v.shape != kshape or q_out.shape != qshape:
         raise ValueError("q, k, v and q_out do not match")
-    for t, nm in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is not None and t.shape != kshape:
-            raise ValueError(f"{nm} must have k's shape")
-    for t, nm in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None and t.numel() != D:
-            raise ValueError(f"{nm} must have D entries")
-    rot = 0 if turns is None else 2 * turns.numel()
-    if not rot:
+    if turns is not None and (half := turns.numel()):
+        rot = 2 * half
+        if positions is None or positions.numel() != n:
+            raise ValueError("positions must have n entries")
+    else:
         positions = turns = None
-    elif positions is None or positions.numel() != n:
-        raise ValueError("positions must have n entries")
-    NB, bs = 0, 16
     if k_cache is not None and v_cache is not None and slot_mapping is not None:
-        if k_cache.dim() != 4:
+        cshape = k_cache.shape
+        if len(cshape) != 4:
             raise ValueError("k_cache must be [NB][Hkv][bs][D]")
-        NB, Hc, bs, Dc = k_cache.shape
-        if Hc != Hkv or Dc != D or v_cache.shape != k_cache.shape:
+        NB, Hc, bs, Dc = cshape
+        if Hc != Hkv or Dc != D or v_cache.shape != cshape:
             raise ValueError("cache shapes do not match k")
         if slot_mapping.numel() != n:
             raise ValueError("slot_mapping must have n entries")
     elif k_cache is not None or v_cache is not None or slot_mapping is not None:
         raise ValueError("k_cache, v_cache and slot_mapping: all or none")
+    if (q_weight is not None and q_weight.numel() != D) or (k_weight is not None and k_weight.numel() != D):
+        raise ValueError("q_weight and k_weight must have D entries")
+    if (k_out is not None and k_out.shape != kshape) or (v_out is not None and v_out.shape != kshape):
+        raise ValueError("k_out and v_out must have k's shape")
     keep = (q, k, v, positions, turns, q_out, k_cache, v_cache, slot_mapping, q_weight, k_weight, k_out, v_out)
-    dev, f16 = q.get_device(), torch.float16
-    ready = dev == _current_device() == k.get_device() == v.get_device() and _ready(
-        dev, f16, *[t for t in (q_out, k_cache, v_cache, q_weight, k_weight, k_out, v_out) if t is not None]) and \
-        _ready(dev, torch.int64, *[t for t in (turns, slot_mapping) if t is not None]) and \
-        (positions is None or _ready(dev, torch.int32, positions))
-    if not ready:
+    dev = q.get_device()
+    qst, kst, vst = q.stride(), k.stride(), v.stride()
+    # the common case in one expression; the checks below only name the failure
+    if not (dev == _current_device() == k.get_device() == v.get_device()
+            and q.dtype is _F16 and k.dtype is _F16 and v.dtype is _F16
+            and qst[2] == kst[2] == vst[2] == 1 and qst[1] == kst[1] == vst[1] == D
+            and _ready(dev, _F16, q_out, q_weight, k_weight, k_out, v_out, k_cache, v_cache)
+            and _ready(dev, _I64, turns, slot_mapping) and _ready(dev, _I32, positions)):
+        qst, kst, vst = ((_token_stride(t, nm),) for t, nm in ((q, "q"), (k, "k"), (v, "v")))
         _same_device(*keep)
         for t, nm in ((q_weight, "q_weight"), (k_weight, "k_weight"), (q_out, "q_out"), (k_out, "k_out"),
                       (v_out, "v_out"), (k_cache, "k_cache"), (v_cache, "v_cache")):
-            _dptr(t, f16, nm)
+            _dptr(t, _F16, nm)
         for t, nm in ((turns, "turns"), (slot_mapping, "slot_mapping")):
-            _dptr(t, torch.int64, nm)
-        _dptr(positions, torch.int32, "positions")
-    args = (qp, qs, kp, ks, vp, vs, n, Hq, Hkv, D, None if q_weight is None else q_weight.data_ptr(),
+            _dptr(t, _I64, nm)
+        _dptr(positions, _I32, "positions")
+    if n == 1:  # a single token's stride means nothing
+        qst, kst, vst = (Hq * D,), (Hkv * D,), (Hkv * D,)
+    args = (q.data_ptr(), qst[0], k.data_ptr(), kst[0], v.data_ptr(), vst[0], n, Hq, Hkv, D,
+            None if q_weight is None else q_weight.data_ptr(),
             None if k_weight is None else k_weight.data_ptr(), float(eps), None if turns is None else turns.data_ptr(), rot,
             1 if interleaved else 0, None if positions is None else positions.data_ptr(), q_out.data_ptr(),
             None if k_out is None else k_out.data_ptr(), None if v_out is None else v_out.data_ptr(),
@@ -897,20 +894,20 @@ def paged_decode_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
         raise ValueError("block_table / context_lens do not match B")
     if masks.shape != (B, T) or (tree_lens is not None and tree_lens.numel() != B):
         raise ValueError("masks must be [B][T] and tree_lens have B entries")
-    f16, i32, odt = torch.float16, torch.int32, out.dtype
-    od = KVC_F16 if odt is f16 else KVC_F32 if odt is torch.float32 else None
+    odt = out.dtype
+    od = KVC_F16 if odt is _F16 else KVC_F32 if odt is _F32 else None
     if od is None:
         raise TypeError("out must be float16 or float32")
     keep = (q, k_cache, v_cache, block_table, context_lens, masks, tree_lens, out, workspace)
     dev = q.get_device()
-    if not (dev == _current_device() and _ready(dev, f16, q, k_cache, v_cache)
-            and _ready(dev, i32, block_table, context_lens) and _ready(dev, torch.int64, masks)
-            and _ready(dev, odt, out) and (tree_lens is None or _ready(dev, i32, tree_lens))
+    if not (dev == _current_device() and _ready(dev, _F16, q, k_cache, v_cache, out if od == KVC_F16 else None)
+            and _ready(dev, _I32, block_table, context_lens, tree_lens) and masks.dtype is _I64
+            and masks.get_device() == dev and masks.is_contiguous() and (od == KVC_F16 or _ready(dev, _F32, out))
             and (workspace is None or _ready(dev, workspace.dtype, workspace))):
         _same_device(*keep)
-        for t, dt, nm in ((q, f16, "q"), (k_cache, f16, "k_cache"), (v_cache, f16, "v_cache"),
-                          (block_table, i32, "block_table"), (context_lens, i32, "context_lens"),
-                          (masks, torch.int64, "masks"), (tree_lens, i32, "tree_lens"), (out, None, "out"),
+        for t, dt, nm in ((q, _F16, "q"), (k_cache, _F16, "k_cache"), (v_cache, _F16, "v_cache"),
+                          (block_table, _I32, "block_table"), (context_lens, _I32, "context_lens"),
+                          (masks, _I64, "masks"), (tree_lens, _I32, "tree_lens"), (out, None, "out"),
                           (workspace, None, "workspace")):
             _dptr(t, dt, nm)
     args = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), NB, block_table.data_ptr(), block_table.shape[1],
@@ -963,16 +960,16 @@ def draft_tree_verify(target_probs: torch.Tensor, draft_probs: torch.Tensor, tok
     if path_len.numel() != B or next_token.numel() != B or (tree_lens is not None and tree_lens.numel() != B):
         raise ValueError("path_len, next_token and tree_lens must have B entries")
     keep = (target_probs, draft_probs, tokens, parents, tree_lens, uniforms, path, path_len, next_token)
-    i32, dev = torch.int32, target_probs.get_device()
+    dev = target_probs.get_device()
     if not (dev == _current_device() == draft_probs.get_device()
-            and _ready(dev, i32, tokens, parents, path, path_len, next_token) and _ready(dev, torch.float32, uniforms)
-            and (tree_lens is None or _ready(dev, i32, tree_lens))):
+            and _ready(dev, _I32, tokens, parents, path, path_len, next_token, tree_lens)
+            and uniforms.dtype is _F32 and uniforms.get_device() == dev and uniforms.is_contiguous()):
         _same_device(*keep)
         for t, nm in ((tokens, "tokens"), (parents, "parents"), (tree_lens, "tree_lens"), (path, "path"),
                       (path_len, "path_len"), (next_token, "next_token")):
-            _dptr(t, i32, nm)
-        _dptr(uniforms, torch.float32, "uniforms")
-    args = (pp, ps, qp, qs, KVC_F32 if pdt is torch.float32 else KVC_F16, tokens.data_ptr(), parents.data_ptr(),
+            _dptr(t, _I32, nm)
+        _dptr(uniforms, _F32, "uniforms")
+    args = (pp, ps, qp, qs, KVC_F32 if pdt is _F32 else KVC_F16, tokens.data_ptr(), parents.data_ptr(),
             None if tree_lens is None else tree_lens.data_ptr(), uniforms.data_ptr(), B, T, V, 1 if distinct else 0,
             path.data_ptr(), path_len.data_ptr(), next_token.data_ptr())
     return _run(_lib.draft_tree_verify, args, "draft_tree_verify", stream, prepare, dev, keep)
@@ -996,13 +993,13 @@ def kv_tree_commit(h: int, block_table: torch.Tensor, context_lens: torch.Tensor
             tree_lens is not None and tree_lens.numel() != B):
         raise ValueError("context_lens, path_len, new_context_lens and tree_lens must have B entries")
     keep = (path, block_table, context_lens, tree_lens, path_len, new_context_lens)
-    i32, dev = torch.int32, path.get_device()
-    if not (dev == _current_device() and _ready(dev, i32, path, block_table, context_lens, path_len, new_context_lens)
-            and (tree_lens is None or _ready(dev, i32, tree_lens))):
+    dev = path.get_device()
+    if not (dev == _current_device()
+            and _ready(dev, _I32, path, block_table, context_lens, path_len, new_context_lens, tree_lens)):
         _same_device(*keep)
         for t, nm in ((path, "path"), (block_table, "block_table"), (context_lens, "context_lens"),
                       (tree_lens, "tree_lens"), (path_len, "path_len"), (new_context_lens, "new_context_lens")):
-            _dptr(t, i32, nm)
+            _dptr(t, _I32, nm)
     args = (h, block_table.data_ptr(), max_blocks, context_lens.data_ptr(),
             None if tree_lens is None else tree_lens.data_ptr(), path.data_ptr(), path_len.data_ptr(), P, B,
             new_context_lens.data_ptr())

@@ -823,11 +823,10 @@ static cudaError_t tree_setup() {
 
 // Clusters of cs CTAs (one per SM) that the device holds at a time; the SMs of a GPC that no whole cluster fills stay
 // idle.  Asked once per device and size.
-static int resident_clusters(int D, int cs, int sms) {
+static int resident_clusters(int dev, int D, int cs, int sms) {
     static std::atomic<int> cache[128][2][tree::kMaxTreeCluster + 1];
     if (cs == 1) return sms;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return sms / cs;
+    if (dev < 0 || dev >= 128) return std::max(1, sms / cs);
     std::atomic<int>& slot = cache[dev][D == 128][cs];
     int n = slot.load(std::memory_order_relaxed);
     if (n > 0) return n;
@@ -869,24 +868,25 @@ cudaError_t tree_plan(int B, int Hq, int Hkv, int D, int max_ctx, int T, TreePla
     const int64_t units = std::max<int64_t>(1, static_cast<int64_t>(B) * Hkv * plan->row_pairs);
     // The split of the context with the shortest run, counted in key tiles: waves of clusters times the tiles of a CTA
     // plus the start and end of a CTA; merging in a cluster costs little, partial states and the combine launch more.
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorNoDevice;
     int64_t best_cost = INT64_MAX;
     for (int nc = 1; nc <= std::min(tiles, 128); ++nc) {
         const int chunk = (tiles + nc - 1) / nc;
         if ((tiles + chunk - 1) / chunk != nc) continue;
-#ifdef KVC_TREE_NC
-        if (nc != KVC_TREE_NC) continue;
-#endif
-        const int cs = std::min(nc, nc <= tree::kMaxTreeCluster ? tree::kMaxTreeCluster : kTreeSplitCluster);
+        const int cs = nc <= tree::kMaxTreeCluster ? nc : kTreeSplitCluster;
         const int nclus = (nc + cs - 1) / cs;
-        const int64_t resident = resident_clusters(D, cs, sms);
+        const int64_t resident = resident_clusters(dev, D, cs, sms);
         const int64_t waves = (units * nclus + resident - 1) / resident;
-        const int64_t cost = waves * (2 * chunk + kTreeCtaCost) + (nc > 1 ? 1 + cs / 2 : 0) + (nclus > 1 ? kTreeCombineCost + nclus / 4 : 0);
+        const int64_t cost = waves * (2 * chunk + kTreeCtaCost) + (nc > 1 ? 1 + cs / 2 : 0) +
+                             (nclus > 1 ? kTreeCombineCost + nclus / 4 : 0);
         if (cost < best_cost) {
             best_cost = cost;
             plan->chunk = chunk;
             plan->cluster = cs;
             plan->nclus = nclus;
         }
+        if (units * nc > 8 * sms) break;  // every SM has its share: more chunks only cost
     }
     plan->workspace_bytes = plan->nclus > 1 ? partials_bytes(static_cast<size_t>(B) * T * Hq * plan->nclus, D) : 0;
     return cudaSuccess;

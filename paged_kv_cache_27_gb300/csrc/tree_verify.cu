@@ -284,7 +284,7 @@ __device__ __forceinline__ uint64_t scaled(float u, uint64_t n) {
 }
 
 template <typename T, int kThreads>
-__global__ void __launch_bounds__(kThreads) draft_tree_verify_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) draft_tree_verify_kernel(const Params p) {
     constexpr int kWarps = kThreads / 32;
     __shared__ float4 s_tree[kMaxTreeNodes];        // a node's (parent, u, p, q): p and q of its token at its parent
     __shared__ uint64_t s_tot[2][kMaxClusterV];     // the CTAs' sums of a pass, by pass parity
