@@ -654,13 +654,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
         tc_fence_after();
         tmem_dealloc(tmem, Geo::kTmemCols);
     }
-    if (*s_bad_block != 0) *s_bad_v = 0;  // the chunk is left out
-    if (p.cluster > 1) {
-        __syncwarp();
-        cluster_sync_all();  // every CTA's states are in its shared memory
-    } else {
-        __syncthreads();
-    }
     // ================= the cluster's states merged: each CTA takes a share of the rows =================
     const int live_rows = min(two_rows ? 2 * kRows : kRows, rows - r0);
     const int share = (live_rows + p.cluster - 1) / p.cluster;
@@ -671,6 +664,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
         const int t = node_of(rr);
         return (static_cast<int64_t>(b) * p.T + t) * p.Hq + hk * p.G + rr - t * p.G;
     };
+    if (*s_bad_block != 0) *s_bad_v = 0;  // the chunk is left out
+    if (p.cluster > 1) {
+        __syncwarp();
+        cluster_sync_all();  // every CTA's states are in its shared memory
+    } else {
+        __syncthreads();
+    }
     // weights of a row's states, s_w[row][state] = (weight, sum): a group of `group` lanes takes a row, a lane a state
     float2* const s_w = reinterpret_cast<float2*>(smem + Geo::kWeightOff);
     {
@@ -762,6 +762,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
     };
     if (nst <= 2)
         merge_rows(std::integral_constant<int, 4>(), std::integral_constant<int, 2>());
+    else if (nst <= 4)
+        merge_rows(std::integral_constant<int, 2>(), std::integral_constant<int, 4>());
     else
         merge_rows(std::integral_constant<int, 1>(), std::integral_constant<int, 8>());
     if (p.cluster > 1) {
