@@ -28,6 +28,12 @@
 namespace kvc {
 namespace rope {
 
+#ifndef KVC_ROPE_LD
+#define KVC_ROPE_LD(p) (*(p))
+#endif
+#ifndef KVC_ROPE_ST
+#define KVC_ROPE_ST(p, v) (*(p) = (v))
+#endif
 #ifndef KVC_ROPE_U
 #define KVC_ROPE_U 2
 #endif
@@ -165,8 +171,8 @@ __global__ void __launch_bounds__(kWarps * 32, KVC_ROPE_CTAS) kv_append_rope_ker
                 const int h = (pass + u) * kRows + rsub;
                 raw[u][0] = raw[u][1] = make_uint4(0u, 0u, 0u, 0u);
                 if (pass + u < last && h < H) {
-                    raw[u][0] = *reinterpret_cast<const uint4*>(src + h * D + c0 * 8);
-                    raw[u][1] = *reinterpret_cast<const uint4*>(src + h * D + c1 * 8);
+                    raw[u][0] = KVC_ROPE_LD(reinterpret_cast<const uint4*>(src + h * D + c0 * 8));
+                    raw[u][1] = KVC_ROPE_LD(reinterpret_cast<const uint4*>(src + h * D + c1 * 8));
                 }
             }
 #pragma unroll
@@ -218,8 +224,8 @@ __global__ void __launch_bounds__(kWarps * 32, KVC_ROPE_CTAS) kv_append_rope_ker
                 }
                 if (h >= H) continue;
                 auto put = [&](__half* row) {
-                    *reinterpret_cast<uint4*>(row + c0 * 8) = o0;
-                    *reinterpret_cast<uint4*>(row + c1 * 8) = o1;
+                    KVC_ROPE_ST(reinterpret_cast<uint4*>(row + c0 * 8), o0);
+                    KVC_ROPE_ST(reinterpret_cast<uint4*>(row + c1 * 8), o1);
                 };
                 if (kKind == 0 || packed != nullptr) put(packed + (t * H + h) * D);
                 if (kKind > 0 && dst >= 0) put(cache + dst + static_cast<int64_t>(h) * kBlockSize * D);

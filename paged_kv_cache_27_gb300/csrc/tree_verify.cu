@@ -36,12 +36,6 @@
 namespace kvc {
 namespace verify {
 
-#ifndef KVC_VERIFY_U
-#define KVC_VERIFY_U 2
-#endif
-#ifndef KVC_VERIFY_WIDE
-#define KVC_VERIFY_WIDE 2
-#endif
 constexpr int kMaxClusterV = 8;
 constexpr int kUnitBits = 45;  // weights are counted in 2^-45; a row's sum has room up to 2^19
 
@@ -191,7 +185,8 @@ __device__ __forceinline__ void unpack16(const uint4& v, uint64_t (&x)[8 / sizeo
     }
 }
 // this lane's share of the weights of entries [b, e).  Rows of one alignment (a vocabulary of any size, but one stride
-// and 16-byte aligned tensors) are read 16 bytes at a time between their first and last few entries.
+// and 16-byte aligned tensors) are read 16 bytes at a time between their first and last few entries (64 sequences x
+// 128,257 entries: 78 -> 59 us), the next vectors ahead of the current ones' arithmetic (50 -> 48 us).
 template <int kMode, typename T>
 __device__ __forceinline__ uint64_t lane_weights(const T* __restrict__ p, const T* __restrict__ q, int b, int e,
                                                  const Factor& f) {
@@ -200,23 +195,32 @@ __device__ __forceinline__ uint64_t lane_weights(const T* __restrict__ p, const 
         add_entries(acc, p, q, b, e, f);
         return acc.sum;
     }
-    constexpr int V = 16 / sizeof(T), U = KVC_VERIFY_U;
+    constexpr int V = 16 / sizeof(T), U = 2;
     const int a = min(e, b + static_cast<int>((0 - reinterpret_cast<uintptr_t>(p + b)) & 15u) / static_cast<int>(sizeof(T)));
     const int nv = (e - a) / V, lane = threadIdx.x & 31;
     const uint4* pv = reinterpret_cast<const uint4*>(p + a);
     const uint4* qv = reinterpret_cast<const uint4*>(q + a);
     add_entries(acc, p, q, b, a, f);
-    for (int i0 = lane; i0 < nv; i0 += 32 * U) {
-        uint4 x[U], y[U];
+    uint4 x[U], y[U], nx[U], ny[U];  // the vectors at work, and the next ones on their way
+    auto fetch = [&](int i0) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int i = i0 + u * 32;
-            x[u] = y[u] = make_uint4(0u, 0u, 0u, 0u);
+            nx[u] = ny[u] = make_uint4(0u, 0u, 0u, 0u);
             if (i < nv) {
-                x[u] = __ldg(pv + i);
-                if constexpr (kMode != kPlain) y[u] = __ldg(qv + i);
+                nx[u] = __ldg(pv + i);
+                if constexpr (kMode != kPlain) ny[u] = __ldg(qv + i);
             }
         }
+    };
+    fetch(lane);
+    for (int i0 = lane; i0 < nv; i0 += 32 * U) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            x[u] = nx[u];
+            y[u] = ny[u];
+        }
+        fetch(i0 + 32 * U);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             uint64_t fx[V / 2], fy[V / 2];
@@ -284,7 +288,7 @@ __device__ __forceinline__ uint64_t scaled(float u, uint64_t n) {
 }
 
 template <typename T, int kThreads>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) draft_tree_verify_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 768 / kThreads) draft_tree_verify_kernel(const Params p) {
     constexpr int kWarps = kThreads / 32;
     __shared__ float4 s_tree[kMaxTreeNodes];        // a node's (parent, u, p, q): p and q of its token at its parent
     __shared__ uint64_t s_tot[2][kMaxClusterV];     // the CTAs' sums of a pass, by pass parity
@@ -513,14 +517,15 @@ cudaError_t launch_tree_verify(const VerifyArgs& a, cudaStream_t stream) {
     p.T = a.T;
     p.V = a.V;
     p.distinct = a.distinct;
-    // CTAs per sequence: a thread should have two entries before it is worth another CTA's share.  512 threads a CTA
-    // while all sequences' CTAs are resident with them (two per SM), else 256.
+    // CTAs per sequence: a thread should have two entries before it is worth another CTA's share (clusters of 4, 8 and
+    // 16 for 64 sequences x 128,257 entries: 59, 50 and 54 us).  512 threads a CTA while every CTA has an SM, else 256,
+    // three CTAs per SM (64 sequences: 60 and 48 us).
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorNoDevice;
     int cs = 1;
     while (cs < verify::kMaxClusterV && a.V > cs * 1024) cs *= 2;
     p.slice = (a.V + cs - 1) / cs;
-    const bool wide = static_cast<int64_t>(a.B) * cs <= KVC_VERIFY_WIDE * sms;
+    const bool wide = static_cast<int64_t>(a.B) * cs <= sms;
     return a.probs_f32 ? launch_verify_t<float>(p, a.B, cs, wide, stream)
                        : launch_verify_t<__half>(p, a.B, cs, wide, stream);
 }
