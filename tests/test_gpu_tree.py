@@ -126,6 +126,29 @@ def test_append_rope_in_place_and_without_a_cache(kvc):
     assert e.value.name == "KVC_ERR_CAPACITY"
 
 
+@pytest.mark.parametrize("n,Hq,Hkv,D", [(6000, 32, 8, 128), (12000, 32, 8, 64)])
+def test_append_rope_of_a_long_prompt_is_its_parts(kvc, n, Hq, Hkv, D):
+    """More rows than L2 holds go another way through it; the rows are the same."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    qkv = torch.randn(n, (Hq + 2 * Hkv) * D, generator=g, device="cuda", dtype=torch.float16)
+    q, k, v = (x.unflatten(1, (-1, D)) for x in qkv.split((Hq * D, Hkv * D, Hkv * D), 1))
+    w = torch.rand(2, D, generator=g, device="cuda").half()
+    turns, pos = dev(kvc.kv_rope_turns(1e4 ** (-np.arange(0, D, 2) / D))), torch.arange(n, dtype=torch.int32, device="cuda")
+    slots = torch.randperm(n, generator=g, device="cuda")
+    got = []
+    for step in (n, 500):
+        out = torch.zeros((n, Hq, D), dtype=torch.float16, device="cuda")
+        kc, vc = (torch.zeros((-(-n // 16), Hkv, 16, D), dtype=torch.float16, device="cuda") for _ in range(2))
+        for a in range(0, n, step):
+            s = slice(a, a + step)
+            kvc.kv_append_rope(q[s], k[s], v[s], pos[s], turns, out[s], kc, vc, slots[s], q_weight=w[0], k_weight=w[1])
+        got.append((out, kc, vc))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    check_rows(host(got[0][0][-3:]), host(q[-3:]), host(w[0]), 1e-6,
+               np.arange(n - 3, n)[:, None] * (1e4 ** (-np.arange(0, D, 2) / D)), False, "last rows")
+
+
 # ---------------------------------------------------------------- tree attention
 class Tree:
     """Random queries, caches and masks; everything past a context, and every block no sequence owns, is NaN."""
