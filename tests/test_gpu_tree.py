@@ -234,6 +234,7 @@ TREES = [
     ([5000, 2500], [8, 1], 8, 14, 2, 64, False),
     ([0, 0], [0, 0], 5, 4, 4, 64, False),
     ([30, 31, 32], [2, 2, 2], 2, 8, 8, 128, False),
+    ([40, 3], [64, 50], 64, 64, 1, 64, False),            # 4096 query rows
     ([30000, 9000, 0], [5, 5, 5], 5, 2, 1, 64, False),    # several clusters of chunks, and their combine
     ([20000, 3], [33, 40], 40, 8, 1, 128, True),          # the same with two row tiles
 ]
@@ -506,6 +507,38 @@ def test_verify_edges(kvc):
     assert got[2][0] == 5 and got[2][3] == 400 and got[2][2] == 17 and got[1][2] > 1 and got[1][3] == 1
 
 
+def test_verify_captured_beside_another(kvc):
+    """Two captured calls replayed at once on two streams (the call has no workspace), with new uniforms each time."""
+    cases = [verify_case(70 + i, 8, 10, 4001, 1.0, distinct=bool(i)) for i in range(2)]
+    runs = []
+    for i, (p, q, tok, par, u) in enumerate(cases):
+        s = torch.cuda.Stream()
+        d = [dev(x) for x in (p, q, tok, par, u)]
+        out = [torch.zeros(8, 10, dtype=torch.int32, device="cuda")] + [torch.zeros(8, dtype=torch.int32, device="cuda")
+                                                                       for _ in range(2)]
+        call = kvc.draft_tree_verify(*d, *out, distinct=bool(i), prepare=True)
+        s.wait_stream(torch.cuda.current_stream())
+        call(s)
+        s.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            call()
+        runs.append((g, s, d, out))
+    for turn in range(3):
+        us = []
+        for i, (g, s, d, out) in enumerate(runs):
+            us.append(np.random.default_rng(100 * turn + i).random((8, 10), dtype=np.float32))
+            d[4].copy_(dev(us[-1]))
+        torch.cuda.synchronize()
+        for g, s, d, out in runs:
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for i, (g, s, d, out) in enumerate(runs):
+            p, q, tok, par, _ = cases[i]
+            check_verify([host(x) for x in out], p, q, tok, par, us[i], distinct=bool(i))
+
+
 def test_verify_flags_bad_trees(kvc):
     p, q, tok, par, u = verify_case(63, 5, 4, 50)
     tok0, par0 = tok.copy(), par.copy()
@@ -571,6 +604,22 @@ def test_commit(kvc, L, hist, lens, T, Hkv, D):
             assert (host(new) == want).all()
             for got, ref in zip(d, pools):
                 assert (host(got).view(np.uint16) == ref.view(np.uint16)).all()
+    finally:
+        kvc.kv_cache_destroy(h)
+
+
+def test_commit_of_a_path_narrower_than_its_tree(kvc):
+    """A tree of 40 nodes whose depth is known to be at most 5: the path is [B][5]."""
+    pools, table, ctx, lens, path, n = commit_case(77, 2, [50, 9], [40, 33], 40, 2, 64)
+    path, n = np.array([[0, 3, 7, 20, 39], [0, 1, 32, -1, -1]], np.int32), np.array([5, 3], np.int32)
+    d = [dev(p.view(np.int16)).view(torch.float16) for p in pools]
+    h = kvc.kv_cache_create(kvc.KvcConfig(2, pools[0].shape[1], 2, 64), *d)
+    try:
+        new = torch.zeros(2, dtype=torch.int32, device="cuda")
+        kvc.kv_tree_commit(h, dev(table), dev(ctx), dev(path), dev(n), new, tree_lens=dev(lens))
+        assert (host(new) == tree.commit(pools, table, ctx, lens, path, n)).all()
+        for got, ref in zip(d, pools):
+            assert (host(got).view(np.uint16) == ref.view(np.uint16)).all()
     finally:
         kvc.kv_cache_destroy(h)
 
