@@ -12,21 +12,27 @@
 // tokens not yet refused (R_k their mass; 1 with replacement), max(0, (p - a q)^+ / S - q / R) is
 // (p - (a + S / R) q)^+ / S, so
 //   a_{k+1} = a_k + S_k / R_k,   S_{k+1} = sum (p - a_{k+1} q)^+,   a_0 = 0, S_0 = R_0 = 1,
-// and a refused token stays at zero: it was refused where p_k(x) <= q_k(x), and a only grows.
+// and a refused token stays at zero: it was refused where p_k(x) <= q_k(x), and a only grows.  (An a above 2^100 counts
+// as 2^100: a q stays finite, and what it leaves of p is a difference only where q is below 2^-100.)
 //
 // Sums.  Which token a draw hits is a comparison of running sums, so they are kept in 64-bit integers, in units of
 // 2^-45.  A weight p - a q is formed in fp32 with every rounding error carried along (a as the sum of two floats, the
-// product's error by fma, the difference's by the two-term difference), and split exactly into a multiple of 2^-23 and a
-// remainder that is rounded to 2^-45, both by adding a constant whose last bit has that value: the sums are integer
+// product's error by fma, the difference's by the two-term difference), and split exactly into a multiple of 2^-23 and
+// a remainder that is rounded to 2^-45, both by adding a constant whose last bit has that value: the sums are integer
 // additions of the results' bits.  (Conversions of floats to 64-bit integers run at the FP64 unit's rate: a pass over
 // 64 x 128,257 entries took 30 us with them.)  Integer sums do not depend on their order, so results repeat bit for bit
-// for every grid.
+// for every grid.  Weights that are not positive are multiplied away by 0 inside the sums' fma instructions: 20
+// instructions for two entries of two rows, four of them the clamps to [0, 1].
 //
-// Layout.  One thread-block cluster per sequence; its CTAs share the vocabulary in slices (a warp a part of a slice)
-// and exchange their sums through distributed shared memory, and all of them follow the same decisions on the same
+// Layout.  One thread-block cluster per sequence; its CTAs share the vocabulary in slices (a warp a part of a slice),
+// every warp sends its sum of a pass to all CTAs of the cluster, and all of them follow the same decisions on the same
 // numbers (the tree's, gathered by rank 0 for all; the sums).
-#include <atomic>
-
+//
+// What bounds it.  A sequence's passes follow one another: each needs the sum of the one before.  64 sequences of
+// 128,257 fp32 entries (16 nodes, three distinct children a node): 2.2 passes on average, 6 at most.  The first passes
+// read 66 MB from memory; of a pass of a cluster alone on its SMs (4.8 us), about 2.5 us are arithmetic and loads from
+// L2, 1.0 the exchange of the sums (the barrier of a cluster takes 0.7), 0.65 the decision.  41 us, where one reading
+// of the two rows of every sequence takes 9.7; one sequence of 32,000 entries (8 nodes, a chain) 7.4 us.
 #include "../../include/kvc.h"
 #include "decode_common.cuh"
 #include "f32x2.cuh"
@@ -63,8 +69,8 @@ __device__ __forceinline__ float prob(float x) { return __saturatef(x); }
 __device__ __forceinline__ float load_prob(const float* row, int i) { return prob(__ldg(row + i)); }
 __device__ __forceinline__ float load_prob(const __half* row, int i) { return prob(__half2float(__ldg(row + i))); }
 
-// (p - a q)^+ <= 1, a = ah + al, as a multiple of 2^-23 (in the bits of the first, above those of 1) and a remainder,
-// at most about 2^-24, in units of 2^-45 (in the bits of the second, above those of kFine)
+// (p - a q)^+ <= 1, a = ah + al >= 0, as a multiple of 2^-23 (in the bits of the first, above those of 1) and a
+// remainder, at most about 2^-24, in units of 2^-45 (in the bits of the second, above those of kFine)
 constexpr float kCoarse = 1.f;            // one ulp is 2^-23 up to 2
 constexpr float kFine = 1.5f * 0x1p-22f;  // one ulp is 2^-45 within 2^-23 on both sides
 struct Split {
@@ -73,37 +79,35 @@ struct Split {
 __device__ __forceinline__ Split split_weight(float p, float q, float ah, float al) {
     const float h = __fmul_rn(ah, q);
     const float e = __fmaf_rn(al, q, __fmaf_rn(ah, q, -h));  // a q = h + e
-    // p - h = r + d exactly
-    float r = __fsub_rn(p, h);
-    const float b = __fsub_rn(r, p);
-    const float d = __fsub_rn(__fsub_rn(p, __fsub_rn(r, b)), __fadd_rn(h, b));
-    float c = __fsub_rn(d, e);
-    // r > e decides the sign: where r and e are of one size, r is exact
-    const bool positive = r > e && h < 2.f;  // (an h of 2 or more, or a product of infinity, leaves nothing: p <= 1)
-    r = positive ? r : 0.f;
-    c = positive ? c : 0.f;
+    // p - h = r + d exactly where r > e: there p >= h, or r itself is exact
+    const float r = __fsub_rn(p, h), d = __fsub_rn(__fsub_rn(p, r), h);
+    const float m = r > e ? 1.f : 0.f;
     Split s;
-    s.coarse = __fadd_rn(r, kCoarse);
-    s.fine = __fadd_rn(__fadd_rn(__fsub_rn(r, __fsub_rn(s.coarse, kCoarse)), c), kFine);
+    s.coarse = __fmaf_rn(r, m, kCoarse);
+    s.fine = __fadd_rn(__fmaf_rn(__fsub_rn(d, e), m, __fmaf_rn(r, m, __fsub_rn(kCoarse, s.coarse))), kFine);
     return s;
 }
-__device__ __forceinline__ int coarse_units(const Split& s) { return __float_as_int(s.coarse) - __float_as_int(kCoarse); }
+__device__ __forceinline__ int coarse_units(const Split& s) {
+    return __float_as_int(s.coarse) - __float_as_int(kCoarse);
+}
 __device__ __forceinline__ int fine_units(const Split& s) { return __float_as_int(s.fine) - __float_as_int(kFine); }
 __device__ __forceinline__ uint64_t units(int64_t coarse, int64_t fine) {
     return static_cast<uint64_t>(coarse * (int64_t(1) << (kUnitBits - 23)) + fine);
 }
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+    const uint32_t m = (1u << 24) - 1;  // 24 bits at a time: their sum over a warp fits 32
+    const uint64_t a = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v) & m);
+    const uint64_t b = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v >> 24) & m);
+    const uint64_t c = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v >> 48));
+    return a + (b << 24) + (c << 48);
 }
 
 __device__ __forceinline__ uint64_t sub_f32x2(uint64_t a, uint64_t b) {
     return fma_f32x2(b, pack_f32x2(-1.f, -1.f), a);  // one rounding of a - b
 }
 // What the entries of a pass are weighed with: nothing (a = 0, the target's row itself), a = 1 (after a node's first
-// refusal, always), any a.  The same numbers come out of each, for less work: of a pair 14, 25 and 29 instructions.
+// refusal, always), any a.  The same numbers come out of each, for less work: of a pair 8, 16 and 20 instructions.
 enum { kPlain = 0, kOne = 1, kAny = 2 };
 struct Factor {
     uint64_t ah, al, neg_ah;  // a = ah + al, twice each
@@ -118,29 +122,29 @@ struct LaneSum {
     uint32_t pairs = 0;
     // the weights of two entries, as split_weight gives them one by one
     __device__ __forceinline__ void add(uint64_t p, uint64_t q, const Factor& f) {
-        uint64_t r = p, c = 0;
-        if constexpr (kMode != kPlain) {
-            const uint64_t nh = kMode == kOne ? q ^ 0x8000000080000000ull : mul_f32x2(f.neg_ah, q);  // -h
-            r = add_f32x2(p, nh);
-            const uint64_t b = sub_f32x2(r, p);
-            c = add_f32x2(sub_f32x2(p, sub_f32x2(r, b)), sub_f32x2(nh, b));
-            float r0, r1, c0, c1, e0 = 0.f, e1 = 0.f, n0 = 0.f, n1 = 0.f;
-            if constexpr (kMode == kAny) {
+        const uint64_t one = pack_f32x2(kCoarse, kCoarse);
+        uint64_t co, rest;
+        if constexpr (kMode == kPlain) {
+            co = add_f32x2(p, one);
+            rest = add_f32x2(p, sub_f32x2(one, co));
+        } else {
+            uint64_t r, c;
+            float e0 = 0.f, e1 = 0.f, r0, r1;
+            if constexpr (kMode == kOne) {
+                r = sub_f32x2(p, q);
+                c = sub_f32x2(sub_f32x2(p, r), q);
+            } else {
+                const uint64_t nh = mul_f32x2(f.neg_ah, q);
                 const uint64_t e = fma_f32x2(f.al, q, fma_f32x2(f.ah, q, nh));
-                c = sub_f32x2(c, e);
+                r = add_f32x2(p, nh);
+                c = sub_f32x2(add_f32x2(sub_f32x2(p, r), nh), e);
                 unpack_f32x2(e, e0, e1);
-                unpack_f32x2(nh, n0, n1);
             }
             unpack_f32x2(r, r0, r1);
-            unpack_f32x2(c, c0, c1);
-            const bool p0 = r0 > e0 && n0 > -2.f, p1 = r1 > e1 && n1 > -2.f;
-            r = pack_f32x2(p0 ? r0 : 0.f, p1 ? r1 : 0.f);
-            c = pack_f32x2(p0 ? c0 : 0.f, p1 ? c1 : 0.f);
+            const uint64_t m = pack_f32x2(r0 > e0 ? 1.f : 0.f, r1 > e1 ? 1.f : 0.f);
+            co = fma_f32x2(r, m, one);
+            rest = fma_f32x2(c, m, fma_f32x2(r, m, sub_f32x2(one, co)));
         }
-        const uint64_t one = pack_f32x2(kCoarse, kCoarse);
-        const uint64_t co = add_f32x2(r, one);
-        uint64_t rest = sub_f32x2(r, sub_f32x2(co, one));
-        if constexpr (kMode != kPlain) rest = add_f32x2(rest, c);
         const uint64_t fi = add_f32x2(rest, pack_f32x2(kFine, kFine));
         coarse += static_cast<uint32_t>(co) + static_cast<uint32_t>(co >> 32);
         fine += static_cast<uint32_t>(fi) + static_cast<uint32_t>(fi >> 32);
@@ -186,7 +190,9 @@ __device__ __forceinline__ void unpack16(const uint4& v, uint64_t (&x)[8 / sizeo
 }
 // this lane's share of the weights of entries [b, e).  Rows of one alignment (a vocabulary of any size, but one stride
 // and 16-byte aligned tensors) are read 16 bytes at a time between their first and last few entries (64 sequences x
-// 128,257 entries: 78 -> 59 us), the next vectors ahead of the current ones' arithmetic (50 -> 48 us).
+// 128,257 entries: 78 -> 59 us), the next vectors ahead of the current ones' arithmetic (50 -> 48 us), the few entries
+// asked for before them (48 -> 47 us).  A ring of asynchronous copies to shared memory in place of the registers is
+// slower, alone on an SM (3.5 -> 4.0 us a pass) and not (43 -> 45 us).
 template <int kMode, typename T>
 __device__ __forceinline__ uint64_t lane_weights(const T* __restrict__ p, const T* __restrict__ q, int b, int e,
                                                  const Factor& f) {
@@ -196,11 +202,16 @@ __device__ __forceinline__ uint64_t lane_weights(const T* __restrict__ p, const 
         return acc.sum;
     }
     constexpr int V = 16 / sizeof(T), U = 2;
-    const int a = min(e, b + static_cast<int>((0 - reinterpret_cast<uintptr_t>(p + b)) & 15u) / static_cast<int>(sizeof(T)));
+    const int skip = static_cast<int>((0 - reinterpret_cast<uintptr_t>(p + b)) & 15u) / static_cast<int>(sizeof(T));
+    const int a = min(e, b + skip);
     const int nv = (e - a) / V, lane = threadIdx.x & 31;
     const uint4* pv = reinterpret_cast<const uint4*>(p + a);
     const uint4* qv = reinterpret_cast<const uint4*>(q + a);
-    add_entries(acc, p, q, b, a, f);
+    // the entries in front of the first vector and behind the last, fewer than V each: one per lane, asked for first
+    const int at = lane < V ? b + lane : a + nv * V + lane - V;
+    const int edge = (lane < V ? at < a : lane < 2 * V && at < e) ? at : -1;
+    const float pe = edge >= 0 ? load_prob(p, edge) : 0.f;
+    const float qe = kMode != kPlain && edge >= 0 ? load_prob(q, edge) : 0.f;
     uint4 x[U], y[U], nx[U], ny[U];  // the vectors at work, and the next ones on their way
     auto fetch = [&](int i0) {
 #pragma unroll
@@ -231,7 +242,8 @@ __device__ __forceinline__ uint64_t lane_weights(const T* __restrict__ p, const 
         }
         acc.flush();
     }
-    add_entries(acc, p, q, a + nv * V, e, f);
+    acc.add(pack_f32x2(pe, 0.f), pack_f32x2(qe, 0.f), f);
+    acc.flush();
     return acc.sum;
 }
 template <typename T>
@@ -291,10 +303,10 @@ template <typename T, int kThreads>
 __global__ void __launch_bounds__(kThreads, 768 / kThreads) draft_tree_verify_kernel(const Params p) {
     constexpr int kWarps = kThreads / 32;
     __shared__ float4 s_tree[kMaxTreeNodes];        // a node's (parent, u, p, q): p and q of its token at its parent
-    __shared__ uint64_t s_tot[2][kMaxClusterV];     // the CTAs' sums of a pass, by pass parity
-    __shared__ uint64_t s_warp[kWarps], s_part[kWarps];
+    __shared__ uint64_t s_tot[2][kMaxClusterV * kWarps];  // the warps' sums of a pass, by pass parity
+    __shared__ uint64_t s_part[kWarps];
     __shared__ float s_a[2];
-    __shared__ int s_cmd, s_node;  // warp 0's decision: 1 = pass over node s_node's rows with a, 0 = draw
+    __shared__ int s_pass, s_node;  // warp 0's decision: a pass over node s_node's rows with a, or the draw
     __shared__ int s_path[kMaxTreeNodes];
     const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = static_cast<int>(blockIdx.x), cs = static_cast<int>(gridDim.x);  // one cluster spans x
@@ -339,29 +351,28 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) draft_tree_verify_ke
     }
     cluster_sync_all();
     const auto parent_of = [&](int t) { return __float_as_int(s_tree[t].x); };
-    if (tid == 0) s_path[0] = 0;
 
     const int v0 = min(rank * p.slice, p.V), v1 = min(v0 + p.slice, p.V);
     const int wsz = ((v1 - v0 + kWarps - 1) / kWarps + 31) / 32 * 32;  // entries per warp
     const int w0 = min(v0 + warp * wsz, v1), w1 = min(w0 + wsz, v1);
 
-    // the walk's state, kept by warp 0
+    // the walk: warp 0 of each CTA takes it, the others have its word
     int cur = 0, len = n_nodes > 0 ? 1 : 0, last = 0;
     const Two zero{0.f, 0.f}, one{1.f, 0.f};
     Two a = zero, S = one, R = one;
-    bool summed = false;  // s_tot holds the sums of (cur, a)
+    bool summed = false;  // s_tot and total hold the sums of (cur, a)
     int parity = 0;
     uint64_t total = 0;
     const bool empty = n_nodes == 0;
     while (!empty) {
         if (warp == 0) {
-            int cmd = -1;
-            while (cmd < 0) {
+            bool pass;
+            for (;;) {
                 // the next child of cur behind `last`
                 const unsigned lo = __ballot_sync(0xffffffffu, lane > last && parent_of(lane) == cur);
                 const unsigned hi = __ballot_sync(0xffffffffu, lane + 32 > last && parent_of(lane + 32) == cur);
                 if ((lo | hi) == 0) {
-                    cmd = summed ? 0 : 1;  // draw, from the sums there are or after a pass
+                    pass = !summed;  // draw, from the sums there are or after a pass
                     break;
                 }
                 const int c = lo ? __ffs(lo) - 1 : 31 + __ffs(hi);
@@ -377,26 +388,30 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) draft_tree_verify_ke
                     a = zero;
                     S = R = one;
                     summed = false;
-                } else {
-                    if (positive(R)) {
-                        const Two next = a + (p.distinct ? S / R : S);
-                        if (next.h != a.h || next.l != a.l) {
-                            a = next;
-                            cmd = 1;
-                        }
+                    continue;
+                }
+                const Two mass = R;
+                if (p.distinct) R = R + Two{-child.w, 0.f};
+                if (positive(mass)) {
+                    Two next = a + (p.distinct ? S / mass : S);
+                    if (!(next.h < 0x1p100f)) next = Two{0x1p100f, 0.f};  // keeps every product finite
+                    if (next.h != a.h || next.l != a.l) {
+                        a = next;
+                        pass = true;
+                        break;
                     }
-                    if (p.distinct) R = R + Two{-child.w, 0.f};
                 }
             }
             if (lane == 0) {
-                s_cmd = cmd;
+                s_pass = pass;
                 s_node = cur;
                 s_a[0] = a.h;
                 s_a[1] = a.l;
             }
         }
         __syncthreads();
-        const int cmd = s_cmd, node = s_node;
+        const bool pass = s_pass;
+        const int node = s_node;
         Factor f;
         f.h = s_a[0];
         f.l = s_a[1];
@@ -406,31 +421,28 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) draft_tree_verify_ke
         f.mode = f.h == 0.f ? kPlain : f.h == 1.f && f.l == 0.f ? kOne : kAny;
         const T* const pr = prow + node * p.p_stride;
         const T* const qr = qrow + node * p.q_stride;
-        if (cmd == 1) {
+        if (pass) {
             const uint64_t ws = warp_sum(lane_weights(pr, qr, w0, w1, f));
-            if (lane == 0) s_warp[warp] = ws;
-            __syncthreads();
-            if (warp == 0) {
-                const uint64_t cta = warp_sum(lane < kWarps ? s_warp[lane] : 0);
-                if (lane < cs) st_cluster_u64(map_to_rank(&s_tot[parity][rank], lane), cta);
-            }
+            if (lane < cs) st_cluster_u64(map_to_rank(&s_tot[parity][rank * kWarps + warp], lane), ws);
             cluster_sync_all();
-            total = 0;
-            for (int r = 0; r < cs; ++r) total += s_tot[parity][r];
+            uint64_t part = 0;
+#pragma unroll
+            for (int i = lane; i < kMaxClusterV * kWarps; i += 32)
+                if (i < cs * kWarps) part += s_tot[parity][i];
+            total = warp_sum(part);
             S = from_units(total);
             summed = true;
             parity ^= 1;
             continue;
         }
         // draw: the first entry whose running weight exceeds u * total
-        const uint64_t* tot = s_tot[parity ^ 1];
         if (total == 0) {
             if (f.mode != kPlain) {  // nothing of the residual is left: the target's own row
                 a = zero;
                 S = one;
                 summed = false;
                 last = kMaxTreeNodes;  // no further child is tried
-                __syncthreads();
+                __syncthreads();       // every warp has read the word that is now replaced
                 continue;
             }
             if (rank == 0 && tid == 0) {
@@ -441,12 +453,25 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) draft_tree_verify_ke
         }
         uint64_t th = scaled(s_tree[0].y, total);
         if (th >= total) th = total - 1;
-        int owner = 0;
-        while (owner < cs - 1 && th >= tot[owner]) th -= tot[owner++];
+        const uint64_t* const sums = s_tot[parity ^ 1];
+        uint64_t tot = 0;  // of the CTA of this lane's number
+        if (lane < cs) {
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) tot += sums[lane * kWarps + (w + lane) % kWarps];
+        }
+        uint64_t incl = tot;
+#pragma unroll
+        for (int o = 1; o < kMaxClusterV; o <<= 1) {
+            const uint64_t below = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += below;
+        }
+        const int owner = __ffs(__ballot_sync(0xffffffffu, incl > th)) - 1;
         if (owner != rank) break;
-        // the CTA's warp whose part holds it (s_warp: this pass's sums), then that part again in kWarps pieces
+        th -= __shfl_sync(0xffffffffu, incl - tot, owner);
+        // the CTA's warp whose part holds it, then that part again in kWarps pieces
+        const uint64_t* const warps = sums + rank * kWarps;
         int sw = 0;
-        while (sw < kWarps - 1 && th >= s_warp[sw]) th -= s_warp[sw++];
+        while (sw < kWarps - 1 && th >= warps[sw]) th -= warps[sw++];
         const int sb = min(v0 + sw * wsz, v1), se = min(sb + wsz, v1);
         const int psz = ((se - sb + kWarps - 1) / kWarps + 31) / 32 * 32;
         const int pb = min(sb + warp * psz, se), pe = min(pb + psz, se);
@@ -456,31 +481,52 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) draft_tree_verify_ke
         int pw = 0;
         while (pw < kWarps - 1 && th >= s_part[pw]) th -= s_part[pw++];
         if (warp != pw) break;
+        constexpr int kRun = 8;  // up to 8 consecutive entries per lane: one prefix sum over the lanes for 256 entries
+        const int run = min((pe - pb + 31) / 32, kRun);
         int found = -1;
-        for (int i0 = pb; i0 < pe && found < 0; i0 += 32) {
-            const int i = i0 + lane;
-            uint64_t incl = 0;
-            if (i < pe) {
-                const Split w = split_weight(load_prob(pr, i), f.mode != kPlain ? load_prob(qr, i) : 0.f, f.h, f.l);
-                incl = units(coarse_units(w), fine_units(w));
+        for (int i0 = pb; i0 < pe && found < 0; i0 += 32 * run) {
+            const int i = i0 + lane * run;
+            uint64_t w[kRun], sum = 0;
+#pragma unroll
+            for (int k = 0; k < kRun; ++k) {
+                w[k] = 0;
+                if (k < run && i + k < pe) {
+                    const float q = f.mode != kPlain ? load_prob(qr, i + k) : 0.f;
+                    const Split s = split_weight(load_prob(pr, i + k), q, f.h, f.l);
+                    w[k] = units(coarse_units(s), fine_units(s));
+                }
+                sum += w[k];
             }
+            uint64_t upto = sum;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const uint64_t below = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += below;
+                const uint64_t below = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += below;
             }
-            const unsigned hit = __ballot_sync(0xffffffffu, incl > th);
-            if (hit != 0)
-                found = i0 + __ffs(hit) - 1;
-            else
-                th -= __shfl_sync(0xffffffffu, incl, 31);
+            const unsigned hit = __ballot_sync(0xffffffffu, upto > th);
+            if (hit != 0) {
+                const int at = __ffs(hit) - 1;
+                uint64_t left = th - (upto - sum);  // in lane `at`
+                int k = 0;
+#pragma unroll
+                for (int j = 0; j < kRun - 1; ++j) {
+                    if (k == j && j < run - 1 && left >= w[j]) {
+                        left -= w[j];
+                        ++k;
+                    }
+                }
+                found = __shfl_sync(0xffffffffu, i + k, at);
+            } else {
+                th -= __shfl_sync(0xffffffffu, upto, 31);
+            }
         }
         if (lane == 0) p.next_token[b] = found;
         break;
     }
     if (rank == 0 && warp == 0) {
         __syncwarp();
-        for (int i = lane; i < p.T; i += 32) p.path[static_cast<int64_t>(b) * p.T + i] = i < len ? s_path[i] : -1;
+        for (int i = lane; i < p.T; i += 32)
+            p.path[static_cast<int64_t>(b) * p.T + i] = i >= len ? -1 : i == 0 ? 0 : s_path[i];
         if (lane == 0) {
             p.path_len[b] = len;
             if (empty) p.next_token[b] = -1;
@@ -518,8 +564,9 @@ cudaError_t launch_tree_verify(const VerifyArgs& a, cudaStream_t stream) {
     p.V = a.V;
     p.distinct = a.distinct;
     // CTAs per sequence: a thread should have two entries before it is worth another CTA's share (clusters of 4, 8 and
-    // 16 for 64 sequences x 128,257 entries: 59, 50 and 54 us).  512 threads a CTA while every CTA has an SM, else 256,
-    // three CTAs per SM (64 sequences: 60 and 48 us).
+    // 16 for 64 sequences x 128,257 entries: 59, 50 and 54 us when this was measured).  512 threads a CTA while every
+    // CTA has an SM (one sequence: 3.2 us a pass, 4.8 with 256), else 256, three CTAs per SM (64 sequences: 60 us with 512
+    // and 48 with 256 when this was measured).
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorNoDevice;
     int cs = 1;
