@@ -46,7 +46,6 @@ constexpr int kLoadKWarp = kRowWarps + 4;
 constexpr int kLoadVWarp = kRowWarps + 5;
 constexpr int kThreads = (kRowWarps + 6) * 32;
 constexpr int kMaxTreeCluster = 8;
-constexpr int kMaxStates = 2 * kMaxTreeCluster;  // states of a row in a cluster
 constexpr uint64_t kWaitNs = 1000000000ull;
 // a scale of 0 is taken as this: the scores of fp16 rows (below 2^40) still vanish next to 1, and a masked score of
 // -inf times it stays -inf
@@ -75,8 +74,8 @@ struct Geom {
     static constexpr int kStateOff = kVOff;
     static constexpr int kMlOff = kStateOff + 2 * kRows * kOStride * 4;
     static constexpr int kWeightOff = kMlOff + 2 * kRows * 8;  // the states' weights of the rows this CTA merges
-    // (rows / CTAs, rounded up, times states: at most 2 * 128 and one more row's)
-    static_assert(kWeightOff + (2 * kRows + kMaxStates) * 8 <= kBarOff, "state area");
+    // (rows / CTAs, rounded up, times CTAs: at most 2 * 128 and one more row's)
+    static_assert(kWeightOff + (2 * kRows + kMaxTreeCluster) * 8 <= kBarOff, "state area");
     // TMEM columns: two buffers of S / P per stream, A [0, 128) and B [128, 256), O_A [256, 256 + D), O_B [256 + D, 256 + 2D)
     static constexpr int kTmemO = 4 * kHalf;
     static constexpr uint32_t kTmemCols = 512;
@@ -630,19 +629,48 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
             ok = __all_sync(0xffffffffu, wait(&o_full[2 * x + ((units - 1) & 1)], ((units - 1) >> 1) & 1, s_abort));
         tc_fence_after();
         row_warps_sync();  // both streams done: the rings are idle, the notes on bad blocks and values complete
-        // the thread's state into the state area: slot x * 128 + row
-        const bool drop = *s_bad_block != 0 || *s_abort != 0 || !ok || units == 0;
-        float2* ml = reinterpret_cast<float2*>(smem + Geo::kMlOff);
+        // the rows' states into the state area: slot x * 128 + row with two row tiles; with one the streams' states of a
+        // row are merged first, each of its two threads for half of the columns
+        const bool drop = *s_bad_block != 0 || *s_abort != 0 || units == 0;  // the same in every thread
+        float2* const ml = reinterpret_cast<float2*>(smem + Geo::kMlOff);
+        float* const states = reinterpret_cast<float*>(smem + Geo::kStateOff);
         ml[x * kRows + row] = drop ? make_float2(-INFINITY, 0.f) : make_float2(m_used, l);
-        if (live_warp && !drop) {
-            float* mine = reinterpret_cast<float*>(smem + Geo::kStateOff) + (x * kRows + row) * Geo::kOStride;
+        if (two_rows) {
+            if (live_warp && !drop) {
+                float* const mine = states + (x * kRows + row) * Geo::kOStride;
 #pragma unroll
-            for (int c = 0; c < D; c += 64) {
-                float o[64];
-                tmem_ld64(tO + c, o);
+                for (int c = 0; c < D; c += 64) {
+                    float o[64];
+                    tmem_ld64(tO + c, o);
 #pragma unroll
-                for (int i = 0; i < 64; i += 4)
-                    *reinterpret_cast<float4*>(mine + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    for (int i = 0; i < 64; i += 4)
+                        *reinterpret_cast<float4*>(mine + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                }
+            }
+        } else {
+            tc_fence_before();
+            row_warps_sync();
+            tc_fence_after();  // the other stream's accumulator
+            const float2 sa = ml[row], sb = ml[kRows + row];
+            const bool ha = sa.y != 0.f, hb = sb.y != 0.f;  // a state with sum 0 holds nothing
+            const float m = fmaxf(ha ? sa.x : -INFINITY, hb ? sb.x : -INFINITY);
+            const float wa = !ha ? 0.f : sa.x == m ? 1.f : ex2(sa.x - m);
+            const float wb = !hb ? 0.f : sb.x == m ? 1.f : ex2(sb.x - m);
+            row_warps_sync();
+            if (x == 0) ml[row] = make_float2(m, (ha ? sa.y * wa : 0.f) + (hb ? sb.y * wb : 0.f));
+            if (live_warp && !drop) {
+                float* const mine = states + row * Geo::kOStride + x * (D / 2);
+#pragma unroll
+                for (int c = 0; c < D / 2; c += 32) {
+                    float oa[32], ob[32];
+                    tmem_ld32(tmem + Geo::kTmemO + lane_base + x * (D / 2) + c, oa);
+                    tmem_ld32(tmem + Geo::kTmemO + D + lane_base + x * (D / 2) + c, ob);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) oa[i] = (ha ? oa[i] * wa : 0.f) + (hb ? ob[i] * wb : 0.f);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<float4*>(mine + c + i) = make_float4(oa[i], oa[i + 1], oa[i + 2], oa[i + 3]);
+                }
             }
         }
     }
@@ -659,7 +687,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
     const int share = (live_rows + p.cluster - 1) / p.cluster;
     const int ra = min(rank * share, live_rows), nr = min(share, live_rows - ra);
     const int ncta = min(p.cluster, (all_tiles - clus * per_clus + p.chunk - 1) / p.chunk);  // CTAs with tiles
-    const int sh = two_rows ? 0 : 1, nst = ncta << sh;  // states of a row: one or two in each CTA
     auto out_row = [&](int rr) {
         const int t = node_of(rr);
         return (static_cast<int64_t>(b) * p.T + t) * p.Hq + hk * p.G + rr - t * p.G;
@@ -676,20 +703,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
     {
         const uint32_t ml0 = smem_u32(smem + Geo::kMlOff), flag0 = smem_u32(const_cast<int*>(s_bad_v));
         int group = 1;
-        while (group < nst) group *= 2;
-        const int s = threadIdx.x & (group - 1), q = s >> sh;
+        while (group < ncta) group *= 2;
+        const int s = threadIdx.x & (group - 1);
         for (int rbase = 0; rbase < nr; rbase += kThreads / group) {  // (group divides 32: whole warps)
             const int r = rbase + threadIdx.x / group;
             float2 st = make_float2(-INFINITY, 0.f);
-            if (r < nr && s < nst) st = ld_cluster_f32x2(cluster_addr(ml0, q) + (ra + r + (s - (q << sh)) * kRows) * 8);
+            if (r < nr && s < ncta) st = ld_cluster_f32x2(cluster_addr(ml0, s) + (ra + r) * 8);
             float m = st.y != 0.f ? st.x : -INFINITY;  // a state with sum 0 holds nothing
             for (int off = group / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
             const float w = st.y == 0.f ? 0.f : st.x == m ? 1.f : ex2(st.x - m);
             float l = st.y != 0.f ? st.y * w : 0.f;
             for (int off = group / 2; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
             const float inv = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
-            if (r < nr && s < nst) {
-                s_w[r * nst + s] = make_float2(w * inv, st.y);
+            if (r < nr && s < ncta) {
+                s_w[r * ncta + s] = make_float2(w * inv, st.y);
                 if (!whole && s == 0)
                     *reinterpret_cast<float2*>(p.part_ml + (out_row(r0 + ra + r) * p.nclus + clus) * 2) = make_float2(m, l);
             }
@@ -708,12 +735,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
             float4 o[U];
 #pragma unroll
             for (int i = 0; i < U; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int s0 = 0; s0 < nst; s0 += S) {
+            for (int s0 = 0; s0 < ncta; s0 += S) {
                 float4 a[U][S];
 #pragma unroll
                 for (int j = 0; j < S; ++j) {
-                    const int s = min(s0 + j, nst - 1), q = s >> sh;
-                    const uint32_t base = cluster_addr(state0, q) + (ra + (s - (q << sh)) * kRows) * (Geo::kOStride * 4);
+                    const uint32_t base = cluster_addr(state0, min(s0 + j, ncta - 1)) + ra * (Geo::kOStride * 4);
 #pragma unroll
                     for (int i = 0; i < U; ++i) {
                         const int e = min(e0 + i * kThreads, nr * kCols - 1);
@@ -725,8 +751,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
                     const int r = min(e0 + i * kThreads, nr * kCols - 1) / kCols;
 #pragma unroll
                     for (int j = 0; j < S; ++j) {
-                        if (s0 + j >= nst) continue;
-                        const float2 w = s_w[r * nst + s0 + j];
+                        if (s0 + j >= ncta) continue;
+                        const float2 w = s_w[r * ncta + s0 + j];
                         if (w.y != 0.f) o[i] = fma4(w.x, a[i][j], o[i]);  // (O of a state that holds nothing: unwritten)
                     }
                 }
@@ -760,9 +786,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
             }
         }
     };
-    if (nst <= 2)
+    if (ncta <= 2)
         merge_rows(std::integral_constant<int, 4>(), std::integral_constant<int, 2>());
-    else if (nst <= 4)
+    else if (ncta <= 4)
         merge_rows(std::integral_constant<int, 2>(), std::integral_constant<int, 4>());
     else
         merge_rows(std::integral_constant<int, 1>(), std::integral_constant<int, 8>());
