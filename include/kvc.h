@@ -503,11 +503,12 @@ kvc_status kv_rope_turns(const double* inv_freq, int n, uint64_t* turns);
  *                multiple of 16 up to D
  *   q_out        device fp16 [n][Hq][D]; may be q itself where q's stride is Hq * D
  *   k_out, v_out device fp16 [n][Hkv][D] or NULL: the rows packed, for
- *                prefill_attention or kv_append_fp8; may be k / v as q_out may be q
+ *                prefill_attention or kv_append_fp8; may be k / v as q_out may
+ *                be q.  An output that overlaps the rows read otherwise is refused
  *   k_cache, v_cache  device fp16 [num_blocks][Hkv][bs][D] (one layer), with
  *                slot_mapping device int64 [n] as in kv_append (negative =
- *                skip, >= num_blocks * bs sets KVC_DEVERR_SLOT); all three NULL:
- *                nothing is appended
+ *                skip, >= num_blocks * bs sets KVC_DEVERR_SLOT; no slot twice);
+ *                all three NULL: nothing is appended
  * Arithmetic in fp32, one rounding to fp16 per value.  Value rows, and rows
  * that are neither normed nor rotated, are copied bit for bit.  16-byte aligned
  * pointers.  One kernel launch. */
@@ -596,7 +597,7 @@ kvc_status draft_tree_verify(const void* target_probs, int64_t p_stride, const v
  *                tree_len; path_len device int32 [B], 0 .. min(P, tree_len)
  *   P            1 .. 64 (a tree of up to 64 nodes may be given a narrower path
  *                with tree_lens)
- *   new_context_lens  device int32 [B], not context_lens itself
+ *   new_context_lens  device int32 [B], apart from all that the call reads
  * A sequence whose lengths (KVC_DEVERR_CONTEXT), path (KVC_DEVERR_TREE) or
  * blocks (KVC_DEVERR_BLOCK_ID) do not fit is flagged and left as it was, with
  * new_context_lens[b] = context_lens[b].  One kernel launch. */

@@ -769,6 +769,12 @@ kvc_status paged_decode_multi_attention(const void* q, const void* k_cache, cons
 }
 
 // ---- tree-drafted decoding ----------------------------------------------------
+// whether `bytes_a` bytes from a and `bytes_b` from b share any
+static bool overlap(const void* a, int64_t bytes_a, const void* b, int64_t bytes_b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + static_cast<uintptr_t>(bytes_b) && y < x + static_cast<uintptr_t>(bytes_a);
+}
+
 kvc_status kv_tree_masks(const int32_t* parents, const int32_t* tree_lens, int B, int T, uint64_t* masks,
                          int32_t* depths) {
     if (B < 0 || T < 1) return fail(KVC_ERR_INVALID, "bad sizes");
@@ -837,6 +843,19 @@ kvc_status kv_append_rope(const void* q, int64_t q_stride, const void* k, int64_
         return fail(KVC_ERR_INVALID, "token strides must be multiples of 8 elements and hold a token's heads");
     if ((q_out == q && q_stride != qrow) || (k_out == k && k_stride != krow) || (v_out == v && v_stride != krow))
         return fail(KVC_ERR_INVALID, "in place only where the rows are packed");
+    {
+        const struct {
+            const void* ptr;
+            int64_t bytes;
+        } in[3] = {{q, ((n - 1) * q_stride + qrow) * 2},
+                   {k, ((n - 1) * k_stride + krow) * 2},
+                   {v, ((n - 1) * v_stride + krow) * 2}},
+          out[3] = {{q_out, n * qrow * 2}, {k_out, n * krow * 2}, {v_out, n * krow * 2}};
+        for (int o = 0; o < 3; ++o)
+            for (int i = 0; i < 3; ++i)
+                if ((i != o || out[o].ptr != in[i].ptr) && overlap(out[o].ptr, out[o].bytes, in[i].ptr, in[i].bytes))
+                    return fail(KVC_ERR_INVALID, "an output overlaps the rows that are read");
+    }
     if (cache) {
         kvc_status st = checked([&]() -> kvc_status {
             std::vector<int64_t> sl;
@@ -1043,7 +1062,11 @@ kvc_status kv_tree_commit(kvc_handle h, const int32_t* block_table, int max_bloc
     if (B > 65535) return fail(KVC_ERR_UNSUPPORTED, "B must be <= 65535");
     if (B == 0) return KVC_OK;
     if (!block_table || !context_lens || !path || !path_len || !new_context_lens) return fail(KVC_ERR_INVALID, "null pointer");
-    if (new_context_lens == context_lens) return fail(KVC_ERR_INVALID, "new_context_lens must not be context_lens");
+    const int64_t per = static_cast<int64_t>(B) * 4;
+    if (overlap(new_context_lens, per, context_lens, per) || overlap(new_context_lens, per, tree_lens, per) ||
+        overlap(new_context_lens, per, path_len, per) || overlap(new_context_lens, per, path, per * P) ||
+        overlap(new_context_lens, per, block_table, per * max_blocks))
+        return fail(KVC_ERR_INVALID, "new_context_lens overlaps what the call reads");
     kvc_status s = checked([&]() -> kvc_status {
         std::vector<int32_t> ctx, tree, nodes, len, table;
         kvc_status e = copy_to_host(ctx, context_lens, static_cast<size_t>(B), as_stream(stream));

@@ -17,6 +17,10 @@
 // lane (chunks l and l + rot_dim / 16, or 2 l and 2 l + 1): no exchange between lanes but the sum of squares.  A warp
 // takes kRows = 512 / D rows at a time and keeps one token's cosines and sines in registers for all its heads; they
 // are computed once per warp (rot_dim / 2 angles over 32 lanes) and handed out through shared memory.
+//
+// What bounds it.  Long prompts: memory, rows read and written once (16,384 tokens, 32 / 8 heads, D = 128: 67.8 us, 88
+// % of a copy's rate).  Fewer rows: the launch, two dependent loads (position and slot, then rows), the angles
+// and the store (512 tokens of the same 5.7 us, 1923 tokens, 14 / 2 heads, D = 64 4.5 us, one token 3.1 us).
 #include <type_traits>
 
 #include "../../include/kvc.h"

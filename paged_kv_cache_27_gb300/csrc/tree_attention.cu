@@ -9,19 +9,34 @@
 //
 // Layout.  The tree_len * G query rows of a (sequence, KV head), G = Hq / Hkv, are the M = 128 side of both products
 // in tiles of 128 rows (row = node * G + head of the group; a TMEM lane and a softmax thread each), the keys the other
-// side in tiles of 128 (8 cache blocks).  A CTA works on two streams A and B of (row tile, key tile) pairs, each with
-// four row warps, its scores / weights and its output accumulator in TMEM:
+// side in tiles of 128 (8 cache blocks), worked on in halves of 64.  A CTA works on two streams A and B, each with four
+// row warps, two buffers of scores / weights and an output accumulator in TMEM:
 //   two row tiles     the streams are the row tiles and share every K/V tile (the tile is read once for 256 rows);
-//   one row tile      the streams are the even and the odd key tiles of the same rows, merged at the end, so that one
-//                     stream's softmax runs while the tensor cores work for the other.
-// Per stream X and tile:  S_X = Q_X K^T (both K-major in shared memory, 128-byte swizzle, as TMA writes the blocks);
-// the row warps take S_X from TMEM, keep the running max lazily (it moves when it has grown by 2^8; O_X is then
-// rescaled in TMEM) and write P_X over S_X in fp16;  O_X += P_X V with P_X from TMEM and V MN-major.
+//   one row tile      the streams are the two halves of every key tile for the same rows, merged at the end.
+// Per stream X and step of 64 keys:  S_X = Q_X K^T (both K-major in shared memory, 128-byte swizzle, as TMA writes the
+// blocks); the row warps take S_X from TMEM, keep the running max lazily (it moves when it has grown by 2^8; O_X is
+// then rescaled in TMEM) and write P_X over S_X in fp16;  O_X += P_X V with P_X from TMEM and V MN-major.  Two buffers
+// let S of the next step run under this step's softmax; steps of 64 keys instead of 128 make room for both.
+// Warps.  Eight row warps; one product warp per stream and product (S_A, S_B, PV_A, PV_B: a wait costs a warp about 200
+// clocks and a product 40 to 90, so that one warp for all of them was the bound); a copy warp each for K and V.  The
+// two buffers and the four product warps together took 8 x 4096 keys, 64 nodes, 32 / 8 heads, D = 128 from 57 to 37 us.
+// Sixteen row warps, two to a row, are slower (40.2 against 38.3 us), and so is one row tile per CTA (42 us).
 // P.  With an fp16 output the weights are one fp16 value and the row sums add the rounded weights, so a row is a
 // convex combination of V rows with weights within 2^-11 relative, which is the output's own rounding; with an fp32
 // output they are an fp16 high part plus residual (two products), ~22 bits.
-// The context is cut into chunks where (sequence, KV head, row tile pair) units are fewer than SMs; a chunk's state
-// (max, sum, O) goes through the workspace to the combine kernel below.
+// Split.  The context is cut into chunks where (sequence, KV head, row tile pair) units are fewer than SMs.  Up to
+// eight CTAs of a unit are a cluster: each leaves its states (max, sum, O) in its shared memory and merges a share of
+// the rows from all of them.  Longer splits are clusters of four whose states go through the workspace to the combine
+// kernel below.  A merge reads about 15 bytes per clock and SM from the other CTAs, whatever the instruction (loads,
+// stores, asynchronous stores and bulk copies: 4.3 to 4.9 K clocks for 64 KB): half of the 9 K clocks between the last
+// product of a CTA with two row tiles and its end.  Through global memory instead that step took 47.6 us.
+// What bounds it (us; bytes and products at the card's measured rates in parentheses):
+//   4 x 65,536 keys, 16 nodes, 32 / 8 heads, D = 128    156   (158)  memory
+//   8 x 4096 keys, 64 nodes, 32 / 8 heads, D = 128      37.5   (21)  3.0 K clocks per key tile for two row tiles, of
+//                                                       which the products alone take 2.05 K, and the merge
+//   32 x <= 2048 keys, 16 nodes, 14 / 2 heads, D = 64   15.3  (4.6)  start (2.2), 1.5 K clocks per key tile (memory,
+//                                                       on 128 of the SMs), end (3.5: last product, barriers, merge)
+//   1 x 2048 keys, 8 nodes, 14 / 2 heads, D = 64         8.3  (0.2)  start, two key tiles, end
 // Every wait is bounded.
 #include <algorithm>
 #include <type_traits>
@@ -76,7 +91,7 @@ struct Geom {
     static constexpr int kWeightOff = kMlOff + 2 * kRows * 8;  // the states' weights of the rows this CTA merges
     // (rows / CTAs, rounded up, times CTAs: at most 2 * 128 and one more row's)
     static_assert(kWeightOff + (2 * kRows + kMaxTreeCluster) * 8 <= kBarOff, "state area");
-    // TMEM columns: two buffers of S / P per stream, A [0, 128) and B [128, 256), O_A [256, 256 + D), O_B [256 + D, 256 + 2D)
+    // TMEM columns: two buffers of S / P per stream, A [0, 128) and B [128, 256), then O_A and O_B, D columns each
     static constexpr int kTmemO = 4 * kHalf;
     static constexpr uint32_t kTmemCols = 512;
 };
@@ -629,8 +644,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
             ok = __all_sync(0xffffffffu, wait(&o_full[2 * x + ((units - 1) & 1)], ((units - 1) >> 1) & 1, s_abort));
         tc_fence_after();
         row_warps_sync();  // both streams done: the rings are idle, the notes on bad blocks and values complete
-        // the rows' states into the state area: slot x * 128 + row with two row tiles; with one the streams' states of a
-        // row are merged first, each of its two threads for half of the columns
+        // the rows' states into the state area: slot x * 128 + row with two row tiles; with one the streams' states of
+        // a row are merged first, each of its two threads for half of the columns
         const bool drop = *s_bad_block != 0 || *s_abort != 0 || units == 0;  // the same in every thread
         float2* const ml = reinterpret_cast<float2*>(smem + Geo::kMlOff);
         float* const states = reinterpret_cast<float*>(smem + Geo::kStateOff);
@@ -834,18 +849,25 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
 
 }  // namespace tree
 
-constexpr int kTreeSplitCluster = 4;  // CTAs per cluster where a context needs several clusters
-constexpr int kTreeCtaCost = 8;       // in half key tiles
+// CTAs per cluster where a context needs several clusters (2 x 16,384 keys, 64 nodes, 16 / 2 heads, clusters of 2, 4
+// and 8: 31.7, 30.0 and 37.1 us; 4 x 65,536, 16 nodes, 32 / 8: 174, 154 and 154)
+constexpr int kTreeSplitCluster = 4;
+// A CTA's start and end, and the combine launch, in half key tiles.  Costs of 5 to 11 and 4 to 10 choose splits within
+// 5 % of each other over ten shapes (1 to 128 sequences, 512 to 65,536 keys).
+constexpr int kTreeCtaCost = 8;
 constexpr int kTreeCombineCost = 6;
 
 template <int D, bool kSplitP>
 static cudaError_t tree_setup() {
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    std::call_once(once, [] {
-        err = cudaFuncSetAttribute(tree::paged_decode_tree_kernel<D, kSplitP>,
-                                   cudaFuncAttributeMaxDynamicSharedMemorySize, tree::Geom<D>::kSmemBytes);
-    });
+    static std::atomic<bool> done[128];  // by device
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const bool kept = dev >= 0 && dev < 128;
+    if (kept && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    err = cudaFuncSetAttribute(tree::paged_decode_tree_kernel<D, kSplitP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               tree::Geom<D>::kSmemBytes);
+    if (err == cudaSuccess && kept) done[dev].store(true, std::memory_order_relaxed);
     return err;
 }
 

@@ -147,6 +147,19 @@ def test_append_rope_refusals():
     assert kvc._lib.kv_append_rope(*{**base, "n": 0}.values()) == 0
 
 
+def test_append_rope_refuses_outputs_that_overlap_its_rows():
+    at = ctypes.c_void_p
+    # two tokens of 4 + 2 + 2 heads of 64 in one projection: rows of 512 values (1024 bytes)
+    base = dict(q=at(4096), qs=512, k=at(4096 + 512), ks=512, v=at(4096 + 768), vs=512, n=2, Hq=4, Hkv=2, D=64, qw=None,
+                kw=None, eps=1e-6, turns=P, rot=64, inter=0, pos=P, qo=at(8192), ko=None, vo=None, kc=None, vc=None, NB=4,
+                bs=16, slots=None, st=None)
+    for change in (dict(qo=at(4096 + 512)), dict(qo=at(4096 - 1008)), dict(qo=at(4096 + 2032)), dict(ko=at(4096)),
+                   dict(ko=at(4096 + 768)), dict(vo=at(4096 + 512)),
+                   # packed rows: in place of one's own rows only, and not shifted
+                   dict(ks=128, k=at(65536), ko=at(65536 + 16)), dict(ks=128, k=at(65536), vo=at(65536))):
+        refused("kv_append_rope", list({**base, **change}.values()), "INVALID", "overlaps")
+
+
 def test_tree_attention_refusals():
     base = dict(q=P, k=P, v=P, NB=64, table=P, mb=8, ctx=P, masks=P, lens=None, T=4, B=2, Hq=4, Hkv=2, D=64, bs=16,
                 most=128, scale=0.125, out=P, od=0, ws=None, wb=0, st=None)
@@ -172,6 +185,20 @@ def test_verify_refusals():
                            (dict(V=2 ** 25, ps=2 ** 25, qs=2 ** 25), "UNSUPPORTED")):
         refused("draft_tree_verify", list({**base, **change}.values()), status)
     assert kvc._lib.draft_tree_verify(*{**base, "B": 0}.values()) == 0
+
+
+def test_commit_refuses_new_lengths_among_its_inputs():
+    hp = ctypes.c_void_p()
+    cfg = kvc.KvcConfig(1, 4, 2, 64)._c()
+    assert kvc._lib.kv_cache_create(ctypes.byref(cfg), P, P, ctypes.byref(hp)) == 0  # never followed below
+    at = ctypes.c_void_p
+    base = dict(h=hp, table=at(4096), mb=4, ctx=at(8192), lens=at(12288), path=at(16384), plen=at(20480), P=4, B=3,
+                new=at(24576), st=None)
+    try:
+        for new in (4096, 4096 + 44, 8192, 8192 + 8, 8192 - 8, 12288, 16384 + 44, 20480, 20480 - 8):
+            refused("kv_tree_commit", list({**base, "new": at(new)}.values()), "INVALID", "overlaps")
+    finally:
+        kvc.kv_cache_destroy(hp)
 
 
 def test_commit_refusals():
