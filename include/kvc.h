@@ -559,8 +559,9 @@ kvc_status paged_decode_tree_attention(const void* q, const void* k_cache, const
  * goes on from it; else p_{k+1} = max(0, p_k - q_k) divided by its sum.
  * distinct 0: children were drawn independently, q_k = q.  distinct 1: they
  * were drawn without replacement, q_{k+1} = q_k without x_k, divided by
- * 1 - q_k(x_k) (a child tried after the draft's mass is spent is refused).  Where no
- * child is kept, the next token is drawn from the last p_k: the smallest index
+ * 1 - q_k(x_k) (a child tried after the draft's mass is spent is refused; a
+ * token tried again at its node is, too, and q_k holds nothing of it any more).
+ * Where no child is kept, the next token is drawn from the last p_k: the smallest index
  * whose running sum exceeds u_0 times the sum (from p itself if nothing of the
  * residual is left).  The kept tokens and the next one are distributed as the
  * target's own samples.

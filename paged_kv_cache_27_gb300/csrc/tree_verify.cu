@@ -302,7 +302,7 @@ __device__ __forceinline__ uint64_t scaled(float u, uint64_t n) {
 template <typename T, int kThreads>
 __global__ void __launch_bounds__(kThreads, 768 / kThreads) draft_tree_verify_kernel(const Params p) {
     constexpr int kWarps = kThreads / 32;
-    __shared__ float4 s_tree[kMaxTreeNodes];        // a node's (parent, u, p, q): p and q of its token at its parent
+    __shared__ float4 s_tree[kMaxTreeNodes];        // a node's (key, u, p, q): p and q of its token at its parent
     __shared__ uint64_t s_tot[2][kMaxClusterV * kWarps];  // the warps' sums of a pass, by pass parity
     __shared__ uint64_t s_part[kWarps];
     __shared__ float s_a[2];
@@ -316,7 +316,8 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) draft_tree_verify_ke
     const T* const qrow = static_cast<const T*>(p.q) + static_cast<int64_t>(b) * p.T * p.q_stride;
     // rank 0 gathers the tree for the whole cluster (decisions must not differ between its CTAs), a thread a node and
     // one or more CTAs to tell
-    float4 mine = make_float4(__int_as_float(-2), 0.f, 0.f, 0.f);  // a node that no walk reaches
+    // key: parent << 24 | token, which is below 2^24; negative: a node that no walk reaches
+    float4 mine = make_float4(__int_as_float(-1), 0.f, 0.f, 0.f);
     if (rank == 0) {
         const int t = tid & (kMaxTreeNodes - 1);
         const bool in = t < p.T;
@@ -329,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) draft_tree_verify_ke
                 if (par < 0 || par >= t || tok < 0 || tok >= p.V) {
                     if (tid == t) atomicOr(p.err, KVC_DEVERR_TREE);
                 } else {
-                    mine.x = __int_as_float(par);
+                    mine.x = __int_as_float(par << 24 | tok);
                     mine.z = load_prob(prow + par * p.p_stride, tok);
                     mine.w = load_prob(qrow + par * p.q_stride, tok);
                 }
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) draft_tree_verify_ke
         }
     }
     cluster_sync_all();
-    const auto parent_of = [&](int t) { return __float_as_int(s_tree[t].x); };
+    const auto key_of = [&](int t) { return __float_as_int(s_tree[t].x); };
 
     const int v0 = min(rank * p.slice, p.V), v1 = min(v0 + p.slice, p.V);
     const int wsz = ((v1 - v0 + kWarps - 1) / kWarps + 31) / 32 * 32;  // entries per warp
@@ -369,8 +370,9 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) draft_tree_verify_ke
             bool pass;
             for (;;) {
                 // the next child of cur behind `last`
-                const unsigned lo = __ballot_sync(0xffffffffu, lane > last && parent_of(lane) == cur);
-                const unsigned hi = __ballot_sync(0xffffffffu, lane + 32 > last && parent_of(lane + 32) == cur);
+                const int key0 = key_of(lane), key1 = key_of(lane + 32);
+                const unsigned lo = __ballot_sync(0xffffffffu, lane > last && key0 >> 24 == cur);
+                const unsigned hi = __ballot_sync(0xffffffffu, lane + 32 > last && key1 >> 24 == cur);
                 if ((lo | hi) == 0) {
                     pass = !summed;  // draw, from the sums there are or after a pass
                     break;
@@ -391,7 +393,12 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) draft_tree_verify_ke
                     continue;
                 }
                 const Two mass = R;
-                if (p.distinct) R = R + Two{-child.w, 0.f};
+                if (p.distinct) {
+                    // its mass leaves the draft's row, unless an earlier child had its token
+                    const int key = __float_as_int(child.x);
+                    if (!__any_sync(0xffffffffu, (lane < c && key0 == key) || (lane + 32 < c && key1 == key)))
+                        R = R + Two{-child.w, 0.f};
+                }
                 if (positive(mass)) {
                     Two next = a + (p.distinct ? S / mass : S);
                     if (!(next.h < 0x1p100f)) next = Two{0x1p100f, 0.f};  // keeps every product finite

@@ -472,6 +472,19 @@ def test_verify_many_refusals_at_one_node(kvc, distinct):
     check_verify(got, p, q, tok, par, u, distinct=distinct)
 
 
+@pytest.mark.parametrize("T,V,parents", [(20, 97, "root"), (64, 40, "root"), (64, 33, "random"), (33, 5, "random")])
+def test_verify_distinct_children_with_a_token_twice(kvc, T, V, parents):
+    """A token that was refused at a node has no mass in the draft's row there any more: trying it again refuses it
+    and takes no further mass."""
+    par = [0] * T if parents == "root" else None
+    p, q, tok, par, u = verify_case(61 + T + V, 32, T, V, 2.0, parents=par)  # drawn with replacement: tokens repeat
+    u[:, 1:] = 1 - u[:, 1:] * 0.05
+    u = np.minimum(u, np.float32(1 - 2.0 ** -24))
+    assert any(len(set(tok[b, 1:][par[b, 1:] == 0])) < (par[b, 1:] == 0).sum() for b in range(32))
+    got = run_verify(kvc, p, q, tok, par, u, distinct=True)
+    check_verify(got, p, q, tok, par, u, distinct=True)
+
+
 def test_verify_ragged_trees_and_strided_rows(kvc):
     B, T, V = 9, 10, 700
     p, q, tok, par, u = verify_case(61, B, T, V)
