@@ -606,6 +606,18 @@ kvc_status kv_tree_commit(kvc_handle h, const int32_t* block_table, int max_bloc
                           const int32_t* tree_lens, const int32_t* path, const int32_t* path_len, int P, int B,
                           int32_t* new_context_lens, void* stream);
 
+/* The launching calls of this section with their arguments as an array of
+ * 64-bit words, for bindings that pay per argument (a call from Python's
+ * ctypes: 2.1 us for kv_append_rope's 26 arguments, 0.6 us this way).  words:
+ * the named call's `count` arguments in order without the stream, pointers and
+ * integers as integers, a float as a double.  KVC_ERR_INVALID for an unknown
+ * call, another count or an integer that does not fit its argument. */
+#define KVC_CALL_APPEND_ROPE 1
+#define KVC_CALL_TREE_ATTENTION 2
+#define KVC_CALL_TREE_VERIFY 3
+#define KVC_CALL_TREE_COMMIT 4
+kvc_status kvc_call(int which, const void* words, int count, void* stream);
+
 /* Varlen packed prefill (xformers article parts 4-5): for every segment s
  * (rows cu_seqlens[s] .. cu_seqlens[s+1]-1) and query head h,
  *   out = softmax(Q K^T * scale + mask) V,

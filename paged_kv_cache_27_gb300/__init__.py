@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -138,6 +139,7 @@ def _load():
                                             SZ, P]),
         "draft_tree_verify": (I, [P, I64, P, I64, I, P, P, P, P, I, I, I, I, P, P, P, P]),
         "kv_tree_commit": (I, [P, P, I, P, P, P, P, I, I, P, P]),
+        "kvc_call": (I, [I, ctypes.c_char_p, I, P]),
         "prefill_attention": (I, [P, P, P, P, I, I, I, I, I, I, ctypes.c_float, I, P, I, P]),
         "prefill_attention_ex": (I, [P, P, P, P, I, I, I, I, I, I, ctypes.c_float, I, I, P, I, P]),
     }
@@ -766,17 +768,35 @@ def _ready(dev: int, dtype, *tensors) -> bool:
     return True
 
 
-def _run(fn, args, name, stream, prepare, dev, keep):
-    """Launch fn(*args, stream) on `stream` or the current one of device dev, or return it as a PreparedCall."""
+class _Words:
+    """A launching call of kvc_call: its number and its arguments' places in the array of words."""
+    __slots__ = ("which", "count", "pack", "name")
+
+    def __init__(self, which: int, name: str):
+        types = getattr(_lib, name).argtypes[:-1]  # without the stream
+        self.which, self.count, self.name = which, len(types), name
+        self.pack = struct.Struct("=" + "".join("d" if t is ctypes.c_float else "q" for t in types)).pack
+
+
+_APPEND_ROPE, _TREE_ATTENTION, _TREE_VERIFY, _TREE_COMMIT = (
+    _Words(i + 1, name) for i, name in enumerate(("kv_append_rope", "paged_decode_tree_attention", "draft_tree_verify",
+                                                  "kv_tree_commit")))
+_call = _lib.kvc_call
+
+
+def _run(call: _Words, args, stream, prepare, dev, keep):
+    """Launch the call with args (0 for a null pointer) on `stream` or the current one of device dev, or return it as a
+    PreparedCall.  The arguments go as one array: ctypes takes ~60 ns for each of up to 26."""
+    words = call.pack(*args)
     if prepare:
-        return PreparedCall(fn, args, name, dev, keep)
+        return PreparedCall(_call, (call.which, words, call.count), call.name, dev, keep)
     if stream is None and _raw_stream is not None:
         st = _raw_stream(dev)
     else:
         st = _stream(stream, keep[0])
-    status = fn(*args, st)
+    status = _call(call.which, words, call.count, st)
     if status:
-        _check(status, name)
+        _check(status, call.name)
     return None
 
 
@@ -854,13 +874,13 @@ def kv_append_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions:
     if n == 1:  # a single token's stride means nothing
         qst, kst, vst = (Hq * D,), (Hkv * D,), (Hkv * D,)
     args = (q.data_ptr(), qst[0], k.data_ptr(), kst[0], v.data_ptr(), vst[0], n, Hq, Hkv, D,
-            None if q_weight is None else q_weight.data_ptr(),
-            None if k_weight is None else k_weight.data_ptr(), float(eps), None if turns is None else turns.data_ptr(), rot,
-            1 if interleaved else 0, None if positions is None else positions.data_ptr(), q_out.data_ptr(),
-            None if k_out is None else k_out.data_ptr(), None if v_out is None else v_out.data_ptr(),
-            None if k_cache is None else k_cache.data_ptr(), None if v_cache is None else v_cache.data_ptr(), NB, bs,
-            None if slot_mapping is None else slot_mapping.data_ptr())
-    return _run(_lib.kv_append_rope, args, "kv_append_rope", stream, prepare, dev, keep)
+            0 if q_weight is None else q_weight.data_ptr(),
+            0 if k_weight is None else k_weight.data_ptr(), float(eps), 0 if turns is None else turns.data_ptr(), rot,
+            1 if interleaved else 0, 0 if positions is None else positions.data_ptr(), q_out.data_ptr(),
+            0 if k_out is None else k_out.data_ptr(), 0 if v_out is None else v_out.data_ptr(),
+            0 if k_cache is None else k_cache.data_ptr(), 0 if v_cache is None else v_cache.data_ptr(), NB, bs,
+            0 if slot_mapping is None else slot_mapping.data_ptr())
+    return _run(_APPEND_ROPE, args, stream, prepare, dev, keep)
 
 
 def paged_decode_tree_plan(B: int, Hq: int, Hkv: int, head_dim: int, max_context_len: int, T: int,
@@ -911,11 +931,11 @@ def paged_decode_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
                           (workspace, None, "workspace")):
             _dptr(t, dt, nm)
     args = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), NB, block_table.data_ptr(), block_table.shape[1],
-            context_lens.data_ptr(), masks.data_ptr(), None if tree_lens is None else tree_lens.data_ptr(), T, B, Hq,
+            context_lens.data_ptr(), masks.data_ptr(), 0 if tree_lens is None else tree_lens.data_ptr(), T, B, Hq,
             Hkv, D, bs, int(max_context_len), float(scale), out.data_ptr(), od,
-            None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.data_ptr(),
             0 if workspace is None else workspace.numel() * workspace.element_size())
-    return _run(_lib.paged_decode_tree_attention, args, "paged_decode_tree_attention", stream, prepare, dev, keep)
+    return _run(_TREE_ATTENTION, args, stream, prepare, dev, keep)
 
 
 def _prob_rows(t: torch.Tensor, name: str):
@@ -970,9 +990,9 @@ def draft_tree_verify(target_probs: torch.Tensor, draft_probs: torch.Tensor, tok
             _dptr(t, _I32, nm)
         _dptr(uniforms, _F32, "uniforms")
     args = (pp, ps, qp, qs, KVC_F32 if pdt is _F32 else KVC_F16, tokens.data_ptr(), parents.data_ptr(),
-            None if tree_lens is None else tree_lens.data_ptr(), uniforms.data_ptr(), B, T, V, 1 if distinct else 0,
+            0 if tree_lens is None else tree_lens.data_ptr(), uniforms.data_ptr(), B, T, V, 1 if distinct else 0,
             path.data_ptr(), path_len.data_ptr(), next_token.data_ptr())
-    return _run(_lib.draft_tree_verify, args, "draft_tree_verify", stream, prepare, dev, keep)
+    return _run(_TREE_VERIFY, args, stream, prepare, dev, keep)
 
 
 def kv_tree_commit(h: int, block_table: torch.Tensor, context_lens: torch.Tensor, path: torch.Tensor,
@@ -1001,6 +1021,6 @@ def kv_tree_commit(h: int, block_table: torch.Tensor, context_lens: torch.Tensor
                       (tree_lens, "tree_lens"), (path_len, "path_len"), (new_context_lens, "new_context_lens")):
             _dptr(t, _I32, nm)
     args = (h, block_table.data_ptr(), max_blocks, context_lens.data_ptr(),
-            None if tree_lens is None else tree_lens.data_ptr(), path.data_ptr(), path_len.data_ptr(), P, B,
+            0 if tree_lens is None else tree_lens.data_ptr(), path.data_ptr(), path_len.data_ptr(), P, B,
             new_context_lens.data_ptr())
-    return _run(_lib.kv_tree_commit, args, "kv_tree_commit", stream, prepare, dev, keep)
+    return _run(_TREE_COMMIT, args, stream, prepare, dev, keep)

@@ -9,7 +9,10 @@
 #include <cstring>
 #include <new>
 #include <string>
+#include <tuple>
+#include <type_traits>
 #include <unordered_map>
+#include <utility>
 #include <vector>
 
 #include "../../include/kvc.h"
@@ -81,6 +84,38 @@ kvc_status checked(F&& check) {
     } catch (...) {
         return KVC_ERR_OOM;
     }
+}
+
+// Arguments from 64-bit words (kvc_call): integers and pointers as they are, a float from a double.
+template <typename T>
+bool from_word(const unsigned char* at, T* out) {
+    if constexpr (std::is_same_v<T, float>) {
+        double d;
+        std::memcpy(&d, at, 8);
+        *out = static_cast<float>(d);
+    } else if constexpr (sizeof(T) == 8) {
+        std::memcpy(out, at, 8);
+    } else {
+        int64_t i;
+        std::memcpy(&i, at, 8);
+        *out = static_cast<T>(i);
+        if (static_cast<int64_t>(*out) != i) return false;
+    }
+    return true;
+}
+template <typename... A, size_t... I>
+kvc_status call_with_words(kvc_status (*fn)(A...), const void* words, int count, void* stream, std::index_sequence<I...>) {
+    constexpr int kCount = sizeof...(I);
+    if (count != kCount) return fail(KVC_ERR_INVALID, "the call has %d arguments, not %d", kCount, count);
+    std::tuple<A...> args;
+    const unsigned char* const w = static_cast<const unsigned char*>(words);
+    if (!(from_word(w + 8 * I, &std::get<I>(args)) && ...)) return fail(KVC_ERR_INVALID, "an argument beyond its type");
+    std::get<kCount>(args) = stream;
+    return std::apply(fn, args);
+}
+template <typename... A>
+kvc_status call_with_words(kvc_status (*fn)(A...), const void* words, int count, void* stream) {
+    return call_with_words(fn, words, count, stream, std::make_index_sequence<sizeof...(A) - 1>());
 }
 
 }  // namespace
@@ -1121,6 +1156,17 @@ kvc_status kv_tree_commit(kvc_handle h, const int32_t* block_table, int max_bloc
     e = kvc::launch_tree_commit(a, as_stream(stream));
     if (e != cudaSuccess) return cuda_fail(e, "kv_tree_commit launch");
     return KVC_OK;
+}
+
+kvc_status kvc_call(int which, const void* words, int count, void* stream) {
+    if (!words) return fail(KVC_ERR_INVALID, "null pointer");
+    switch (which) {
+        case KVC_CALL_APPEND_ROPE: return call_with_words(kv_append_rope, words, count, stream);
+        case KVC_CALL_TREE_ATTENTION: return call_with_words(paged_decode_tree_attention, words, count, stream);
+        case KVC_CALL_TREE_VERIFY: return call_with_words(draft_tree_verify, words, count, stream);
+        case KVC_CALL_TREE_COMMIT: return call_with_words(kv_tree_commit, words, count, stream);
+        default: return fail(KVC_ERR_INVALID, "unknown call %d", which);
+    }
 }
 
 kvc_status prefill_attention_ex(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int nseq,

@@ -1,6 +1,7 @@
 """Pins of the fp64 definitions of tree-drafted decoding (oracle/tree.py), and the library's host helpers (no GPU)."""
 import ctypes
 import math
+import struct
 
 import numpy as np
 import pytest
@@ -221,3 +222,28 @@ def test_commit_refusals():
         assert kvc._lib.kv_tree_commit(*{**base, "B": 0}.values()) == 0
     finally:
         kvc.kv_cache_destroy(hp)
+
+
+# ---------------------------------------------------------------- the calls with their arguments as words
+def test_calls_with_words_are_the_calls():
+    words = lambda *a: struct.pack("=%dq" % len(a), *a)  # noqa: E731
+    call = kvc._lib.kvc_call
+    names = ("kv_append_rope", "paged_decode_tree_attention", "draft_tree_verify", "kv_tree_commit")
+    for i, name in enumerate(names):
+        n = len(getattr(kvc._lib, name).argtypes) - 1
+        for which, w, count, text in ((i + 1, words(*[0] * (n + 1)), n + 1, f"{n} arguments"),
+                                      (i + 1, words(*[0] * n), n - 1, f"{n} arguments"), (i + 1, None, n, "null pointer")):
+            assert kvc.STATUS[call(which, w, count, None)] == "KVC_ERR_INVALID"
+            assert text in kvc._lib.kvc_last_error_string().decode()
+    for which in (0, 5, -1):
+        assert kvc.STATUS[call(which, words(0), 1, None)] == "KVC_ERR_INVALID"
+    # the commit's arguments in order: handle, table, max_blocks, lengths, tree lengths, path, its length, P, B, new
+    assert kvc.STATUS[call(4, words(0, 4096, 4, 4096, 0, 4096, 4096, 4, 1, 8192), 10, None)] == "KVC_ERR_INVALID"
+    assert "null handle" in kvc._lib.kvc_last_error_string().decode()
+    assert kvc.STATUS[call(4, words(0, 4096, 4, 4096, 0, 4096, 4096, 2 ** 32 + 4, 1, 8192), 10, None)] == "KVC_ERR_INVALID"
+    assert "beyond its type" in kvc._lib.kvc_last_error_string().decode()
+    # a float is a double: the tree's scale, place 16
+    args = [4096, 4096, 4096, 64, 4096, 8, 4096, 4096, 0, 4, 2, 4, 2, 64, 16, 128, float("nan"), 4096, 0, 0, 0]
+    w = struct.pack("=16qd4q", *args)
+    assert kvc.STATUS[call(2, w, 21, None)] == "KVC_ERR_INVALID"
+    assert "scale" in kvc._lib.kvc_last_error_string().decode()
