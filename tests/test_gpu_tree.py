@@ -258,6 +258,68 @@ def test_tree_attention_scales_and_peaks(kvc, scale):
     w.check(w.run(kvc), torch.float16, f"scale {scale}")
 
 
+MANY = [
+    # sequences, T, Hq, Hkv, D, histories up to, trees of nothing among them: more units than SMs
+    (45, 9, 8, 8, 64, 300, 0),
+    (100, 40, 14, 2, 64, 200, 0),      # 280 rows: pairs of two and of one row tile
+    (60, 33, 16, 4, 128, 400, 0),      # 132 rows
+    (90, 64, 8, 2, 128, 700, 0),
+    (300, 3, 4, 2, 64, 60, 0),
+    (1000, 2, 2, 1, 64, 40, 960),      # long runs of empty trees between units
+    (40, 12, 32, 8, 128, 1500, 3),
+]
+
+
+def many(case, T, Hq, Hkv, D, B, far, none, empty=True):
+    rng = np.random.default_rng([54, case])
+    hist, lens = rng.integers(0, far + 1, B), rng.integers(1, T + 1, B)
+    lens[rng.permutation(B)[:none]] = 0
+    lens[0], hist[1 % B], hist[2 % B] = T, 0, far
+    return Tree(100 + case, hist, lens, T, Hq, Hkv, D, empty)
+
+
+@pytest.mark.parametrize("case", range(len(MANY)))
+@pytest.mark.parametrize("out_dtype", [torch.float16, torch.float32])
+def test_tree_attention_of_more_units_than_sms(kvc, case, out_dtype):
+    B, T, Hq, Hkv, D, far, none = MANY[case]
+    w = many(case, T, Hq, Hkv, D, B, far, none)
+    got = w.run(kvc, out_dtype)
+    assert kvc.kvc_device_error_flags() == 0
+    w.check(got, out_dtype, f"many units, case {case}")
+    again = w.run(kvc, out_dtype)
+    assert (again == got).all()
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D", [(6, 8, 8, 64), (40, 14, 2, 64), (20, 16, 2, 128)])
+def test_many_units_with_bad_ones_among_them(kvc, T, Hq, Hkv, D):
+    """Lengths that do not fit, block ids out of range, infinities and NaN in V rows of nodes: of the sequences they are
+    in, not of the others that the same CTAs take."""
+    B = 700 // Hkv
+    w = many(20, T, Hq, Hkv, D, B, 150, 0, empty=False)
+    w.masks[:] = np.uint64(1) << np.arange(T, dtype=np.uint64)  # each node sees itself alone, and the history
+    w.lens[:], w.ctx[:] = np.minimum(w.lens, T), w.ctx
+    good = w.run(kvc)
+    bad_ctx, bad_table, pick = w.ctx.copy(), w.table.copy(), np.random.default_rng(7).permutation(B)
+    short, block, inf = pick[:9], pick[9:20], pick[20:50]
+    bad_ctx[short] = w.lens[short] - 1
+    bad_table[block, 0] = len(w.k)
+    v = w.v.copy()
+    for b in inf:
+        p = int(w.ctx[b] - 1)
+        v[w.table[b][p // 16], :, p % 16, 5] = np.inf
+    got = w.run(kvc, ctx=dev(bad_ctx), table=dev(bad_table), v=dev(v))
+    assert kvc.kvc_device_error_flags(clear=True) == kvc.DEVERR["CONTEXT"] | kvc.DEVERR["BLOCK_ID"]
+    for b in range(B):
+        L = int(w.lens[b])
+        if b in short or b in block:
+            assert (got[b, :L] == 0).all(), b
+        else:
+            want = good[b].copy()
+            if b in inf:
+                want[L - 1, :, 5] = np.inf
+            assert (got[b] == want).all(), b
+
+
 def test_tree_of_a_chain_is_the_multi_token_decode(kvc):
     wl = workloads.multi_token_decode(21, [8, 40, 900], 8)
     d = [dev(x) for x in (wl.q, wl.k_pool, wl.v_pool, wl.block_table, wl.ctx)]
