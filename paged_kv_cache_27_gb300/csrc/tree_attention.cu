@@ -917,17 +917,6 @@ cudaError_t tree_plan(int B, int Hq, int Hkv, int D, int max_ctx, int T, TreePla
     int dev = 0;
     if (sms <= 0 || cudaGetDevice(&dev) != cudaSuccess) return cudaErrorNoDevice;
     if (D != 64 && D != 128) return cudaErrorInvalidValue;
-    // a step's layers ask for the same sizes again
-    struct Sizes {
-        int v[7];
-    };
-    static thread_local Sizes last_sizes = {};
-    static thread_local TreePlan last_plan;
-    const Sizes sizes = {{dev, B, Hq, Hkv, D, max_ctx, T}};
-    if (D == last_sizes.v[4] && std::equal(sizes.v, sizes.v + 7, last_sizes.v)) {
-        *plan = last_plan;
-        return cudaSuccess;
-    }
     const int G = Hq / Hkv;
     const int row_tiles = (T * G + tree::kRows - 1) / tree::kRows;
     plan->row_pairs = (row_tiles + 1) / 2;
@@ -936,30 +925,32 @@ cudaError_t tree_plan(int B, int Hq, int Hkv, int D, int max_ctx, int T, TreePla
     const int d = D == 128, two = row_tiles > 1;
     // The split with the shortest run: waves of clusters times a CTA's tiles, start and end; then the merges.  The
     // clusters are of 1, 2, 4 or 8 CTAs, or of all chunks of a context.
+    const int cta = kCtaCost[d][two], tile = kTileCost[d][two], merge = kMergeCost[d][two];
+    const uint32_t all = static_cast<uint32_t>(std::min<int64_t>(units, 1 << 30));
     int64_t best_cost = INT64_MAX;
-    for (int nc = 1; nc <= std::min(tiles, 128); ++nc) {
-        const int chunk = (tiles + nc - 1) / nc;
-        if ((tiles + chunk - 1) / chunk != nc) continue;
-        for (int cs = 1; cs <= tree::kMaxTreeCluster && cs <= nc; ++cs) {
-            if ((cs & (cs - 1)) != 0 && cs != nc) continue;
-            const int nclus = (nc + cs - 1) / cs;
-            const int64_t resident = resident_clusters(dev, D, cs, sms);
-            const int64_t waves = (units * nclus + resident - 1) / resident;
-            const int64_t cost = waves * (kCtaCost[d][two] + chunk * kTileCost[d][two]) +
-                                 (cs > 1 ? kMergeCost[d][two] + kMergeCtaCost * cs : 0) +
-                                 (nclus > 1 ? kCombineCost + kStateCost * nclus + kPartialCost * nclus * units / sms : 0);
+    // numbers of chunks in turn that chunks of one size divide a context into
+    for (int chunk = tiles, nc = 1;;) {
+        for (int cs = nc <= tree::kMaxTreeCluster ? nc : tree::kMaxTreeCluster; cs > 0;) {
+            const uint32_t nclus = static_cast<uint32_t>(nc + cs - 1) / cs;  // (all * nclus: below 8 * SMs + all)
+            const uint32_t resident = static_cast<uint32_t>(resident_clusters(dev, D, cs, sms));
+            const int64_t waves = (all * nclus + resident - 1) / resident;
+            int64_t cost = waves * (cta + static_cast<int64_t>(chunk) * tile);
+            if (cs > 1) cost += merge + kMergeCtaCost * cs;
+            if (nclus > 1) cost += kCombineCost + kStateCost * nclus + kPartialCost * nclus * all / sms;
             if (cost < best_cost) {
                 best_cost = cost;
                 plan->chunk = chunk;
                 plan->cluster = cs;
-                plan->nclus = nclus;
+                plan->nclus = static_cast<int>(nclus);
             }
+            cs = cs > 4 ? 4 : cs > 2 ? 2 : cs > 1 ? 1 : 0;  // all of up to eight, then 4, 2, 1
         }
-        if (units * nc > 8 * sms) break;  // every SM has its share: more chunks only cost
+        if (units * nc > 8 * sms || chunk == 1) break;  // every SM has its share: more chunks only cost
+        nc = (tiles + chunk - 2) / (chunk - 1);         // the next number with smaller chunks
+        chunk = (tiles + nc - 1) / nc;
+        if (nc > 128) break;
     }
     plan->workspace_bytes = plan->nclus > 1 ? partials_bytes(static_cast<size_t>(B) * T * Hq * plan->nclus, D) : 0;
-    last_sizes = sizes;
-    last_plan = *plan;
     return cudaSuccess;
 }
 
