@@ -800,6 +800,15 @@ def _run(call: _Words, args, stream, prepare, dev, keep):
     return None
 
 
+def kvc_call(which: int, words: bytes, stream=None) -> None:
+    """A launching call by its number (KVC_CALL_* of the header) with its arguments as 64-bit words, on `stream` or the
+    current one.  The four calls' own functions build the words from tensors and check them."""
+    if len(words) % 8:
+        raise ValueError("words must be whole 64-bit words")
+    st = torch.cuda.current_stream().cuda_stream if stream is None and torch.cuda.is_available() else _stream(stream)
+    _check(_call(which, words, len(words) // 8, st), "kvc_call")
+
+
 def _token_stride(t: torch.Tensor, name: str) -> int:
     """Token stride of an [n][H][D] fp16 tensor whose heads are packed and whose tokens may be apart."""
     if not isinstance(t, torch.Tensor):

@@ -247,3 +247,7 @@ def test_calls_with_words_are_the_calls():
     w = struct.pack("=16qd4q", *args)
     assert kvc.STATUS[call(2, w, 21, None)] == "KVC_ERR_INVALID"
     assert "scale" in kvc._lib.kvc_last_error_string().decode()
+    with pytest.raises(kvc.KvcError, match="unknown call"):
+        kvc.kvc_call(9, words(0))
+    with pytest.raises(ValueError):
+        kvc.kvc_call(1, b"1234567")
