@@ -467,7 +467,10 @@ kvc_status paged_decode_attention_static_workspace(const void* q, const void* k_
  * position for the rotation is (history length + depth).  A step is, per
  * layer, kv_append_rope and paged_decode_tree_attention; then, once,
  * draft_tree_verify on the target's probabilities and kv_tree_commit, after
- * which the kept path is the end of an ordinary context. */
+ * which the kept path is the end of an ordinary context.  The four calls keep
+ * the stream's order whatever kvc_set_launch_overlap says: their kernels are
+ * launched under the end of the kernel in front, but read and write nothing
+ * before it is done, and release nothing early themselves. */
 
 /* Host helper: from parents [B][T] (parents[b][0] is not read; otherwise
  * 0 <= parents[b][t] < t) and tree_lens [B] (NULL: T each) the masks [B][T]

@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv_append_rope_kernel
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
     const int64_t t = w / p.split;
+    grid_dependency_wait();  // nothing is read or written before the kernel in front is done
     if (t >= p.n) return;  // whole warps
     const int l = lane % kLanes, rsub = lane / kLanes;
 
@@ -291,13 +292,12 @@ cudaError_t launch_append_rope(const RopeArgs& a, cudaStream_t stream) {
     const bool stream_by = a.n * (a.Hq + 2 * a.Hkv) * a.D * 4 > (int64_t(128) << 20);
     const dim3 grid(static_cast<unsigned>(blocks)), block(rope::kWarps * 32);
     switch (a.D + (stream_by ? 1 : 0)) {
-        case 64: rope::kv_append_rope_kernel<64, false><<<grid, block, 0, stream>>>(p); break;
-        case 65: rope::kv_append_rope_kernel<64, true><<<grid, block, 0, stream>>>(p); break;
-        case 128: rope::kv_append_rope_kernel<128, false><<<grid, block, 0, stream>>>(p); break;
-        case 129: rope::kv_append_rope_kernel<128, true><<<grid, block, 0, stream>>>(p); break;
+        case 64: return launch(rope::kv_append_rope_kernel<64, false>, grid, block, 0, stream, true, 1u, p);
+        case 65: return launch(rope::kv_append_rope_kernel<64, true>, grid, block, 0, stream, true, 1u, p);
+        case 128: return launch(rope::kv_append_rope_kernel<128, false>, grid, block, 0, stream, true, 1u, p);
+        case 129: return launch(rope::kv_append_rope_kernel<128, true>, grid, block, 0, stream, true, 1u, p);
         default: return cudaErrorInvalidValue;
     }
-    return cudaGetLastError();
 }
 
 }  // namespace kvc

@@ -266,6 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
         const int page = (c0 + j) * kPages + lane;
         return page < p.max_blocks ? table_row[page] : 0;
     };
+    grid_dependency_wait();  // nothing is read or written before the kernel in front is done
     const int tree = p.tree_lens != nullptr ? p.tree_lens[b] : p.T, ctx = p.context_lens[b];
     int ids = 0;
     constexpr int kQLoads = D / 8;  // 16-byte chunks of two row tiles per row thread
@@ -992,7 +993,7 @@ static cudaError_t launch_tree_d(const TreeArgs& a, const TreePlan& plan, cudaSt
     p.negate = a.scale < 0.f;
     p.scale_log2 = std::max(std::fabs(a.scale) * kLog2e, tree::kMinScaleLog2);
     const dim3 grid(static_cast<unsigned>(plan.row_pairs * plan.nclus * plan.cluster), a.Hkv, a.B);
-    e = launch(tree::paged_decode_tree_kernel<D, kSplitP>, grid, dim3(tree::kThreads), Geo::kSmemBytes, stream, false,
+    e = launch(tree::paged_decode_tree_kernel<D, kSplitP>, grid, dim3(tree::kThreads), Geo::kSmemBytes, stream, true,
                static_cast<unsigned>(plan.cluster), tmK, tmV, p);
     if (e != cudaSuccess || plan.nclus == 1) return e;
     const int64_t nrows = static_cast<int64_t>(a.B) * a.T * a.Hq;

@@ -36,6 +36,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv_tree_commit_kernel(const Param
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.y;
     const int w = blockIdx.x * kWarps + warp;  // (layer, K or V, part of the heads)
     __shared__ int2 s_move[kWarps][kMaxTreeNodes];  // (from, to): block * 16 + offset of the rows that move
+    grid_dependency_wait();  // nothing is read or written before the kernel in front is done
     if (w >= p.L * 2 * p.head_parts) return;  // whole warps
     const int part = w % p.head_parts, kv = (w / p.head_parts) & 1, layer = w / p.head_parts / 2;
     const bool first = w == 0;
@@ -138,8 +139,7 @@ cudaError_t launch_tree_commit(const CommitArgs& a, cudaStream_t stream) {
     p.head_parts = (a.Hkv + p.heads_per_warp - 1) / p.heads_per_warp;
     const int64_t warps = static_cast<int64_t>(a.L) * 2 * p.head_parts;
     const dim3 grid(static_cast<unsigned>((warps + commit::kWarps - 1) / commit::kWarps), a.B);
-    commit::kv_tree_commit_kernel<<<grid, commit::kWarps * 32, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch(commit::kv_tree_commit_kernel, grid, dim3(commit::kWarps * 32), 0, stream, true, 1u, p);
 }
 
 }  // namespace kvc

@@ -311,6 +311,7 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) draft_tree_verify_ke
     const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = static_cast<int>(blockIdx.x), cs = static_cast<int>(gridDim.x);  // one cluster spans x
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA runs
+    grid_dependency_wait();  // nothing is read or written before the kernel in front is done
     int n_nodes = p.tree_lens != nullptr ? p.tree_lens[b] : p.T;
     const T* const prow = static_cast<const T*>(p.p) + static_cast<int64_t>(b) * p.T * p.p_stride;
     const T* const qrow = static_cast<const T*>(p.q) + static_cast<int64_t>(b) * p.T * p.q_stride;
@@ -546,9 +547,9 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) draft_tree_verify_ke
 template <typename T>
 static cudaError_t launch_verify_t(const verify::Params& p, int B, int cs, bool wide, cudaStream_t stream) {
     const dim3 grid(cs, B);
-    return wide ? launch(verify::draft_tree_verify_kernel<T, 512>, grid, dim3(512), 0, stream, false,
+    return wide ? launch(verify::draft_tree_verify_kernel<T, 512>, grid, dim3(512), 0, stream, true,
                          static_cast<unsigned>(cs), p)
-                : launch(verify::draft_tree_verify_kernel<T, 256>, grid, dim3(256), 0, stream, false,
+                : launch(verify::draft_tree_verify_kernel<T, 256>, grid, dim3(256), 0, stream, true,
                          static_cast<unsigned>(cs), p);
 }
 

@@ -811,3 +811,45 @@ def test_a_whole_step_then_an_ordinary_decode(kvc):
     ref = oracle.decode(host(q), host(s.k_pool[1]), host(s.v_pool[1]), wl.block_table[keep], new_ctx[keep], wl.scale)
     assert np.abs(host(out) - ref).max() <= 2e-3
     s.close()
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_calls_wait_for_the_kernel_in_front(kvc, graph):
+    """Every call is launched as a programmatic dependent: what a kernel right in front of it writes is what it reads,
+    and a buffer that the kernel in front still reads is not overwritten early."""
+    from paged_kv_cache_27_gb300.harness import TreeSession
+    wl = workloads.tree_decode(2, [40, 300, 7], [12, 9, 12], 12, L=2)
+    s = TreeSession(wl)
+    fresh = [x.clone() for x in (s.k_pool, s.v_pool)]
+    results = lambda: [host(x) for x in (s.out, s.path, s.path_len, s.next_token, s.new_context_lens, s.k_pool, s.v_pool)]  # noqa: E731
+    s.step()
+    torch.cuda.synchronize()
+    want = results()
+    late = {0: s.qkv[0], 1: s.masks, 2: s.qkv[1], 3: s.tree_lens, 4: s.p, 5: s.block_table}  # of the calls in order
+    right = {i: x.clone() for i, x in late.items()}
+    big = torch.zeros(64 << 20, device="cuda")
+    seen = torch.empty_like(s.q_rot[1])
+
+    def step():
+        for pool, x in zip((s.k_pool, s.v_pool), fresh):
+            torch.add(x, 0, out=pool)
+        for i, call in enumerate(s._calls):
+            late[i].fill_(0)
+            big.add_(1)  # long, so that its successors queue up
+            torch.add(right[i], 0, out=late[i])
+            call()
+            if i == 2:
+                torch.add(s.q_rot[1], 0, out=seen)
+    step()
+    torch.cuda.synchronize()
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        s.out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+    assert kvc.kvc_device_error_flags() == 0
+    for a, b in zip(results(), want):
+        assert np.array_equal(a.view(np.uint8), b.view(np.uint8))
+    assert (seen == s.q_rot[1]).all()
