@@ -32,7 +32,7 @@
 // 128,257 fp32 entries (16 nodes, three distinct children a node): 2.2 passes on average, 6 at most.  The first passes
 // read 66 MB from memory; of a pass of a cluster alone on its SMs (4.8 us), about 2.5 us are arithmetic and loads from
 // L2, 1.0 the exchange of the sums (the barrier of a cluster takes 0.7), 0.65 the decision.  41 us, where one reading
-// of the two rows of every sequence takes 9.7; one sequence of 32,000 entries (8 nodes, a chain) 7.4 us.
+// of the two rows of every sequence takes 9.7; one sequence of 32,000 entries (8 nodes, a chain) 6.9 us.
 #include "../../include/kvc.h"
 #include "decode_common.cuh"
 #include "f32x2.cuh"
