@@ -31,8 +31,11 @@
 // What bounds it.  A sequence's passes follow one another: each needs the sum of the one before.  64 sequences of
 // 128,257 fp32 entries (16 nodes, three distinct children a node): 2.2 passes on average, 6 at most.  The first passes
 // read 66 MB from memory; of a pass of a cluster alone on its SMs (4.8 us), about 2.5 us are arithmetic and loads from
-// L2, 1.0 the exchange of the sums (the barrier of a cluster takes 0.7), 0.65 the decision.  41 us, where one reading
+// L2, 1.0 the exchange of the sums (the barrier of a cluster takes 0.7), 0.65 the decision.  39 us, where one reading
 // of the two rows of every sequence takes 9.7; one sequence of 32,000 entries (8 nodes, a chain) 6.9 us.
+#include <algorithm>
+#include <atomic>
+
 #include "../../include/kvc.h"
 #include "decode_common.cuh"
 #include "f32x2.cuh"
@@ -553,6 +556,39 @@ static cudaError_t launch_verify_t(const verify::Params& p, int B, int cs, bool 
                          static_cast<unsigned>(cs), p);
 }
 
+// Clusters of cs CTAs that the device holds at a time (a GPC's SMs that no whole cluster fills stay idle).  Asked once
+// per device, type and size.
+static int resident_clusters(bool f32, bool wide, int cs, int sms) {
+    const int per_sm = wide ? 1 : 768 / 256;
+    if (cs == 1) return sms * per_sm;
+    static std::atomic<int> cache[128][2][2][verify::kMaxClusterV + 1];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return std::max(1, sms * per_sm / cs);
+    std::atomic<int>& slot = cache[dev][f32][wide][cs];
+    int n = slot.load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = cs;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(cs);
+    cfg.blockDim = dim3(wide ? 512 : 256);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const auto ask = [&](auto kernel) { return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg); };
+    const cudaError_t e = f32 ? (wide ? ask(verify::draft_tree_verify_kernel<float, 512>)
+                                      : ask(verify::draft_tree_verify_kernel<float, 256>))
+                              : (wide ? ask(verify::draft_tree_verify_kernel<__half, 512>)
+                                      : ask(verify::draft_tree_verify_kernel<__half, 256>));
+    if (e != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        n = std::max(1, sms * per_sm / cs);
+    }
+    slot.store(n, std::memory_order_relaxed);
+    return n;
+}
+
 cudaError_t launch_tree_verify(const VerifyArgs& a, cudaStream_t stream) {
     if (a.B <= 0) return cudaSuccess;
     verify::Params p;
@@ -571,16 +607,34 @@ cudaError_t launch_tree_verify(const VerifyArgs& a, cudaStream_t stream) {
     p.T = a.T;
     p.V = a.V;
     p.distinct = a.distinct;
-    // CTAs per sequence: a thread should have two entries before it is worth another CTA's share (clusters of 4, 8 and
-    // 16 for 64 sequences x 128,257 entries: 59, 50 and 54 us when this was measured).  512 threads a CTA while every
-    // CTA has an SM (one sequence: 3.2 us a pass, 4.8 with 256), else 256, three CTAs per SM (64 sequences: 60 us with 512
-    // and 48 with 256 when this was measured).
+    // CTAs per sequence and threads per CTA: the choice with the shortest run of two passes, in us.  A pass takes an
+    // exchange of the sums (1.1, in a cluster 1.55) and a CTA's arithmetic (87 ns per 1000 entries with 512 threads,
+    // one CTA per SM; 197 with 256, three), or the memory's time for all rows that are read at once: the second pass
+    // reads them from L2 where they fit.  A start takes 2; clusters that are not resident wait for others.  (Clusters
+    // of eight for every larger V, 512 threads while every CTA had an SM: 512 sequences x 8000 entries 47.6 us, here
+    // 11.3; 19 x 128,257 12.0, here 8.2; 64 x 128,257 with four refusals each 44.7, here 37.7.)
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorNoDevice;
+    constexpr double kMemory = 6.8e6, kL2 = 13.6e6, kL2Bytes = 100e6;  // bytes per us; bytes that stay
+    double best = 1e300;
     int cs = 1;
-    while (cs < verify::kMaxClusterV && a.V > cs * 1024) cs *= 2;
+    bool wide = false;
+    for (int w = 1; w >= 0; --w) {
+        for (const int c : {8, 6, 4, 3, 2, 1}) {
+            const int resident = resident_clusters(a.probs_f32, w != 0, c, sms);
+            const double work = static_cast<double>(a.V) / c * (w ? 87e-6 : 197e-6);
+            const double bytes = static_cast<double>(std::min(a.B, resident)) * a.V * (a.probs_f32 ? 8 : 4);
+            const double passes = 2 * (c > 1 ? 1.55 : 1.1) + 0.2 * work + std::max(work, bytes / kMemory) +
+                                  std::max(work, bytes / (bytes <= kL2Bytes ? kL2 : kMemory));
+            const double waves = a.B <= resident ? 1. : static_cast<double>(a.B) / resident + 0.2;
+            if (waves * (2. + passes) < best) {
+                best = waves * (2. + passes);
+                cs = c;
+                wide = w != 0;
+            }
+        }
+    }
     p.slice = (a.V + cs - 1) / cs;
-    const bool wide = static_cast<int64_t>(a.B) * cs <= sms;
     return a.probs_f32 ? launch_verify_t<float>(p, a.B, cs, wide, stream)
                        : launch_verify_t<__half>(p, a.B, cs, wide, stream);
 }
