@@ -521,6 +521,30 @@ def test_verify(kvc, case):
     assert all((a == b).all() for a, b in zip(first, again))
 
 
+MANY_VERIFY = [
+    # B, T, V, fp16, distinct: clusters of other sizes than a few sequences get
+    (64, 2, 128257, False, False),
+    (19, 3, 128257, False, True),
+    (30, 3, 90001, True, False),
+    (130, 2, 60007, False, False),
+    (160, 3, 30011, True, True),
+    (500, 4, 601, False, True),
+    (200, 3, 9001, False, False),
+]
+
+
+@pytest.mark.parametrize("case", range(len(MANY_VERIFY)))
+def test_verify_of_many_sequences(kvc, case):
+    B, T, V, half, distinct = MANY_VERIFY[case]
+    p, q, tok, par, u = verify_case(70 + case, B, T, V, 1.5, half, distinct, parents=[0] * T)
+    u[:, 1:] = np.minimum(1 - u[:, 1:] * 0.3, np.float32(1 - 2.0 ** -24))  # refusals
+    got = run_verify(kvc, p, q, tok, par, u, distinct=distinct)
+    assert kvc.kvc_device_error_flags() == 0
+    check_verify(got, p, q, tok, par, u, distinct=distinct)
+    assert (got[1] == 1).any() and (got[1] > 1).any()
+    assert all((a == b).all() for a, b in zip(got, run_verify(kvc, p, q, tok, par, u, distinct=distinct)))
+
+
 @pytest.mark.parametrize("distinct", [False, True])
 def test_verify_many_refusals_at_one_node(kvc, distinct):
     """All nodes are the root's children, under uniforms near 1, so that most are refused; the same token twice."""
