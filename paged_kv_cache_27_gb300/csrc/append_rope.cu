@@ -106,7 +106,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv_append_rope_kernel
     __shared__ float2 s_cs[kWarps][D / 2];  // (cos, sin) of the warp's token
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-    const int64_t t = w / p.split;
+    // (a 64-bit division takes longer than a row; tokens are split only where they are few)
+    const uint32_t part = p.split == 1 ? 0u : static_cast<uint32_t>(w) % static_cast<uint32_t>(p.split);
+    const int64_t t = p.split == 1 ? w : static_cast<uint32_t>(w) / static_cast<uint32_t>(p.split);
     grid_dependency_wait();  // nothing is read or written before the kernel in front is done
     if (t >= p.n) return;  // whole warps
     const int l = lane % kLanes, rsub = lane / kLanes;
@@ -157,7 +159,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv_append_rope_kernel
     }
 
     // The warp's share of the passes: query rows, key rows, value rows, kRows heads at a time.
-    const int pass0 = static_cast<int>(w % p.split) * p.passes_per_warp, pass1 = pass0 + p.passes_per_warp;
+    const int pass0 = static_cast<int>(part) * p.passes_per_warp, pass1 = pass0 + p.passes_per_warp;
     const int pq = (p.Hq + kRows - 1) / kRows, pk = (p.Hkv + kRows - 1) / kRows;
     const auto rows = [&](auto kind, int first, int last) {  // passes [first, last) of one kind of rows
         constexpr int kKind = decltype(kind)::value;  // 0 query, 1 key, 2 value
