@@ -39,6 +39,7 @@
 //   1 x 2048 keys, 8 nodes, 14 / 2 heads, D = 64         8.3  (0.2)  start, two key tiles, end
 // Every wait is bounded.
 #include <algorithm>
+#include <cfloat>
 #include <type_traits>
 
 #include "../../include/kvc.h"
@@ -66,6 +67,13 @@ constexpr uint64_t kWaitNs = 1000000000ull;
 // -inf times it stays -inf
 constexpr float kMinScaleLog2 = 0x1p-100f;
 constexpr float kRescaleLog2 = 8.f;  // P stays below 2^8, far inside fp16
+// Scores of finite fp16 rows reach 2^41, where neighbouring fp32 exponents x lie 2^18 apart: x - m, exact in the
+// weights' multiply-add, can then be any number although m came from the same score.  So m is rounded down (the largest
+// score's x - m is never negative: no row is lost), and weights are cut off at fp16's largest value: scores as close as
+// their own rounding count as equal.  The conversion of an fp16-output weight does that by itself (a branch over the
+// scores in its place cost 2 % of 8 x 4096 keys with 64 nodes); the split weights' exponents are cut off where a row's m
+// is beyond kFar, from where on a step is no longer small against fp16's range.
+constexpr float kFar = 0x1p22f;
 
 template <int D>
 struct Geom {
@@ -114,7 +122,7 @@ struct Params {
     int row_pairs;  // pairs of row tiles of the widest tree
     uint32_t g_magic;  // ceil(2^18 / G): row * g_magic >> 18 = row / G for rows below 4096
     int negate;      // scale < 0: the query rows change sign as they are loaded
-    float scale_log2;  // |scale| * log2 e, at least kMinScaleLog2
+    float scale_log2;  // |scale| * log2 e, at least kMinScaleLog2 and finite
 };
 
 __device__ __forceinline__ uint32_t sw128(int row, int c) {
@@ -128,6 +136,12 @@ __device__ __forceinline__ float add_halves(uint32_t h, float acc) {
         : "+f"(acc)
         : "r"(h));
     return acc;
+}
+// two values as fp16, beyond fp16's range its largest one; NaN stays NaN
+__device__ __forceinline__ uint32_t pack_half2_finite(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 __device__ __forceinline__ float max3f(float a, float b, float c) {
     float r;
@@ -557,6 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
         const float sl2 = p.scale_log2;
         const uint64_t sc2 = pack_f32x2(sl2, sl2);
         float m_used = -INFINITY, l = 0.f;
+        bool far = false;  // some row of the warp has its m beyond kFar, or sees nothing yet
         bool ok = true;
         for (int u = 0; u < units; ++u) {
             const int buf = 2 * x + (u & 1);
@@ -588,20 +603,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
                     for (int i = 0; i < 4; ++i) e[i] = max3f(e[i], s[c + i], s[c + 4 + i]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) e[i] = fmaxf(e[i], s[kHalf - 4 + i]);
-                const float mx = max3f(e[0], e[1], fmaxf(e[2], e[3])) * sl2;  // -inf: nothing seen
+                const float mx = __fmul_rd(max3f(e[0], e[1], fmaxf(e[2], e[3])), sl2);  // -inf: nothing seen
                 float alpha = 1.f;
                 if (mx > m_used + kRescaleLog2) {  // includes the first finite max (m_used = -inf)
                     alpha = m_used == -INFINITY ? 0.f : ex2(m_used - mx);
                     m_used = mx;
                 }
-                if (u > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                if (__any_sync(0xffffffffu, alpha != 1.f)) {
+                    if constexpr (kSplitP) far = __any_sync(0xffffffffu, fabsf(m_used) >= kFar);
                     // rescale O_X, which idles once the stream's previous product is complete (this unit's P is not
                     // there yet)
-                    ok = __all_sync(0xffffffffu, wait(&o_full[buf ^ 1], ((u - 1) >> 1) & 1, s_abort));
+                    if (u > 0) ok = __all_sync(0xffffffffu, wait(&o_full[buf ^ 1], ((u - 1) >> 1) & 1, s_abort));
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
+                    for (int c = 0; u > 0 && c < D; c += 32) {
                         float o[32];
                         tmem_ld32(tO + c, o);
 #pragma unroll
@@ -611,7 +627,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
                 }
                 const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
                 float ls[4] = {0.f, 0.f, 0.f, 0.f};
-                const uint64_t nm2 = pack_f32x2(neg_m, neg_m);
+                uint64_t by2 = sc2, nm2 = pack_f32x2(neg_m, neg_m);
+                if (kSplitP && far) {
+#pragma unroll
+                    for (int c = 0; c < kHalf; ++c) {
+                        const float d = fmaf(s[c], sl2, neg_m);
+                        s[c] = d > kRescaleLog2 ? kRescaleLog2 : d;
+                    }
+                    by2 = pack_f32x2(1.f, 1.f);
+                    nm2 = 0;
+                }
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {  // 32 keys at a time
                     uint32_t hv[16], lv[16];
@@ -619,10 +644,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
                     for (int i = 0; i < 16; ++i) {
                         const int c = hh * 32 + 2 * i;
                         float x0, x1;
-                        unpack_f32x2(fma_f32x2(pack_f32x2(s[c], s[c + 1]), sc2, nm2), x0, x1);
+                        unpack_f32x2(fma_f32x2(pack_f32x2(s[c], s[c + 1]), by2, nm2), x0, x1);
                         x0 = ex2(x0);
                         x1 = ex2(x1);
-                        hv[i] = pack_half2(x0, x1);
+                        hv[i] = kSplitP ? pack_half2(x0, x1) : pack_half2_finite(x0, x1);
                         if constexpr (kSplitP) {
                             const float2 f = unpack_half2(hv[i]);
                             lv[i] = pack_half2(x0 - f.x, x1 - f.y);
@@ -991,7 +1016,7 @@ static cudaError_t launch_tree_d(const TreeArgs& a, const TreePlan& plan, cudaSt
     p.nclus = plan.nclus;
     p.row_pairs = plan.row_pairs;
     p.negate = a.scale < 0.f;
-    p.scale_log2 = std::max(std::fabs(a.scale) * kLog2e, tree::kMinScaleLog2);
+    p.scale_log2 = std::min(std::max(std::fabs(a.scale) * kLog2e, tree::kMinScaleLog2), FLT_MAX);
     const dim3 grid(static_cast<unsigned>(plan.row_pairs * plan.nclus * plan.cluster), a.Hkv, a.B);
     e = launch(tree::paged_decode_tree_kernel<D, kSplitP>, grid, dim3(tree::kThreads), Geo::kSmemBytes, stream, true,
                static_cast<unsigned>(plan.cluster), tmK, tmV, p);
