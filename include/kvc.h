@@ -540,9 +540,10 @@ kvc_status kv_append_rope(const void* q, int64_t q_stride, const void* k, int64_
  * cache already (kv_append_rope or kv_append).  What the cache holds past a
  * context, and in nodes that a row does not see, cannot reach that row's
  * output, infinities and NaN included.  With fp16 out the softmax weights
- * multiply V in fp16 and the row sums add the same rounded weights (within
- * 2^-11 relative, as in paged_decode_multi_attention); with fp32 out they keep
- * ~22 bits.  A sequence whose lengths do not fit is flagged
+ * multiply V in fp16 and the row sums add the same rounded weights: each is
+ * within 2^-11 of itself, or within 2^-36 of its row's largest one where that
+ * is more; with fp32 out they are two fp16 parts, 2^-20 and the same 2^-36.
+ * A sequence whose lengths do not fit is flagged
  * (KVC_DEVERR_CONTEXT) and its rows are zero; a block id out of range is
  * flagged (KVC_DEVERR_BLOCK_ID) and the chunk of the context it lies in is
  * left out.  One kernel launch, or two where the context is split (the plan's

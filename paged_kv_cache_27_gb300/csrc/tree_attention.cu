@@ -14,7 +14,7 @@
 //   two row tiles     the streams are the row tiles and share every K/V tile (the tile is read once for 256 rows);
 //   one row tile      the streams are the two halves of every key tile for the same rows, merged at the end.
 // Per stream X and step of 64 keys:  S_X = Q_X K^T (both K-major in shared memory, 128-byte swizzle, as TMA writes the
-// blocks); the row warps take S_X from TMEM, keep the running max lazily (it moves when it has grown by 2^8; O_X is
+// blocks); the row warps take S_X from TMEM, keep the running max lazily (it moves when it has grown by 2^4; O_X is
 // then rescaled in TMEM) and write P_X over S_X in fp16;  O_X += P_X V with P_X from TMEM and V MN-major.  Two buffers
 // let S of the next step run under this step's softmax; steps of 64 keys instead of 128 make room for both.
 // Warps.  Eight row warps; one product warp per stream and product (S_A, S_B, PV_A, PV_B: a wait costs a warp about 200
@@ -22,8 +22,8 @@
 // two buffers and the four product warps together took 8 x 4096 keys, 64 nodes, 32 / 8 heads, D = 128 from 57 to 37 us.
 // Sixteen row warps, two to a row, are slower (40.2 against 38.3 us), and so is one row tile per CTA (42 us).
 // P.  With an fp16 output the weights are one fp16 value and the row sums add the rounded weights, so a row is a
-// convex combination of V rows with weights within 2^-11 relative, which is the output's own rounding; with an fp32
-// output they are an fp16 high part plus residual (two products), ~22 bits.
+// convex combination of V rows; with an fp32 output they are an fp16 high part plus residual (two products).  A weight
+// is within 2^-11 / 2^-20 of itself, or 2^-36 of its row's largest one where that is more (see kWeightLog2).
 // Split.  The context is cut into chunks where (sequence, KV head, row tile pair) units are fewer than SMs.  Up to
 // eight CTAs of a unit are a cluster: each leaves its states (max, sum, O) in its shared memory and merges a share of
 // the rows from all of them.  Where a unit has several clusters their states go through the workspace to the combine
@@ -66,7 +66,12 @@ constexpr uint64_t kWaitNs = 1000000000ull;
 // a scale of 0 is taken as this: the scores of fp16 rows (below 2^40) still vanish next to 1, and a masked score of
 // -inf times it stays -inf
 constexpr float kMinScaleLog2 = 0x1p-100f;
-constexpr float kRescaleLog2 = 8.f;  // P stays below 2^8, far inside fp16
+// A weight is 2^(x - m) for a score of exponent x.  The running m lies 2^11 below the largest score so far and moves
+// when a score is 2^15 above it, inside fp16's 2^16: a weight keeps fp16's 11 bits down to 2^-25 of its row's largest one
+// and 2^-36 of that below.  The factor is in the row's sum too and costs no time.  (With the largest weight at 1, a key
+// 2^25 below another one was lost, and 65,536 of those are 1.4e-3 of a row.)
+constexpr float kWeightLog2 = 11.f;
+constexpr float kRescaleLog2 = 15.f;
 // Scores of finite fp16 rows reach 2^41, where neighbouring fp32 exponents x lie 2^18 apart: x - m, exact in the
 // weights' multiply-add, can then be any number although m came from the same score.  So m is rounded down (the largest
 // score's x - m is never negative: no row is lost), and weights are cut off at fp16's largest value: scores as close as
@@ -606,8 +611,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_tree_kernel(const __
                 const float mx = __fmul_rd(max3f(e[0], e[1], fmaxf(e[2], e[3])), sl2);  // -inf: nothing seen
                 float alpha = 1.f;
                 if (mx > m_used + kRescaleLog2) {  // includes the first finite max (m_used = -inf)
-                    alpha = m_used == -INFINITY ? 0.f : ex2(m_used - mx);
-                    m_used = mx;
+                    const float m_new = __fsub_rd(mx, kWeightLog2);
+                    alpha = m_used == -INFINITY ? 0.f : ex2(m_used - m_new);
+                    m_used = m_new;
                 }
                 if (__any_sync(0xffffffffu, alpha != 1.f)) {
                     if constexpr (kSplitP) far = __any_sync(0xffffffffu, fabsf(m_used) >= kFar);

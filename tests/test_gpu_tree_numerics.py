@@ -1,4 +1,13 @@
 """Numerics of a tree-drafted step where scores, weights and angles are far apart, against the definitions in fp64.
+
+Every output of the tree attention is held to its own row's bound, with e_i the relative error of key i's weight w_i:
+  |err| <= sum_i w_i e_i (|v_i| + |out|) + 2^-36 max(w) sum_i (|v_i| + |out|) + sums + the store's half step,
+  e_i = the weight's own rounding (2^-11 with fp16 outputs, 2^-22 with fp32 ones) + its exponential (2^-22)
+        + D 2^-24 of the score's terms' magnitudes + 4 * 2^-24 of its exponent (its distance to the row's largest
+        score, and the 11 ln 2 < 8 by which weights are carried higher) + 2^-18 for the rescalings of a row's state
+        (at most 16 factors of 2^-22),
+  sums = 2^-23 per product instruction of 16 keys of numerator and row sum, and 2^-21 inside one.
+The second term is what the call documents for weights below fp16's normal range.
 """
 import numpy as np
 import pytest
@@ -8,6 +17,56 @@ from test_gpu_tree import Tree, kvc  # noqa: F401  (kvc is a fixture)
 from oracle import tree
 
 pytestmark = pytest.mark.gpu
+
+
+def rows_and_bounds(w, out_dtype, b, hk, tiles=False):
+    """For the rows (node, query head of KV head hk) of sequence b: fp64 outputs and their bounds [rows][D]; with tiles
+    also the outputs [tile][rows][D] that come of leaving out a tile of 128 keys."""
+    G, L, n, D = w.Hq // w.Hkv, int(w.lens[b]), int(w.ctx[b]), w.D
+    half = out_dtype == torch.float16
+    hist = n - L
+    K, V = (tree.rows_of(c[:, hk:hk + 1], w.table[b], n)[:, 0].astype(np.float64) for c in (w.k, w.v))
+    q = w.q[b, :L, hk * G:(hk + 1) * G].astype(np.float64).reshape(L * G, D)
+    seen = np.ones((L, n), bool)
+    seen[:, hist:] = (w.masks[b, :L, None] >> np.arange(L, dtype=np.uint64)) & np.uint64(1) == 1
+    seen = np.repeat(seen, G, 0)
+    x = np.where(seen, q @ np.where(np.isfinite(K), K, 0).T * w.scale, -np.inf)
+    top = x.max(1, keepdims=True)
+    top = np.where(np.isfinite(top), top, 0.0)
+    e = np.exp(x - top)
+    total = np.maximum(e.sum(1, keepdims=True), 1e-300)
+    p = e / total
+    out = p @ V
+    far = np.where(seen, top - x, 0.0)
+    terms = np.abs(q) @ np.abs(K).T * abs(w.scale)
+    rel = (2.0 ** -11 if half else 2.0 ** -22) + 2.0 ** -22 + D * 2.0 ** -24 * terms + 4 * 2.0 ** -24 * (far + 8) + 2.0 ** -18
+    A, size = np.abs(V), np.abs(out)
+    pr = p * rel
+    bound = pr @ A + pr.sum(1, keepdims=True) * size
+    bound += 2.0 ** -36 / total * (seen @ A + seen.sum(1, keepdims=True) * size)
+    bound += (n / 16 * 2.0 ** -23 + 2.0 ** -21) * (p @ A + size)
+    bound = 1.01 * bound + ((2.0 ** -11 if half else 2.0 ** -24) * size + 2.0 ** -25)
+    if not tiles:
+        return out, bound
+    starts = np.arange(0, n, 128)
+    part = np.stack([e[:, s:s + 128] @ V[s:s + 128] for s in starts])
+    mass = np.add.reduceat(e, starts, 1).T[:, :, None]
+    with np.errstate(invalid="ignore", divide="ignore"):
+        without = (out * total - part) / (total - mass)
+    return out, bound, without
+
+
+def check(w, got, out_dtype, what, rows=None):
+    G = w.Hq // w.Hkv
+    for b in range(len(w.ctx)):
+        L = int(w.lens[b])
+        assert (got[b, L:] == 55.0).all(), f"{what}: a row behind a tree was written"
+        for hk in range(w.Hkv if L else 0):
+            ref, bound = rows_and_bounds(w, out_dtype, b, hk)
+            have = got[b, :L, hk * G:(hk + 1) * G].reshape(L * G, w.D)
+            err = np.abs(have - ref)
+            assert (err <= bound).all(), (f"{what}, sequence {b}, KV head {hk}: {np.nanmax(err / bound):.3f} of the "
+                                          f"bound, {int((~(err <= bound)).sum())} outputs")
 
 
 # ---------------------------------------------------------------- scores far from zero
@@ -47,3 +106,37 @@ def test_scores_beyond_what_fp32_resolves(kvc, D, Hq, Hkv, hist, T, out_dtype):
                 few = (win.sum() / 16 * 2.0 ** -23 + 2.0 ** -20) * np.abs(V[win, hk]).mean(0)
                 tol = few + 2.0 ** -25 + (2.0 ** -11 if out_dtype == torch.float16 else 2.0 ** -24) * np.abs(want)
                 assert (np.abs(got[0, t, h] - want) <= tol).all(), (sign, t, h)
+
+
+# ---------------------------------------------------------------- weights far below the largest
+@pytest.mark.parametrize("out_dtype", [torch.float16, torch.float32])
+@pytest.mark.parametrize("nats", [9.0, 16.0, 17.4, 20.0])
+@pytest.mark.parametrize("D,Hq,Hkv,T,at", [(64, 2, 1, 3, 0), (128, 8, 1, 20, 0), (64, 2, 2, 2, 65535),
+                                           (128, 4, 2, 64, 40000)])
+def test_a_long_tail_below_one_key(kvc, D, Hq, Hkv, T, at, nats, out_dtype):
+    """An attention sink: one key of 65,536 with a value of 0, `nats` above all others, whose values are about 1.  What
+    comes out is the others' mass, whatever part of the context the sink stands in."""
+    hist = 65536
+    w = Tree(62, [hist], [T], T, Hq, Hkv, D)
+    n = hist + T
+    w.scale = 1.0
+    w.q[:] = 0
+    w.q[..., 0] = 8.0
+    pos = np.arange(n)
+    w.k[w.table[0][pos // 16], :, pos % 16] = 0
+    w.k[w.table[0][at // 16], :, at % 16, 0] = nats / 8
+    v = np.abs(w.v) * np.float16(0.25) + np.float16(1)
+    w.v[w.table[0][pos // 16], :, pos % 16] = v[w.table[0][pos // 16], :, pos % 16]
+    w.v[w.table[0][at // 16], :, at % 16] = 0
+    got = w.run(kvc, out_dtype)
+    mass = n * np.exp(-nats)
+    assert (np.abs(got[0] / (mass / (1 + mass)) - 1.2) < 0.2).all()
+    check(w, got, out_dtype, f"sink {nats} nats above")
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float16, torch.float32])
+def test_weights_of_every_size(kvc, out_dtype):
+    """Scores spread over 30 nats, their largest anywhere, so that every range of weights carries some of the output."""
+    w = Tree(63, [40000, 7000], [10, 3], 10, 8, 2, 64, sharp=6.0)
+    w.v[:] = np.where(np.isnan(w.v), w.v, np.abs(w.v))
+    check(w, w.run(kvc, out_dtype), out_dtype, "sharp scores")
