@@ -13,7 +13,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_tree import Tree, kvc  # noqa: F401  (kvc is a fixture)
+from test_gpu_tree import MANY, TREES, Tree, kvc, many  # noqa: F401  (kvc is a fixture)
 from oracle import tree
 
 pytestmark = pytest.mark.gpu
@@ -140,3 +140,60 @@ def test_weights_of_every_size(kvc, out_dtype):
     w = Tree(63, [40000, 7000], [10, 3], 10, 8, 2, 64, sharp=6.0)
     w.v[:] = np.where(np.isnan(w.v), w.v, np.abs(w.v))
     check(w, w.run(kvc, out_dtype), out_dtype, "sharp scores")
+
+
+# ---------------------------------------------------------------- each row by its own bound
+LONG = [i for i, t in enumerate(TREES) if max(t[0]) >= 500] + [5, 6, 13]
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float16, torch.float32])
+@pytest.mark.parametrize("case", LONG)
+def test_every_output_within_its_rows_bound(kvc, case, out_dtype):
+    hist, lens, T, Hq, Hkv, D, empty = TREES[case]
+    w = Tree(70 + case, hist, lens, T, Hq, Hkv, D, empty)
+    check(w, w.run(kvc, out_dtype), out_dtype, f"case {case}")
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float16, torch.float32])
+@pytest.mark.parametrize("case", [2, 4, 6])
+def test_every_output_of_many_sequences_within_its_rows_bound(kvc, case, out_dtype):
+    B, T, Hq, Hkv, D, far, none = MANY[case]
+    w = many(case, T, Hq, Hkv, D, B, far, none)
+    check(w, w.run(kvc, out_dtype), out_dtype, f"many, case {case}")
+
+
+PLANTED = [
+    # hist, tree lens, T, Hq, Hkv, D: one cluster of several CTAs; several clusters; one, two and four pairs of row tiles
+    ([4000, 2100], [12, 12], 12, 8, 1, 128),
+    ([30000, 9000, 700], [5, 5, 5], 5, 2, 1, 64),
+    ([20000], [40], 40, 8, 1, 128),
+    ([9000], [64], 64, 14, 2, 64),
+    ([6000, 200], [64, 64], 64, 16, 1, 64),
+    ([65536], [16], 16, 4, 1, 128),
+]
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float16, torch.float32])
+@pytest.mark.parametrize("case", range(len(PLANTED)))
+def test_no_tile_of_keys_is_lost(kvc, case, out_dtype):
+    """Every tile of 128 keys of the history holds a key that carries much of some row's mass: an output without any one
+    of them lies far outside the bound, which is shown on the definition first."""
+    hist, lens, T, Hq, Hkv, D = PLANTED[case]
+    w = Tree(80 + case, hist, lens, T, Hq, Hkv, D)
+    rng = np.random.default_rng([81, case])
+    G = Hq // Hkv
+    for b, h in enumerate(hist):
+        for hk in range(Hkv):
+            for i, s in enumerate(range(0, h, 128)):
+                t, g = divmod(i % (lens[b] * G), G)
+                row = w.q[b, t, hk * G + g].astype(np.float64)
+                at = s + int(rng.integers(0, min(128, h - s)))
+                w.k[w.table[b][at // 16], hk, at % 16] = row * (np.log(h) / (w.scale * (row @ row)))
+    got = w.run(kvc, out_dtype)
+    check(w, got, out_dtype, f"planted case {case}")
+    for b, h in enumerate(hist):
+        for hk in range(Hkv):
+            ref, bound, without = rows_and_bounds(w, out_dtype, b, hk, tiles=True)
+            whole = h // 128  # (the tile that reaches into the tree may be all that a row of it sees)
+            lost = np.abs(without[:whole] - ref) > 3 * bound
+            assert lost.any((1, 2)).all(), f"case {case}: leaving out tiles {np.flatnonzero(~lost.any((1, 2)))} would pass"
