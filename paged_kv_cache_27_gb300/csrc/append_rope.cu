@@ -99,7 +99,11 @@ __device__ __forceinline__ void store16(__half* p, uint4 v) {
         *reinterpret_cast<uint4*>(p) = v;
 }
 
-template <int D, bool kStream>
+// kAll: the whole row is rotated.  Otherwise a lane behind rot_dim computes along and keeps its values by a select (a
+// rotation by nothing would add 0 times the other value, NaN where that is not finite).  16,384 tokens, 32 / 8 heads,
+// D = 128: 66.2 us with kAll, 67.4 without; a branch in place of the selects takes longer (1923 tokens, 14 / 2 heads,
+// D = 64, half rotated: 4.3 us against 4.0).
+template <int D, bool kStream, bool kAll>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv_append_rope_kernel(const Params p) {
     constexpr int kLanes = D / 16;        // lanes of a row
     constexpr int kRows = 32 / kLanes;    // rows a warp handles at a time
@@ -122,26 +126,16 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv_append_rope_kernel
     }
     __syncwarp();
 
-    // this lane's two chunks and, per chunk, whether it is rotated
+    // this lane's two chunks, and whether they are rotated (both or neither: rot_dim is a multiple of 16)
     const int hc = p.rot / 16;  // chunks of the first half of the rotated dims
-    int c0, c1;
-    bool r0, r1;
-    if (p.interleaved) {
-        c0 = 2 * l;
-        c1 = c0 + 1;
-        r0 = c0 * 8 < p.rot;
-        r1 = c1 * 8 < p.rot;
-    } else {
-        r0 = r1 = l < hc;
-        c0 = r0 ? l : 2 * l;  // behind the pairs: 2 hc + 2 (l - hc)
-        c1 = r0 ? l + hc : 2 * l + 1;
-    }
+    const bool on = kAll || l < hc;
+    const bool apart = on && !p.interleaved;
+    const int c0 = apart ? l : 2 * l, c1 = apart ? l + hc : 2 * l + 1;  // (behind the pairs: 2 hc + 2 (l - hc))
     // cosines and sines of the lane's 8 pairs
     uint64_t cs[4], sn[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int a = p.interleaved ? (i < 2 ? c0 * 4 + 2 * i : c1 * 4 + 2 * i - 4) : c0 * 8 + 2 * i;
-        const bool on = p.interleaved ? (i < 2 ? r0 : r1) : r0;
         const float2 x = on ? s_cs[warp][a] : make_float2(1.f, 0.f), y = on ? s_cs[warp][a + 1] : make_float2(1.f, 0.f);
         cs[i] = pack_f32x2(x.x, y.x);
         sn[i] = pack_f32x2(x.y, y.y);
@@ -217,20 +211,26 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv_append_rope_kernel
                     if (p.interleaved) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            x[i] = rotate_pair(x[i], cs[i / 2], sn[i / 2], i & 1);
-                            y[i] = rotate_pair(y[i], cs[2 + i / 2], sn[2 + i / 2], i & 1);
+                            const uint64_t ra = rotate_pair(x[i], cs[i / 2], sn[i / 2], i & 1);
+                            const uint64_t rb = rotate_pair(y[i], cs[2 + i / 2], sn[2 + i / 2], i & 1);
+                            x[i] = on ? ra : x[i];
+                            y[i] = on ? rb : y[i];
                         }
                     } else {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const uint64_t a = x[i], b = y[i];
-                            x[i] = fma_f32x2(a, cs[i], neg_f32x2(mul_f32x2(b, sn[i])));
-                            y[i] = fma_f32x2(b, cs[i], mul_f32x2(a, sn[i]));
+                            const uint64_t ra = fma_f32x2(a, cs[i], neg_f32x2(mul_f32x2(b, sn[i])));
+                            const uint64_t rb = fma_f32x2(b, cs[i], mul_f32x2(a, sn[i]));
+                            x[i] = on ? ra : a;
+                            y[i] = on ? rb : b;
                         }
                     }
                     // without a norm, dims that are not rotated keep their bits
-                    if (wt != nullptr || r0) o0 = pack8(x);
-                    if (wt != nullptr || r1) o1 = pack8(y);
+                    if (wt != nullptr || on) {
+                        o0 = pack8(x);
+                        o1 = pack8(y);
+                    }
                 }
                 if (h >= H) continue;
                 auto put = [&](__half* row) {
@@ -293,11 +293,16 @@ cudaError_t launch_append_rope(const RopeArgs& a, cudaStream_t stream) {
     // 67.9 us.  Smaller calls (512 tokens: 5.7 us either way) leave their rows there for the attention that follows.
     const bool stream_by = a.n * (a.Hq + 2 * a.Hkv) * a.D * 4 > (int64_t(128) << 20);
     const dim3 grid(static_cast<unsigned>(blocks)), block(rope::kWarps * 32);
-    switch (a.D + (stream_by ? 1 : 0)) {
-        case 64: return launch(rope::kv_append_rope_kernel<64, false>, grid, block, 0, stream, true, 1u, p);
-        case 65: return launch(rope::kv_append_rope_kernel<64, true>, grid, block, 0, stream, true, 1u, p);
-        case 128: return launch(rope::kv_append_rope_kernel<128, false>, grid, block, 0, stream, true, 1u, p);
-        case 129: return launch(rope::kv_append_rope_kernel<128, true>, grid, block, 0, stream, true, 1u, p);
+    const auto go = [&](auto kernel) { return launch(kernel, grid, block, 0, stream, true, 1u, p); };
+    switch (a.D + (stream_by ? 2 : 0) + (a.rot_dim == a.D ? 1 : 0)) {
+        case 64: return go(rope::kv_append_rope_kernel<64, false, false>);
+        case 65: return go(rope::kv_append_rope_kernel<64, false, true>);
+        case 66: return go(rope::kv_append_rope_kernel<64, true, false>);
+        case 67: return go(rope::kv_append_rope_kernel<64, true, true>);
+        case 128: return go(rope::kv_append_rope_kernel<128, false, false>);
+        case 129: return go(rope::kv_append_rope_kernel<128, false, true>);
+        case 130: return go(rope::kv_append_rope_kernel<128, true, false>);
+        case 131: return go(rope::kv_append_rope_kernel<128, true, true>);
         default: return cudaErrorInvalidValue;
     }
 }

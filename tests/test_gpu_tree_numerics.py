@@ -13,7 +13,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_tree import MANY, TREES, Tree, kvc, many  # noqa: F401  (kvc is a fixture)
+import workloads
+from test_gpu_tree import MANY, TREES, Tree, dev, host, kvc, many  # noqa: F401  (kvc is a fixture)
 from oracle import tree
 
 pytestmark = pytest.mark.gpu
@@ -197,3 +198,32 @@ def test_no_tile_of_keys_is_lost(kvc, case, out_dtype):
             whole = h // 128  # (the tile that reaches into the tree may be all that a row of it sees)
             lost = np.abs(without[:whole] - ref) > 3 * bound
             assert lost.any((1, 2)).all(), f"case {case}: leaving out tiles {np.flatnonzero(~lost.any((1, 2)))} would pass"
+
+
+# ---------------------------------------------------------------- norm, rotation, append
+@pytest.mark.parametrize("D,rot,inter", [(64, 32, False), (64, 16, True), (128, 64, True), (128, 96, False), (64, 0, False)])
+def test_an_infinity_behind_the_rotated_values_stays_there(kvc, D, rot, inter):
+    """A row with an infinity is normed to NaN where that is and to 0 elsewhere; values behind rot_dim take nothing from
+    one another."""
+    n, H = 5, 3
+    rng = np.random.default_rng([90, D, rot])
+    x = workloads.normal_f16(rng, (n, H, D))
+    at = rng.integers(rot, D, n)
+    x[np.arange(n), 1, at] = np.inf
+    x[0, 1, at[0]] = -np.inf
+    w = workloads.normal_f16(rng, (D,))
+    pos = np.arange(n, dtype=np.int32) + 3
+    freq = 1e4 ** (-np.arange(0, rot, 2) / max(rot, 1))
+    out, k_out = (torch.empty((n, H, D), dtype=torch.float16, device="cuda") for _ in range(2))
+    q = dev(x)
+    kvc.kv_append_rope(q, q, q, dev(pos), dev(kvc.kv_rope_turns(freq)), out, q_weight=dev(w), k_weight=dev(w),
+                       interleaved=inter, k_out=k_out)
+    with np.errstate(invalid="ignore"):
+        ref = tree.norm_rotate(x, w, 1e-6, pos[:, None] * freq, inter)
+    hit = np.zeros((n, D), bool)
+    hit[np.arange(n), at] = True
+    assert (np.isnan(ref[:, 1]) == hit).all() and (ref[:, 1][~hit] == 0).all()
+    for got in (host(out), host(k_out)):
+        assert (np.isnan(got) == np.isnan(ref)).all() and (got[:, 1][~hit] == 0).all()
+        rest = [0, 2]  # heads without one
+        assert (np.abs(got[:, rest] - ref[:, rest]) <= 2.0 ** -10 * np.abs(ref[:, rest]) + 2.0 ** -14).all()
