@@ -10,8 +10,9 @@
 //
 // Angles.  fp32 has no room for position * frequency (a position of 100,000 leaves 2^-7 of a radian), so a frequency
 // is held as the fraction of a full turn it advances per position, a 64-bit integer in units of 2^-64 turns
-// (kv_rope_turns).  The product with the position then wraps modulo one turn by itself, exactly; its top 32 bits are
-// the angle in units of 2^-32 turns, and sincospif takes them as a multiple of pi (error 2^-24 turns / 2).
+// (kv_rope_turns).  The product with the position then wraps modulo one turn by itself, exactly; it is rounded to 2^-32
+// turn (off by 2^-33), and to fp32 as a multiple of pi for sincospif (by 2^-26 turn at most, half a step below half a
+// turn).
 //
 // Layout.  A row is D / 16 lanes of two 16-byte chunks each, chosen so that both values of every pair sit in one
 // lane (chunks l and l + rot_dim / 16, or 2 l and 2 l + 1): no exchange between lanes but the sum of squares.  A warp
@@ -119,7 +120,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv_append_rope_kernel
 
     const int64_t pos = p.rot > 0 ? p.positions[t] : 0;
     for (int i = lane; i < p.rot / 2; i += 32) {
-        const int32_t a = static_cast<int32_t>((static_cast<uint64_t>(pos) * p.turns[i]) >> 32);
+        const int32_t a = static_cast<int32_t>((static_cast<uint64_t>(pos) * p.turns[i] + 0x80000000u) >> 32);
         float s, c;
         sincospif(static_cast<float>(a) * 0x1p-31f, &s, &c);
         s_cs[warp][i] = make_float2(c, s);

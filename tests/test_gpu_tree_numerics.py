@@ -227,3 +227,24 @@ def test_an_infinity_behind_the_rotated_values_stays_there(kvc, D, rot, inter):
         assert (np.isnan(got) == np.isnan(ref)).all() and (got[:, 1][~hit] == 0).all()
         rest = [0, 2]  # heads without one
         assert (np.abs(got[:, rest] - ref[:, rest]) <= 2.0 ** -10 * np.abs(ref[:, rest]) + 2.0 ** -14).all()
+
+
+@pytest.mark.parametrize("pos", [1, 3, 2 ** 16 + 1, 2 ** 31 - 1, -1])
+def test_angles_are_rounded_to_the_nearest(kvc, pos):
+    """An angle is within 2^-33 turn (the product rounded to 2^-32) and half an fp32 step (2^-24 of at most half a
+    turn) of position x frequency; here it is that of (0, 65504) turned by about 2^-32 turn."""
+    D = 64
+    far = [2 ** 32 - 1 - 5 * i if i % 2 else 2 ** 31 + 1 + 5 * i for i in range(D // 2)]  # position x frequency
+    turns = np.array([x * pow(pos % 2 ** 64, -1, 2 ** 64) % 2 ** 64 for x in far], np.uint64)
+    q = np.zeros((1, 1, D), np.float16)
+    q[..., D // 2:] = 65504
+    out = torch.empty((1, 1, D), dtype=torch.float16, device="cuda")
+    d = dev(q)
+    kvc.kv_append_rope(d, d, d, dev(np.array([pos], np.int32)), dev(turns.view(np.int64)), out)
+    angle = np.array(far, np.float64) * (2 * np.pi / 2.0 ** 64)
+    half = np.abs(angle) * 2.0 ** -24 + 2 * np.pi * 2.0 ** -33
+    got = host(out)[0, 0].astype(np.float64)
+    for have, want in ((got[:D // 2], -65504 * np.sin(angle)), (got[D // 2:], 65504 * np.cos(angle))):
+        # cosine, sine, product: 2^-22; the angle's error turns the vector; the store
+        bound = 65504 * half + 2.0 ** -22 * np.abs(want) + 2.0 ** -11 * np.abs(want) + 2.0 ** -25
+        assert (np.abs(have - want) <= bound).all(), np.max(np.abs(have - want) / bound)
