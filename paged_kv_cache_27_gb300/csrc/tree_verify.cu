@@ -69,8 +69,10 @@ __device__ __forceinline__ void st_cluster_u64(uint32_t addr, uint64_t v) {
 
 // a probability: NaN and negative values count as 0, values above 1 as 1
 __device__ __forceinline__ float prob(float x) { return __saturatef(x); }
-__device__ __forceinline__ float load_prob(const float* row, int i) { return prob(__ldg(row + i)); }
-__device__ __forceinline__ float load_prob(const __half* row, int i) { return prob(__half2float(__ldg(row + i))); }
+// (Ordinary loads: the rows may be written by the kernel in front, under whose end this one is launched, so they are not
+// constant for its whole life, which loads through the read-only path ask for.)
+__device__ __forceinline__ float load_prob(const float* row, int i) { return prob(row[i]); }
+__device__ __forceinline__ float load_prob(const __half* row, int i) { return prob(__half2float(row[i])); }
 
 // (p - a q)^+ <= 1, a = ah + al >= 0, as a multiple of 2^-23 (in the bits of the first, above those of 1) and a
 // remainder, at most about 2^-24, in units of 2^-45 (in the bits of the second, above those of kFine)
@@ -161,8 +163,8 @@ struct LaneSum {
 };
 // this lane's share of the weights of entries [b, e), one at a time: entries b + lane, b + lane + 32, ...
 template <int kMode, typename T>
-__device__ __forceinline__ void add_entries(LaneSum<kMode>& acc, const T* __restrict__ p, const T* __restrict__ q, int b,
-                                            int e, const Factor& f) {
+__device__ __forceinline__ void add_entries(LaneSum<kMode>& acc, const T* p, const T* q, int b, int e,
+                                            const Factor& f) {
     constexpr int U = 8;
     for (int i0 = b + (threadIdx.x & 31); i0 < e; i0 += 32 * U) {
         float pv[U], qv[U];
@@ -197,8 +199,7 @@ __device__ __forceinline__ void unpack16(const uint4& v, uint64_t (&x)[8 / sizeo
 // asked for before them (48 -> 47 us).  A ring of asynchronous copies to shared memory in place of the registers is
 // slower, alone on an SM (3.5 -> 4.0 us a pass) and not (43 -> 45 us).
 template <int kMode, typename T>
-__device__ __forceinline__ uint64_t lane_weights(const T* __restrict__ p, const T* __restrict__ q, int b, int e,
-                                                 const Factor& f) {
+__device__ __forceinline__ uint64_t lane_weights(const T* p, const T* q, int b, int e, const Factor& f) {
     LaneSum<kMode> acc;
     if (kMode != kPlain && (reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15u) {
         add_entries(acc, p, q, b, e, f);
@@ -222,8 +223,8 @@ __device__ __forceinline__ uint64_t lane_weights(const T* __restrict__ p, const 
             const int i = i0 + u * 32;
             nx[u] = ny[u] = make_uint4(0u, 0u, 0u, 0u);
             if (i < nv) {
-                nx[u] = __ldg(pv + i);
-                if constexpr (kMode != kPlain) ny[u] = __ldg(qv + i);
+                nx[u] = pv[i];
+                if constexpr (kMode != kPlain) ny[u] = qv[i];
             }
         }
     };

@@ -1,6 +1,8 @@
 """Pins of the fp64 definitions of tree-drafted decoding (oracle/tree.py), and the library's host helpers (no GPU)."""
 import ctypes
 import math
+import os
+import re
 import struct
 
 import numpy as np
@@ -251,3 +253,14 @@ def test_calls_with_words_are_the_calls():
         kvc.kvc_call(9, words(0))
     with pytest.raises(ValueError):
         kvc.kvc_call(1, b"1234567")
+
+
+def test_the_steps_kernels_read_nothing_as_constant():
+    """They are launched before the kernel in front of them has ended, and may read what it writes: no load through the
+    read-only path, which is defined only for data that is constant for a kernel's whole life, and no pointer that is
+    promised to be read alone."""
+    csrc = os.path.join(os.path.dirname(kvc.__file__), "csrc")
+    for name in ("append_rope.cu", "tree_attention.cu", "tree_verify.cu", "tree_commit.cu"):
+        with open(os.path.join(csrc, name)) as f:
+            code = re.sub(r"//.*", "", f.read())
+        assert not re.search(r"__ldg|__restrict__|\.nc\b|ld_nc", code), name
