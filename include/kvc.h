@@ -470,7 +470,9 @@ kvc_status paged_decode_attention_static_workspace(const void* q, const void* k_
  * which the kept path is the end of an ordinary context.  The four calls keep
  * the stream's order whatever kvc_set_launch_overlap says: their kernels are
  * launched under the end of the kernel in front, but read and write nothing
- * before it is done, and release nothing early themselves. */
+ * before it is done, and release nothing early themselves.  An output (or
+ * workspace) that shares memory with anything its call reads or with another
+ * output is refused, but for kv_append_rope's rows in place. */
 
 /* Host helper: from parents [B][T] (parents[b][0] is not read; otherwise
  * 0 <= parents[b][t] < t) and tree_lens [B] (NULL: T each) the masks [B][T]

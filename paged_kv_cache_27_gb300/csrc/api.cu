@@ -2,11 +2,13 @@
 // host-side block management; device work is forwarded to the launchers.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <new>
 #include <string>
 #include <tuple>
@@ -809,12 +811,34 @@ static bool overlap(const void* a, int64_t bytes_a, const void* b, int64_t bytes
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return a && b && x < y + static_cast<uintptr_t>(bytes_b) && y < x + static_cast<uintptr_t>(bytes_a);
 }
+struct Span {
+    const void* at;  // null: left out
+    int64_t bytes;
+};
+// n rows of `row` elements of `size` bytes, `stride` elements apart
+static Span rows_span(const void* at, int64_t n, int64_t stride, int64_t row, int64_t size) {
+    const __int128 bytes = (static_cast<__int128>(n - 1) * stride + row) * size, most = __int128(1) << 56;
+    return {at, static_cast<int64_t>(std::min(bytes, most))};
+}
+// Outputs that share memory with an input or with each other: other CTAs may still read what one has written.
+static kvc_status check_overlap(std::initializer_list<Span> out, std::initializer_list<Span> in) {
+    for (const Span* o = out.begin(); o != out.end(); ++o) {
+        for (const Span& i : in)
+            if (overlap(o->at, o->bytes, i.at, i.bytes)) return fail(KVC_ERR_INVALID, "an output overlaps what the call reads");
+        for (const Span* other = out.begin(); other != o; ++other)
+            if (overlap(o->at, o->bytes, other->at, other->bytes)) return fail(KVC_ERR_INVALID, "an output overlaps another");
+    }
+    return KVC_OK;
+}
 
 kvc_status kv_tree_masks(const int32_t* parents, const int32_t* tree_lens, int B, int T, uint64_t* masks,
                          int32_t* depths) {
     if (B < 0 || T < 1) return fail(KVC_ERR_INVALID, "bad sizes");
     if (T > kvc::kMaxTreeNodes) return fail(KVC_ERR_UNSUPPORTED, "trees of %d nodes not supported (%d)", T, kvc::kMaxTreeNodes);
     if (B > 0 && (!parents || !masks)) return fail(KVC_ERR_INVALID, "null pointer");
+    const int64_t nodes = static_cast<int64_t>(B) * T;
+    kvc_status s = check_overlap({{masks, nodes * 8}, {depths, nodes * 4}}, {{parents, nodes * 4}, {tree_lens, B * int64_t(4)}});
+    if (s != KVC_OK) return s;
     for (int b = 0; b < B; ++b) {  // everything is checked before anything is written
         const int len = tree_lens ? tree_lens[b] : T;
         if (len < 0 || len > T) return fail(KVC_ERR_INVALID, "sequence %d: tree length %d outside [0, %d]", b, len, T);
@@ -879,17 +903,23 @@ kvc_status kv_append_rope(const void* q, int64_t q_stride, const void* k, int64_
     if ((q_out == q && q_stride != qrow) || (k_out == k && k_stride != krow) || (v_out == v && v_stride != krow))
         return fail(KVC_ERR_INVALID, "in place only where the rows are packed");
     {
-        const struct {
-            const void* ptr;
-            int64_t bytes;
-        } in[3] = {{q, ((n - 1) * q_stride + qrow) * 2},
-                   {k, ((n - 1) * k_stride + krow) * 2},
-                   {v, ((n - 1) * v_stride + krow) * 2}},
-          out[3] = {{q_out, n * qrow * 2}, {k_out, n * krow * 2}, {v_out, n * krow * 2}};
-        for (int o = 0; o < 3; ++o)
-            for (int i = 0; i < 3; ++i)
-                if ((i != o || out[o].ptr != in[i].ptr) && overlap(out[o].ptr, out[o].bytes, in[i].ptr, in[i].bytes))
-                    return fail(KVC_ERR_INVALID, "an output overlaps the rows that are read");
+        // in place: an output that is its own input's rows
+        const int64_t cache_bytes = static_cast<int64_t>(num_blocks) * krow * block_size * 2;
+        const Span q_in = rows_span(q, n, q_stride, qrow, 2), k_in = rows_span(k, n, k_stride, krow, 2),
+                   v_in = rows_span(v, n, v_stride, krow, 2);
+        const Span none = {nullptr, 0}, q_o = {q_out, n * qrow * 2}, k_o = {k_out, n * krow * 2}, v_o = {v_out, n * krow * 2};
+        const Span kc = {k_cache, cache_bytes}, vc = {v_cache, cache_bytes};
+        const Span qw = {q_weight, head_dim * 2}, kw = {k_weight, head_dim * 2};
+        const Span tn = {rot_dim ? turns : nullptr, rot_dim * 4}, ps = {rot_dim ? positions : nullptr, n * int64_t(4)};
+        const Span sl = {slot_mapping, n * int64_t(8)};
+        for (const auto& [o, own, a, b] : {std::tuple(q_o, q_in, k_in, v_in), std::tuple(k_o, k_in, q_in, v_in),
+                                           std::tuple(v_o, v_in, q_in, k_in)}) {
+            kvc_status st = check_overlap({o}, {o.at == own.at ? none : own, a, b});
+            if (st != KVC_OK) return st;
+        }
+        kvc_status st = check_overlap({kc, vc}, {q_in, k_in, v_in});
+        if (st == KVC_OK) st = check_overlap({q_o, k_o, v_o, kc, vc}, {qw, kw, tn, ps, sl});
+        if (st != KVC_OK) return st;
     }
     if (cache) {
         kvc_status st = checked([&]() -> kvc_status {
@@ -973,6 +1003,13 @@ kvc_status paged_decode_tree_attention(const void* q, const void* k_cache, const
         return fail(KVC_ERR_CAPACITY, "max_context_len %d beyond max_blocks * block_size", max_context_len);
     if (out_dtype != KVC_F16 && out_dtype != KVC_F32) return fail(KVC_ERR_INVALID, "bad out_dtype");
     if (!std::isfinite(scale)) return fail(KVC_ERR_INVALID, "scale is not finite");
+    const int64_t rows = static_cast<int64_t>(B) * T * Hq * head_dim;
+    const int64_t cache = static_cast<int64_t>(num_blocks) * Hkv * block_size * head_dim * 2;
+    const Span in[] = {{q, rows * 2}, {k_cache, cache}, {v_cache, cache}, {block_table, static_cast<int64_t>(B) * max_blocks * 4},
+                       {context_lens, B * int64_t(4)}, {masks, static_cast<int64_t>(B) * T * 8}, {tree_lens, B * int64_t(4)}};
+    const Span out_span = {out, rows * (out_dtype == KVC_F32 ? 4 : 2)};
+    s = check_overlap({out_span}, {in[0], in[1], in[2], in[3], in[4], in[5], in[6]});
+    if (s != KVC_OK) return s;
     s = checked([&]() -> kvc_status {
         std::vector<int32_t> ctx, tree, table;
         kvc_status e = copy_to_host(ctx, context_lens, static_cast<size_t>(B), as_stream(stream));
@@ -997,6 +1034,9 @@ kvc_status paged_decode_tree_attention(const void* q, const void* k_cache, const
     cudaError_t e = kvc::tree_plan(B, Hq, Hkv, head_dim, max_context_len, T, &plan);
     if (e != cudaSuccess) return cuda_fail(e, "tree plan");
     s = check_workspace(plan.workspace_bytes, workspace, workspace_bytes);
+    if (s == KVC_OK && plan.workspace_bytes)
+        s = check_overlap({{workspace, static_cast<int64_t>(plan.workspace_bytes)}},
+                          {out_span, in[0], in[1], in[2], in[3], in[4], in[5], in[6]});
     if (s != KVC_OK) return s;
     kvc::TreeArgs a;
     a.q = static_cast<const __half*>(q);
@@ -1043,7 +1083,13 @@ kvc_status draft_tree_verify(const void* target_probs, int64_t p_stride, const v
     const uintptr_t size = prob_dtype == KVC_F32 ? 4 : 2;
     if (reinterpret_cast<uintptr_t>(target_probs) % size || reinterpret_cast<uintptr_t>(draft_probs) % size)
         return fail(KVC_ERR_INVALID, "probabilities must be aligned to their type");
-    kvc_status s = checked([&]() -> kvc_status {
+    const int64_t nodes_bytes = static_cast<int64_t>(B) * T * 4, per = B * int64_t(4);
+    kvc_status s = check_overlap({{path, nodes_bytes}, {path_len, per}, {next_token, per}},
+                                 {rows_span(target_probs, static_cast<int64_t>(B) * T, p_stride, V, size),
+                                  rows_span(draft_probs, static_cast<int64_t>(B) * T, q_stride, V, size),
+                                  {tokens, nodes_bytes}, {parents, nodes_bytes}, {uniforms, nodes_bytes}, {tree_lens, per}});
+    if (s != KVC_OK) return s;
+    s = checked([&]() -> kvc_status {
         std::vector<int32_t> tok, par, len;
         const size_t n = static_cast<size_t>(B) * T;
         kvc_status e = copy_to_host(tok, tokens, n, as_stream(stream));
@@ -1098,11 +1144,13 @@ kvc_status kv_tree_commit(kvc_handle h, const int32_t* block_table, int max_bloc
     if (B == 0) return KVC_OK;
     if (!block_table || !context_lens || !path || !path_len || !new_context_lens) return fail(KVC_ERR_INVALID, "null pointer");
     const int64_t per = static_cast<int64_t>(B) * 4;
-    if (overlap(new_context_lens, per, context_lens, per) || overlap(new_context_lens, per, tree_lens, per) ||
-        overlap(new_context_lens, per, path_len, per) || overlap(new_context_lens, per, path, per * P) ||
-        overlap(new_context_lens, per, block_table, per * max_blocks))
-        return fail(KVC_ERR_INVALID, "new_context_lens overlaps what the call reads");
-    kvc_status s = checked([&]() -> kvc_status {
+    const int64_t layer = static_cast<int64_t>(h->cfg.num_blocks) * h->cfg.num_kv_heads * h->cfg.block_size * h->cfg.head_dim;
+    kvc_status s = check_overlap({{new_context_lens, per}, rows_span(h->k_pool, h->cfg.num_layers, layer, layer, 2),
+                                  rows_span(h->v_pool, h->cfg.num_layers, layer, layer, 2)},
+                                 {{context_lens, per}, {tree_lens, per}, {path_len, per}, {path, per * P},
+                                  {block_table, per * max_blocks}});
+    if (s != KVC_OK) return s;
+    s = checked([&]() -> kvc_status {
         std::vector<int32_t> ctx, tree, nodes, len, table;
         kvc_status e = copy_to_host(ctx, context_lens, static_cast<size_t>(B), as_stream(stream));
         if (e == KVC_OK && tree_lens) e = copy_to_host(tree, tree_lens, static_cast<size_t>(B), as_stream(stream));

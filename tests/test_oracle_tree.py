@@ -264,3 +264,62 @@ def test_the_steps_kernels_read_nothing_as_constant():
         with open(os.path.join(csrc, name)) as f:
             code = re.sub(r"//.*", "", f.read())
         assert not re.search(r"__ldg|__restrict__|\.nc\b|ld_nc", code), name
+
+
+# ---------------------------------------------------------------- outputs among the inputs, or among each other
+def at(i, off=0):
+    """The i-th of addresses 16 MB apart, more than any buffer below holds."""
+    return ctypes.c_void_p((i << 24) + off)
+
+
+def test_append_rope_refuses_outputs_among_all_it_reads():
+    base = dict(q=at(1), qs=256, k=at(2), ks=128, v=at(3), vs=128, n=20, Hq=4, Hkv=2, D=64, qw=at(4), kw=at(5), eps=1e-6,
+                turns=at(6), rot=64, inter=0, pos=at(7), qo=at(8), ko=at(9), vo=at(10), kc=at(11), vc=at(12), NB=4, bs=16,
+                slots=at(13), st=None)
+    cache = 4 * 2 * 16 * 64 * 2
+    for change in (dict(kc=at(1)), dict(vc=at(2, -16)), dict(kc=at(3, 20 * 256 - 16)), dict(kc=at(1, 16 - cache)),
+                   dict(qo=at(4)), dict(ko=at(5, 112)), dict(vo=at(6, 240)), dict(qo=at(7, 64)), dict(qo=at(13, 144)),
+                   dict(kc=at(4)), dict(vc=at(13)), dict(kc=at(7, 64)), dict(ko=at(8)), dict(vo=at(9, 16)),
+                   dict(qo=at(11, 16)), dict(vo=at(12)), dict(vc=at(11, cache - 16)), dict(qs=2 ** 60, qo=at(1, 2 ** 40))):
+        refused("kv_append_rope", list({**base, **change}.values()), "INVALID", "overlaps")
+
+
+def test_tree_attention_refuses_an_output_among_its_inputs():
+    base = dict(q=at(1), k=at(2), v=at(3), NB=64, table=at(4), mb=8, ctx=at(5), masks=at(6), lens=at(7), T=4, B=2, Hq=4,
+                Hkv=2, D=64, bs=16, most=128, scale=0.125, out=at(8), od=0, ws=None, wb=0, st=None)
+    size = 2 * 4 * 4 * 64
+    for change in (dict(out=at(1)), dict(out=at(1, size * 2 - 16)), dict(out=at(1, 16 - size * 2)),
+                   dict(out=at(1, 16 - size * 4), od=1), dict(out=at(2)), dict(out=at(3, 64 * 2 * 16 * 64 * 2 - 16)),
+                   dict(out=at(4, 48)), dict(out=at(5)), dict(out=at(6, 48)), dict(out=at(7))):
+        refused("paged_decode_tree_attention", list({**base, **change}.values()), "INVALID", "overlaps")
+
+
+def test_verify_refuses_outputs_among_its_inputs_and_each_other():
+    base = dict(p=at(1), ps=104, q=at(2), qs=100, dt=1, tok=at(3), par=at(4), lens=at(5), u=at(6), B=3, T=4, V=100,
+                distinct=0, path=at(7), plen=at(8), nxt=at(9), st=None)
+    for change in (dict(path=at(3)), dict(path=at(4, 44)), dict(plen=at(5)), dict(nxt=at(5, 8)), dict(plen=at(6, 44)),
+                   dict(nxt=at(3, 8)), dict(path=at(1, 11 * 104 * 4 + 396)), dict(path=at(2, -44)),
+                   dict(nxt=at(1, 8), dt=0), dict(plen=at(7, 44)), dict(nxt=at(8, 8)), dict(path=at(9, -44))):
+        refused("draft_tree_verify", list({**base, **change}.values()), "INVALID", "overlaps")
+
+
+def test_commit_refuses_lengths_and_tables_in_its_pools():
+    hp = ctypes.c_void_p()
+    cfg = kvc.KvcConfig(2, 4, 2, 64)._c()
+    assert kvc._lib.kv_cache_create(ctypes.byref(cfg), at(1), at(2), ctypes.byref(hp)) == 0  # never followed below
+    size = 2 * 4 * 2 * 16 * 64 * 2
+    base = dict(h=hp, table=at(3), mb=4, ctx=at(4), lens=at(5), path=at(6), plen=at(7), P=4, B=3, new=at(8), st=None)
+    try:
+        for change in (dict(new=at(1)), dict(new=at(2, size - 4)), dict(table=at(1, size - 4)), dict(ctx=at(2, -8)),
+                       dict(path=at(1, 64)), dict(plen=at(2)), dict(lens=at(1))):
+            refused("kv_tree_commit", list({**base, **change}.values()), "INVALID", "overlaps")
+    finally:
+        kvc.kv_cache_destroy(hp)
+
+
+def test_tree_masks_refuse_outputs_among_their_inputs():
+    par, masks = np.zeros((2, 4), np.int32), np.zeros((2, 4), np.int64)
+    p = lambda a, off=0: ctypes.c_void_p(a.ctypes.data + off)  # noqa: E731
+    for args in ((p(masks, 32), None, 2, 4, p(masks), None), (p(par), None, 2, 4, p(masks), p(par)),
+                 (p(par), p(masks, 56), 2, 4, p(masks), None), (p(par), None, 2, 4, p(masks), p(masks, 32))):
+        refused("kv_tree_masks", args, "INVALID", "overlaps")
