@@ -820,6 +820,12 @@ static Span rows_span(const void* at, int64_t n, int64_t stride, int64_t row, in
     const __int128 bytes = (static_cast<__int128>(n - 1) * stride + row) * size, most = __int128(1) << 56;
     return {at, static_cast<int64_t>(std::min(bytes, most))};
 }
+// whether each of some arrays of elements of `size` bytes starts at one (a misaligned load is a fault on the device)
+static bool aligned_to(uintptr_t size, std::initializer_list<const void*> arrays) {
+    for (const void* a : arrays)
+        if (reinterpret_cast<uintptr_t>(a) % size) return false;
+    return true;
+}
 // Outputs that share memory with an input or with each other: other CTAs may still read what one has written.
 static kvc_status check_overlap(std::initializer_list<Span> out, std::initializer_list<Span> in) {
     for (const Span* o = out.begin(); o != out.end(); ++o) {
@@ -897,6 +903,8 @@ kvc_status kv_append_rope(const void* q, int64_t q_stride, const void* k, int64_
                             static_cast<const void*>(v_out), static_cast<const void*>(k_cache),
                             static_cast<const void*>(v_cache)})
         if (!aligned16(ptr)) return fail(KVC_ERR_INVALID, "device buffers must be 16-byte aligned");
+    if (!aligned_to(4, {rot_dim ? positions : nullptr}) || !aligned_to(8, {rot_dim ? turns : nullptr, slot_mapping}))
+        return fail(KVC_ERR_INVALID, "positions, turns and slot_mapping must be aligned to their types");
     const int64_t qrow = static_cast<int64_t>(Hq) * head_dim, krow = static_cast<int64_t>(Hkv) * head_dim;
     if (q_stride % 8 || k_stride % 8 || v_stride % 8 || q_stride < qrow || k_stride < krow || v_stride < krow)
         return fail(KVC_ERR_INVALID, "token strides must be multiples of 8 elements and hold a token's heads");
@@ -995,7 +1003,9 @@ kvc_status paged_decode_tree_attention(const void* q, const void* k_cache, const
         return fail(KVC_ERR_INVALID, "null pointer");
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
         return fail(KVC_ERR_INVALID, "q, caches and out must be 16-byte aligned");
-    if (reinterpret_cast<uintptr_t>(masks) & 7u) return fail(KVC_ERR_INVALID, "masks must be 8-byte aligned");
+    if (!aligned_to(8, {masks})) return fail(KVC_ERR_INVALID, "masks must be 8-byte aligned");
+    if (!aligned_to(4, {block_table, context_lens, tree_lens}))
+        return fail(KVC_ERR_INVALID, "block_table, context_lens and tree_lens must be 4-byte aligned");
     if (num_blocks < 1 || max_blocks < 1) return fail(KVC_ERR_INVALID, "num_blocks and max_blocks must be positive");
     if (static_cast<int64_t>(num_blocks) * Hkv * block_size >= (int64_t(1) << 31))
         return fail(KVC_ERR_UNSUPPORTED, "num_blocks * Hkv * block_size must be < 2^31");
@@ -1081,8 +1091,10 @@ kvc_status draft_tree_verify(const void* target_probs, int64_t p_stride, const v
     if (!target_probs || !draft_probs || !tokens || !parents || !uniforms || !path || !path_len || !next_token)
         return fail(KVC_ERR_INVALID, "null pointer");
     const uintptr_t size = prob_dtype == KVC_F32 ? 4 : 2;
-    if (reinterpret_cast<uintptr_t>(target_probs) % size || reinterpret_cast<uintptr_t>(draft_probs) % size)
+    if (!aligned_to(size, {target_probs, draft_probs}))
         return fail(KVC_ERR_INVALID, "probabilities must be aligned to their type");
+    if (!aligned_to(4, {tokens, parents, tree_lens, uniforms, path, path_len, next_token}))
+        return fail(KVC_ERR_INVALID, "the tree's arrays must be 4-byte aligned");
     const int64_t nodes_bytes = static_cast<int64_t>(B) * T * 4, per = B * int64_t(4);
     kvc_status s = check_overlap({{path, nodes_bytes}, {path_len, per}, {next_token, per}},
                                  {rows_span(target_probs, static_cast<int64_t>(B) * T, p_stride, V, size),
@@ -1143,6 +1155,8 @@ kvc_status kv_tree_commit(kvc_handle h, const int32_t* block_table, int max_bloc
     if (B > 65535) return fail(KVC_ERR_UNSUPPORTED, "B must be <= 65535");
     if (B == 0) return KVC_OK;
     if (!block_table || !context_lens || !path || !path_len || !new_context_lens) return fail(KVC_ERR_INVALID, "null pointer");
+    if (!aligned_to(4, {block_table, context_lens, tree_lens, path, path_len, new_context_lens}))
+        return fail(KVC_ERR_INVALID, "the arrays must be 4-byte aligned");
     const int64_t per = static_cast<int64_t>(B) * 4;
     const int64_t layer = static_cast<int64_t>(h->cfg.num_blocks) * h->cfg.num_kv_heads * h->cfg.block_size * h->cfg.head_dim;
     kvc_status s = check_overlap({{new_context_lens, per}, rows_span(h->k_pool, h->cfg.num_layers, layer, layer, 2),

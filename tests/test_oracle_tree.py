@@ -323,3 +323,27 @@ def test_tree_masks_refuse_outputs_among_their_inputs():
     for args in ((p(masks, 32), None, 2, 4, p(masks), None), (p(par), None, 2, 4, p(masks), p(par)),
                  (p(par), p(masks, 56), 2, 4, p(masks), None), (p(par), None, 2, 4, p(masks), p(masks, 32))):
         refused("kv_tree_masks", args, "INVALID", "overlaps")
+
+
+def test_arrays_that_are_not_aligned_to_their_types_are_refused():
+    """A misaligned load would be a fault on the device."""
+    rope = dict(q=at(1), qs=256, k=at(2), ks=128, v=at(3), vs=128, n=20, Hq=4, Hkv=2, D=64, qw=None, kw=None, eps=1e-6,
+                turns=at(6), rot=64, inter=0, pos=at(7), qo=at(8), ko=None, vo=None, kc=at(11), vc=at(12), NB=4, bs=16,
+                slots=at(13), st=None)
+    attention = dict(q=at(1), k=at(2), v=at(3), NB=64, table=at(4), mb=8, ctx=at(5), masks=at(6), lens=at(7), T=4, B=2,
+                     Hq=4, Hkv=2, D=64, bs=16, most=128, scale=0.125, out=at(8), od=0, ws=None, wb=0, st=None)
+    verify = dict(p=at(1), ps=104, q=at(2), qs=100, dt=1, tok=at(3), par=at(4), lens=at(5), u=at(6), B=3, T=4, V=100,
+                  distinct=0, path=at(7), plen=at(8), nxt=at(9), st=None)
+    hp = ctypes.c_void_p()
+    cfg = kvc.KvcConfig(2, 4, 2, 64)._c()
+    assert kvc._lib.kv_cache_create(ctypes.byref(cfg), at(1), at(2), ctypes.byref(hp)) == 0  # never followed below
+    commit = dict(h=hp, table=at(3), mb=4, ctx=at(4), lens=at(5), path=at(6), plen=at(7), P=4, B=3, new=at(8), st=None)
+    try:
+        for fn, base, arrays in (("kv_append_rope", rope, dict(turns=4, pos=2, slots=4)),
+                                 ("paged_decode_tree_attention", attention, dict(table=2, ctx=1, masks=4, lens=2)),
+                                 ("draft_tree_verify", verify, dict(p=2, q=1, tok=2, par=3, lens=2, u=2, path=1, plen=2, nxt=2)),
+                                 ("kv_tree_commit", commit, dict(table=2, ctx=1, lens=2, path=3, plen=2, new=2))):
+            for name, off in arrays.items():
+                refused(fn, list({**base, name: ctypes.c_void_p(base[name].value + off)}.values()), "INVALID", "aligned")
+    finally:
+        kvc.kv_cache_destroy(hp)
