@@ -536,6 +536,7 @@ kvc_status kv_append_rope(const void* q, int64_t q_stride, const void* k, int64_
  *   tree_lens    device int32 [B], 0 .. T, or NULL: T each.  Rows t >= tree_len
  *                of out are left as they were
  *   T            1 .. 64
+ *   max_context_len  up to 2^30
  *   out          device [B][T][Hq][D], out_dtype KVC_F16 or KVC_F32
  *   workspace    device, 16-byte aligned, >= paged_decode_tree_plan's bytes; as
  *                with the other decode calls, calls that share one must not

@@ -978,6 +978,8 @@ static kvc_status check_tree_shape(int B, int Hq, int Hkv, int head_dim, int blo
     if (s != KVC_OK) return s;
     if (T < 1 || T > kvc::kMaxTreeNodes)
         return fail(KVC_ERR_UNSUPPORTED, "trees of %d nodes not supported (1..%d)", T, kvc::kMaxTreeNodes);
+    if (max_context_len > kvc::kMaxTreeContext)  // key positions and tiles are 32-bit, with room behind the last one
+        return fail(KVC_ERR_UNSUPPORTED, "max_context_len must be <= %d", kvc::kMaxTreeContext);
     return KVC_OK;
 }
 

@@ -137,6 +137,7 @@ int launch_overlap();
 
 // ---- tree-drafted decoding -----------------------------------------------------
 constexpr int kMaxTreeNodes = 64;  // a node's mask is one 64-bit word
+constexpr int kMaxTreeContext = 1 << 30;
 
 // query / key norm, position rotation and append (append_rope.cu)
 struct RopeArgs {

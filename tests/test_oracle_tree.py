@@ -347,3 +347,14 @@ def test_arrays_that_are_not_aligned_to_their_types_are_refused():
                 refused(fn, list({**base, name: ctypes.c_void_p(base[name].value + off)}.values()), "INVALID", "aligned")
     finally:
         kvc.kv_cache_destroy(hp)
+
+
+def test_contexts_beyond_32_bit_positions_are_refused():
+    """The plan's number of key tiles overflowed for the last 127 lengths below 2^31: a workspace of nothing."""
+    base = dict(q=at(1), k=at(2), v=at(3), NB=64, table=at(4), mb=2 ** 27, ctx=at(5), masks=at(6), lens=None, T=4, B=1,
+                Hq=4, Hkv=2, D=64, bs=16, most=2 ** 30 + 1, scale=0.125, out=at(8), od=0, ws=None, wb=0, st=None)
+    for most in (2 ** 30 + 1, 2 ** 31 - 1):
+        refused("paged_decode_tree_attention", list({**base, "most": most}.values()), "UNSUPPORTED", "max_context_len")
+        with pytest.raises(kvc.KvcError) as e:
+            kvc.paged_decode_tree_plan(1, 4, 2, 64, most, 4)
+        assert e.value.name == "KVC_ERR_UNSUPPORTED"
