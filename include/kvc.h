@@ -505,6 +505,7 @@ kvc_status kv_rope_turns(const double* inv_freq, int n, uint64_t* turns);
  *                q_stride / k_stride / v_stride elements apart (multiples of 8,
  *                at least heads * D): they may be parts of one projection
  *   q_weight, k_weight  device fp16 [D], or NULL: those rows are not normed
+ *   eps          finite, not negative (unused without weights)
  *   turns        device uint64 [rot_dim / 2] (kv_rope_turns); positions device
  *                int32 [n], any value; both unused at rot_dim 0.  rot_dim: a
  *                multiple of 16 up to D

@@ -891,6 +891,8 @@ kvc_status kv_append_rope(const void* q, int64_t q_stride, const void* k, int64_
     if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 16)
         return fail(KVC_ERR_UNSUPPORTED, "rot_dim %d is not a multiple of 16 up to head_dim", rot_dim);
     if (interleaved != 0 && interleaved != 1) return fail(KVC_ERR_INVALID, "interleaved must be 0 or 1");
+    if ((q_weight || k_weight) && !(eps >= 0.f && std::isfinite(eps)))
+        return fail(KVC_ERR_INVALID, "eps must be finite and not negative");
     const bool cache = k_cache || v_cache || slot_mapping;
     if (cache && block_size != kvc::kBlockSize) return fail(KVC_ERR_UNSUPPORTED, "block_size %d not supported", block_size);
     if (n == 0) return KVC_OK;

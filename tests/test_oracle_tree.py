@@ -358,3 +358,11 @@ def test_contexts_beyond_32_bit_positions_are_refused():
         with pytest.raises(kvc.KvcError) as e:
             kvc.paged_decode_tree_plan(1, 4, 2, 64, most, 4)
         assert e.value.name == "KVC_ERR_UNSUPPORTED"
+
+
+def test_append_rope_refuses_an_eps_that_no_norm_has():
+    base = dict(q=at(1), qs=256, k=at(2), ks=128, v=at(3), vs=128, n=20, Hq=4, Hkv=2, D=64, qw=None, kw=at(5), eps=1e-6,
+                turns=None, rot=0, inter=0, pos=None, qo=at(8), ko=at(9), vo=None, kc=None, vc=None, NB=0, bs=16, slots=None,
+                st=None)
+    for eps in (-1e-6, float("nan"), float("inf")):
+        refused("kv_append_rope", list({**base, "eps": eps}.values()), "INVALID", "eps")
