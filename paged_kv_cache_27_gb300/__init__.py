@@ -867,7 +867,7 @@ def kv_append_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions:
     dev = q.get_device()
     qst, kst, vst = q.stride(), k.stride(), v.stride()
     # the common case in one expression; the checks below only name the failure
-    if not (dev == _current_device() == k.get_device() == v.get_device()
+    if not (dev >= 0 and dev == _current_device() == k.get_device() == v.get_device()
             and q.dtype is _F16 and k.dtype is _F16 and v.dtype is _F16
             and qst[2] == kst[2] == vst[2] == 1 and qst[1] == kst[1] == vst[1] == D
             and _ready(dev, _F16, q_out, q_weight, k_weight, k_out, v_out, k_cache, v_cache)
@@ -929,7 +929,7 @@ def paged_decode_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache:
         raise TypeError("out must be float16 or float32")
     keep = (q, k_cache, v_cache, block_table, context_lens, masks, tree_lens, out, workspace)
     dev = q.get_device()
-    if not (dev == _current_device() and _ready(dev, _F16, q, k_cache, v_cache, out if od == KVC_F16 else None)
+    if not (dev >= 0 and dev == _current_device() and _ready(dev, _F16, q, k_cache, v_cache, out if od == KVC_F16 else None)
             and _ready(dev, _I32, block_table, context_lens, tree_lens) and masks.dtype is _I64
             and masks.get_device() == dev and masks.is_contiguous() and (od == KVC_F16 or _ready(dev, _F32, out))
             and (workspace is None or _ready(dev, workspace.dtype, workspace))):
@@ -990,7 +990,7 @@ def draft_tree_verify(target_probs: torch.Tensor, draft_probs: torch.Tensor, tok
         raise ValueError("path_len, next_token and tree_lens must have B entries")
     keep = (target_probs, draft_probs, tokens, parents, tree_lens, uniforms, path, path_len, next_token)
     dev = target_probs.get_device()
-    if not (dev == _current_device() == draft_probs.get_device()
+    if not (dev >= 0 and dev == _current_device() == draft_probs.get_device()
             and _ready(dev, _I32, tokens, parents, path, path_len, next_token, tree_lens)
             and uniforms.dtype is _F32 and uniforms.get_device() == dev and uniforms.is_contiguous()):
         _same_device(*keep)
@@ -1023,7 +1023,7 @@ def kv_tree_commit(h: int, block_table: torch.Tensor, context_lens: torch.Tensor
         raise ValueError("context_lens, path_len, new_context_lens and tree_lens must have B entries")
     keep = (path, block_table, context_lens, tree_lens, path_len, new_context_lens)
     dev = path.get_device()
-    if not (dev == _current_device()
+    if not (dev >= 0 and dev == _current_device()
             and _ready(dev, _I32, path, block_table, context_lens, path_len, new_context_lens, tree_lens)):
         _same_device(*keep)
         for t, nm in ((path, "path"), (block_table, "block_table"), (context_lens, "context_lens"),

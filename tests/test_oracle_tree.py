@@ -7,6 +7,7 @@ import struct
 
 import numpy as np
 import pytest
+import torch
 
 import oracle
 import paged_kv_cache_27_gb300 as kvc
@@ -366,3 +367,23 @@ def test_append_rope_refuses_an_eps_that_no_norm_has():
                 st=None)
     for eps in (-1e-6, float("nan"), float("inf")):
         refused("kv_append_rope", list({**base, "eps": eps}.values()), "INVALID", "eps")
+
+
+def test_host_tensors_are_refused_as_such():
+    """Also where there is no GPU, whose current device cannot be asked for."""
+    t = lambda dt, *shape: torch.zeros(shape, dtype=dt)  # noqa: E731
+    f16, f32, i32, i64 = torch.float16, torch.float32, torch.int32, torch.int64
+    h = kvc.kv_cache_create(kvc.KvcConfig(1, 4, 2, 64))
+    try:
+        for call in (lambda: kvc.kv_append_rope(t(f16, 3, 4, 64), t(f16, 3, 2, 64), t(f16, 3, 2, 64), None, None,
+                                                t(f16, 3, 4, 64)),
+                     lambda: kvc.paged_decode_tree_attention(t(f16, 1, 2, 4, 64), t(f16, 4, 2, 16, 64),
+                                                             t(f16, 4, 2, 16, 64), t(i32, 1, 4), t(i32, 1), t(i64, 1, 2),
+                                                             0.125, t(f16, 1, 2, 4, 64), None, 64),
+                     lambda: kvc.draft_tree_verify(t(f32, 1, 2, 9), t(f32, 1, 2, 9), t(i32, 1, 2), t(i32, 1, 2),
+                                                   t(f32, 1, 2), t(i32, 1, 2), t(i32, 1), t(i32, 1)),
+                     lambda: kvc.kv_tree_commit(h, t(i32, 1, 4), t(i32, 1), t(i32, 1, 4), t(i32, 1), t(i32, 1))):
+            with pytest.raises(ValueError, match="must be on a CUDA device"):
+                call()
+    finally:
+        kvc.kv_cache_destroy(h)
