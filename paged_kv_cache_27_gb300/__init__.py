@@ -18,6 +18,7 @@ from typing import Optional, Sequence
 
 import numpy as np
 import torch  # loads the CUDA runtime that libkvc.so links against
+from torch.multiprocessing.reductions import StorageWeakRef
 
 from ._build import LIB as _LIB_PATH
 from ._build import build
@@ -209,6 +210,20 @@ class PreparedCall:
         _check(self._fn(*self._args, st), self._name)
 
 
+class _PreparedCacheCall(PreparedCall):
+    """A PreparedCall that holds a cache's handle: it keeps the pools alive too, and refuses after kv_cache_destroy."""
+    __slots__ = ("_cache",)
+
+    def __init__(self, fn, args, name, device, keep, cache):
+        super().__init__(fn, args, name, device, keep + tuple(cache.pools()))
+        self._cache = cache
+
+    def __call__(self, stream=None) -> None:
+        if not self._cache.open:
+            raise ValueError(f"{self._name}: the cache of this call was destroyed")
+        super().__call__(stream)
+
+
 def _launch(fn, args, name, stream, prepare, keep):
     """Launch fn(*args, stream), or return it as a PreparedCall; keep[0] is a CUDA tensor of the call."""
     if prepare:
@@ -304,6 +319,32 @@ def kv_cache_pool_bytes(cfg: KvcConfig) -> int:
     return n.value
 
 
+class _Cache:
+    """What stands behind a handle of kv_cache_create: whether it is open, and its pools' storages, which it does not keep
+    alive (they are the caller's)."""
+    __slots__ = ("open", "_pools")
+
+    def __init__(self, pools):
+        self.open, self._pools = True, [StorageWeakRef(t.untyped_storage()) for t in pools]
+
+    def pools(self):
+        """The pools' storages, to be kept alive."""
+        return [torch.UntypedStorage._new_with_weak_ptr(p.cdata) for p in self._pools]
+
+
+_caches: dict = {}  # by handle, until kv_cache_destroy
+
+
+def _open_cache(h: int) -> _Cache:
+    cache = _caches.get(h)
+    if cache is None:
+        raise ValueError("h is not an open cache of kv_cache_create")
+    for p in cache._pools:
+        if p.expired():
+            raise ValueError("the cache's pools are freed")
+    return cache
+
+
 def kv_cache_create(cfg: KvcConfig, k_pool: Optional[torch.Tensor] = None,
                     v_pool: Optional[torch.Tensor] = None) -> int:
     """Handle over caller-owned pools (fp16 [L][NB][Hkv][bs][D]); None, None = host-only pool."""
@@ -318,10 +359,14 @@ def kv_cache_create(cfg: KvcConfig, k_pool: Optional[torch.Tensor] = None,
     c = cfg._c()
     _check(_lib.kv_cache_create(ctypes.byref(c), _dptr(k_pool, torch.float16, "k_pool"),
                                 _dptr(v_pool, torch.float16, "v_pool"), ctypes.byref(h)), "kv_cache_create")
+    _caches[h.value] = _Cache([] if k_pool is None else [k_pool, v_pool])
     return h.value
 
 
 def kv_cache_destroy(h: int) -> None:
+    cache = _caches.pop(getattr(h, "value", h), None)
+    if cache is not None:
+        cache.open = False
     _check(_lib.kv_cache_destroy(h), "kv_cache_destroy")
 
 
@@ -784,10 +829,12 @@ _APPEND_ROPE, _TREE_ATTENTION, _TREE_VERIFY, _TREE_COMMIT = (
 _call = _lib.kvc_call
 
 
-def _run(call: _Words, args, stream, prepare, dev, keep):
+def _run(call: _Words, args, stream, prepare, dev, keep, cache=None):
     """Launch the call with args (0 for a null pointer) on `stream` or the current one of device dev, or return it as a
     PreparedCall.  The arguments go as one array: ctypes takes ~60 ns for each of up to 26."""
     words = call.pack(*args)
+    if prepare and cache is not None:
+        return _PreparedCacheCall(_call, (call.which, words, call.count), call.name, dev, keep, cache)
     if prepare:
         return PreparedCall(_call, (call.which, words, call.count), call.name, dev, keep)
     if stream is None and _raw_stream is not None:
@@ -1011,7 +1058,9 @@ def kv_tree_commit(h: int, block_table: torch.Tensor, context_lens: torch.Tensor
     the end of their contexts and write the new context lengths (int32 [B], not context_lens itself).
 
     block_table int32 [B][max_blocks] and context_lens int32 [B] (trees included) as the attention call had them;
-    tree_lens int32 [B] (None: P nodes each).  prepare=True returns a PreparedCall."""
+    tree_lens int32 [B] (None: P nodes each).  prepare=True returns a PreparedCall, which also keeps the pools alive and
+    raises ValueError once the cache is destroyed."""
+    cache = _open_cache(h)
     if path.dim() != 2 or block_table.dim() != 2:
         raise ValueError("path must be [B][P] and block_table [B][max_blocks]")
     B, P = path.shape
@@ -1032,4 +1081,4 @@ def kv_tree_commit(h: int, block_table: torch.Tensor, context_lens: torch.Tensor
     args = (h, block_table.data_ptr(), max_blocks, context_lens.data_ptr(),
             0 if tree_lens is None else tree_lens.data_ptr(), path.data_ptr(), path_len.data_ptr(), P, B,
             new_context_lens.data_ptr())
-    return _run(_TREE_COMMIT, args, stream, prepare, dev, keep)
+    return _run(_TREE_COMMIT, args, stream, prepare, dev, keep, cache)

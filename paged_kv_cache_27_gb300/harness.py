@@ -279,6 +279,8 @@ class TreeSession:
 
     def step(self, stream=None):
         """The whole step on `stream` or the current one (asynchronous)."""
+        if not self.h:
+            raise ValueError("the session's cache was destroyed")
         for call in self._calls:
             call(stream)
 

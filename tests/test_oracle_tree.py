@@ -387,3 +387,16 @@ def test_host_tensors_are_refused_as_such():
                 call()
     finally:
         kvc.kv_cache_destroy(h)
+
+
+def test_commit_refuses_a_destroyed_cache():
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    args = (i32(1, 4), i32(1), i32(1, 4), i32(1), i32(1))
+    h = kvc.kv_cache_create(kvc.KvcConfig(1, 4, 2, 64))
+    with pytest.raises(ValueError, match="CUDA"):  # open: it is the tensors that are refused
+        kvc.kv_tree_commit(h, *args)
+    kvc.kv_cache_destroy(h)
+    for handle in (h, 0, None):
+        for prepare in (False, True):
+            with pytest.raises(ValueError, match="not an open cache"):
+                kvc.kv_tree_commit(handle, *args, prepare=prepare)
