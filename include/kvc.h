@@ -470,7 +470,12 @@ kvc_status paged_decode_attention_static_workspace(const void* q, const void* k_
  * which the kept path is the end of an ordinary context.  The four calls keep
  * the stream's order whatever kvc_set_launch_overlap says: their kernels are
  * launched under the end of the kernel in front, but read and write nothing
- * before it is done, and release nothing early themselves.  An output (or
+ * before it is done, and release nothing early themselves.  That is their own
+ * side of it: with launch overlap on, a decode call right behind one of them
+ * reads its block table, context lengths and cache rows early (see there), so
+ * where those are what kv_append_rope or kv_tree_commit has just written,
+ * another kernel, a copy or an event goes between the two, or overlap is off.
+ * An output (or
  * workspace) that shares memory with anything its call reads or with another
  * output is refused, but for kv_append_rope's rows in place. */
 
@@ -495,7 +500,9 @@ kvc_status kv_rope_turns(const double* inv_freq, int n, uint64_t* turns);
 
 /* Query / key norm, position rotation and append in one pass over a step's
  * (or a prompt's) projected rows; stands where kv_append does for models that
- * rotate, and replaces the separate norm and rotation passes.
+ * rotate, and replaces the separate norm and rotation passes.  (As behind
+ * kv_append, with launch overlap on something goes between it and an ordinary
+ * decode call that reads the rows; paged_decode_tree_attention follows at once.)
  *   y_i = x_i * rsqrt(mean(x^2) + eps) * weight_i   per query / key head row
  *   (y_a, y_b) = (y_a cos g - y_b sin g, y_b cos g + y_a sin g),
  *   g = positions[t] * frequency, for the rot_dim / 2 pairs (a, b) of the first
@@ -601,6 +608,8 @@ kvc_status draft_tree_verify(const void* target_probs, int64_t p_stride, const v
  * tree_len, position base + i takes the row of position base + path[b][i] for
  * i < path_len[b], and new_context_lens[b] = base + path_len[b].  The rows of
  * the other nodes are left behind it and are overwritten by later appends.
+ * (With launch overlap on, something goes between this call and a decode call
+ * that reads the rows or new_context_lens.)
  *   block_table  device int32 [B][max_blocks], as the attention call had it; the
  *                blocks of the tree are the sequence's own (not shared)
  *   tree_lens    device int32 [B], or NULL: P each

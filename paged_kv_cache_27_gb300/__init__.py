@@ -261,7 +261,9 @@ def kvc_set_multi_tc(on: bool) -> None:
 
 
 def kvc_set_launch_overlap(on: bool) -> None:
-    """Launch decode kernels as programmatic dependents of the previous kernel (see include/kvc.h)."""
+    """Launch decode kernels as programmatic dependents of the previous kernel (see include/kvc.h).  While it is on,
+    something (a kernel, a copy, an event) goes between a call that writes a decode call's cache rows, block table or
+    lengths, kv_append_rope and kv_tree_commit among them, and that decode call."""
     _check(_lib.kvc_set_launch_overlap(int(bool(on))), "kvc_set_launch_overlap")
 
 

@@ -81,3 +81,38 @@ def test_a_closed_session_does_not_step(kvc):
     with pytest.raises(ValueError, match="destroyed"):
         s.step()
     torch.cuda.synchronize()
+
+
+def test_an_ordinary_decode_behind_a_step_under_launch_overlap(kvc):
+    """With another kernel between the commit and the decode call, as the header asks, the decode follows the lengths and
+    rows that the commit wrote, launch overlap on or off."""
+    from paged_kv_cache_27_gb300.harness import TreeSession
+    wl = workloads.tree_decode(4, [700, 33, 300], [12, 7, 9], 12, L=2)
+    s = TreeSession(wl)
+    fresh = [p.clone() for p in (s.k_pool, s.v_pool)]
+    q = torch.randn(3, wl.Hq, wl.D, device="cuda").half()
+    _, _, need = kvc.paged_decode_plan(3, wl.Hq, wl.Hkv, wl.D, s.max_ctx)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+    big = torch.zeros(32 << 20, device="cuda")
+    outs = []
+    try:
+        for on in (False, True, True):
+            kvc.kvc_set_launch_overlap(on)
+            for p, x in zip((s.k_pool, s.v_pool), fresh):
+                p.copy_(x)
+            s.new_context_lens.fill_(1)
+            out = torch.empty((2, 3, wl.Hq, wl.D), dtype=torch.float32, device="cuda")
+            torch.cuda.synchronize()
+            big.add_(1)  # long, so that its successors queue up
+            s.step()
+            big[:1].add_(1)
+            for layer in range(2):
+                kvc.paged_decode_attention(q, s.k_pool[layer], s.v_pool[layer], s.block_table, s.new_context_lens,
+                                           wl.scale, out[layer], ws, s.max_ctx)
+            torch.cuda.synchronize()
+            outs.append(out)
+    finally:
+        kvc.kvc_set_launch_overlap(False)
+    assert kvc.kvc_device_error_flags() == 0
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    s.close()
