@@ -1,12 +1,15 @@
 """Calls of a tree-drafted step that its documentation allows or refuses, beside the operators' own tests."""
+import dataclasses
 import gc
 
+import numpy as np
 import pytest
 import torch
 from torch.multiprocessing.reductions import StorageWeakRef
 
 import workloads
-from test_gpu_tree import Tree, kvc  # noqa: F401  (kvc is a fixture)
+from oracle import tree
+from test_gpu_tree import Tree, dev, host, kvc, reference_step  # noqa: F401  (kvc is a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -116,3 +119,72 @@ def test_an_ordinary_decode_behind_a_step_under_launch_overlap(kvc):
     assert kvc.kvc_device_error_flags() == 0
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
     s.close()
+
+
+def test_steps_in_a_row_from_the_lengths_on_the_device(kvc):
+    """Three steps: positions, slots and lengths of each follow on the device from what the commit before it wrote, with
+    nothing read on the host in between; every step is checked against its definition on the sequences so far."""
+    hist, lens, T, L = [0, 15, 300, 77], [6, 6, 4, 1], 24, 2
+    steps = [workloads.tree_decode(40 + i, hist, lens, T, L=L) for i in range(3)]
+    wl = steps[0]
+    B, Hq, Hkv, D = 4, wl.Hq, wl.Hkv, wl.D
+    i32 = dict(dtype=torch.int32, device="cuda")
+    k_pool, v_pool = dev(wl.k_pool), dev(wl.v_pool)
+    h = kvc.kv_cache_create(kvc.KvcConfig(L, wl.NB, Hkv, D), k_pool, v_pool)
+    table, tree_lens, turns = dev(wl.block_table), dev(wl.tree_lens), dev(kvc.kv_rope_turns(wl.inv_freq))
+    most = table.shape[1] * 16
+    ws = torch.empty(max(16, kvc.paged_decode_tree_plan(B, Hq, Hkv, D, most, T)), dtype=torch.uint8, device="cuda")
+    node = torch.arange(T, **i32)
+    now = torch.tensor(hist, **i32)  # the sequences' lengths
+    done = []
+    for x in steps:
+        masks, depths = kvc.kv_tree_masks(x.parents, x.tree_lens)
+        at = now[:, None] + node
+        slots = table.gather(1, (at // 16).clamp(max=table.shape[1] - 1).long()).long() * 16 + at % 16
+        slots = torch.where(node < tree_lens[:, None], slots, -1).flatten()
+        positions, ctx = (now[:, None] + dev(depths)).flatten(), now + tree_lens
+        q_rot, out = (torch.zeros((L, B, T, Hq, D), dtype=torch.float16, device="cuda") for _ in range(2))
+        qkv, qw, kw, masks = dev(x.qkv), dev(x.q_weight), dev(x.k_weight), dev(masks)
+        for layer in range(L):
+            q, k, v = (r.unflatten(1, (-1, D)) for r in qkv[layer].split((Hq * D, Hkv * D, Hkv * D), 1))
+            kvc.kv_append_rope(q, k, v, positions, turns, q_rot[layer].view(B * T, Hq, D), k_pool[layer], v_pool[layer],
+                               slots, q_weight=qw[layer], k_weight=kw[layer], eps=x.eps)
+            kvc.paged_decode_tree_attention(q_rot[layer], k_pool[layer], v_pool[layer], table, ctx, masks, x.scale,
+                                            out[layer], ws, most, tree_lens=tree_lens)
+        path = torch.zeros((B, T), **i32)
+        n, token, new = (torch.zeros(B, **i32) for _ in range(3))
+        kvc.draft_tree_verify(dev(x.p), dev(x.q), dev(x.tokens), dev(x.parents), dev(x.uniforms), path, n, token,
+                              tree_lens=tree_lens)
+        kvc.kv_tree_commit(h, table, ctx, path, n, new, tree_lens=tree_lens)
+        done.append((out, path, n, token, new, k_pool.clone(), v_pool.clone()))
+        now = new
+    torch.cuda.synchronize()
+    assert kvc.kvc_device_error_flags() == 0
+    length, pools = np.array(hist, np.int32), [wl.k_pool, wl.v_pool]
+    live = node.cpu().numpy()[None] < wl.tree_lens[:, None]
+    for x, (out, path, n, token, new, k_dev, v_dev) in zip(steps, done):
+        ref = dataclasses.replace(x, hist=length, k_pool=pools[0], v_pool=pools[1], block_table=wl.block_table)
+        masks, qs, pools = reference_step(ref)
+        for layer in range(L):
+            want, spread = tree.tree_attention(qs[layer], pools[0][layer], pools[1][layer], wl.block_table,
+                                               length + wl.tree_lens, masks, wl.tree_lens, x.scale)
+            # the query's and the keys' own fp16 roundings, as in the single step's test
+            qk = np.abs(qs[layer].astype(np.float64)).max() * np.abs(pools[0][layer].astype(np.float64)).max() * x.scale
+            bound = 2 * (2.0 ** -10 * qk * np.sqrt(D) + 2.0 ** -11) * spread + 2.0 ** -11 * np.abs(want) + 2e-4
+            assert (np.abs(host(out[layer]).astype(np.float64) - want)[live] <= bound[live]).all()
+        walks = [tree.verify(x.p[b, :m], x.q[b, :m], x.tokens[b, :m], x.parents[b, :m],
+                             x.uniforms[b, :m].astype(np.float64), False) for b, m in enumerate(lens)]
+        paths = np.full((B, T), -1, np.int32)
+        for b, (walk, _) in enumerate(walks):
+            paths[b, :len(walk)] = walk
+        assert (host(path) == paths).all() and host(token).tolist() == [w[1] for w in walks]
+        length = tree.commit(pools, wl.block_table, length + wl.tree_lens, wl.tree_lens, paths, host(n))
+        assert (host(new) == length).all()
+        for pool, got in zip(pools, (k_dev, v_dev)):
+            for b in range(B):
+                for layer in range(L):
+                    rows = tree.rows_of(pool[layer], wl.block_table[b], int(length[b])).astype(np.float64)
+                    have = tree.rows_of(host(got[layer]), wl.block_table[b], int(length[b]))
+                    assert np.abs(have - rows).max() <= 2.0 ** -10 * np.abs(rows).max()
+    assert (length > np.array(hist) + 3).any()  # some path was longer than its root
+    kvc.kv_cache_destroy(h)
