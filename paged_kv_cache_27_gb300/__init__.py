@@ -322,12 +322,13 @@ def kv_cache_pool_bytes(cfg: KvcConfig) -> int:
 
 
 class _Cache:
-    """What stands behind a handle of kv_cache_create: whether it is open, and its pools' storages, which it does not keep
-    alive (they are the caller's)."""
-    __slots__ = ("open", "_pools")
+    """What stands behind a handle of kv_cache_create: whether it is open, its pools' device, and their storages, which it
+    does not keep alive (they are the caller's)."""
+    __slots__ = ("open", "device", "_pools")
 
     def __init__(self, pools):
         self.open, self._pools = True, [StorageWeakRef(t.untyped_storage()) for t in pools]
+        self.device = pools[0].get_device() if pools else None
 
     def pools(self):
         """The pools' storages, to be kept alive."""
@@ -353,6 +354,8 @@ def kv_cache_create(cfg: KvcConfig, k_pool: Optional[torch.Tensor] = None,
     if (k_pool is None) != (v_pool is None):
         raise ValueError("k_pool and v_pool: both or neither")
     if k_pool is not None:
+        if k_pool.device != v_pool.device:
+            raise ValueError("k_pool and v_pool are on several devices")
         need = kv_cache_pool_bytes(cfg)
         for t, nm in ((k_pool, "k_pool"), (v_pool, "v_pool")):
             if t.numel() * t.element_size() < need:
@@ -1080,6 +1083,8 @@ def kv_tree_commit(h: int, block_table: torch.Tensor, context_lens: torch.Tensor
         for t, nm in ((path, "path"), (block_table, "block_table"), (context_lens, "context_lens"),
                       (tree_lens, "tree_lens"), (path_len, "path_len"), (new_context_lens, "new_context_lens")):
             _dptr(t, _I32, nm)
+    if cache.device is not None and cache.device != dev:
+        raise ValueError(f"the tensors are on cuda:{dev}, the cache's pools on cuda:{cache.device}")
     args = (h, block_table.data_ptr(), max_blocks, context_lens.data_ptr(),
             0 if tree_lens is None else tree_lens.data_ptr(), path.data_ptr(), path_len.data_ptr(), P, B,
             new_context_lens.data_ptr())

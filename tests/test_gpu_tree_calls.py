@@ -188,3 +188,16 @@ def test_steps_in_a_row_from_the_lengths_on_the_device(kvc):
                     assert np.abs(have - rows).max() <= 2.0 ** -10 * np.abs(rows).max()
     assert (length > np.array(hist) + 3).any()  # some path was longer than its root
     kvc.kv_cache_destroy(h)
+
+
+def test_a_commit_to_pools_of_another_device_is_refused(kvc):
+    pools = [torch.zeros((1, 4, 2, 16, 64), dtype=torch.float16, device="cuda") for _ in range(2)]
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    h = kvc.kv_cache_create(kvc.KvcConfig(1, 4, 2, 64), *pools)
+    try:
+        assert kvc._caches[h].device == 0
+        kvc._caches[h].device = 1
+        with pytest.raises(ValueError, match="pools on cuda:1"):
+            kvc.kv_tree_commit(h, i32(2, 3).view(1, 2), i32(6), i32(0, 3).view(1, 2), i32(2), i32(0), tree_lens=i32(4))
+    finally:
+        kvc.kv_cache_destroy(h)
