@@ -519,7 +519,7 @@ kvc_status kv_rope_turns(const double* inv_freq, int n, uint64_t* turns);
  *   q_out        device fp16 [n][Hq][D]; may be q itself where q's stride is Hq * D
  *   k_out, v_out device fp16 [n][Hkv][D] or NULL: the rows packed, for
  *                prefill_attention or kv_append_fp8; may be k / v as q_out may
- *                be q.  An output that overlaps the rows read otherwise is refused
+ *                be q.  An output that overlaps what is read otherwise is refused
  *   k_cache, v_cache  device fp16 [num_blocks][Hkv][bs][D] (one layer), with
  *                slot_mapping device int64 [n] as in kv_append (negative =
  *                skip, >= num_blocks * bs sets KVC_DEVERR_SLOT; no slot twice);
@@ -540,7 +540,8 @@ kvc_status kv_append_rope(const void* q, int64_t q_stride, const void* k, int64_
  *   context_lens device int32 [B], including the tree (tree_len <= ctx <=
  *                min(max_blocks * bs, max_context_len))
  *   masks        device uint64 [B][T] (kv_tree_masks, or any other bits; a row
- *                that sees nothing, without history and bits, gives 0)
+ *                that sees nothing, without history and bits, gives 0, and so
+ *                does one whose scores are all minus infinity)
  *   tree_lens    device int32 [B], 0 .. T, or NULL: T each.  Rows t >= tree_len
  *                of out are left as they were
  *   T            1 .. 64
@@ -629,7 +630,8 @@ kvc_status kv_tree_commit(kvc_handle h, const int32_t* block_table, int max_bloc
  * 64-bit words, for bindings that pay per argument (a call from Python's
  * ctypes: 2.1 us for kv_append_rope's 26 arguments, 0.6 us this way).  words:
  * the named call's `count` arguments in order without the stream, pointers and
- * integers as integers, a float as a double.  KVC_ERR_INVALID for an unknown
+ * integers as integers, a float as a double (addresses are taken as they are,
+ * as in the named call itself).  KVC_ERR_INVALID for an unknown
  * call, another count or an integer that does not fit its argument. */
 #define KVC_CALL_APPEND_ROPE 1
 #define KVC_CALL_TREE_ATTENTION 2

@@ -854,7 +854,9 @@ def _run(call: _Words, args, stream, prepare, dev, keep, cache=None):
 
 def kvc_call(which: int, words: bytes, stream=None) -> None:
     """A launching call by its number (KVC_CALL_* of the header) with its arguments as 64-bit words, on `stream` or the
-    current one.  The four calls' own functions build the words from tensors and check them."""
+    current one: the library's call as it is, for bindings of one's own.  Addresses are not checked (a wrong one is a
+    fault on the device), nor is what they belong to kept alive; the four calls' own functions build the words from
+    tensors, check those and keep them."""
     if len(words) % 8:
         raise ValueError("words must be whole 64-bit words")
     st = torch.cuda.current_stream().cuda_stream if stream is None and torch.cuda.is_available() else _stream(stream)

@@ -19,9 +19,11 @@
 // takes kRows = 512 / D rows at a time and keeps one token's cosines and sines in registers for all its heads; they
 // are computed once per warp (rot_dim / 2 angles over 32 lanes) and handed out through shared memory.
 //
-// What bounds it.  Long prompts: memory, rows read and written once (16,384 tokens, 32 / 8 heads, D = 128: 67.8 us, 88
-// % of a copy's rate).  Fewer rows: the launch, two dependent loads (position and slot, then rows), the angles
-// and the store (512 tokens of the same 5.7 us, 1923 tokens, 14 / 2 heads, D = 64 4.5 us, one token 3.1 us).
+// What bounds it.  Long prompts: memory, rows read and written once (16,384 tokens, 32 / 8 heads, D = 128: 66.2 us, 90
+// % of a copy's rate).  Many tokens of few heads (60,000, 14 / 2, D = 64: 82 us, twice what its bytes take): each kind of
+// rows is a loop of its own whose loads follow the last one's stores, and 18 rows fill 18 of a warp's 4 x 8 places.  Fewer
+// rows: the launch, two dependent loads (position and slot, then rows), the angles and the store (512 tokens of the
+// first 5.1 us, 1923 tokens, 14 / 2 heads, D = 64 4.1 us, one token 2.5 us).
 #include <type_traits>
 
 #include "../../include/kvc.h"

@@ -32,11 +32,12 @@
 // product of a CTA with two row tiles and its end.  Through global memory instead that step took 47.6 us.
 // What bounds it (us; bytes and products at the card's measured rates in parentheses):
 //   4 x 65,536 keys, 16 nodes, 32 / 8 heads, D = 128    156   (158)  memory
-//   8 x 4096 keys, 64 nodes, 32 / 8 heads, D = 128      37.5   (21)  3.0 K clocks per key tile for two row tiles, of
+//   8 x 4096 keys, 64 nodes, 32 / 8 heads, D = 128      37.0   (21)  3.0 K clocks per key tile for two row tiles, of
 //                                                       which the products alone take 2.05 K, and the merge
-//   32 x <= 2048 keys, 16 nodes, 14 / 2 heads, D = 64   15.3  (4.6)  start (2.2), 1.5 K clocks per key tile (memory,
+//   32 x <= 2048 keys, 16 nodes, 14 / 2 heads, D = 64   15.0  (4.6)  start (2.2), 1.5 K clocks per key tile (memory,
 //                                                       on 128 of the SMs), end (3.5: last product, barriers, merge)
-//   1 x 2048 keys, 8 nodes, 14 / 2 heads, D = 64         8.3  (0.2)  start, two key tiles, end
+//   1 x 2048 keys, 8 nodes, 14 / 2 heads, D = 64         8.1  (0.2)  start, two key tiles, end
+// With fp32 outputs (twice the P V products) 160, 46.0, 16.4 and 8.6.
 // Every wait is bounded.
 #include <algorithm>
 #include <cfloat>
@@ -883,9 +884,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
 }  // namespace tree
 
 // What a split of the contexts costs, in units of 0.01 us, by [D = 128][two row tiles]: a CTA's start and end, a key
-// tile, and a merge in a cluster.  Fitted to 56 shapes (1 to 64 sequences, 1 to 65,536 keys, every head layout of the
-// tests) measured with every split: the split chosen is 0.6 % slower than the best one on average, 6 % at worst (with
-// clusters of all chunks up to eight, else of four, as the only choice: 2.9 % and 20 %).
+// tile, and a merge in a cluster.  Fitted to 56 shapes (1 to 128 sequences, 1 to 65,536 keys, every head layout of the
+// tests) measured with every split: the split chosen is 0.5 % slower than the best one on average, 5 % at worst.
 constexpr int kCtaCost[2][2] = {{480, 580}, {680, 1000}};
 constexpr int kTileCost[2][2] = {{70, 130}, {100, 135}};
 constexpr int kMergeCost[2][2] = {{60, 200}, {30, 30}};

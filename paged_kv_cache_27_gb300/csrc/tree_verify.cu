@@ -31,8 +31,9 @@
 // What bounds it.  A sequence's passes follow one another: each needs the sum of the one before.  64 sequences of
 // 128,257 fp32 entries (16 nodes, three distinct children a node): 2.2 passes on average, 6 at most.  The first passes
 // read 66 MB from memory; of a pass of a cluster alone on its SMs (4.8 us), about 2.5 us are arithmetic and loads from
-// L2, 1.0 the exchange of the sums (the barrier of a cluster takes 0.7), 0.65 the decision.  39 us, where one reading
-// of the two rows of every sequence takes 9.7; one sequence of 32,000 entries (8 nodes, a chain) 6.9 us.
+// L2, 1.0 the exchange of the sums (the barrier of a cluster takes 0.7), 0.65 the decision.  29 to 45 us by the walks
+// that are drawn (16 draws, median 36.4; with fp16 rows 31 to 47, median 37.2: half the bytes, and conversions in
+// front of the same arithmetic), where one reading of the two rows of every sequence takes 9.7; one sequence of 32,000 entries (8 nodes, a chain) 6.6 us.
 #include <algorithm>
 #include <atomic>
 
@@ -257,7 +258,8 @@ __device__ __forceinline__ uint64_t lane_weights(const T* p, const T* q, int b, 
                             : lane_weights<kAny, T>(p, q, b, e, f);
 }
 
-// Sums of two floats, ~48 bits: the walk's scalars (the FP64 unit is slow: a trial took 0.6 us on it).
+// Sums of two floats, ~48 bits: the walk's scalars (the FP64 unit is slow: a trial took 0.6 us on it).  The error-free
+// sum is Knuth's, the error-free product one rounded product and its error by fma.
 struct Two {
     float h, l;
 };
