@@ -579,10 +579,11 @@ kvc_status paged_decode_tree_attention(const void* q, const void* k_cache, const
  * were drawn without replacement, q_{k+1} = q_k without x_k, divided by
  * 1 - q_k(x_k) (a child tried after the draft's mass is spent is refused; a
  * token tried again at its node is, too, and q_k holds nothing of it any more).
- * Where no child is kept, the next token is drawn from the last p_k: the smallest index
- * whose running sum exceeds u_0 times the sum (from p itself if nothing of the
- * residual is left).  The kept tokens and the next one are distributed as the
- * target's own samples.
+ * Where no child is kept, the next token is drawn from the last p_k: the
+ * smallest index whose running sum exceeds u_0 times the sum.  Where nothing of
+ * the residual is left (every p - a q below 2^-46) no further child of the node
+ * is kept, and the token is drawn from p itself.  The kept tokens and the next
+ * one are distributed as the target's own samples.
  *   target_probs, draft_probs  device [B][T][V], prob_dtype KVC_F16 or KVC_F32
  *                for both; row t of a sequence is the distribution behind node
  *                t; rows p_stride / q_stride elements apart (>= V).  They are

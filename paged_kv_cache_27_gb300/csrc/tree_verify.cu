@@ -388,9 +388,10 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) draft_tree_verify_ke
                 last = c;
                 const float4 child = s_tree[c];
                 const Two uq = two_prod(child.y, child.w);
-                // u q S < (p - a q)^+ R; at a node's first child u q < p
+                // u q S < (p - a q)^+ R; at a node's first child u q < p; where the residual's sum is 0, nothing of it is
+                // left, whatever a single difference's sign (its rounding's, mostly) may be
                 const Two left = Two{child.z, 0.f} + -(a * Two{child.w, 0.f});
-                if (positive(R) && positive(left) && positive(left * R + -(uq * S))) {
+                if (positive(R) && positive(S) && positive(left) && positive(left * R + -(uq * S))) {
                     if (lane == 0) s_path[len] = c;
                     ++len;
                     cur = c;

@@ -201,3 +201,20 @@ def test_a_commit_to_pools_of_another_device_is_refused(kvc):
             kvc.kv_tree_commit(h, i32(2, 3).view(1, 2), i32(6), i32(0, 3).view(1, 2), i32(2), i32(0), tree_lens=i32(4))
     finally:
         kvc.kv_cache_destroy(h)
+
+
+@pytest.mark.parametrize("V", [2, 33, 5000])
+def test_no_child_is_kept_of_a_residual_that_is_nothing(kvc, V):
+    """Two refusals leave 3 * 2^-49 of the last child's token, which is nothing in the sums' units of 2^-45: the child is
+    refused, although that difference by itself is positive, and the token comes from the target's own row."""
+    p, q = np.zeros((2, 4, V), np.float32)
+    x, y = 0, V - 1
+    q[0, x], q[0, y] = 0.5, 0.5 - 2.0 ** -25
+    p[0, x], p[0, y] = 0.5 - 2.0 ** -24, 0.5 + 2.0 ** -24
+    i32 = lambda *a: torch.tensor([a], dtype=torch.int32, device="cuda")  # noqa: E731
+    for u0, token in ((0.25, x), (0.75, y)):
+        u = torch.tensor([[u0, 1 - 2.0 ** -24, 0.5, 0.5]], dtype=torch.float32, device="cuda")
+        path, n, nxt = i32(9, 9, 9, 9), i32(9)[0], i32(9)[0]
+        kvc.draft_tree_verify(dev(p[None]), dev(q[None]), i32(0, x, x, y), i32(-1, 0, 0, 0), u, path, n, nxt, distinct=True)
+        assert path.tolist() == [[0, -1, -1, -1]] and n.item() == 1 and nxt.item() == token
+    assert kvc.kvc_device_error_flags() == 0
