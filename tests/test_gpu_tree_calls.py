@@ -218,3 +218,163 @@ def test_no_child_is_kept_of_a_residual_that_is_nothing(kvc, V):
         kvc.draft_tree_verify(dev(p[None]), dev(q[None]), i32(0, x, x, y), i32(-1, 0, 0, 0), u, path, n, nxt, distinct=True)
         assert path.tolist() == [[0, -1, -1, -1]] and n.item() == 1 and nxt.item() == token
     assert kvc.kvc_device_error_flags() == 0
+
+
+def test_as_many_sequences_as_a_call_takes(kvc):
+    """65,535 sequences of one block each: append, attention of two-node chains, verification, commit."""
+    B, D, n = 65535, 64, 2
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rows = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=torch.float16)  # noqa: E731
+    pools = [rows(1, B, 1, 16, D) for _ in range(2)]
+    table = torch.randperm(B, generator=g, device="cuda").int()[:, None].contiguous()
+    hist = torch.randint(0, 14, (B,), generator=g, device="cuda", dtype=torch.int32)
+    ctx = hist + n
+    node = torch.arange(n, dtype=torch.int32, device="cuda")
+    at = hist[:, None] + node
+    slots = (table.long() * 16 + at).flatten()
+    q, k, v = rows(B * n, 1, D), rows(B * n, 1, D), rows(B * n, 1, D)
+    q_out = torch.empty_like(q)
+    kvc.kv_append_rope(q, k, v, None, None, q_out, pools[0][0], pools[1][0], slots)
+    assert torch.equal(q_out, q)
+    assert torch.equal(pools[0].view(-1, D)[slots], k[:, 0]) and torch.equal(pools[1].view(-1, D)[slots], v[:, 0])
+    masks = torch.tensor([[1, 3]], dtype=torch.int64, device="cuda").expand(B, n).contiguous()
+    out = torch.empty((B, n, 1, D), dtype=torch.float32, device="cuda")
+    ws = torch.empty(max(16, kvc.paged_decode_tree_plan(B, 1, 1, D, 16, n)), dtype=torch.uint8, device="cuda")
+    kvc.paged_decode_tree_attention(q_out.view(B, n, 1, D), pools[0][0], pools[1][0], table, ctx, masks, 0.125, out, ws, 16)
+    K, V = (p.view(B, 16, D)[table[:, 0].long()].double() for p in pools)
+    s = q.view(B, n, D).double() @ K.transpose(1, 2) * 0.125
+    seen = torch.arange(16, device="cuda")[None, None] <= at[:, :, None]
+    w = torch.softmax(s.masked_fill(~seen, -float("inf")), -1)
+    # per weight 2^-20, D 2^-24 of its score's terms (below 64 * 25 * 0.125) and the sums'; values up to 6
+    assert (out[:, :, 0] - w @ V).abs().max() < 2 * (2.0 ** -20 + 64 * 2.0 ** -24 * 200 + 2.0 ** -20) * 6
+    p = torch.rand(B, n, 3, generator=g, device="cuda")
+    p /= p.sum(-1, keepdim=True)
+    tokens, parents = torch.full((B, n), 1, dtype=torch.int32, device="cuda"), (node - 1).expand(B, n).contiguous()
+    u = torch.rand(B, n, generator=g, device="cuda")
+    path = torch.zeros((B, n), dtype=torch.int32, device="cuda")
+    length, token, new = (torch.zeros(B, dtype=torch.int32, device="cuda") for _ in range(3))
+    kvc.draft_tree_verify(p, p.flip(-1).contiguous(), tokens, parents, u, path, length, token)
+    kept = u[:, 1] < 1  # token 1 has the same mass in both rows
+    assert bool(kept.all()) and (length == 2).all() and torch.equal(path, node.expand(B, n))
+    c = p[:, 1].double().cumsum(-1)
+    near = ((c - u[:, :1].double() * c[:, -1:]).abs().amin(-1) < 2.0 ** -40)
+    assert ((token == (c <= u[:, :1].double() * c[:, -1:]).sum(-1)) | near).all()
+    # node 1 alone behind the root's place: a path of the root keeps one row, all others two
+    length[::3] = 1
+    h = kvc.kv_cache_create(kvc.KvcConfig(1, B, 1, D), *pools)
+    before = [x.clone() for x in pools]
+    kvc.kv_tree_commit(h, table, ctx, path, length, new)
+    assert torch.equal(new, hist + length) and all(torch.equal(a, b) for a, b in zip(before, pools))
+    kvc.kv_cache_destroy(h)
+    assert kvc.kvc_device_error_flags() == 0
+
+
+@pytest.mark.parametrize("graphs", [False, True])
+def test_two_sessions_at_once(kvc, graphs):
+    """Whole steps of two caches on two streams, over and over: each as if it were alone."""
+    from paged_kv_cache_27_gb300.harness import TreeSession
+    wls = [workloads.tree_decode(5, [3000, 40, 900], [12, 9, 12], 12, L=3),
+           workloads.tree_decode(6, [100] * 30, [24] * 30, 24, L=3, Hq=8, Hkv=1)]
+    sessions = [TreeSession(wl) for wl in wls]
+    fresh = [[p.clone() for p in (s.k_pool, s.v_pool)] for s in sessions]
+    results = lambda s: [x.clone() for x in (s.out, s.path, s.path_len, s.next_token, s.new_context_lens, s.k_pool, s.v_pool)]  # noqa: E731
+
+    def run(s, first):
+        for p, x in zip((s.k_pool, s.v_pool), first):
+            p.copy_(x)
+        s.step()
+    alone = []
+    for s, first in zip(sessions, fresh):
+        run(s, first)
+        torch.cuda.synchronize()
+        alone.append(results(s))
+    streams = [torch.cuda.Stream() for _ in sessions]
+    captured = []
+    if graphs:
+        for s, first, st in zip(sessions, fresh, streams):
+            captured.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(captured[-1], stream=st):
+                run(s, first)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s in sessions:
+            s.out.zero_()
+            s.path.zero_()
+        torch.cuda.synchronize()
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                if graphs:
+                    captured[i].replay()
+                else:
+                    run(sessions[i], fresh[i])
+        torch.cuda.synchronize()
+        for s, want in zip(sessions, alone):
+            # (bit patterns: cache rows that nobody owns may be NaN)
+            assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(results(s), want))
+    assert kvc.kvc_device_error_flags() == 0
+    for s in sessions:
+        s.close()
+
+
+def test_offsets_beyond_32_bits(kvc):
+    """Pools, projected rows and probabilities of more than 2^31 elements: what lies at their far end comes out as it does
+    in small ones."""
+    D, NB, T = 128, 1_200_000, 5
+    g = torch.Generator(device="cuda").manual_seed(2)
+    rows = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=torch.float16)  # noqa: E731
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    turns = dev(kvc.kv_rope_turns(1e4 ** (-np.arange(0, D, 2) / D)))
+    # a sequence of 37 tokens, 5 of them nodes, at a pool's far end and in a pool of its own
+    small = [rows(1, 4, 1, 16, D) for _ in range(2)]
+    far = [torch.empty((1, NB, 1, 16, D), dtype=torch.float16, device="cuda") for _ in range(2)]
+    assert far[0].numel() > 2 ** 31
+    where = {0: NB - 1, 1: 3, 2: NB - 2}  # block of the small pool: block of the large one
+    for s, f in zip(small, far):
+        for a, b in where.items():
+            f[0, b] = s[0, a]
+    q, k, v = rows(T, 4, D), rows(T, 1, D), rows(T, 1, D)
+    v[2, 0, 7] = float("inf")  # the way that looks values up again by their place in the pool
+    pos = torch.arange(32, 37, dtype=torch.int32, device="cuda")
+    masks = torch.tensor([[1, 3, 7, 11, 19]], dtype=torch.int64, device="cuda")
+    done = []
+    for pools, blocks in ((small, [0, 1, 2]), (far, [where[i] for i in range(3)])):
+        table, slots = i32(*blocks).view(1, 3), blocks[2] * 16 + torch.arange(T, device="cuda")
+        q_out, out = torch.empty_like(q), torch.empty((1, T, 4, D), dtype=torch.float16, device="cuda")
+        kvc.kv_append_rope(q, k, v, pos, turns, q_out, pools[0][0], pools[1][0], slots)
+        kvc.paged_decode_tree_attention(q_out[None], pools[0][0], pools[1][0], table, i32(37), masks, D ** -0.5, out, None, 48)
+        h, new = kvc.kv_cache_create(kvc.KvcConfig(1, pools[0].shape[1], 1, D), *pools), i32(0)
+        kvc.kv_tree_commit(h, table, i32(37), i32(0, 2, 4).view(1, 3), i32(3), new, tree_lens=i32(T))
+        done.append((q_out, out, new, *(p[0, blocks[2], 0, :T].clone() for p in pools)))
+        kvc.kv_cache_destroy(h)
+    assert torch.isinf(done[0][1]).any()
+    for a, b in zip(*done):
+        assert torch.equal(a, b)
+    del far
+    # projected rows, in place
+    n = 2 ** 20 + 3
+    x = torch.empty((n, 17, D), dtype=torch.float16, device="cuda")
+    assert x.numel() > 2 ** 31
+    x[-9:] = rows(9, 17, D)
+    k, v = rows(9, 1, D), rows(9, 1, D)
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    ref, want = x[-9:].clone(), torch.empty((9, 17, D), dtype=torch.float16, device="cuda")
+    kvc.kv_append_rope(ref, k, v, pos[-9:].clone(), turns, want)
+    kv = torch.zeros((n, 1, D), dtype=torch.float16, device="cuda")
+    kvc.kv_append_rope(x, kv, kv, pos, turns, x)
+    assert torch.equal(x[-9:], want)
+    del x, kv
+    # probabilities: the last sequence's chain of nodes is kept to its end, and its last row drawn from
+    B, T, V = 3, 64, 2 ** 24
+    p = torch.zeros((B, T, V), dtype=torch.float16, device="cuda")
+    assert p.numel() > 2 ** 31
+    tokens = torch.randint(0, V, (B, T), generator=g, device="cuda", dtype=torch.int32)
+    tokens[-1, -1] = V - 1
+    for t in range(T - 1):
+        p[torch.arange(B), t, tokens[:, t + 1].long()] = 1
+    p[:, T - 1, V - 2] = 1
+    parents = torch.arange(-1, T - 1, device="cuda", dtype=torch.int32).expand(B, T).contiguous()
+    path = torch.zeros((B, T), dtype=torch.int32, device="cuda")
+    length, token = i32(0, 0, 0), i32(0, 0, 0)
+    kvc.draft_tree_verify(p, p, tokens, parents, torch.rand((B, T), generator=g, device="cuda"), path, length, token)
+    assert length.tolist() == [T] * B and torch.equal(path, parents + 1) and token.tolist() == [V - 2] * B
+    assert kvc.kvc_device_error_flags() == 0
