@@ -494,8 +494,8 @@ kvc_status kv_tree_masks(const int32_t* parents, const int32_t* tree_lens, int B
  * position modulo one turn in integers, exactly, and takes the result to fp32:
  * within 2^-26 + 2^-33 turn (1e-7 radians) at any int32 position.  (turns is
  * computed in double: 2^-52 of a frequency, times the position, comes on top;
- * 2^-24 turn at position 2^31 and one radian per position.)  KVC_ERR_INVALID for a negative or
- * non-finite frequency. */
+ * 2^-24 turn at position 2^31 and one radian per position.)  KVC_ERR_INVALID
+ * for a negative or non-finite frequency. */
 kvc_status kv_rope_turns(const double* inv_freq, int n, uint64_t* turns);
 
 /* Query / key norm, position rotation and append in one pass over a step's

@@ -29,11 +29,12 @@
 // numbers (the tree's, gathered by rank 0 for all; the sums).
 //
 // What bounds it.  A sequence's passes follow one another: each needs the sum of the one before.  64 sequences of
-// 128,257 fp32 entries (16 nodes, three distinct children a node): 2.2 passes on average, 6 at most.  The first passes
+// 128,257 fp32 entries (16 nodes, three distinct children a node): 2.1 passes on average, 6 at most.  The first passes
 // read 66 MB from memory; of a pass of a cluster alone on its SMs (4.8 us), about 2.5 us are arithmetic and loads from
 // L2, 1.0 the exchange of the sums (the barrier of a cluster takes 0.7), 0.65 the decision.  29 to 45 us by the walks
 // that are drawn (16 draws, median 36.4; with fp16 rows 31 to 47, median 37.2: half the bytes, and conversions in
-// front of the same arithmetic), where one reading of the two rows of every sequence takes 9.7; one sequence of 32,000 entries (8 nodes, a chain) 6.6 us.
+// front of the same arithmetic), where one reading of the two rows of every sequence takes 9.7; one sequence of 32,000
+// entries (8 nodes, a chain) 6.6 us.
 #include <algorithm>
 #include <atomic>
 
