@@ -72,6 +72,7 @@ typedef enum { KVC_F16 = 0, KVC_F32 = 1 } kvc_dtype;
 #define KVC_DEVERR_TIMEOUT 0x8u    /* a bounded wait on a copy expired (the work was skipped) */
 #define KVC_DEVERR_SEQLENS 0x10u   /* cu_seqlens not non-decreasing / beyond total_tokens */
 #define KVC_DEVERR_TREE 0x20u      /* a drafted tree: size, parent, token or path out of range, or a row without mass */
+#define KVC_DEVERR_BLOCKS 0x40u    /* kv_block_tables: the step needs more blocks or slots than it was given */
 
 typedef struct {
     int num_layers;   /* L */
@@ -627,8 +628,133 @@ kvc_status kv_tree_commit(kvc_handle h, const int32_t* block_table, int max_bloc
                           const int32_t* tree_lens, const int32_t* path, const int32_t* path_len, int P, int B,
                           int32_t* new_context_lens, void* stream);
 
-/* The launching calls of this section with their arguments as an array of
- * 64-bit words, for bindings that pay per argument (a call from Python's
+/* ---- windows, an 8-bit cache with block scales, tables built on the GPU --
+ * A sliding window: a query at position t sees the newest `window` positions
+ * (t - window < j <= t, its own among them) and the first `sinks` positions
+ * (j < sinks), which stay visible however long the sequence gets.  window and
+ * sinks are at most 2^30; positions are absolute (a rotation applied before
+ * the cache stays as it was).  Blocks in which nothing is visible are never
+ * read, nor are their table entries, and what masked positions hold cannot
+ * reach an output, infinities and NaN included.
+ * The five calls keep the stream's order: their kernels are launched under the
+ * end of the kernel in front, but read and write nothing before it is done.
+ * The two decode calls do so while launch overlap is off; while it is on they
+ * follow kvc_set_launch_overlap's contract like the other decode calls (and
+ * something goes between them and a kv_block_tables, kv_append_fp8_block or
+ * other append whose table entries, scales or rows they read).  An output (or
+ * workspace) that shares memory with anything its call reads or with another
+ * output is refused. */
+
+/* Block tables, slots and positions of one step, built on the GPU from the
+ * request lengths, for the steps of a loop that does not return to the host
+ * (on the host: kv_step_prepare, kv_slot_mapping).  Sequence b goes from
+ * lens_before[b] to lens_after[b] tokens; its new blocks come from a list of
+ * blocks that the caller has claimed from its pool (kv_block_alloc) and not
+ * used yet, in the order of the sequences and within one of its positions.
+ *   lens_before  device int32 [B], or NULL: 0 each (prompts)
+ *   lens_after   device int32 [B], at least lens_before, at most max_blocks * bs
+ *   free_blocks  device int32 [num_free]; placed device int32 [1]: how many of
+ *                them earlier steps have used
+ *   window       0, or the model's window: a sequence then goes through
+ *                ceil((window + bs - 1) / bs) blocks in turn, behind the
+ *                ceil(sinks / bs) of its sinks, and takes no more than these from
+ *                the list however long it gets: block j of its table is the one
+ *                that block j - ceil((window + bs - 1) / bs) was, of which
+ *                nothing is visible any more.  This holds for steps of one token
+ *                and for prompts (prefill_window_attention reads no cache).  The
+ *                same window and sinks in every step of a sequence
+ *   sinks        0 without a window
+ *   block_table  device int32 [B][max_blocks]; entries of the new blocks are
+ *                written, others left (and read, where the window comes round)
+ *   new_placed   device int32 [1]: placed, and what this step used
+ *   cu_tokens    device int32 [B + 1]: prefix sums of the new tokens, 0 first
+ *                (prefill_attention's cu_seqlens)
+ *   slot_mapping device int64 [num_slots]: of every new token, packed; -1 for a
+ *                token of a prompt whose block a later one of the same prompt takes
+ *                (it is no longer visible), and behind the last token, so that
+ *                buffers of a fixed size serve steps of any number of tokens
+ *   positions    device int32 [num_slots] or NULL: of every new token; 0 behind
+ * All or nothing: where the list or num_slots is too short, or placed is not
+ * between 0 and num_free, KVC_DEVERR_BLOCKS is set, the table stays as it was,
+ * new_placed is placed, cu_tokens are 0 and the slots -1.  A sequence whose
+ * lengths do not fit is flagged (KVC_DEVERR_CONTEXT) and gets nothing; the
+ * others are placed.  B up to 65535.  One kernel launch. */
+kvc_status kv_block_tables(const int32_t* lens_before, const int32_t* lens_after, int B, const int32_t* free_blocks,
+                           int num_free, const int32_t* placed, int window, int sinks, int32_t* block_table,
+                           int max_blocks, int block_size, int32_t* new_placed, int32_t* cu_tokens,
+                           int64_t* slot_mapping, int32_t* positions, int num_slots, void* stream);
+
+/* paged_decode_attention over what a window and sinks leave visible: the
+ * query of sequence b is at position context_lens[b] - 1.
+ *   window >= 1, sinks >= 0
+ *   k_new, v_new  device fp16 [B][Hkv][D], or both NULL: appended at position
+ *                 context_lens[b] - 1 first, as in paged_decode_append_attention
+ *   workspace     device, 16-byte aligned, >= paged_decode_window_plan's bytes
+ * Other arguments as there; scale is finite, max_blocks * bs below 2^31.  A
+ * context length out of range is flagged (KVC_DEVERR_CONTEXT) and its rows are
+ * zero; a block id out of range is flagged (KVC_DEVERR_BLOCK_ID) and its block
+ * left out.  A row whose scores are all minus infinity is 0.  Weights as fp16
+ * high part plus residual, row sums in fp32.  One kernel launch, or two where
+ * the plan's workspace is not 0. */
+kvc_status paged_decode_window_plan(int B, int Hq, int Hkv, int head_dim, int block_size, int max_context_len,
+                                    int window, int sinks, size_t* workspace_bytes);
+kvc_status paged_decode_window_attention(const void* q, const void* k_new, const void* v_new, void* k_cache,
+                                         void* v_cache, int num_blocks, const int32_t* block_table, int max_blocks,
+                                         const int32_t* context_lens, int window, int sinks, int B, int Hq, int Hkv,
+                                         int head_dim, int block_size, int max_context_len, float scale, void* out,
+                                         int out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* A cache of e4m3 codes with one scale for each (block, KV head) of K and one
+ * of V, in plain arrays:
+ *   codes   device [num_blocks][Hkv][2][bs][D] bytes (one layer): K's rows, V's rows
+ *   scales  device float [num_blocks][Hkv][2]; a cached value is code * scale
+ * (kv_append_fp8's cache has a scale per row and interleaves codes and scales
+ * in records of its own.)
+ * kv_append_fp8_block writes rows to their slots.  A block's scale is 2^e with
+ * the least e for which no value of its rows exceeds 448 * 2^e (2^-32 for zeros);
+ * codes are x * 2^-e, rounded to nearest even.  A block's rows are appended in
+ * the order of its slots: those in front of the first one that a call appends
+ * are the block's own, and where the scale grows they are recoded (exactly, but
+ * for codes that become subnormal: they are rounded again); those behind are
+ * not; a call that appends a block's first row starts the block anew.
+ * Infinities become +-448 and NaN stays NaN; neither counts for a scale.
+ *   k_new, v_new  device fp16 [n][Hkv][D], the tokens k_stride / v_stride
+ *                 elements apart (multiples of 8, at least Hkv * D)
+ *   slot_mapping  device int64 [n]; negative = skip, >= num_blocks * bs sets
+ *                 KVC_DEVERR_SLOT and is skipped.  The tokens of one block are
+ *                 consecutive in the call, with consecutive slots (checked mode
+ *                 verifies it; otherwise that block's contents are undefined)
+ * codes and scales 16-byte aligned; num_blocks * Hkv * bs below 2^30.  One
+ * kernel launch. */
+kvc_status kv_append_fp8_block(const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride, int n,
+                               const int64_t* slot_mapping, void* codes, float* scales, int num_blocks, int Hkv,
+                               int head_dim, int block_size, void* stream);
+/* paged_decode_attention over such a cache, of all of a context (window 0) or
+ * what a window and sinks leave visible; workspace >=
+ * paged_decode_fp8_block_plan's bytes for the same window and sinks.  Codes are
+ * multiplied as they are: the K scale goes into the scores and the V scale into
+ * the weights and, where scales of a context differ by more than 2^6, the
+ * accumulators (exactly, for scales that are powers of two; others are taken
+ * too).  Otherwise as paged_decode_window_attention. */
+kvc_status paged_decode_fp8_block_plan(int B, int Hq, int Hkv, int head_dim, int block_size, int max_context_len,
+                                       int window, int sinks, size_t* workspace_bytes);
+kvc_status paged_decode_attention_fp8_block(const void* q, const void* codes, const float* scales, int num_blocks,
+                                            const int32_t* block_table, int max_blocks, const int32_t* context_lens,
+                                            int window, int sinks, int B, int Hq, int Hkv, int head_dim,
+                                            int block_size, int max_context_len, float scale, void* out, int out_dtype,
+                                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* prefill_attention_ex, causal, over what a window and sinks leave visible:
+ * row i of a segment sees the rows j <= i with j > i - window or j < sinks.
+ * window >= 1; work grows with window + sinks, not with the segment.  Here too
+ * what masked positions hold cannot reach an output: a row that comes out
+ * infinite or NaN is computed again from its visible keys alone (slowly). */
+kvc_status prefill_window_attention(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int nseq,
+                                    int total_tokens, int max_seqlen, int Hq, int Hkv, int head_dim, float scale,
+                                    int window, int sinks, int p_precision, void* out, int out_dtype, void* stream);
+
+/* The launching calls of this section and the one before with their arguments
+ * as an array of 64-bit words, for bindings that pay per argument (a call from Python's
  * ctypes: 2.1 us for kv_append_rope's 26 arguments, 0.6 us this way).  words:
  * the named call's `count` arguments in order without the stream, pointers and
  * integers as integers, a float as a double (addresses are taken as they are,
@@ -638,6 +764,11 @@ kvc_status kv_tree_commit(kvc_handle h, const int32_t* block_table, int max_bloc
 #define KVC_CALL_TREE_ATTENTION 2
 #define KVC_CALL_TREE_VERIFY 3
 #define KVC_CALL_TREE_COMMIT 4
+#define KVC_CALL_BLOCK_TABLES 16
+#define KVC_CALL_APPEND_FP8_BLOCK 17
+#define KVC_CALL_ATTENTION_FP8_BLOCK 18
+#define KVC_CALL_WINDOW_ATTENTION 19
+#define KVC_CALL_PREFILL_WINDOW 20
 kvc_status kvc_call(int which, const void* words, int count, void* stream);
 
 /* Varlen packed prefill (xformers article parts 4-5): for every segment s

@@ -38,13 +38,16 @@ __all__ = [
     "prefill_attention", "prefill_attention_ex", "fp8_v_position", "DEVERR",
     "kv_tree_masks", "kv_rope_turns", "kv_append_rope", "paged_decode_tree_plan", "paged_decode_tree_attention",
     "draft_tree_verify", "kv_tree_commit",
+    "kv_block_tables", "kv_append_fp8_block", "paged_decode_fp8_block_plan", "paged_decode_attention_fp8_block",
+    "paged_decode_window_plan", "paged_decode_window_attention", "prefill_window_attention",
 ]
 
 KVC_F16, KVC_F32 = 0, 1
 KVC_PREFILL_P_F16, KVC_PREFILL_P_SPLIT = 0, 1
 STATUS = {0: "KVC_OK", 1: "KVC_ERR_INVALID", 2: "KVC_ERR_OOM", 3: "KVC_ERR_CAPACITY", 4: "KVC_ERR_CUDA",
           5: "KVC_ERR_UNSUPPORTED"}
-DEVERR = {"BLOCK_ID": 0x1, "CONTEXT": 0x2, "SLOT": 0x4, "TIMEOUT": 0x8, "SEQLENS": 0x10, "TREE": 0x20}
+DEVERR = {"BLOCK_ID": 0x1, "CONTEXT": 0x2, "SLOT": 0x4, "TIMEOUT": 0x8, "SEQLENS": 0x10, "TREE": 0x20,
+          "BLOCKS": 0x40}
 
 
 class KvcError(RuntimeError):
@@ -140,6 +143,15 @@ def _load():
                                             SZ, P]),
         "draft_tree_verify": (I, [P, I64, P, I64, I, P, P, P, P, I, I, I, I, P, P, P, P]),
         "kv_tree_commit": (I, [P, P, I, P, P, P, P, I, I, P, P]),
+        "kv_block_tables": (I, [P, P, I, P, I, P, I, I, P, I, I, P, P, P, P, I, P]),
+        "kv_append_fp8_block": (I, [P, I64, P, I64, I, P, P, P, I, I, I, I, P]),
+        "paged_decode_fp8_block_plan": (I, [I, I, I, I, I, I, I, I, PSZ]),
+        "paged_decode_attention_fp8_block": (I, [P, P, P, I, P, I, P, I, I, I, I, I, I, I, I, ctypes.c_float, P, I, P,
+                                                 SZ, P]),
+        "paged_decode_window_plan": (I, [I, I, I, I, I, I, I, I, PSZ]),
+        "paged_decode_window_attention": (I, [P, P, P, P, P, I, P, I, P, I, I, I, I, I, I, I, I, ctypes.c_float, P, I,
+                                              P, SZ, P]),
+        "prefill_window_attention": (I, [P, P, P, P, I, I, I, I, I, I, ctypes.c_float, I, I, I, P, I, P]),
         "kvc_call": (I, [I, ctypes.c_char_p, I, P]),
         "prefill_attention": (I, [P, P, P, P, I, I, I, I, I, I, ctypes.c_float, I, P, I, P]),
         "prefill_attention_ex": (I, [P, P, P, P, I, I, I, I, I, I, ctypes.c_float, I, I, P, I, P]),
@@ -831,6 +843,10 @@ class _Words:
 _APPEND_ROPE, _TREE_ATTENTION, _TREE_VERIFY, _TREE_COMMIT = (
     _Words(i + 1, name) for i, name in enumerate(("kv_append_rope", "paged_decode_tree_attention", "draft_tree_verify",
                                                   "kv_tree_commit")))
+_BLOCK_TABLES, _APPEND_FP8_BLOCK, _ATTENTION_FP8_BLOCK, _WINDOW_ATTENTION, _PREFILL_WINDOW = (
+    _Words(i + 16, name) for i, name in enumerate((
+        "kv_block_tables", "kv_append_fp8_block", "paged_decode_attention_fp8_block", "paged_decode_window_attention",
+        "prefill_window_attention")))
 _call = _lib.kvc_call
 
 
@@ -855,7 +871,7 @@ def _run(call: _Words, args, stream, prepare, dev, keep, cache=None):
 def kvc_call(which: int, words: bytes, stream=None) -> None:
     """A launching call by its number (KVC_CALL_* of the header) with its arguments as 64-bit words, on `stream` or the
     current one: the library's call as it is, for bindings of one's own.  Addresses are not checked (a wrong one is a
-    fault on the device), nor is what they belong to kept alive; the four calls' own functions build the words from
+    fault on the device), nor is what they belong to kept alive; the calls' own functions build the words from
     tensors, check those and keep them."""
     if len(words) % 8:
         raise ValueError("words must be whole 64-bit words")
@@ -1091,3 +1107,212 @@ def kv_tree_commit(h: int, block_table: torch.Tensor, context_lens: torch.Tensor
             0 if tree_lens is None else tree_lens.data_ptr(), path.data_ptr(), path_len.data_ptr(), P, B,
             new_context_lens.data_ptr())
     return _run(_TREE_COMMIT, args, stream, prepare, dev, keep, cache)
+
+
+# ------------------------------------------------------------ windows, the block-scaled cache, tables built on the GPU
+def _check_all(keep, *named) -> None:
+    """The checks of a call whose common case failed: they name what is wrong.  named: (tensor or None, type, name)."""
+    for t, _, nm in named:
+        if t is not None and not isinstance(t, torch.Tensor):
+            raise TypeError(f"{nm} must be a torch.Tensor")
+    _same_device(*keep)
+    for t, dt, nm in named:
+        _dptr(t, dt, nm)
+
+
+def kv_block_tables(lens_before: Optional[torch.Tensor], lens_after: torch.Tensor, free_blocks: torch.Tensor,
+                    placed: torch.Tensor, block_table: torch.Tensor, new_placed: torch.Tensor, cu_tokens: torch.Tensor,
+                    slot_mapping: torch.Tensor, positions: Optional[torch.Tensor] = None, window: int = 0,
+                    sinks: int = 0, block_size: int = 16, stream=None, prepare: bool = False):
+    """Block tables, slots and positions of one step, built on the GPU from the request lengths.
+
+    lens_before (None: prompts, 0 each) / lens_after int32 [B]; free_blocks int32: blocks claimed from the pool, of which
+    placed (int32 [1]) are used already; block_table int32 [B][max_blocks], the new blocks' entries written; new_placed
+    int32 [1]; cu_tokens int32 [B + 1]; slot_mapping int64 [num_slots], -1 behind the last token; positions int32
+    [num_slots].  With a window (and sinks) a sequence's blocks are used in turn, see include/kvc.h.
+    prepare=True returns a PreparedCall instead of launching."""
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B][max_blocks]")
+    B, max_blocks = block_table.shape
+    num_slots = slot_mapping.numel()
+    if lens_after.numel() != B or (lens_before is not None and lens_before.numel() != B) or cu_tokens.numel() != B + 1:
+        raise ValueError("lens_before and lens_after must have B entries and cu_tokens B + 1")
+    if placed.numel() != 1 or new_placed.numel() != 1:
+        raise ValueError("placed and new_placed must have one entry")
+    if positions is not None and positions.numel() != num_slots:
+        raise ValueError("positions must have slot_mapping's size")
+    keep = (block_table, lens_before, lens_after, free_blocks, placed, new_placed, cu_tokens, slot_mapping, positions)
+    dev = block_table.get_device()
+    if not (dev >= 0 and dev == _current_device()
+            and _ready(dev, _I32, block_table, lens_before, lens_after, free_blocks, placed, new_placed, cu_tokens,
+                       positions) and _ready(dev, _I64, slot_mapping)):
+        _check_all(keep, (block_table, _I32, "block_table"), (lens_before, _I32, "lens_before"),
+                   (lens_after, _I32, "lens_after"), (free_blocks, _I32, "free_blocks"), (placed, _I32, "placed"),
+                   (new_placed, _I32, "new_placed"), (cu_tokens, _I32, "cu_tokens"),
+                   (slot_mapping, _I64, "slot_mapping"), (positions, _I32, "positions"))
+    args = (0 if lens_before is None else lens_before.data_ptr(), lens_after.data_ptr(), B, free_blocks.data_ptr(),
+            free_blocks.numel(), placed.data_ptr(), int(window), int(sinks), block_table.data_ptr(), max_blocks,
+            int(block_size), new_placed.data_ptr(), cu_tokens.data_ptr(), slot_mapping.data_ptr(),
+            0 if positions is None else positions.data_ptr(), num_slots)
+    return _run(_BLOCK_TABLES, args, stream, prepare, dev, keep)
+
+
+def _code_dtype(codes: torch.Tensor):
+    """Codes come as torch.float8_e4m3fn or as their bytes."""
+    if not isinstance(codes, torch.Tensor) or codes.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise TypeError("codes must be a torch.float8_e4m3fn or torch.uint8 tensor")
+    return codes.dtype
+
+
+def _code_shape(codes: torch.Tensor, scales: torch.Tensor, D: int):
+    """(NB, Hkv, bs) of a block-scaled cache layer."""
+    if codes.dim() != 5:
+        raise ValueError("codes must be [NB][Hkv][2][bs][D]")
+    NB, Hkv, two, bs, Dk = codes.shape
+    if two != 2 or Dk != D or scales.shape != (NB, Hkv, 2):
+        raise ValueError("codes must be [NB][Hkv][2][bs][D] and scales [NB][Hkv][2]")
+    return NB, Hkv, bs
+
+
+def kv_append_fp8_block(k_new: torch.Tensor, v_new: torch.Tensor, slot_mapping: torch.Tensor, codes: torch.Tensor,
+                        scales: torch.Tensor, stream=None, prepare: bool = False):
+    """Quantize k_new / v_new (fp16 [n][Hkv][D]; the tokens may be apart, as parts of one projection's output) into a
+    block-scaled cache layer: codes [NB][Hkv][2][bs][D] (float8_e4m3fn or uint8: K's rows, V's rows) and scales float32
+    [NB][Hkv][2], powers of two; slot_mapping int64 [n], the tokens of a block consecutive (see include/kvc.h).
+    prepare=True returns a PreparedCall instead of launching."""
+    kshape = k_new.shape
+    if len(kshape) != 3 or v_new.shape != kshape:
+        raise ValueError("k_new and v_new must be [n][Hkv][D]")
+    n, Hkv, D = kshape
+    NB, Hc, bs = _code_shape(codes, scales, D)
+    if Hc != Hkv or slot_mapping.numel() != n:
+        raise ValueError("codes do not match k_new, or slot_mapping has not n entries")
+    dt = _code_dtype(codes)
+    keep = (k_new, v_new, slot_mapping, codes, scales)
+    dev = k_new.get_device()
+    kst, vst = k_new.stride(), v_new.stride()
+    if not (dev >= 0 and dev == _current_device() == v_new.get_device() and k_new.dtype is _F16 and v_new.dtype is _F16
+            and kst[2] == vst[2] == 1 and kst[1] == vst[1] == D and _ready(dev, _I64, slot_mapping)
+            and _ready(dev, dt, codes) and _ready(dev, _F32, scales)):
+        kst, vst = ((_token_stride(t, nm),) for t, nm in ((k_new, "k_new"), (v_new, "v_new")))
+        _check_all(keep, (slot_mapping, _I64, "slot_mapping"), (codes, dt, "codes"), (scales, _F32, "scales"))
+    if n == 1:  # a single token's stride means nothing
+        kst, vst = (Hkv * D,), (Hkv * D,)
+    args = (k_new.data_ptr(), kst[0], v_new.data_ptr(), vst[0], n, slot_mapping.data_ptr(), codes.data_ptr(),
+            scales.data_ptr(), NB, Hkv, D, bs)
+    return _run(_APPEND_FP8_BLOCK, args, stream, prepare, dev, keep)
+
+
+def paged_decode_fp8_block_plan(B: int, Hq: int, Hkv: int, head_dim: int, max_context_len: int, window: int = 0,
+                                sinks: int = 0, block_size: int = 16) -> int:
+    """Workspace bytes of paged_decode_attention_fp8_block for these sizes."""
+    ws = ctypes.c_size_t()
+    _check(_lib.paged_decode_fp8_block_plan(B, Hq, Hkv, head_dim, block_size, max_context_len, int(window), int(sinks),
+                                            ctypes.byref(ws)), "paged_decode_fp8_block_plan")
+    return ws.value
+
+
+def _decode_shapes(q, block_table, context_lens, out):
+    """Output type of a decode call whose q, tables, lengths and out agree."""
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if block_table.dim() != 2 or block_table.shape[0] != q.shape[0] or context_lens.numel() != q.shape[0]:
+        raise ValueError("block_table / context_lens do not match B")
+    od = KVC_F16 if out.dtype is _F16 else KVC_F32 if out.dtype is _F32 else None
+    if od is None:
+        raise TypeError("out must be float16 or float32")
+    return od
+
+
+def paged_decode_attention_fp8_block(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                                     block_table: torch.Tensor, context_lens: torch.Tensor, scale: float,
+                                     out: torch.Tensor, workspace: Optional[torch.Tensor], max_context_len: int,
+                                     window: int = 0, sinks: int = 0, stream=None, prepare: bool = False):
+    """paged_decode_attention over a block-scaled cache layer (codes and scales as kv_append_fp8_block writes them), of
+    all of a context (window 0) or of its newest `window` and first `sinks` positions; workspace:
+    paged_decode_fp8_block_plan bytes.  prepare=True returns a PreparedCall instead of launching."""
+    B, Hq, D = q.shape
+    NB, Hkv, bs = _code_shape(codes, scales, D)
+    od = _decode_shapes(q, block_table, context_lens, out)
+    dt = _code_dtype(codes)
+    keep = (q, codes, scales, block_table, context_lens, out, workspace)
+    dev = q.get_device()
+    if not (dev >= 0 and dev == _current_device() and _ready(dev, _F16, q) and _ready(dev, dt, codes)
+            and _ready(dev, _F32, scales) and _ready(dev, _I32, block_table, context_lens)
+            and _ready(dev, out.dtype, out) and (workspace is None or _ready(dev, workspace.dtype, workspace))):
+        _check_all(keep, (q, _F16, "q"), (codes, dt, "codes"), (scales, _F32, "scales"),
+                   (block_table, _I32, "block_table"), (context_lens, _I32, "context_lens"), (out, None, "out"),
+                   (workspace, None, "workspace"))
+    args = (q.data_ptr(), codes.data_ptr(), scales.data_ptr(), NB, block_table.data_ptr(), block_table.shape[1],
+            context_lens.data_ptr(), int(window), int(sinks), B, Hq, Hkv, D, bs, int(max_context_len), float(scale),
+            out.data_ptr(), od, 0 if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel() * workspace.element_size())
+    return _run(_ATTENTION_FP8_BLOCK, args, stream, prepare, dev, keep)
+
+
+def paged_decode_window_plan(B: int, Hq: int, Hkv: int, head_dim: int, max_context_len: int, window: int,
+                             sinks: int = 0, block_size: int = 16) -> int:
+    """Workspace bytes of paged_decode_window_attention for these sizes."""
+    ws = ctypes.c_size_t()
+    _check(_lib.paged_decode_window_plan(B, Hq, Hkv, head_dim, block_size, max_context_len, int(window), int(sinks),
+                                         ctypes.byref(ws)), "paged_decode_window_plan")
+    return ws.value
+
+
+def paged_decode_window_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                  block_table: torch.Tensor, context_lens: torch.Tensor, window: int, sinks: int,
+                                  scale: float, out: torch.Tensor, workspace: Optional[torch.Tensor],
+                                  max_context_len: int, k_new: Optional[torch.Tensor] = None,
+                                  v_new: Optional[torch.Tensor] = None, stream=None, prepare: bool = False):
+    """paged_decode_attention over the newest `window` positions of every sequence and its first `sinks`; with
+    k_new / v_new ([B][Hkv][D] fp16) these are appended at position ctx-1 first, in the same kernel.  Blocks in which
+    nothing is visible are not read, nor their table entries; workspace: paged_decode_window_plan bytes.
+    prepare=True returns a PreparedCall instead of launching."""
+    B, Hq, D = q.shape
+    NB, Hkv, bs, Dk = k_cache.shape
+    if Dk != D or v_cache.shape != k_cache.shape:
+        raise ValueError("cache shapes do not match q")
+    od = _decode_shapes(q, block_table, context_lens, out)
+    if (k_new is None) != (v_new is None):
+        raise ValueError("k_new and v_new: both or neither")
+    if k_new is not None and (k_new.shape != (B, Hkv, D) or v_new.shape != (B, Hkv, D)):
+        raise ValueError("k_new/v_new must be [B][Hkv][D]")
+    keep = (q, k_cache, v_cache, block_table, context_lens, out, workspace, k_new, v_new)
+    dev = q.get_device()
+    if not (dev >= 0 and dev == _current_device() and _ready(dev, _F16, q, k_cache, v_cache, k_new, v_new)
+            and _ready(dev, _I32, block_table, context_lens) and _ready(dev, out.dtype, out)
+            and (workspace is None or _ready(dev, workspace.dtype, workspace))):
+        _check_all(keep, (q, _F16, "q"), (k_cache, _F16, "k_cache"), (v_cache, _F16, "v_cache"),
+                   (k_new, _F16, "k_new"), (v_new, _F16, "v_new"), (block_table, _I32, "block_table"),
+                   (context_lens, _I32, "context_lens"), (out, None, "out"), (workspace, None, "workspace"))
+    args = (q.data_ptr(), 0 if k_new is None else k_new.data_ptr(), 0 if v_new is None else v_new.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), NB, block_table.data_ptr(), block_table.shape[1],
+            context_lens.data_ptr(), int(window), int(sinks), B, Hq, Hkv, D, bs, int(max_context_len), float(scale),
+            out.data_ptr(), od, 0 if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel() * workspace.element_size())
+    return _run(_WINDOW_ATTENTION, args, stream, prepare, dev, keep)
+
+
+def prefill_window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                             max_seqlen: int, window: int, sinks: int, scale: float, out: torch.Tensor, stream=None,
+                             precise: bool = False, prepare: bool = False):
+    """Packed varlen prefill, causal, each row over the newest `window` rows of its segment and the first `sinks`:
+    q [T][Hq][D], k/v [T][Hkv][D] fp16, cu_seqlens int32 [nseq+1] -> out [T][Hq][D] fp16 or fp32.  precise as in
+    prefill_attention.  prepare=True returns a PreparedCall instead of launching."""
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    if k.shape != (T, Hkv, D) or v.shape != k.shape or out.shape != q.shape:
+        raise ValueError("shape mismatch")
+    od = KVC_F16 if out.dtype is _F16 else KVC_F32 if out.dtype is _F32 else None
+    if od is None:
+        raise TypeError("out must be float16 or float32")
+    keep = (q, k, v, cu_seqlens, out)
+    dev = q.get_device()
+    if not (dev >= 0 and dev == _current_device() and _ready(dev, _F16, q, k, v) and _ready(dev, _I32, cu_seqlens)
+            and _ready(dev, out.dtype, out)):
+        _check_all(keep, (q, _F16, "q"), (k, _F16, "k"), (v, _F16, "v"), (cu_seqlens, _I32, "cu_seqlens"),
+                   (out, None, "out"))
+    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), cu_seqlens.numel() - 1, T, int(max_seqlen),
+            Hq, Hkv, D, float(scale), int(window), int(sinks), KVC_PREFILL_P_SPLIT if precise else KVC_PREFILL_P_F16,
+            out.data_ptr(), od)
+    return _run(_PREFILL_WINDOW, args, stream, prepare, dev, keep)

@@ -1224,6 +1224,286 @@ kvc_status kv_tree_commit(kvc_handle h, const int32_t* block_table, int max_bloc
     return KVC_OK;
 }
 
+// ---- windows, the block-scaled cache, tables built on the GPU ------------------
+static kvc_status check_window(int window, int sinks, int least) {
+    if (window < least || sinks < 0) return fail(KVC_ERR_INVALID, "window must be at least %d and sinks not negative", least);
+    if (window == 0 && sinks != 0) return fail(KVC_ERR_INVALID, "sinks without a window");
+    if (window > kvc::kMaxWindow || sinks > kvc::kMaxWindow)
+        return fail(KVC_ERR_UNSUPPORTED, "window and sinks must be <= %d", kvc::kMaxWindow);
+    return KVC_OK;
+}
+
+kvc_status kv_block_tables(const int32_t* lens_before, const int32_t* lens_after, int B, const int32_t* free_blocks,
+                           int num_free, const int32_t* placed, int window, int sinks, int32_t* block_table,
+                           int max_blocks, int block_size, int32_t* new_placed, int32_t* cu_tokens,
+                           int64_t* slot_mapping, int32_t* positions, int num_slots, void* stream) {
+    if (B < 0 || num_free < 0 || num_slots < 0 || max_blocks < 1) return fail(KVC_ERR_INVALID, "bad sizes");
+    if (B > 65535) return fail(KVC_ERR_UNSUPPORTED, "B must be <= 65535");
+    if (block_size != kvc::kBlockSize) return fail(KVC_ERR_UNSUPPORTED, "block_size %d not supported", block_size);
+    if (max_blocks > kvc::kMaxTableBlocks) return fail(KVC_ERR_UNSUPPORTED, "max_blocks * block_size must be < 2^31");
+    kvc_status s = check_window(window, sinks, 0);
+    if (s != KVC_OK) return s;
+    if (!placed || !new_placed || !cu_tokens || (B > 0 && (!lens_after || !block_table)) ||
+        (num_free > 0 && !free_blocks) || (num_slots > 0 && !slot_mapping))
+        return fail(KVC_ERR_INVALID, "null pointer");
+    if (!aligned_to(4, {lens_before, lens_after, free_blocks, placed, block_table, new_placed, cu_tokens, positions}) ||
+        !aligned_to(8, {slot_mapping}))
+        return fail(KVC_ERR_INVALID, "the arrays must be aligned to their types");
+    const int64_t per = static_cast<int64_t>(B) * 4;
+    s = check_overlap({{block_table, per * max_blocks}, {new_placed, 4}, {cu_tokens, per + 4},
+                       {slot_mapping, num_slots * int64_t(8)}, {positions, num_slots * int64_t(4)}},
+                      {{lens_before, per}, {lens_after, per}, {free_blocks, num_free * int64_t(4)}, {placed, 4}});
+    if (s != KVC_OK) return s;
+    s = checked([&]() -> kvc_status {
+        std::vector<int32_t> before, after, used;
+        kvc_status e = copy_to_host(after, lens_after, static_cast<size_t>(B), as_stream(stream));
+        if (e == KVC_OK && lens_before) e = copy_to_host(before, lens_before, static_cast<size_t>(B), as_stream(stream));
+        if (e == KVC_OK) e = copy_to_host(used, placed, 1, as_stream(stream));
+        if (e != KVC_OK) return e;
+        if (used[0] < 0 || used[0] > num_free)
+            return fail(KVC_ERR_INVALID, "%d of the %d blocks are placed", used[0], num_free);
+        int64_t need = 0, tokens = 0;
+        const int64_t most = window > 0 ? (sinks + block_size - 1) / block_size + (window + 2 * block_size - 2) / block_size
+                                        : max_blocks;
+        for (int b = 0; b < B; ++b) {
+            const int64_t from = lens_before ? before[b] : 0, to = after[b];
+            if (from < 0 || to < from) return fail(KVC_ERR_INVALID, "sequence %d: lengths %lld and %lld", b,
+                                                   static_cast<long long>(from), static_cast<long long>(to));
+            if (to > static_cast<int64_t>(max_blocks) * block_size)
+                return fail(KVC_ERR_CAPACITY, "sequence %d: length %lld beyond the table", b, static_cast<long long>(to));
+            need += std::min<int64_t>((to + block_size - 1) / block_size, most) -
+                    std::min<int64_t>((from + block_size - 1) / block_size, most);
+            tokens += to - from;
+        }
+        if (need > num_free - used[0])
+            return fail(KVC_ERR_OOM, "the step needs %lld blocks, %d are left", static_cast<long long>(need), num_free - used[0]);
+        if (tokens > num_slots)
+            return fail(KVC_ERR_CAPACITY, "the step has %lld tokens, there is room for %d", static_cast<long long>(tokens), num_slots);
+        return KVC_OK;
+    });
+    if (s != KVC_OK) return s;
+    kvc::BlockTableArgs a;
+    a.lens_before = lens_before;
+    a.lens_after = lens_after;
+    a.free_blocks = free_blocks;
+    a.placed = placed;
+    a.B = B;
+    a.num_free = num_free;
+    a.window = window;
+    a.sinks = sinks;
+    a.block_table = block_table;
+    a.max_blocks = max_blocks;
+    a.new_placed = new_placed;
+    a.cu_tokens = cu_tokens;
+    a.slots = slot_mapping;
+    a.positions = positions;
+    a.num_slots = num_slots;
+    cudaError_t e = kvc::device_error_word(&a.err);
+    if (e != cudaSuccess) return cuda_fail(e, "device error word");
+    e = kvc::launch_block_tables(a, as_stream(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "kv_block_tables launch");
+    return KVC_OK;
+}
+
+// The block-scaled cache's own limits.
+static kvc_status check_block_codes(const void* codes, const float* scales, int num_blocks, int Hkv, int block_size) {
+    if (num_blocks < 1) return fail(KVC_ERR_INVALID, "num_blocks must be positive");
+    if (!codes || !scales) return fail(KVC_ERR_INVALID, "null pointer");
+    if (!aligned16(codes) || !aligned16(scales)) return fail(KVC_ERR_INVALID, "codes and scales must be 16-byte aligned");
+    if (static_cast<int64_t>(num_blocks) * Hkv * block_size >= (int64_t(1) << 30))
+        return fail(KVC_ERR_UNSUPPORTED, "num_blocks * Hkv * block_size must be < 2^30");
+    return KVC_OK;
+}
+
+kvc_status kv_append_fp8_block(const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride, int n,
+                               const int64_t* slot_mapping, void* codes, float* scales, int num_blocks, int Hkv,
+                               int head_dim, int block_size, void* stream) {
+    if (n < 0 || Hkv < 1) return fail(KVC_ERR_INVALID, "bad sizes");
+    if (Hkv > 65535) return fail(KVC_ERR_UNSUPPORTED, "Hkv must be <= 65535");
+    if (head_dim != 64 && head_dim != 128) return fail(KVC_ERR_UNSUPPORTED, "head_dim %d not supported", head_dim);
+    if (block_size != kvc::kBlockSize) return fail(KVC_ERR_UNSUPPORTED, "block_size %d not supported", block_size);
+    if (n == 0) return KVC_OK;
+    if (!k_new || !v_new || !slot_mapping) return fail(KVC_ERR_INVALID, "null pointer");
+    kvc_status s = check_block_codes(codes, scales, num_blocks, Hkv, block_size);
+    if (s != KVC_OK) return s;
+    if (!aligned16(k_new) || !aligned16(v_new)) return fail(KVC_ERR_INVALID, "k_new and v_new must be 16-byte aligned");
+    if (!aligned_to(8, {slot_mapping})) return fail(KVC_ERR_INVALID, "slot_mapping must be 8-byte aligned");
+    const int64_t row = static_cast<int64_t>(Hkv) * head_dim, tiles = static_cast<int64_t>(num_blocks) * Hkv * 2;
+    if (k_stride % 8 || v_stride % 8 || k_stride < row || v_stride < row)
+        return fail(KVC_ERR_INVALID, "token strides must be multiples of 8 elements and hold a token's heads");
+    s = check_overlap({{codes, tiles * block_size * head_dim}, {scales, tiles * 4}},
+                      {rows_span(k_new, n, k_stride, row, 2), rows_span(v_new, n, v_stride, row, 2),
+                       {slot_mapping, n * int64_t(8)}});
+    if (s != KVC_OK) return s;
+    s = checked([&]() -> kvc_status {
+        std::vector<int64_t> sl;
+        kvc_status e = copy_to_host(sl, slot_mapping, static_cast<size_t>(n), as_stream(stream));
+        if (e != KVC_OK) return e;
+        std::unordered_map<int64_t, int> seen;  // block -> its last token
+        for (int t = 0; t < n; ++t) {
+            if (sl[t] < 0) continue;
+            if (sl[t] >= static_cast<int64_t>(num_blocks) * block_size)
+                return fail(KVC_ERR_CAPACITY, "token %d: slot %lld beyond the cache", t, static_cast<long long>(sl[t]));
+            const auto [at, fresh] = seen.try_emplace(sl[t] / block_size, t);
+            if (!fresh && (at->second != t - 1 || sl[t - 1] + 1 != sl[t]))
+                return fail(KVC_ERR_INVALID, "token %d: its block's tokens are not consecutive", t);
+            at->second = t;
+        }
+        return KVC_OK;
+    });
+    if (s != KVC_OK) return s;
+    kvc::AppendFp8BlockArgs a;
+    a.k = static_cast<const __half*>(k_new);
+    a.v = static_cast<const __half*>(v_new);
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.slots = slot_mapping;
+    a.n = n;
+    a.codes = static_cast<uint8_t*>(codes);
+    a.scales = scales;
+    a.num_blocks = num_blocks;
+    a.Hkv = Hkv;
+    a.D = head_dim;
+    cudaError_t e = kvc::device_error_word(&a.err);
+    if (e != cudaSuccess) return cuda_fail(e, "device error word");
+    e = kvc::launch_append_fp8_block(a, as_stream(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "kv_append_fp8_block launch");
+    return KVC_OK;
+}
+
+static kvc_status window_plan(int B, int Hq, int Hkv, int head_dim, int block_size, int max_context_len, int window,
+                              int sinks, bool block8, size_t* workspace_bytes) {
+    kvc_status s = check_decode_shape(B, Hq, Hkv, head_dim, block_size, max_context_len);
+    if (s == KVC_OK) s = check_window(window, sinks, block8 ? 0 : 1);
+    if (s != KVC_OK) return s;
+    kvc::DecodePlan plan;
+    cudaError_t e = kvc::decode_window_plan(B, Hq, Hkv, head_dim, max_context_len, window, sinks, block8, &plan);
+    if (e != cudaSuccess) return cuda_fail(e, "decode plan");
+    if (workspace_bytes) *workspace_bytes = plan.workspace_bytes;
+    return KVC_OK;
+}
+
+kvc_status paged_decode_window_plan(int B, int Hq, int Hkv, int head_dim, int block_size, int max_context_len,
+                                    int window, int sinks, size_t* workspace_bytes) {
+    return window_plan(B, Hq, Hkv, head_dim, block_size, max_context_len, window, sinks, false, workspace_bytes);
+}
+
+kvc_status paged_decode_fp8_block_plan(int B, int Hq, int Hkv, int head_dim, int block_size, int max_context_len,
+                                       int window, int sinks, size_t* workspace_bytes) {
+    return window_plan(B, Hq, Hkv, head_dim, block_size, max_context_len, window, sinks, true, workspace_bytes);
+}
+
+// The two decode calls behind their own arguments' checks; a holds everything but the workspace and the error word.
+static kvc_status decode_window(kvc::DecodeArgs& a, std::initializer_list<Span> caches, int out_dtype, void* workspace,
+                                size_t workspace_bytes, const char* name, void* stream) {
+    if (!a.q || !a.block_table || !a.context_lens || !a.out) return fail(KVC_ERR_INVALID, "null pointer");
+    if (!aligned16(a.q) || !aligned16(a.out)) return fail(KVC_ERR_INVALID, "q and out must be 16-byte aligned");
+    if (!aligned_to(4, {a.block_table, a.context_lens}))
+        return fail(KVC_ERR_INVALID, "block_table and context_lens must be 4-byte aligned");
+    if (a.max_blocks < 1) return fail(KVC_ERR_INVALID, "max_blocks must be positive");
+    if (a.max_blocks > kvc::kMaxTableBlocks) return fail(KVC_ERR_UNSUPPORTED, "max_blocks * block_size must be < 2^31");
+    if (a.max_context_len > a.max_blocks * kvc::kBlockSize)
+        return fail(KVC_ERR_CAPACITY, "max_context_len %d beyond max_blocks * block_size", a.max_context_len);
+    if (out_dtype != KVC_F16 && out_dtype != KVC_F32) return fail(KVC_ERR_INVALID, "bad out_dtype");
+    if (!std::isfinite(a.scale)) return fail(KVC_ERR_INVALID, "scale is not finite");
+    const int64_t rows = static_cast<int64_t>(a.B) * a.Hq * a.D, per = a.B * int64_t(4);
+    const int64_t new_rows = static_cast<int64_t>(a.B) * a.Hkv * a.D * 2;
+    const Span q = {a.q, rows * 2}, table = {a.block_table, per * a.max_blocks}, lens = {a.context_lens, per},
+               kn = {a.k_new, new_rows}, vn = {a.v_new, new_rows}, out = {a.out, rows * (out_dtype == KVC_F32 ? 4 : 2)};
+    kvc_status s = check_overlap({out}, caches);
+    if (s == KVC_OK) s = check_overlap({out}, {q, table, lens, kn, vn});
+    if (s == KVC_OK && a.k_new) {  // the caches are written too
+        const Span k = *caches.begin(), v = *(caches.begin() + 1);
+        s = check_overlap({k, v}, {q, table, lens, kn, vn});
+    }
+    if (s != KVC_OK) return s;
+    s = checked([&]() -> kvc_status {
+        std::vector<int32_t> ctx, entries;
+        kvc_status e = copy_to_host(ctx, a.context_lens, static_cast<size_t>(a.B), as_stream(stream));
+        if (e == KVC_OK) e = copy_to_host(entries, a.block_table, static_cast<size_t>(a.B) * a.max_blocks, as_stream(stream));
+        if (e != KVC_OK) return e;
+        for (int b = 0; b < a.B; ++b) {
+            if (ctx[b] < 1 || ctx[b] > a.max_context_len)
+                return fail(KVC_ERR_CAPACITY, "sequence %d: context length %d outside [1, %d]", b, ctx[b], a.max_context_len);
+            const kvc::Visible v = kvc::visible_blocks(ctx[b], a.window, a.sinks);
+            for (int i = 0; i < v.nblk; ++i) {
+                const int j = i < v.ns ? i : i - v.ns + v.w0;
+                const int32_t blk = entries[static_cast<size_t>(b) * a.max_blocks + j];
+                if (blk < 0 || blk >= a.num_blocks)
+                    return fail(KVC_ERR_INVALID, "sequence %d: block-table entry %d = %d outside [0, %d)", b, j, blk, a.num_blocks);
+            }
+        }
+        return KVC_OK;
+    });
+    if (s != KVC_OK) return s;
+    kvc::DecodePlan plan;
+    cudaError_t e = kvc::decode_window_plan(a.B, a.Hq, a.Hkv, a.D, a.max_context_len, a.window, a.sinks,
+                                            a.codes != nullptr, &plan);
+    if (e != cudaSuccess) return cuda_fail(e, "decode plan");
+    s = check_workspace(plan.workspace_bytes, workspace, workspace_bytes);
+    if (s == KVC_OK && plan.workspace_bytes) {
+        const Span ws = {workspace, static_cast<int64_t>(plan.workspace_bytes)};
+        s = check_overlap({ws}, caches);
+        if (s == KVC_OK) s = check_overlap({ws}, {out, q, table, lens, kn, vn});
+    }
+    if (s != KVC_OK) return s;
+    a.out_f32 = out_dtype == KVC_F32;
+    a.workspace = workspace;
+    a.workspace_bytes = workspace_bytes;
+    a.blocks_per_split = 0;
+    e = kvc::device_error_word(&a.err);
+    if (e != cudaSuccess) return cuda_fail(e, "device error word");
+    e = kvc::launch_decode_window(a, as_stream(stream));
+    if (e != cudaSuccess) return cuda_fail(e, name);
+    return KVC_OK;
+}
+
+kvc_status paged_decode_window_attention(const void* q, const void* k_new, const void* v_new, void* k_cache,
+                                         void* v_cache, int num_blocks, const int32_t* block_table, int max_blocks,
+                                         const int32_t* context_lens, int window, int sinks, int B, int Hq, int Hkv,
+                                         int head_dim, int block_size, int max_context_len, float scale, void* out,
+                                         int out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    kvc_status s = check_decode_shape(B, Hq, Hkv, head_dim, block_size, max_context_len);
+    if (s == KVC_OK) s = check_window(window, sinks, 1);
+    if (s != KVC_OK || B == 0) return s;
+    if (!k_cache || !v_cache) return fail(KVC_ERR_INVALID, "null pointer");
+    if ((k_new == nullptr) != (v_new == nullptr)) return fail(KVC_ERR_INVALID, "k_new and v_new: both or neither");
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_new) || !aligned16(v_new))
+        return fail(KVC_ERR_INVALID, "caches, k_new and v_new must be 16-byte aligned");
+    if (num_blocks < 1) return fail(KVC_ERR_INVALID, "num_blocks must be positive");
+    if (static_cast<int64_t>(num_blocks) * Hkv * block_size >= (int64_t(1) << 31))
+        return fail(KVC_ERR_UNSUPPORTED, "num_blocks * Hkv * block_size must be < 2^31");
+    kvc::DecodeArgs a = decode_args(q, k_new, v_new, k_cache, v_cache, num_blocks, block_table, max_blocks, context_lens,
+                                    B, Hq, Hkv, head_dim, max_context_len, scale, out, out_dtype, nullptr, 0, 0);
+    a.window = window;
+    a.sinks = sinks;
+    const int64_t cache = static_cast<int64_t>(num_blocks) * Hkv * block_size * head_dim * 2;
+    return decode_window(a, {{k_cache, cache}, {v_cache, cache}}, out_dtype, workspace, workspace_bytes,
+                         "paged_decode_window_attention launch", stream);
+}
+
+kvc_status paged_decode_attention_fp8_block(const void* q, const void* codes, const float* scales, int num_blocks,
+                                            const int32_t* block_table, int max_blocks, const int32_t* context_lens,
+                                            int window, int sinks, int B, int Hq, int Hkv, int head_dim,
+                                            int block_size, int max_context_len, float scale, void* out, int out_dtype,
+                                            void* workspace, size_t workspace_bytes, void* stream) {
+    kvc_status s = check_decode_shape(B, Hq, Hkv, head_dim, block_size, max_context_len);
+    if (s == KVC_OK) s = check_window(window, sinks, 0);
+    if (s != KVC_OK || B == 0) return s;
+    s = check_block_codes(codes, scales, num_blocks, Hkv, block_size);
+    if (s != KVC_OK) return s;
+    kvc::DecodeArgs a = decode_args(q, nullptr, nullptr, nullptr, nullptr, num_blocks, block_table, max_blocks,
+                                    context_lens, B, Hq, Hkv, head_dim, max_context_len, scale, out, out_dtype, nullptr,
+                                    0, 0);
+    a.codes = static_cast<const uint8_t*>(codes);
+    a.scales = scales;
+    a.window = window;
+    a.sinks = sinks;
+    const int64_t tiles = static_cast<int64_t>(num_blocks) * Hkv * 2;
+    return decode_window(a, {{codes, tiles * block_size * head_dim}, {scales, tiles * 4}}, out_dtype, workspace,
+                         workspace_bytes, "paged_decode_attention_fp8_block launch", stream);
+}
+
 kvc_status kvc_call(int which, const void* words, int count, void* stream) {
     if (!words) return fail(KVC_ERR_INVALID, "null pointer");
     switch (which) {
@@ -1231,13 +1511,20 @@ kvc_status kvc_call(int which, const void* words, int count, void* stream) {
         case KVC_CALL_TREE_ATTENTION: return call_with_words(paged_decode_tree_attention, words, count, stream);
         case KVC_CALL_TREE_VERIFY: return call_with_words(draft_tree_verify, words, count, stream);
         case KVC_CALL_TREE_COMMIT: return call_with_words(kv_tree_commit, words, count, stream);
+        case KVC_CALL_BLOCK_TABLES: return call_with_words(kv_block_tables, words, count, stream);
+        case KVC_CALL_APPEND_FP8_BLOCK: return call_with_words(kv_append_fp8_block, words, count, stream);
+        case KVC_CALL_ATTENTION_FP8_BLOCK: return call_with_words(paged_decode_attention_fp8_block, words, count, stream);
+        case KVC_CALL_WINDOW_ATTENTION: return call_with_words(paged_decode_window_attention, words, count, stream);
+        case KVC_CALL_PREFILL_WINDOW: return call_with_words(prefill_window_attention, words, count, stream);
         default: return fail(KVC_ERR_INVALID, "unknown call %d", which);
     }
 }
 
-kvc_status prefill_attention_ex(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int nseq,
-                                int total_tokens, int max_seqlen, int Hq, int Hkv, int head_dim, float scale,
-                                int causal, int p_precision, void* out, int out_dtype, void* stream) {
+// (window 0: none)
+static kvc_status prefill_common(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int nseq,
+                                 int total_tokens, int max_seqlen, int Hq, int Hkv, int head_dim, float scale,
+                                 int causal, int window, int sinks, int p_precision, void* out, int out_dtype,
+                                 const char* name, void* stream) {
     if (p_precision != KVC_PREFILL_P_F16 && p_precision != KVC_PREFILL_P_SPLIT)
         return fail(KVC_ERR_INVALID, "bad p_precision %d", p_precision);
     if (nseq < 0 || total_tokens < 0 || max_seqlen < 0 || Hq < 1 || Hkv < 1) return fail(KVC_ERR_INVALID, "bad sizes");
@@ -1274,12 +1561,38 @@ kvc_status prefill_attention_ex(const void* q, const void* k, const void* v, con
     a.causal = causal ? 1 : 0;
     a.out = out;
     a.out_f32 = out_dtype == KVC_F32;
+    a.window = window;
+    a.sinks = sinks;
     a.split_p = p_precision == KVC_PREFILL_P_SPLIT;
     cudaError_t e = kvc::device_error_word(&a.err);
     if (e != cudaSuccess) return cuda_fail(e, "device error word");
     e = kvc::launch_prefill(a, as_stream(stream));
-    if (e != cudaSuccess) return cuda_fail(e, "prefill_attention launch");
+    if (e != cudaSuccess) return cuda_fail(e, name);
     return KVC_OK;
+}
+
+kvc_status prefill_attention_ex(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int nseq,
+                                int total_tokens, int max_seqlen, int Hq, int Hkv, int head_dim, float scale,
+                                int causal, int p_precision, void* out, int out_dtype, void* stream) {
+    return prefill_common(q, k, v, cu_seqlens, nseq, total_tokens, max_seqlen, Hq, Hkv, head_dim, scale, causal, 0, 0,
+                          p_precision, out, out_dtype, "prefill_attention launch", stream);
+}
+
+kvc_status prefill_window_attention(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int nseq,
+                                    int total_tokens, int max_seqlen, int Hq, int Hkv, int head_dim, float scale,
+                                    int window, int sinks, int p_precision, void* out, int out_dtype, void* stream) {
+    kvc_status s = check_window(window, sinks, 1);
+    if (s != KVC_OK) return s;
+    if (!std::isfinite(scale)) return fail(KVC_ERR_INVALID, "scale is not finite");
+    if (nseq > 0 && total_tokens > 0 && Hq > 0 && Hkv > 0 && head_dim > 0) {
+        if (!aligned_to(4, {cu_seqlens})) return fail(KVC_ERR_INVALID, "cu_seqlens must be 4-byte aligned");
+        const int64_t qn = static_cast<int64_t>(total_tokens) * Hq * head_dim, kn = static_cast<int64_t>(total_tokens) * Hkv * head_dim;
+        s = check_overlap({{out, qn * (out_dtype == KVC_F32 ? 4 : 2)}},
+                          {{q, qn * 2}, {k, kn * 2}, {v, kn * 2}, {cu_seqlens, (nseq + int64_t(1)) * 4}});
+        if (s != KVC_OK) return s;
+    }
+    return prefill_common(q, k, v, cu_seqlens, nseq, total_tokens, max_seqlen, Hq, Hkv, head_dim, scale, 1, window, sinks,
+                          p_precision, out, out_dtype, "prefill_window_attention launch", stream);
 }
 
 kvc_status prefill_attention(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int nseq,

@@ -41,6 +41,8 @@
 //    previous kernel: it fetches block tables, context lengths and cached K/V
 //    before waiting for that kernel, and reads q, k_new, v_new (and writes
 //    anything) only after.
+#include <cfloat>
+
 #include "decode_common.cuh"
 
 namespace kvc {
@@ -54,6 +56,7 @@ struct DecodeKernelParams {
     __half* k_cache;      // generic pointers to the same layer as the tensor maps (append target)
     __half* v_cache;
     const uint8_t* kv_fp8;   // fp8: the layer's records, one per (block, KV head) (fp8_record_bytes each)
+    const float* scales;     // block-scaled fp8: [NB][Hkv][2], K and V
     const int32_t* block_table;
     const int32_t* context_lens;
     void* out;
@@ -71,6 +74,8 @@ struct DecodeKernelParams {
     int out_f32;
     int len_order;  // 1: the CTAs at position z along the sequences take the z-th longest context
     float scale_log2;
+    int window, sinks;  // kWindow: what a query sees (window 0: all)
+    int wait_first;     // kWindow or block-scaled: 1 = nothing is read before the kernel in front is done
     unsigned trace_seq;  // launch counter, used by the optional trace only
 };
 
@@ -127,11 +132,31 @@ __device__ unsigned g_trace_n;
 // follow the same permutation, which leaves the dot products unchanged); for V the token order of the rows
 // does the same.  The K scale multiplies the scores and the V scale the probabilities before the P V product,
 // so the arithmetic is the fp16 path's
-template <int D, bool kSuffix, bool kFp8 = false>
-__global__ void __launch_bounds__(DecodeCfg<D, kFp8>::kThreads, KVC_DEC_MIN_CTAS)
+//
+// kCacheFp8Block: e4m3 codes with one power-of-two scale for a block's K and one for its V (per KV head), rows of
+// dims as they are, brought in by TMA with a swizzle that makes ldmatrix free of bank conflicts.  K fragments: ldmatrix
+// of 16-byte chunks gives lane (g, t) dims 4t..4t+3 of token g, as with the rows' codes above.  V fragments: the
+// transposing ldmatrix of dim pairs gives lane (g, t) dims 2g, 2g+1 of tokens 2t and 2t+1; converted and regrouped by
+// token pairs they are rows g and g + 8 of an A tile whose rows are dims 2g and 2g + 1.  The K scale multiplies the
+// scores.  The V scale goes into the weights, over a reference: a block whose scale is above the reference, or less
+// than kScaleBand times it, moves the reference and rescales O, exactly, so that weights keep fp16's range and no code
+// is multiplied.
+//
+// kWindow: the query sees the newest `window` positions and the first `sinks`.  The blocks that hold them are numbered
+// consecutively and split like a context of that length; blocks between sinks and window are never read, nor are their
+// table entries.  Positions that are not visible inside a block take no weight and their V rows are zeroed.
+//
+// Both of these forms carry their weights 2^kWeightLog2 times as large: fp16's 11 bits then last down to 2^-21 of a
+// row's largest weight, and the residual's down to 2^-32.
+template <int D, bool kSuffix, int kCache = kCacheF16, bool kWindow = false>
+__global__ void __launch_bounds__(DecodeCfg<D, kCache>::kThreads, KVC_DEC_MIN_CTAS)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         const DecodeKernelParams p) {
-    using C = DecodeCfg<D, kFp8>;
+    using C = DecodeCfg<D, kCache>;
+    constexpr bool kFp8 = kCache == kCacheFp8Row, kBlock8 = kCache == kCacheFp8Block, kNew = kWindow || kBlock8;
+    constexpr float kWeightLog2 = kNew ? 7.f : 0.f;
+    constexpr float kLazyMax = kNew ? 15.f : KVC_DEC_LAZY_MAX;  // weights stay <= 2^this
+    constexpr float kScaleBand = 0x1p-6f;
     constexpr int NW = C::kWarps, ST = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -143,6 +168,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, kFp8>::kThreads, KVC_DEC_MIN_CTAS
     float* s_inbox = reinterpret_cast<float*>(smem + C::kRingBytes + C::kBarBytes + C::kStateBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t4 = lane & 3;
+    if constexpr (kNew) {
+        if (p.wait_first) grid_dependency_wait();
+    }
     // a KV head's G query heads go in chunks of at most 8 (the mma tiles' 8 columns) to consecutive CTAs along y,
     // which read the same K/V blocks at about the same time (the second read is mostly an L2 hit)
     __shared__ int s_len_hist[33];
@@ -196,16 +224,39 @@ __global__ void __launch_bounds__(DecodeCfg<D, kFp8>::kThreads, KVC_DEC_MIN_CTAS
     const int cb0 = cidx * p.bpc;
     const int nwarps_cl = cs * NW;
     const int gw = rank * NW + warp;  // warp index within the cluster
-    const int row_end = min(cb0 + p.bpc, p.max_blocks - off);
     int first_phys[ST];
-#pragma unroll
-    for (int s = 0; s < ST; ++s) {
-        const int j = cb0 + gw + s * nwarps_cl;
-        first_phys[s] = (lane == 0 && j < row_end) ? table[j] : -1;
-    }
-    const int nload = max(0, row_end - cb0);
-    for (int t = threadIdx.x; t < nload; t += C::kThreads) s_table[t] = table[cb0 + t];
+    float2 sc_lane = make_float2(0.f, 0.f);  // kBlock8: lane s holds the K and V scales of stage s's block
+    auto load_scales = [&](int phys) {
+        return phys >= 0 && phys < p.num_blocks
+                   ? *(reinterpret_cast<const float2*>(p.scales) + static_cast<int64_t>(phys) * p.Hkv + kvh)
+                   : make_float2(0.f, 0.f);
+    };
+    Visible vis = {};
+    // entry j of the row that the cluster's blocks are numbered by
+    auto table_at = [&](int j) {
+        if constexpr (kWindow) return table[j < vis.ns ? j : j - vis.ns + vis.w0];
+        return table[j];
+    };
     const int ctx_full = p.context_lens[b];
+    auto first_loads = [&](int row_end) {
+        if constexpr (kNew) {
+            const int j = cb0 + gw + lane * nwarps_cl;
+            const int phys = lane < ST && j < row_end ? table_at(j) : -1;
+            if constexpr (kBlock8) sc_lane = load_scales(phys);
+#pragma unroll
+            for (int s = 0; s < ST; ++s) first_phys[s] = __shfl_sync(0xffffffffu, phys, s);
+        } else {
+#pragma unroll
+            for (int s = 0; s < ST; ++s) {
+                const int j = cb0 + gw + s * nwarps_cl;
+                first_phys[s] = (lane == 0 && j < row_end) ? table[j] : -1;
+            }
+        }
+        const int nload = max(0, row_end - cb0);
+        for (int t = threadIdx.x; t < nload; t += C::kThreads) s_table[t] = table_at(cb0 + t);
+    };
+    // (the context length is asked for before the table's entries, but nothing waits for it there)
+    if constexpr (!kWindow) first_loads(min(cb0 + p.bpc, p.max_blocks - off));
     const int ctx = ctx_full - off * kBlockSize;  // tokens this call covers (all of them without an offset)
     // every CTA of a cluster sees the same (b, kvh): these exits are uniform over the cluster
     if (!off_ok || ctx_full < 1 || ctx_full > p.max_blocks * kBlockSize || ctx_full > p.max_ctx || ctx < 1) {
@@ -218,9 +269,11 @@ __global__ void __launch_bounds__(DecodeCfg<D, kFp8>::kThreads, KVC_DEC_MIN_CTAS
         }
         return;
     }
-    const int nblk = (ctx + kBlockSize - 1) / kBlockSize;
+    if constexpr (kWindow) vis = visible_blocks(ctx, p.window, p.sinks);
+    const int nblk = kWindow ? vis.nblk : (ctx + kBlockSize - 1) / kBlockSize;
     const int nclus = (nblk + p.bpc - 1) / p.bpc;  // clusters this sequence needs
     if (cidx >= nclus) return;                     // the whole cluster is past the context
+    if constexpr (kWindow) first_loads(min(cb0 + p.bpc, nblk));
     const int cb1 = min(cb0 + p.bpc, nblk);        // this cluster covers blocks [cb0, cb1)
 
     uint8_t* wring = smem + warp * C::kWarpRingBytes;
@@ -237,7 +290,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, kFp8>::kThreads, KVC_DEC_MIN_CTAS
         uint8_t* st = wring + s * C::kStageBytes;
         mbar_arrive_expect_tx(bar, C::kStageBytes);
         const int y = (phys * p.Hkv + kvh) * kBlockSize;
-        if constexpr (kFp8) {  // the block's record: K codes and scales, V codes and scales, in one copy
+        if constexpr (kBlock8) {
+            tma_load_2d(st, &tmK, bar, 0, 2 * y, policy);
+        } else if constexpr (kFp8) {  // the block's record: K codes and scales, V codes and scales, in one copy
             bulk_load(st, p.kv_fp8 + static_cast<int64_t>(phys * p.Hkv + kvh) * C::kStageBytes, C::kStageBytes, bar);
         } else {
 #pragma unroll
@@ -258,7 +313,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, kFp8>::kThreads, KVC_DEC_MIN_CTAS
     if (lane == 0) {
         if (!kFp8 && warp == 0) {  // the fp8 records come by bulk copies (the maps are unused)
             prefetch_tensormap(&tmK);
-            prefetch_tensormap(&tmV);
+            if (!kBlock8) prefetch_tensormap(&tmV);
         }
 #pragma unroll
         for (int s = 0; s < ST; ++s)
@@ -292,14 +347,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, kFp8>::kThreads, KVC_DEC_MIN_CTAS
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
             // fp8: k indices 2t, 2t+1 / 2t+8, 2t+9 of the group are dims 4t, 4t+1 / 4t+2, 4t+3 (see above)
-            const int c0 = kFp8 ? 4 * t4 : 2 * t4, c1 = kFp8 ? 4 * t4 + 2 : 8 + 2 * t4;
+            constexpr bool kPerm = kFp8 || kBlock8;
+            const int c0 = kPerm ? 4 * t4 : 2 * t4, c1 = kPerm ? 4 * t4 + 2 : 8 + 2 * t4;
             qa[ks][0] = row_ok ? *reinterpret_cast<const uint32_t*>(qrow + ks * 16 + c0) : 0u;
             qa[ks][1] = row_ok ? *reinterpret_cast<const uint32_t*>(qrow + ks * 16 + c1) : 0u;
         }
     }
     // fused append: any warp of the last cluster may get the block of position ctx-1; each holds the
     // new row (lanes 0-15: K chunks, 16-31: V chunks) to write it to the cache and patch its tile
-    const int app_blk = !kFp8 && p.k_new != nullptr && cidx == nclus - 1 ? nblk - 1 : -1;
+    const int app_blk = kCache == kCacheF16 && p.k_new != nullptr && cidx == nclus - 1 ? nblk - 1 : -1;
     const int app_row = (ctx - 1) % kBlockSize;
     uint4 app_val = make_uint4(0, 0, 0, 0);
     if (app_blk >= 0 && (lane & 15) < D / 8) {
@@ -319,8 +375,11 @@ __global__ void __launch_bounds__(DecodeCfg<D, kFp8>::kThreads, KVC_DEC_MIN_CTAS
     float o[D / 16][4];
 #pragma unroll
     for (int mt = 0; mt < D / 16; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
-    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+    // (kNew: a block whose scores are all minus infinity leaves a finite maximum, against which its weights are 0)
+    constexpr float kNoMax = kNew ? -FLT_MAX : -INFINITY;
+    float m_run[2] = {kNoMax, kNoMax}, l_run[2] = {0.f, 0.f};
     const float sl2 = p.scale_log2;
+    float v_ref = 0.f, v_inv = 0.f;  // kBlock8: O is in units of v_ref (0: nothing in it yet), and 1 / v_ref
     uint32_t phase = 0;  // bit s: parity of stage s's next completion
     bool timed_out = false;
 
@@ -329,7 +388,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, kFp8>::kThreads, KVC_DEC_MIN_CTAS
         __syncwarp();
         const int nj = next_j;
         next_j += nwarps_cl;
-        if (nj < cb1 && lane == 0) issue(s, s_table[nj - cb0]);
+        if constexpr (kBlock8) {
+            if (nj < cb1) {
+                const int phys = s_table[nj - cb0];
+                if (lane == 0) issue(s, phys);
+                if (lane == s) sc_lane = load_scales(phys);
+            }
+        } else {
+            if (nj < cb1 && lane == 0) issue(s, s_table[nj - cb0]);
+        }
 #if KVC_DEC_TRIGGER == 3
         if (nj >= cb1 && nj < cb1 + nwarps_cl) grid_dependents_launch();  // this warp's last copy is out
 #elif KVC_DEC_TRIGGER == 2
@@ -358,15 +425,22 @@ __global__ void __launch_bounds__(DecodeCfg<D, kFp8>::kThreads, KVC_DEC_MIN_CTAS
             }
             const int phys = s_table[jj - cb0];
             if (phys >= 0 && phys < p.num_blocks) {
-                const int rem = ctx - jj * kBlockSize;  // valid tokens in this block (>= 1)
+                const int pos0 = kWindow ? (jj < vis.ns ? jj : jj - vis.ns + vis.w0) * kBlockSize : jj * kBlockSize;
+                const int rem = ctx - pos0;  // tokens of the context in this block (>= 1)
+                // is token tau of the block seen?
+                auto seen = [&](int tau) {
+                    if constexpr (kWindow) return tau < rem && (pos0 + tau >= vis.start || pos0 + tau < vis.sinks);
+                    return tau < rem;
+                };
+                const bool all_seen = rem >= kBlockSize && (!kWindow || pos0 >= vis.start || pos0 + kBlockSize <= vis.sinks);
                 // scores of tokens g and g+8 carry sl2 (times their K scales with an fp8 cache); the V scales
                 // of tokens g and g+8 (0 past the context) multiply their probabilities before P V
                 float sl2g = sl2, sl2g8 = sl2, vsg = 1.f, vsg8 = 1.f;
                 // rows of V past the context may hold any bits (even NaN): zero them in registers
                 uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-                if (rem < kBlockSize) {
-                    keep0 = (2 * t4 < rem ? 0x0000ffffu : 0u) | (2 * t4 + 1 < rem ? 0xffff0000u : 0u);
-                    keep1 = (8 + 2 * t4 < rem ? 0x0000ffffu : 0u) | (9 + 2 * t4 < rem ? 0xffff0000u : 0u);
+                if (!all_seen) {
+                    keep0 = (seen(2 * t4) ? 0x0000ffffu : 0u) | (seen(2 * t4 + 1) ? 0xffff0000u : 0u);
+                    keep1 = (seen(8 + 2 * t4) ? 0x0000ffffu : 0u) | (seen(9 + 2 * t4) ? 0xffff0000u : 0u);
                 }
                 float sc[4] = {0.f, 0.f, 0.f, 0.f};
                 uint32_t va[D / 16][4];
@@ -427,6 +501,67 @@ __global__ void __launch_bounds__(DecodeCfg<D, kFp8>::kThreads, KVC_DEC_MIN_CTAS
                     }
                     refill(s);
                     refilled = true;
+                } else if constexpr (kBlock8) {
+                    const uint32_t kbase = smem_u32(wring + s * C::kStageBytes);
+                    sl2g = sl2g8 = sl2 * __shfl_sync(0xffffffffu, sc_lane.x, s);
+                    vsg = vsg8 = __shfl_sync(0xffffffffu, sc_lane.y, s);
+                    float sc2[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {  // two chunks of 16 dims at a time
+                        uint32_t r[4];
+                        ldsm_x4(kbase + swz8<D>((mi & 1) * 8 + (lane & 7), 2 * c + (mi >> 1)), r[0], r[1], r[2], r[3]);
+                        mma_f16_16816(sc, e4m3x2_to_half2(r[0]), e4m3x2_to_half2(r[1]), e4m3x2_to_half2(r[0] >> 16),
+                                      e4m3x2_to_half2(r[1] >> 16), qa[2 * c][0], qa[2 * c][1]);
+                        mma_f16_16816(sc2, e4m3x2_to_half2(r[2]), e4m3x2_to_half2(r[3]), e4m3x2_to_half2(r[2] >> 16),
+                                      e4m3x2_to_half2(r[3] >> 16), qa[2 * c + 1][0], qa[2 * c + 1][1]);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sc[k] += sc2[k];
+                    uint32_t vr[D / 16][2];
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c)
+                        ldsm_x4_t(kbase + C::kCodeTileBytes + swz8<D>((mi & 1) * 8 + (lane & 7), 2 * c + (mi >> 1)),
+                                  vr[2 * c][0], vr[2 * c][1], vr[2 * c + 1][0], vr[2 * c + 1][1]);
+                    // (the copy may overwrite the stage once these reads have returned, see below)
+                    uint32_t dep = 0;
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c)
+                        asm volatile("xor.b32 %0, %0, %1;" : "+r"(dep) : "r"(vr[2 * c][0]));
+                    refill(s);
+                    refilled = true;
+#pragma unroll
+                    for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t even = e4m3x2_to_half2(vr[mt][k]), odd = e4m3x2_to_half2(vr[mt][k] >> 16);
+                            va[mt][2 * k] = __byte_perm(even, odd, 0x5410);
+                            va[mt][2 * k + 1] = __byte_perm(even, odd, 0x7632);
+                        }
+                    if (!all_seen) {
+#pragma unroll
+                        for (int mt = 0; mt < D / 16; ++mt) {
+                            va[mt][0] &= keep0;
+                            va[mt][1] &= keep0;
+                            va[mt][2] &= keep1;
+                            va[mt][3] &= keep1;
+                        }
+                    }
+                    // the block's V scale against the reference
+                    if (vsg > v_ref || vsg < v_ref * kScaleBand) {  // the same in every lane
+                        // (a scale that no append writes - 0, negative, not a number - leaves the reference alone)
+                        if (v_ref > 0.f && vsg > 0.f) {
+                            const float r = v_ref / vsg;
+#pragma unroll
+                            for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) o[mt][k] *= r;
+                        }
+                        if (vsg > 0.f) {
+                            v_ref = vsg;
+                            v_inv = 1.f / vsg;
+                        }
+                    }
+                    vsg = vsg8 = vsg * v_inv;
                 } else {
                     const uint32_t kbase = smem_u32(wring + s * C::kStageBytes);
                     vbase = kbase + C::kTileBytes;
@@ -464,7 +599,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, kFp8>::kThreads, KVC_DEC_MIN_CTAS
                     for (int mt = 0; mt < D / 16; ++mt)
                         ldsm_x4_t(vbase + swz((mi >> 1) * 8 + (lane & 7), 2 * mt + (mi & 1)), va[mt][0], va[mt][1],
                                   va[mt][2], va[mt][3]);
-                    if (rem < kBlockSize) {  // the context's last block (warp-uniform)
+                    if (!all_seen) {  // the context's last block, or an edge of the window (warp-uniform)
 #pragma unroll
                         for (int mt = 0; mt < D / 16; ++mt) {
                             va[mt][0] &= keep0;
@@ -486,21 +621,22 @@ __global__ void __launch_bounds__(DecodeCfg<D, kFp8>::kThreads, KVC_DEC_MIN_CTAS
                 }
                 // ---- online softmax per head (column): this lane holds tokens g, g+8 of heads 2*t4, 2*t4+1 ----
                 float x[4];
-                x[0] = g < rem ? sc[0] * sl2g : -INFINITY;
-                x[1] = g < rem ? sc[1] * sl2g : -INFINITY;
-                x[2] = g + 8 < rem ? sc[2] * sl2g8 : -INFINITY;
-                x[3] = g + 8 < rem ? sc[3] * sl2g8 : -INFINITY;
+                const bool see0 = seen(g), see1 = seen(g + 8);
+                x[0] = see0 ? sc[0] * sl2g : -INFINITY;
+                x[1] = see0 ? sc[1] * sl2g : -INFINITY;
+                x[2] = see1 ? sc[2] * sl2g8 : -INFINITY;
+                x[3] = see1 ? sc[3] * sl2g8 : -INFINITY;
                 float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
                 // the running maxima move only when a score exceeds them by more than 2^KVC_DEC_LAZY_MAX (always
                 // in the first block, where they are -inf); the weights below stay <= 2^KVC_DEC_LAZY_MAX
-                if (KVC_DEC_LAZY_MAX == 0 || __any_sync(0xffffffffu, mx0 > m_run[0] + KVC_DEC_LAZY_MAX ||
-                                                                      mx1 > m_run[1] + KVC_DEC_LAZY_MAX)) {
+                if (KVC_DEC_LAZY_MAX == 0 ||
+                    __any_sync(0xffffffffu, mx0 > m_run[0] + kLazyMax || mx1 > m_run[1] + kLazyMax)) {
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) {
                         mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
                         mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
                     }
-                    const float mn0 = fmaxf(m_run[0], mx0), mn1 = fmaxf(m_run[1], mx1);
+                    const float mn0 = fmaxf(m_run[0], mx0 - kWeightLog2), mn1 = fmaxf(m_run[1], mx1 - kWeightLog2);
                     const float al0 = ex2(m_run[0] - mn0), al1 = ex2(m_run[1] - mn1);
                     m_run[0] = mn0;
                     m_run[1] = mn1;
@@ -519,7 +655,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, kFp8>::kThreads, KVC_DEC_MIN_CTAS
                 // P^T as the B operand (k = tokens, n = heads): transpose the two 8x8 halves in registers;
                 // P = hi + lo, both fp16, so the P V product keeps ~fp32 accuracy
                 const float q0 = p0 * vsg, q1 = p1 * vsg, q2 = p2 * vsg8, q3 = p3 * vsg8;
-                const uint32_t h01 = pack_half2(q0, q1), h23 = pack_half2(q2, q3);
+                // (kNew: scores beyond 2^27 can lie a little more than kLazyMax above the maximum, their own rounding)
+                const uint32_t h01 = kNew ? pack_half2_finite(q0, q1) : pack_half2(q0, q1),
+                               h23 = kNew ? pack_half2_finite(q2, q3) : pack_half2(q2, q3);
                 const float2 f01 = unpack_half2(h01), f23 = unpack_half2(h23);
                 const uint32_t bh0 = movmatrix_trans(h01), bh1 = movmatrix_trans(h23);
                 constexpr bool kOneP = kFp8 && KVC_DEC_FP8_ONE_P;
@@ -589,6 +727,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, kFp8>::kThreads, KVC_DEC_MIN_CTAS
     float* wo = wm + 16;
 #pragma unroll
     for (int mt = 0; mt < D / 16; ++mt) {
+        if constexpr (kBlock8) {  // rows g and g + 8 are dims 2g and 2g + 1
+            const int d = mt * 16 + 2 * g;
+            *reinterpret_cast<float2*>(wo + (2 * t4) * C::kMergeStride + d) = make_float2(o[mt][0] * v_ref, o[mt][2] * v_ref);
+            *reinterpret_cast<float2*>(wo + (2 * t4 + 1) * C::kMergeStride + d) = make_float2(o[mt][1] * v_ref, o[mt][3] * v_ref);
+            continue;
+        }
         const int d = mt * 16 + g;
         wo[(2 * t4) * C::kMergeStride + d] = o[mt][0];
         wo[(2 * t4 + 1) * C::kMergeStride + d] = o[mt][1];
@@ -697,17 +841,19 @@ __global__ void __launch_bounds__(DecodeCfg<D, kFp8>::kThreads, KVC_DEC_MIN_CTAS
     // slot c of the merge: c == 0 is this CTA's own state, c >= 1 the inbox slot of rank c; a CTA without
     // blocks has l = 0 and takes no part
     auto src = [&](int c) -> const float* { return c == 0 ? s_m : s_inbox + (c - 1) * stride; };
+    // (kNew: a NaN among the scores that a query sees is one in its output, whichever CTA had it)
+    auto takes_part = [](float l) { return kNew ? !(l <= 0.f) : l > 0.f; };
     for (int e = 4 * threadIdx.x; e < Gc * D; e += 4 * C::kThreads) {
         const int gg = e / D, d = e % D;
         float M = -INFINITY;
         for (int c = 0; c < cs; ++c)
-            if (src(c)[8 + gg] > 0.f) M = fmaxf(M, src(c)[gg]);
+            if (takes_part(src(c)[8 + gg])) M = fmaxf(M, src(c)[gg]);
         float L = 0.f;
         float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int c = 0; c < cs; ++c) {
             const float* r = src(c);
             const float l = r[8 + gg];
-            const float w = l > 0.f ? ex2(r[gg] - M) : 0.f;
+            const float w = takes_part(l) ? ex2(r[gg] - M) : 0.f;
             L += l * w;
             O = fma4(w, *reinterpret_cast<const float4*>(r + 16 + e), O);
         }
@@ -750,6 +896,7 @@ __global__ void __launch_bounds__(256) paged_decode_combine_kernel(const Combine
     // launch made the next grid's clusters land piecemeal in the slots the current one frees, and the layer of a
     // 24-layer step slowed (B = 1 x 131072: 17.1 -> 20.2 us; B = 1 x 4096: 6.0 -> 4.9 us, where it fits).
     if (KVC_COMBINE_EARLY_TRIGGER && p.early_release) grid_dependents_launch();
+    if (p.wait_first) grid_dependency_wait();
     // context lengths and prefix offsets are never written by the kernel before (the launch-overlap contract):
     // they are read before the dependency wait, the parts and the output only after it
     const int ctx_full = p.context_lens[b];
@@ -757,7 +904,8 @@ __global__ void __launch_bounds__(256) paged_decode_combine_kernel(const Combine
     const int ctx = ctx_full - off * kBlockSize;  // tokens of the suffix parts
     const bool bad = off < 0 || off >= p.max_blocks || ctx_full < p.q_len || ctx_full > p.max_blocks * kBlockSize ||
                      ctx_full > p.max_ctx || ctx < 1;
-    const int nsuf = bad ? 0 : ((ctx + kBlockSize - 1) / kBlockSize + p.bpc - 1) / p.bpc;
+    const int nvis = bad ? 0 : p.window > 0 ? visible_blocks(ctx, p.window, p.sinks).nblk : (ctx + kBlockSize - 1) / kBlockSize;
+    const int nsuf = bad ? 0 : (nvis + p.bpc - 1) / p.bpc;
     const int npre = off > 0 && p.prefix_chunk > 0 ? (off + p.prefix_chunk - 1) / p.prefix_chunk : 0;
     if (!bad && !p.cascade && nsuf <= 1) {  // the cluster wrote the output itself
         leave_before_dependency_wait();
@@ -789,7 +937,8 @@ __global__ void __launch_bounds__(256) paged_decode_combine_kernel(const Combine
         const int64_t r = part_row(s);
         const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + r * 2);
         const float4 a = *reinterpret_cast<const float4*>(p.part_acc + r * D + 4 * q);
-        if (ml.y > 0.f) {  // a part that saw no token adds nothing
+        // a part that saw no token adds nothing (and a NaN is not dropped where the parts are of a new form)
+        if (ml.y > 0.f || (p.keep_nan && ml.y != ml.y)) {
             const float mn = fmaxf(mt, ml.x);
             const float c_old = mt == -INFINITY ? 0.f : ex2(mt - mn), c_new = ex2(ml.x - mn);
             O = fma4(c_new, a, scale4(O, c_old));
@@ -879,36 +1028,32 @@ __global__ void __launch_bounds__(256) paged_decode_combine_kernel(const Combine
 // host side
 // ---------------------------------------------------------------------------
 // one-time kernel attributes (largest shared-memory size this kernel can be launched with)
-template <int D>
+template <int D, int kCache = kCacheF16, bool kWindow = false>
 static cudaError_t decode_setup() {
-    using C = DecodeCfg<D>;
+    using C = DecodeCfg<D, kCache>;
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
     std::call_once(once, [] {
-        for (auto kern : {paged_decode_kernel<D, false>, paged_decode_kernel<D, true>}) {
+        auto prepare = [](auto kern) {
             if (err == cudaSuccess)
                 err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            C::smem_bytes(kMaxCluster, 8, kMaxClusterBlocks));
             if (err == cudaSuccess && kMaxCluster > 8)
                 err = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        }
-        if (err == cudaSuccess)
-            err = cudaFuncSetAttribute(paged_decode_kernel<D, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       DecodeCfg<D, true>::smem_bytes(kMaxCluster, 8, kMaxClusterBlocks));
-        if (err == cudaSuccess && kMaxCluster > 8)
-            err = cudaFuncSetAttribute(paged_decode_kernel<D, false, true>,
-                                       cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        };
+        prepare(paged_decode_kernel<D, false, kCache, kWindow>);
+        if constexpr (kCache == kCacheF16 && !kWindow) prepare(paged_decode_kernel<D, true>);
     });
     return err;
 }
 
 // resident CTAs per SM of the decode kernel with `smem` bytes of dynamic shared memory (cached)
-template <int D>
+template <int D, int kCache = kCacheF16, bool kWindow = false>
 static cudaError_t decode_occupancy(int smem, int* ctas) {
-    using C = DecodeCfg<D>;
+    using C = DecodeCfg<D, kCache>;
     static std::mutex mu;
     static int cached_smem[64] = {0}, cached_occ[64] = {0};
-    cudaError_t e = decode_setup<D>();
+    cudaError_t e = decode_setup<D, kCache, kWindow>();
     if (e != cudaSuccess) return e;
     std::lock_guard<std::mutex> lk(mu);
     for (int i = 0; i < 64; ++i)
@@ -917,7 +1062,8 @@ static cudaError_t decode_occupancy(int smem, int* ctas) {
             return cudaSuccess;
         }
     int occ = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, paged_decode_kernel<D, false>, C::kThreads, smem);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, paged_decode_kernel<D, false, kCache, kWindow>, C::kThreads,
+                                                      smem);
     if (e != cudaSuccess) return e;
     if (occ < 1) return cudaErrorInvalidConfiguration;
     for (int i = 0; i < 64; ++i)
@@ -933,12 +1079,12 @@ static cudaError_t decode_occupancy(int smem, int* ctas) {
 // thread-block clusters of cs CTAs (smem bytes of dynamic shared memory each) that can be resident at once: the
 // clusters of one launch are placed within a GPC each, so this is below SMs x CTAs-per-SM / cs for larger clusters
 // (cached per (cs, smem))
-template <int D>
+template <int D, int kCache = kCacheF16, bool kWindow = false>
 static cudaError_t decode_resident_clusters(int cs, int smem, int* clusters) {
-    using C = DecodeCfg<D>;
+    using C = DecodeCfg<D, kCache>;
     static std::mutex mu;
     static int cached_key[256] = {0}, cached_val[256] = {0};
-    cudaError_t e = decode_setup<D>();
+    cudaError_t e = decode_setup<D, kCache, kWindow>();
     if (e != cudaSuccess) return e;
     int dev = 0;
     e = cudaGetDevice(&dev);
@@ -962,7 +1108,7 @@ static cudaError_t decode_resident_clusters(int cs, int smem, int* clusters) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, paged_decode_kernel<D, false>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&n, paged_decode_kernel<D, false, kCache, kWindow>, &cfg);
     if (e != cudaSuccess) return e;
     for (int i = 0; i < 256; ++i)
         if (cached_key[i] == 0) {
@@ -974,10 +1120,11 @@ static cudaError_t decode_resident_clusters(int cs, int smem, int* clusters) {
     return cudaSuccess;
 }
 
-template <int D>
-static cudaError_t plan_d(int B, int Hq, int Hkv, int max_ctx, int bpc_req, DecodePlan* plan) {
-    using C = DecodeCfg<D>;
-    const int nblk = std::max((max_ctx + kBlockSize - 1) / kBlockSize, 1);
+// (nblk: the blocks of the longest context, or what of them is visible)
+template <int D, int kCache = kCacheF16, bool kWindow = false>
+static cudaError_t plan_d(int B, int Hq, int Hkv, int nblk, int bpc_req, DecodePlan* plan) {
+    using C = DecodeCfg<D, kCache>;
+    nblk = std::max(nblk, 1);
     const int Gfull = std::max(1, Hq / std::max(Hkv, 1));
     const int G = std::min(Gfull, 8);            // query heads of one CTA
     const int hchunks = (Gfull + 7) / 8;          // CTAs per (sequence, KV head) along the heads
@@ -996,17 +1143,18 @@ static cudaError_t plan_d(int B, int Hq, int Hkv, int max_ctx, int bpc_req, Deco
         // waves).
         const int smem_est = C::smem_bytes(kMaxCluster, G, std::min(nblk, kMaxClusterBlocks));
         int occ = 0;
-        cudaError_t e = decode_occupancy<D>(smem_est, &occ);
+        cudaError_t e = decode_occupancy<D, kCache, kWindow>(smem_est, &occ);
         if (e != cudaSuccess) return e;
         const int64_t segs = std::max<int64_t>(1, static_cast<int64_t>(B) * Hkv * hchunks);
         const int64_t min_ncl = (nblk + kMaxClusterBlocks - 1) / kMaxClusterBlocks;
-        const int64_t kv_bytes = static_cast<int64_t>(B) * Hkv * nblk * (2 * kBlockSize * D * 2);
+        const int64_t kv_bytes =
+            static_cast<int64_t>(B) * Hkv * nblk * (2 * kBlockSize * D * (kCache == kCacheFp8Block ? 1 : 2));
         int64_t ncl = min_ncl;
         cs = 1;
         for (int c = kMaxCluster; c >= 1; --c) {
             if (c > 1 && (static_cast<int64_t>(c - 1) * C::kWarps >= nblk)) continue;  // a CTA would have no block
             int resident = 0;
-            e = decode_resident_clusters<D>(c, C::smem_bytes(c, G, std::min(nblk, kMaxClusterBlocks)), &resident);
+            e = decode_resident_clusters<D, kCache, kWindow>(c, C::smem_bytes(c, G, std::min(nblk, kMaxClusterBlocks)), &resident);
             if (e != cudaSuccess) return e;
             const int64_t usable = static_cast<int64_t>(resident) * std::min(occ, KVC_DEC_PLAN_CTAS) / occ;
             const int64_t per_seg = usable / segs;
@@ -1033,10 +1181,24 @@ static cudaError_t plan_d(int B, int Hq, int Hkv, int max_ctx, int bpc_req, Deco
 
 cudaError_t decode_plan(int B, int Hq, int Hkv, int D, int max_ctx, int bpc_req, DecodePlan* plan) {
     switch (D) {
-        case 64: return plan_d<64>(B, Hq, Hkv, max_ctx, bpc_req, plan);
-        case 128: return plan_d<128>(B, Hq, Hkv, max_ctx, bpc_req, plan);
+        case 64: return plan_d<64>(B, Hq, Hkv, (max_ctx + kBlockSize - 1) / kBlockSize, bpc_req, plan);
+        case 128: return plan_d<128>(B, Hq, Hkv, (max_ctx + kBlockSize - 1) / kBlockSize, bpc_req, plan);
         default: return cudaErrorInvalidValue;
     }
+}
+
+cudaError_t decode_window_plan(int B, int Hq, int Hkv, int D, int max_ctx, int window, int sinks, bool block8,
+                               DecodePlan* plan) {
+    const int nblk = most_visible_blocks(max_ctx, window, sinks);
+    if (D != 64 && D != 128) return cudaErrorInvalidValue;
+    if (!block8)
+        return D == 64 ? plan_d<64, kCacheF16, true>(B, Hq, Hkv, nblk, 0, plan)
+                       : plan_d<128, kCacheF16, true>(B, Hq, Hkv, nblk, 0, plan);
+    if (window > 0)
+        return D == 64 ? plan_d<64, kCacheFp8Block, true>(B, Hq, Hkv, nblk, 0, plan)
+                       : plan_d<128, kCacheFp8Block, true>(B, Hq, Hkv, nblk, 0, plan);
+    return D == 64 ? plan_d<64, kCacheFp8Block, false>(B, Hq, Hkv, nblk, 0, plan)
+                   : plan_d<128, kCacheFp8Block, false>(B, Hq, Hkv, nblk, 0, plan);
 }
 
 // kernel parameters of a plain decode call (one part per cluster, final output where one cluster covers
@@ -1068,6 +1230,10 @@ static DecodeKernelParams decode_params(const DecodeArgs& a, const DecodePlan& p
     p.part_stride = plan.num_parts;
     p.blk_off = nullptr;
     p.kv_fp8 = a.kv_fp8;
+    p.scales = a.scales;
+    p.window = a.window;
+    p.sinks = a.sinks;
+    p.wait_first = 0;
     p.out_f32 = a.out_f32;
     p.len_order = 0;
     p.scale_log2 = a.scale * kLog2e;
@@ -1078,11 +1244,11 @@ static DecodeKernelParams decode_params(const DecodeArgs& a, const DecodePlan& p
 
 // 1 where the grid has more CTAs than can be resident at once (several waves): the kernel then dispatches the
 // longest contexts first
-template <int D>
+template <int D, int kCache = kCacheF16, bool kWindow = false>
 static int len_order_for(const DecodeArgs& a, const DecodePlan& plan, int hchunks, int smem) {
     if (!KVC_DEC_LEN_ORDER || a.B < 2 || a.B > kLenOrderMaxB) return 0;
     int occ = 0;
-    if (decode_occupancy<D>(smem, &occ) != cudaSuccess) return 0;
+    if (decode_occupancy<D, kCache, kWindow>(smem, &occ) != cudaSuccess) return 0;
     const int64_t ctas = static_cast<int64_t>(plan.num_splits) * a.Hkv * hchunks * a.B;
     return ctas > static_cast<int64_t>(occ) * sm_count() ? 1 : 0;
 }
@@ -1094,6 +1260,8 @@ static cudaError_t launch_decode_d(const DecodeArgs& a, const DecodePlan& plan, 
     if (e != cudaSuccess) return e;
     const int64_t rows = static_cast<int64_t>(a.num_blocks) * a.Hkv * kBlockSize;
     const bool fp8 = a.kv_fp8 != nullptr;
+    if (fp8) e = decode_setup<D, kCacheFp8Row>();
+    if (e != cudaSuccess) return e;
     CUtensorMap tmK, tmV;  // fp8: the records come by bulk copies and the maps are unused
     if (fp8) {
         memset(&tmK, 0, sizeof(tmK));
@@ -1110,12 +1278,12 @@ static cudaError_t launch_decode_d(const DecodeArgs& a, const DecodePlan& plan, 
     const bool pdl = g_launch_overlap.load(std::memory_order_relaxed) != 0;
     dim3 grid(plan.num_splits, a.Hkv * p.hchunks, a.B);
     p.len_order = len_order_for<D>(a, plan, p.hchunks,
-                                   fp8 ? DecodeCfg<D, true>::smem_bytes(plan.cluster, std::min(p.G, 8),
+                                   fp8 ? DecodeCfg<D, kCacheFp8Row>::smem_bytes(plan.cluster, std::min(p.G, 8),
                                                                         plan.blocks_per_split)
                                        : C::smem_bytes(plan.cluster, std::min(p.G, 8), plan.blocks_per_split));
     if (fp8)
-        e = launch(paged_decode_kernel<D, false, true>, grid, dim3(DecodeCfg<D, true>::kThreads),
-                   DecodeCfg<D, true>::smem_bytes(plan.cluster, std::min(p.G, 8), plan.blocks_per_split), stream, pdl,
+        e = launch(paged_decode_kernel<D, false, kCacheFp8Row>, grid, dim3(DecodeCfg<D, kCacheFp8Row>::kThreads),
+                   DecodeCfg<D, kCacheFp8Row>::smem_bytes(plan.cluster, std::min(p.G, 8), plan.blocks_per_split), stream, pdl,
                    static_cast<unsigned>(plan.cluster),
                    tmK, tmV, p);
     else
@@ -1163,6 +1331,72 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
         case 128: return launch_decode_d<128>(a, plan, stream);
         default: return cudaErrorInvalidValue;
     }
+}
+
+// The windowed and the block-scaled forms.  Without launch overlap they are programmatic dependents all the same, that
+// wait for the kernel in front before their first read: only the launch itself runs under that kernel's end.
+template <int D, int kCache, bool kWindow>
+static cudaError_t launch_window_d(const DecodeArgs& a, cudaStream_t stream) {
+    using C = DecodeCfg<D, kCache>;
+    DecodePlan plan;
+    cudaError_t e = plan_d<D, kCache, kWindow>(a.B, a.Hq, a.Hkv, most_visible_blocks(a.max_context_len, a.window, a.sinks),
+                                               0, &plan);
+    if (e == cudaSuccess) e = decode_setup<D, kCache, kWindow>();
+    if (e != cudaSuccess) return e;
+    if (plan.workspace_bytes > a.workspace_bytes) return cudaErrorInvalidValue;
+    const int64_t rows = static_cast<int64_t>(a.num_blocks) * a.Hkv * kBlockSize;
+    CUtensorMap tmK, tmV;
+    if constexpr (kCache == kCacheFp8Block) {
+        e = make_code_map(&tmK, a.codes, D, 2 * rows);
+        tmV = tmK;
+    } else {
+        e = make_tile_map(&tmK, a.k_cache, D, rows);
+        if (e == cudaSuccess) e = make_tile_map(&tmV, a.v_cache, D, rows);
+    }
+    if (e != cudaSuccess) return e;
+    const size_t nrow = static_cast<size_t>(a.B) * a.Hq * plan.num_parts;
+    float* part_ml = plan.num_parts > 1 ? static_cast<float*>(a.workspace) : nullptr;
+    DecodeKernelParams p = decode_params(a, plan, part_ml, part_ml ? partials_acc(part_ml, nrow) : nullptr);
+    p.wait_first = g_launch_overlap.load(std::memory_order_relaxed) == 0;
+    const int smem = C::smem_bytes(plan.cluster, std::min(p.G, 8), plan.blocks_per_split);
+    p.len_order = len_order_for<D, kCache, kWindow>(a, plan, p.hchunks, smem);
+    const dim3 grid(plan.num_splits, a.Hkv * p.hchunks, a.B);
+    e = launch(paged_decode_kernel<D, false, kCache, kWindow>, grid, dim3(C::kThreads), smem, stream, true,
+               static_cast<unsigned>(plan.cluster), tmK, tmV, p);
+    if (e != cudaSuccess || plan.num_parts == 1) return e;
+    CombineParams c = {};
+    c.part_ml = p.part_ml;
+    c.part_acc = p.part_acc;
+    c.context_lens = a.context_lens;
+    c.out = a.out;
+    c.err = a.err;
+    c.Hq = a.Hq;
+    c.part_stride = plan.num_parts;
+    c.bpc = plan.blocks_per_split;
+    c.max_blocks = a.max_blocks;
+    c.max_ctx = a.max_context_len;
+    c.out_f32 = a.out_f32;
+    c.q_len = 1;
+    c.window = a.window;
+    c.sinks = a.sinks;
+    c.keep_nan = 1;
+    c.wait_first = p.wait_first;
+    // (see launch_decode_d)
+    int occ = 0;
+    if (!p.wait_first && decode_occupancy<D, kCache, kWindow>(smem, &occ) == cudaSuccess)
+        c.early_release = 2 * static_cast<int64_t>(grid.x) * grid.y * grid.z <= static_cast<int64_t>(occ) * sm_count();
+    return launch_combine(c, D, a.B, stream);
+}
+
+cudaError_t launch_decode_window(const DecodeArgs& a, cudaStream_t stream) {
+    if (a.D != 64 && a.D != 128) return cudaErrorInvalidValue;
+    if (a.codes == nullptr)
+        return a.D == 64 ? launch_window_d<64, kCacheF16, true>(a, stream) : launch_window_d<128, kCacheF16, true>(a, stream);
+    if (a.window > 0)
+        return a.D == 64 ? launch_window_d<64, kCacheFp8Block, true>(a, stream)
+                         : launch_window_d<128, kCacheFp8Block, true>(a, stream);
+    return a.D == 64 ? launch_window_d<64, kCacheFp8Block, false>(a, stream)
+                     : launch_window_d<128, kCacheFp8Block, false>(a, stream);
 }
 
 cudaError_t launch_combine(const CombineParams& c, int D, int rows, cudaStream_t stream) {

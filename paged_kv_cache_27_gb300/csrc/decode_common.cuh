@@ -35,6 +35,13 @@ namespace kvc {
 #ifndef KVC_DEC_STAGES128_FP8
 #define KVC_DEC_STAGES128_FP8 2
 #endif
+// cache of e4m3 codes with a scale per block (kCacheFp8Block): blocks in flight per warp
+#ifndef KVC_DEC_STAGES64_FP8_BLOCK
+#define KVC_DEC_STAGES64_FP8_BLOCK 4
+#endif
+#ifndef KVC_DEC_STAGES128_FP8_BLOCK
+#define KVC_DEC_STAGES128_FP8_BLOCK 4
+#endif
 #ifndef KVC_DEC_WARPS128
 #define KVC_DEC_WARPS128 4
 #endif
@@ -128,6 +135,9 @@ constexpr int kLenOrderMaxB = 1024;  // batches up to this size (the order costs
 
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
+// what the decode kernel reads: fp16 pools; e4m3 records with a scale per row; e4m3 codes with a scale per
+// (block, KV head) of K and of V
+constexpr int kCacheF16 = 0, kCacheFp8Row = 1, kCacheFp8Block = 2;
 constexpr int kMaxCluster = KVC_DEC_MAX_CLUSTER;
 // blocks one cluster covers at most: its slice of the block table sits in shared memory (16 KiB at 4096 blocks,
 // which keeps two 8-warp CTAs per SM)
@@ -138,17 +148,21 @@ constexpr int kMaxClusterBlocks = 4096;
 // scales, its V codes (D dim rows of 16 token bytes in the order vt_pos gives) and its 16 V scales.  A stage is
 // one record, brought in by one bulk copy; the codes go from shared memory straight into the mma.sync fragments
 // (one 32-bit load per fragment row).
-template <int D, bool kFp8 = false>
+// With kCacheFp8Block a stage is the 32 rows of codes (16 of K, 16 of V) of a (block, KV head), one TMA box.
+template <int D, int kCache = kCacheF16>
 struct DecodeCfg {
+    static constexpr bool kFp8 = kCache == kCacheFp8Row, kBlock8 = kCache == kCacheFp8Block;
     static constexpr int kWarps = D == 64 ? KVC_DEC_WARPS64 : KVC_DEC_WARPS128;
-    static constexpr int kStages = kFp8 ? (D == 64 ? KVC_DEC_STAGES64_FP8 : KVC_DEC_STAGES128_FP8)
+    static constexpr int kStages = kBlock8 ? (D == 64 ? KVC_DEC_STAGES64_FP8_BLOCK : KVC_DEC_STAGES128_FP8_BLOCK)
+                                   : kFp8 ? (D == 64 ? KVC_DEC_STAGES64_FP8 : KVC_DEC_STAGES128_FP8)
                                         : (D == 64 ? KVC_DEC_STAGES64 : KVC_DEC_STAGES128);
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kTileBytes = kBlockSize * D * 2;    // one 16 x D fp16 tile
     static constexpr int kCodeTileBytes = kBlockSize * D;    // one 16 x D e4m3 tile
     static constexpr int kScaleBytes = kBlockSize * 4;       // 16 float scales
-    static constexpr int kStageBytes = kFp8 ? fp8_record_bytes(D)  // one record: K codes, K scales, V codes, V scales
-                                            : 2 * kTileBytes;     // K tile + V tile
+    static constexpr int kStageBytes = kBlock8 ? 2 * kCodeTileBytes      // K codes, V codes
+                                       : kFp8  ? fp8_record_bytes(D)  // one record: K codes, K scales, V codes, V scales
+                                               : 2 * kTileBytes;      // K tile + V tile
     // a warp's ring starts on a 1024-byte boundary (the fp16 tiles' TMA swizzle repeats every 1024 bytes)
     static constexpr int kWarpRingBytes = (kStages * kStageBytes + 1023) / 1024 * 1024;
     static constexpr int kRingBytes = kWarps * kWarpRingBytes;
@@ -169,6 +183,14 @@ struct DecodeCfg {
 // rows x 64 columns with the 128-byte swizzle
 __device__ __forceinline__ uint32_t swz(int row, int chunk) {
     return static_cast<uint32_t>(((chunk >> 3) << 11) + (row << 7) + (((chunk & 7) ^ (row & 7)) << 4));
+}
+
+// the same for 16-byte chunk `chunk` of row `row` of a tile of e4m3 codes, rows of D bytes, as TMA's 64-byte (D = 64)
+// or 128-byte (D = 128) swizzle writes it: eight rows' equal chunks lie on distinct banks
+template <int D>
+__device__ __forceinline__ uint32_t swz8(int row, int chunk) {
+    return D == 64 ? static_cast<uint32_t>((row << 6) + ((chunk ^ ((row >> 1) & 3)) << 4))
+                   : static_cast<uint32_t>((row << 7) + ((chunk ^ (row & 7)) << 4));
 }
 
 __device__ __forceinline__ void store_out(void* out, int out_f32, int64_t idx, float v) {
@@ -297,6 +319,19 @@ inline cudaError_t make_tile_map(CUtensorMap* map, const void* base, int D, int6
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// 2-D view of one layer's e4m3 codes: rows of D bytes, 32 (16 of K, 16 of V) for each (block, KV head), one box each
+inline cudaError_t make_code_map(CUtensorMap* map, const void* base, int D, int64_t rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return cudaErrorNotSupported;
+    cuuint64_t gdim[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows)};
+    cuuint64_t gstride[1] = {static_cast<cuuint64_t>(D)};
+    cuuint32_t box[2] = {static_cast<cuuint32_t>(D), 2 * static_cast<cuuint32_t>(kBlockSize)};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), gdim, gstride, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
 
 template <typename Kern, typename... Args>
 inline cudaError_t launch(Kern kern, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, bool pdl,

@@ -11,6 +11,8 @@ namespace kvc {
 constexpr int kBlockSize = 16;  // tokens per block (the page size used throughout the pages)
 // query heads per KV head the decode paths take (the decode kernel in chunks of 8 heads per CTA)
 constexpr int kMaxGroupHeads = 64;
+constexpr int kMaxWindow = 1 << 30;               // window and sinks
+constexpr int kMaxTableBlocks = (1 << 27) - 1;  // a table's row, so that positions are 32-bit
 
 // Device address of the sticky error word of the current device.
 cudaError_t device_error_word(unsigned** ptr);
@@ -37,6 +39,34 @@ cudaError_t launch_copy_blocks(const int32_t* src, const int32_t* dst, int n, __
                                int L, int num_blocks, int64_t block_elems, cudaStream_t stream);
 
 // ---- decode (decode.cu) ------------------------------------------------------
+// What a decode query sees of its context: the newest `window` positions (its own among them; 0: all of them) and
+// the first `sinks`.  The visible positions lie in the blocks [0, sink blocks) and [first window block, last block],
+// which the kernels number consecutively.
+struct Visible {
+    int start;  // first position of the window
+    int sinks;  // positions before it that are visible
+    int ns;     // blocks of those sinks
+    int w0;     // first block of the window that is not one of them
+    int nblk;   // visible blocks
+};
+__host__ __device__ inline Visible visible_blocks(int ctx, int window, int sinks) {
+    Visible v;
+    v.start = window > 0 && ctx > window ? ctx - window : 0;
+    v.sinks = sinks < v.start ? sinks : v.start;
+    v.ns = (v.sinks + kBlockSize - 1) / kBlockSize;
+    v.w0 = v.start / kBlockSize > v.ns ? v.start / kBlockSize : v.ns;
+    v.nblk = v.ns + (ctx + kBlockSize - 1) / kBlockSize - v.w0;
+    return v;
+}
+// most blocks that any context up to max_ctx has visible
+inline int most_visible_blocks(int max_ctx, int window, int sinks) {
+    const int64_t all = (static_cast<int64_t>(max_ctx) + kBlockSize - 1) / kBlockSize;
+    if (window <= 0) return static_cast<int>(all);
+    const int64_t near = (static_cast<int64_t>(window) + 2 * kBlockSize - 2) / kBlockSize;
+    const int64_t first = (static_cast<int64_t>(sinks) + kBlockSize - 1) / kBlockSize;
+    return static_cast<int>(all < near + first ? all : near + first);
+}
+
 struct DecodePlan {
     int num_splits;        // grid.x = num_parts * cluster
     int blocks_per_split;  // blocks of 16 tokens one cluster covers
@@ -67,8 +97,17 @@ struct DecodeArgs {
     unsigned* err;
     // fp8 cache instead of k_cache / v_cache when set: one record per (block, KV head), [NB][Hkv][record]
     const uint8_t* kv_fp8 = nullptr;
+    // or e4m3 codes [NB][Hkv][2][16][D] with one scale (a power of two) per (block, KV head) of K and of V
+    const uint8_t* codes = nullptr;
+    const float* scales = nullptr;  // [NB][Hkv][2]
+    // what a query sees (window 0: all of its context); used by launch_decode_window
+    int window = 0, sinks = 0;
 };
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
+// the same over what a window and sinks leave visible (window > 0), or over a block-scaled cache (block8; window 0 or more)
+cudaError_t decode_window_plan(int B, int Hq, int Hkv, int D, int max_context_len, int window, int sinks, bool block8,
+                               DecodePlan* plan);
+cudaError_t launch_decode_window(const DecodeArgs& a, cudaStream_t stream);
 
 // Partial states of query rows (m, l, acc) merged into the output by the combine kernel (decode.cu).
 struct CombineParams {
@@ -83,6 +122,9 @@ struct CombineParams {
     int cascade;       // 1: only partials were written; this kernel writes every output row
     int q_len;         // query rows per sequence (multi-token decode; 1 otherwise): row y is sequence y / q_len
     int early_release; // 1: the next kernel may launch as soon as this one starts (see the combine kernel)
+    int window = 0, sinks = 0;  // the parts cover the visible blocks (window 0: all)
+    int keep_nan = 0;    // 1: parts whose sum is NaN take part
+    int wait_first = 0;  // 1: nothing is read before the kernel in front is done
 };
 // grid (Hq, rows): one CTA per (query head, query row)
 cudaError_t launch_combine(const CombineParams& c, int D, int rows, cudaStream_t stream);
@@ -228,6 +270,39 @@ struct CommitArgs {
 };
 cudaError_t launch_tree_commit(const CommitArgs& a, cudaStream_t stream);
 
+// ---- windows and the block-scaled cache ----------------------------------------
+// block tables, slots and positions from request lengths (block_tables.cu)
+struct BlockTableArgs {
+    const int32_t* lens_before;  // null: zeros
+    const int32_t* lens_after;
+    const int32_t* free_blocks;
+    const int32_t* placed;
+    int B, num_free, window, sinks;
+    int32_t* block_table;
+    int max_blocks;
+    int32_t* new_placed;
+    int32_t* cu_tokens;
+    int64_t* slots;
+    int32_t* positions;  // null: not asked for
+    int num_slots;
+    unsigned* err;
+};
+cudaError_t launch_block_tables(const BlockTableArgs& a, cudaStream_t stream);
+
+// append to e4m3 codes with a scale per (block, KV head) (append_fp8_block.cu)
+struct AppendFp8BlockArgs {
+    const __half* k;
+    const __half* v;
+    int64_t k_stride, v_stride;
+    const int64_t* slots;
+    int64_t n;
+    uint8_t* codes;  // [NB][Hkv][2][16][D]
+    float* scales;   // [NB][Hkv][2]
+    int num_blocks, Hkv, D;
+    unsigned* err;
+};
+cudaError_t launch_append_fp8_block(const AppendFp8BlockArgs& a, cudaStream_t stream);
+
 // Records `msg` as the calling thread's last error (kvc_last_error_string) and returns `status`.
 int set_last_error(int status, const char* msg);
 
@@ -244,6 +319,7 @@ struct PrefillArgs {
     void* out;
     int out_f32;
     int split_p;  // P as fp16 high part + fp16 residual (else one fp16 value)
+    int window = 0, sinks = 0;  // window > 0 (causal): a row sees the newest `window` positions and the first `sinks`
     unsigned* err;
 };
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);

@@ -143,12 +143,6 @@ __device__ __forceinline__ float add_halves(uint32_t h, float acc) {
         : "r"(h));
     return acc;
 }
-// two values as fp16, beyond fp16's range its largest one; NaN stays NaN
-__device__ __forceinline__ uint32_t pack_half2_finite(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 __device__ __forceinline__ float max3f(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
