@@ -747,8 +747,10 @@ kvc_status paged_decode_attention_fp8_block(const void* q, const void* codes, co
 /* prefill_attention_ex, causal, over what a window and sinks leave visible:
  * row i of a segment sees the rows j <= i with j > i - window or j < sinks.
  * window >= 1; work grows with window + sinks, not with the segment.  Here too
- * what masked positions hold cannot reach an output: a row that comes out
- * infinite or NaN is computed again from its visible keys alone (slowly). */
+ * infinities and NaN in masked positions cannot reach an output: a row that
+ * comes out infinite or NaN is computed again from its visible keys alone,
+ * slowly and with fp32 weights (its rounding may differ, by what the p_precision
+ * of the call allows). */
 kvc_status prefill_window_attention(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int nseq,
                                     int total_tokens, int max_seqlen, int Hq, int Hkv, int head_dim, float scale,
                                     int window, int sinks, int p_precision, void* out, int out_dtype, void* stream);
