@@ -1453,7 +1453,7 @@ static kvc_status decode_window(kvc::DecodeArgs& a, std::initializer_list<Span> 
     a.blocks_per_split = 0;
     e = kvc::device_error_word(&a.err);
     if (e != cudaSuccess) return cuda_fail(e, "device error word");
-    e = kvc::launch_decode_window(a, as_stream(stream));
+    e = kvc::launch_decode_window(a, plan, as_stream(stream));
     if (e != cudaSuccess) return cuda_fail(e, name);
     return KVC_OK;
 }

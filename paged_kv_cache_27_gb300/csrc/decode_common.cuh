@@ -35,12 +35,12 @@ namespace kvc {
 #ifndef KVC_DEC_STAGES128_FP8
 #define KVC_DEC_STAGES128_FP8 2
 #endif
-// cache of e4m3 codes with a scale per block (kCacheFp8Block): blocks in flight per warp
+// cache of e4m3 codes with a scale per block (kCacheFp8Block): stages (pairs of blocks) per warp
 #ifndef KVC_DEC_STAGES64_FP8_BLOCK
-#define KVC_DEC_STAGES64_FP8_BLOCK 4
+#define KVC_DEC_STAGES64_FP8_BLOCK 2
 #endif
 #ifndef KVC_DEC_STAGES128_FP8_BLOCK
-#define KVC_DEC_STAGES128_FP8_BLOCK 4
+#define KVC_DEC_STAGES128_FP8_BLOCK 2
 #endif
 #ifndef KVC_DEC_WARPS128
 #define KVC_DEC_WARPS128 4
@@ -81,6 +81,12 @@ namespace kvc {
 #endif
 #ifndef KVC_DEC_MIN_CTAS  // resident CTAs per SM the register allocation must allow
 #define KVC_DEC_MIN_CTAS 1
+#endif
+#ifndef KVC_DEC_MIN_CTAS128_FP8_BLOCK
+#define KVC_DEC_MIN_CTAS128_FP8_BLOCK 3
+#endif
+#ifndef KVC_DEC_MIN_CTAS64_FP8_BLOCK
+#define KVC_DEC_MIN_CTAS64_FP8_BLOCK 2
 #endif
 #ifndef KVC_DEC_PLAN_CTAS  // CTAs per SM one launch is sized for; the rest lets the next launch start early
 #define KVC_DEC_PLAN_CTAS 2
@@ -148,7 +154,7 @@ constexpr int kMaxClusterBlocks = 4096;
 // scales, its V codes (D dim rows of 16 token bytes in the order vt_pos gives) and its 16 V scales.  A stage is
 // one record, brought in by one bulk copy; the codes go from shared memory straight into the mma.sync fragments
 // (one 32-bit load per fragment row).
-// With kCacheFp8Block a stage is the 32 rows of codes (16 of K, 16 of V) of a (block, KV head), one TMA box.
+// With kCacheFp8Block a stage is two blocks' codes (for each, 16 rows of K and 16 of V, one TMA box).
 template <int D, int kCache = kCacheF16>
 struct DecodeCfg {
     static constexpr bool kFp8 = kCache == kCacheFp8Row, kBlock8 = kCache == kCacheFp8Block;
@@ -157,10 +163,14 @@ struct DecodeCfg {
                                    : kFp8 ? (D == 64 ? KVC_DEC_STAGES64_FP8 : KVC_DEC_STAGES128_FP8)
                                         : (D == 64 ? KVC_DEC_STAGES64 : KVC_DEC_STAGES128);
     static constexpr int kThreads = kWarps * 32;
+    // resident CTAs per SM that the registers must allow
+    static constexpr int kMinCtas = !kBlock8 ? KVC_DEC_MIN_CTAS
+                                    : D == 64 ? KVC_DEC_MIN_CTAS64_FP8_BLOCK : KVC_DEC_MIN_CTAS128_FP8_BLOCK;
     static constexpr int kTileBytes = kBlockSize * D * 2;    // one 16 x D fp16 tile
     static constexpr int kCodeTileBytes = kBlockSize * D;    // one 16 x D e4m3 tile
     static constexpr int kScaleBytes = kBlockSize * 4;       // 16 float scales
-    static constexpr int kStageBytes = kBlock8 ? 2 * kCodeTileBytes      // K codes, V codes
+    static constexpr int kPair = kBlock8 ? 2 : 1;  // blocks of a stage
+    static constexpr int kStageBytes = kBlock8 ? kPair * 2 * kCodeTileBytes  // K codes, V codes of a block, of the next
                                        : kFp8  ? fp8_record_bytes(D)  // one record: K codes, K scales, V codes, V scales
                                                : 2 * kTileBytes;      // K tile + V tile
     // a warp's ring starts on a 1024-byte boundary (the fp16 tiles' TMA swizzle repeats every 1024 bytes)
@@ -185,12 +195,15 @@ __device__ __forceinline__ uint32_t swz(int row, int chunk) {
     return static_cast<uint32_t>(((chunk >> 3) << 11) + (row << 7) + (((chunk & 7) ^ (row & 7)) << 4));
 }
 
-// the same for 16-byte chunk `chunk` of row `row` of a tile of e4m3 codes, rows of D bytes, as TMA's 64-byte (D = 64)
-// or 128-byte (D = 128) swizzle writes it: eight rows' equal chunks lie on distinct banks
+// the same for 16-byte chunk `chunk` of row `row` of a tile of e4m3 codes, loaded as boxes of 128-byte rows (one row
+// of codes at D = 128, two at D = 64): eight rows' equal chunks lie on distinct banks
 template <int D>
 __device__ __forceinline__ uint32_t swz8(int row, int chunk) {
-    return D == 64 ? static_cast<uint32_t>((row << 6) + ((chunk ^ ((row >> 1) & 3)) << 4))
-                   : static_cast<uint32_t>((row << 7) + ((chunk ^ (row & 7)) << 4));
+    if (D == 64) {
+        chunk += (row & 1) << 2;
+        row >>= 1;
+    }
+    return static_cast<uint32_t>((row << 7) + ((chunk ^ (row & 7)) << 4));
 }
 
 __device__ __forceinline__ void store_out(void* out, int out_f32, int64_t idx, float v) {
@@ -319,17 +332,19 @@ inline cudaError_t make_tile_map(CUtensorMap* map, const void* base, int D, int6
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// 2-D view of one layer's e4m3 codes: rows of D bytes, 32 (16 of K, 16 of V) for each (block, KV head), one box each
-inline cudaError_t make_code_map(CUtensorMap* map, const void* base, int D, int64_t rows) {
+// 2-D view of one layer's e4m3 codes, `bytes` in all: rows of 128 bytes whatever the head dim (boxes of 64-byte rows
+// take the copy engine twice the requests), one box of D / 4 of them for each (block, KV head): 16 rows of K's codes
+// and 16 of V's
+inline cudaError_t make_code_map(CUtensorMap* map, const void* base, int D, int64_t bytes) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return cudaErrorNotSupported;
-    cuuint64_t gdim[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows)};
-    cuuint64_t gstride[1] = {static_cast<cuuint64_t>(D)};
-    cuuint32_t box[2] = {static_cast<cuuint32_t>(D), 2 * static_cast<cuuint32_t>(kBlockSize)};
+    cuuint64_t gdim[2] = {128, static_cast<cuuint64_t>(bytes / 128)};
+    cuuint64_t gstride[1] = {128};
+    cuuint32_t box[2] = {128, static_cast<cuuint32_t>(D / 4)};
     cuuint32_t estr[2] = {1, 1};
     CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), gdim, gstride, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 

@@ -107,7 +107,7 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
 // the same over what a window and sinks leave visible (window > 0), or over a block-scaled cache (block8; window 0 or more)
 cudaError_t decode_window_plan(int B, int Hq, int Hkv, int D, int max_context_len, int window, int sinks, bool block8,
                                DecodePlan* plan);
-cudaError_t launch_decode_window(const DecodeArgs& a, cudaStream_t stream);
+cudaError_t launch_decode_window(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t stream);
 
 // Partial states of query rows (m, l, acc) merged into the output by the combine kernel (decode.cu).
 struct CombineParams {

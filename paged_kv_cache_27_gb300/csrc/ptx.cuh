@@ -191,6 +191,13 @@ __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two_codes) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(h));
     return r;
 }
+// the same for the four codes of a register
+__device__ __forceinline__ void e4m3x4_to_half2x2(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(codes));
+}
 // Two floats -> two e4m3 codes, round to nearest even, saturating at +-448 (lo in the low byte).
 __device__ __forceinline__ uint16_t float2_to_e4m3x2(float lo, float hi) {
     uint16_t r;
