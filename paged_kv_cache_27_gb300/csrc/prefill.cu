@@ -414,10 +414,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
             // (kWindow: nor does one that every row sees, or that holds sinks alone)
             const bool masked = k0 + kPfKeys > len || (p.causal && k0 + kPfKeys - 1 > rx) ||
                                 (kWindow && k0 <= rx + kPfRows - 1 - p.window && k0 + kPfKeys > p.sinks);
-            auto visible = [&](int kj) {
-                if constexpr (kWindow) return kj < len && window_sees(qi, kj, p.window, p.sinks);
-                return kj < len && (!p.causal || kj <= qi);
-            };
             float alpha = 1.f;       // rescale of O and of the l of earlier tiles
             float lsum[2] = {0.f, 0.f};  // per 64-key half: sum of the weights written
             // One pass per 64-key half: the half's extreme score, the lazy running max (it moves only when the
@@ -429,13 +425,18 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
                 float s[64];
                 tmem_ld64(tS + hh * 64, s);
                 float e[4];
-                if (masked) {
+                if (kWindow && masked) {
+                    const uint32_t bits[2] = {window_bits(qi, k0 + hh * 64, len, p.window, p.sinks),
+                                              window_bits(qi, k0 + hh * 64 + 32, len, p.window, p.sinks)};
+                    mask_scores(s, bits, fill);
+                }
+                if (!kWindow && masked) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) e[i] = fill;
 #pragma unroll
                     for (int c = 0; c < 64; ++c) {
                         const int kj = k0 + hh * 64 + c;
-                        const bool valid = visible(kj);
+                        const bool valid = kj < len && (!p.causal || kj <= qi);
                         const float v = valid ? s[c] : fill;
                         e[c & 3] = neg_scale ? fminf(e[c & 3], v) : fmaxf(e[c & 3], v);
                     }
@@ -494,14 +495,19 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
                     if constexpr (kSplitP) tmem_st32(tS + 32, r);
                     if (a_h != 1.f) lsum[0] = s0;
                     tmem_ld64(tS + 64, s);
+                    if (kWindow && masked) {
+                        const uint32_t bits[2] = {window_bits(qi, k0 + 64, len, p.window, p.sinks),
+                                                  window_bits(qi, k0 + 96, len, p.window, p.sinks)};
+                        mask_scores(s, bits, fill);
+                    }
                 }
                 alpha *= a_h;
                 const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
-                if (masked) {
+                if (!kWindow && masked) {
 #pragma unroll
                     for (int c = 0; c < 64; ++c) {
                         const int kj = k0 + hh * 64 + c;
-                        const bool valid = visible(kj);
+                        const bool valid = kj < len && (!p.causal || kj <= qi);
                         s[c] = valid ? ex2(fmaf(s[c], sl2, neg_m)) : 0.f;
                     }
                 } else {
@@ -716,6 +722,7 @@ static cudaError_t launch_prefill_d(const PrefillArgs& a, cudaStream_t stream) {
     p.causal = a.causal;
     p.out_f32 = a.out_f32;
     p.scale_log2 = a.scale * kPfLog2e;
+    if (kWindow && std::fabs(p.scale_log2) < kMinWindowScaleLog2) p.scale_log2 = kMinWindowScaleLog2;
     const int64_t nblocks = static_cast<int64_t>(p.tiles_per_seq) * a.nseq * a.Hq;
     if (nblocks > 2147483647LL) return cudaErrorInvalidConfiguration;
     p.window = a.window;

@@ -379,18 +379,18 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
             // (kWindow: nor does one that every row sees, or that holds sinks alone)
             const bool masked = k0 + kPfPartKeys > len || (p.causal && k0 + kPfPartKeys - 1 > r0) ||
                                 (kWindow && k0 <= r0 + kPfRows - 1 - p.window && k0 + kPfPartKeys > p.sinks);
-            auto visible = [&](int kj) {
-                if constexpr (kWindow) return kj < len && window_sees(qi, kj, p.window, p.sinks);
-                return kj < len && (!p.causal || kj <= qi);
-            };
             float e[4];
-            if (masked) {
+            if (kWindow && masked) {
+                const uint32_t bits = window_bits(qi, k0, len, p.window, p.sinks);
+                mask_scores(s, &bits, fill);
+            }
+            if (!kWindow && masked) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) e[i] = fill;
 #pragma unroll
                 for (int c = 0; c < kPfPartKeys; ++c) {
                     const int kj = k0 + c;
-                    const bool valid = visible(kj);
+                    const bool valid = kj < len && (!p.causal || kj <= qi);
                     const float v = valid ? s[c] : fill;
                     e[c & 3] = neg_scale ? fminf(e[c & 3], v) : fmaxf(e[c & 3], v);
                 }
@@ -439,11 +439,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
             // P = 2^(s * scale * log2 e - m) written over this part's S columns in fp16, keys (2i, 2i + 1) in
             // column i (split form: the high part there, the residual in column 16 + i).  l sums the fp16
             // weights written (split form: P in fp32).
-            if (masked) {
+            if (!kWindow && masked) {
 #pragma unroll
                 for (int c = 0; c < kPfPartKeys; ++c) {
                     const int kj = k0 + c;
-                    const bool valid = visible(kj);
+                    const bool valid = kj < len && (!p.causal || kj <= qi);
                     s[c] = valid ? ex2(fmaf(s[c], sl2, neg_m)) : 0.f;
                 }
             } else {
@@ -633,6 +633,7 @@ static cudaError_t launch_prefill_d(const PrefillArgs& a, cudaStream_t stream) {
     p.causal = a.causal;
     p.out_f32 = a.out_f32;
     p.scale_log2 = a.scale * kPfLog2e;
+    if (kWindow && std::fabs(p.scale_log2) < kMinWindowScaleLog2) p.scale_log2 = kMinWindowScaleLog2;
     const int64_t nblocks = static_cast<int64_t>(p.tiles_per_seq) * a.nseq * a.Hq;
     if (nblocks > 2147483647LL) return cudaErrorInvalidConfiguration;
     p.window = a.window;

@@ -8,10 +8,25 @@
 
 namespace kvc {
 
-// Key `kj` is visible to row `qi` of the same segment (both below the segment's length).
-__device__ __forceinline__ bool window_sees(int qi, int kj, int window, int sinks) {
-    return kj <= qi && (kj > qi - window || kj < sinks);
+// The n lowest of 32 bits.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
+
+// Bit i: key k0 + i is visible to row qi of a segment of len rows.
+__device__ __forceinline__ uint32_t window_bits(int qi, int k0, int len, int window, int sinks) {
+    const int end = min(qi + 1, len);
+    return (low_bits(end - k0) & ~low_bits(qi - window + 1 - k0)) | low_bits(min(sinks, end) - k0);
 }
+
+// Scores of keys that are not visible become `fill`, whose weight is 0 whatever the scale is (which is not 0, see
+// kMinWindowScaleLog2): after that a tile needs no mask.  (Comparing positions key by key, in the maximum and again in
+// the weights, a masked tile took three times the time of another one.)
+template <int N>
+__device__ __forceinline__ void mask_scores(float (&s)[N], const uint32_t* bits, float fill) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) s[c] = (bits[c >> 5] >> (c & 31)) & 1u ? s[c] : fill;
+}
+// a scale of 0 is taken as this: scores of fp16 rows (below 2^41) still vanish next to 1, and a masked one stays infinite
+constexpr float kMinWindowScaleLog2 = 0x1p-100f;
 
 // 32 columns (lane: column col0 + lane) of row qi's output from its visible keys alone, two passes over them: for rows
 // that came out infinite or NaN.  The products give 0 * inf = NaN where a key that the row does not see holds an
