@@ -1225,17 +1225,21 @@ static cudaError_t decode_resident_clusters(int cs, int smem, int* clusters) {
     return cudaSuccess;
 }
 
-// The block-scaled cache's plan: clusters of c CTAs, and n of them along a context, over `segs` (sequence, KV head, head
-// chunk) units.  A round is what is resident at once (k units): a warp takes a pair of blocks in kPairUs, or, where the
-// SM's issue slots are what it waits for, in kIssueUs for each of the SM's warps; memory delivers kBytesPerUs.  Whole
-// rounds, then what is left over; clusters merge on chip, parts by a second kernel.  The constants are fitted to 15 shapes
-// (1 to 100 sequences of 1000 to 131,072 tokens, each in 10 to 40 forms): the form taken is 2 % slower than the best one
-// on average, 9 % at worst.
-template <int D, bool kWindow>
-static cudaError_t plan_block8(int64_t segs, int64_t rows, int G, int nblk, int* cs, int* bpc) {
-    using C = DecodeCfg<D, kCacheFp8Block>;
-    constexpr double kPairUs = D == 64 ? 1.27 : 2.1, kIssueUs = D == 64 ? 0.095 : 0.159, kStartUs = 2.6, kClusterUs = 2.5,
-                     kCombineUs = 2.9, kBytesPerUs = 6.6e6;
+// The plan of the windowed and the block-scaled forms: clusters of c CTAs, and n of them along a context, over `segs`
+// (sequence, KV head, head chunk) units.  A round is what is resident at once (k units): a warp takes a step (a block; a
+// pair of block-scaled ones) in kStepUs, or, where the SM's issue slots are what it waits for, in kIssueUs for each of
+// the SM's warps; memory delivers kBytesPerUs.  Whole rounds, then what is left over; clusters merge on chip, parts by a
+// second kernel.  The constants are fitted to 12 and 15 shapes (1 to 200 sequences, 500 to 131,072 visible tokens, each
+// in 10 to 40 forms): the form taken is 2 % slower than the best one on average, 9 % at worst.  (64 sequences x 4096
+// visible, 32 / 8 heads, D = 128: 180 us with the plain decode's plan, 512 CTAs where 456 are resident, 163 with this.)
+template <int D, int kCache, bool kWindow>
+static cudaError_t plan_by_model(int64_t segs, int64_t rows, int G, int nblk, int* cs, int* bpc) {
+    using C = DecodeCfg<D, kCache>;
+    constexpr int kSize = kCache == kCacheFp8Block ? 1 : 2;  // bytes of a value
+    constexpr bool k8 = kCache == kCacheFp8Block;
+    constexpr double kHalf = D == 64 ? 0.6 : 1.0;
+    constexpr double kStepUs = (k8 ? 2.1 : 1.5) * kHalf, kIssueUs = (k8 ? 0.16 : 0.15) * kHalf, kStartUs = 2.6,
+                     kClusterUs = k8 ? 2.5 : 1.5, kCombineUs = 2.9, kBytesPerUs = 6.6e6;
     constexpr int kParts[] = {1, 2, 3, 4, 6, 8, 10, 14, 19, 28, 38, 57, 76, 114, 152};
     const int sms = std::max(1, sm_count());
     const int min_n = (nblk + kMaxClusterBlocks - 1) / kMaxClusterBlocks;
@@ -1245,22 +1249,22 @@ static cudaError_t plan_block8(int64_t segs, int64_t rows, int G, int nblk, int*
         if (c > 1 && (c - 1) * C::kWarps * C::kPair >= nblk) break;  // a CTA would have no pair
         int last_slice = 0, resident = 1;
         for (int part : kParts) {
-            const int n = std::max(part, min_n), per = (nblk + n - 1) / n, pairs = (per + 1) / 2;
+            const int n = std::max(part, min_n), per = (nblk + n - 1) / n, pairs = (per + C::kPair - 1) / C::kPair;
             if (n > min_n && (pairs < 2 * warps || n > nblk)) break;
             int slice = 64;  // a table slice, up to the next power of two: few shared-memory sizes to ask about
             while (slice < per) slice *= 2;
             if (slice != last_slice) {
-                cudaError_t e = decode_resident_clusters<D, kCacheFp8Block, kWindow>(
+                cudaError_t e = decode_resident_clusters<D, kCache, kWindow>(
                     c, C::smem_bytes(c, G, std::min(slice, kMaxClusterBlocks)), &resident);
                 if (e != cudaSuccess) return e;
                 last_slice = slice;
                 resident = std::max(1, resident);
             }
-            const double unit_us = static_cast<double>(per) * (2 * kBlockSize * D) / kBytesPerUs;
+            const double unit_us = static_cast<double>(per) * (2 * kBlockSize * D * kSize) / kBytesPerUs;
             const int turns = (pairs + warps - 1) / warps;
             const int64_t total = segs * n, rounds = total / resident, left = total - rounds * resident;
             auto warp_us = [&](int64_t k) {
-                return turns * std::max(kPairUs, kIssueUs * static_cast<double>(k) * warps / sms);
+                return turns * std::max(kStepUs, kIssueUs * static_cast<double>(k) * warps / sms);
             };
             double t = rounds * std::max((rounds > 1 ? 0.5 : 1.0) * kStartUs + warp_us(resident), resident * unit_us);
             if (left > 0) t += std::max(kStartUs + warp_us(left), left * unit_us);
@@ -1288,8 +1292,8 @@ static cudaError_t plan_d(int B, int Hq, int Hkv, int nblk, int bpc_req, DecodeP
     if (bpc_req > 0) {
         bpc = std::min(bpc_req, kMaxClusterBlocks);
         cs = std::max(1, std::min(kMaxCluster, (bpc + C::kWarps - 1) / C::kWarps));
-    } else if constexpr (kCache == kCacheFp8Block) {
-        cudaError_t e = plan_block8<D, kWindow>(std::max<int64_t>(1, static_cast<int64_t>(B) * Hkv * hchunks),
+    } else if constexpr (kCache == kCacheFp8Block || kWindow) {
+        cudaError_t e = plan_by_model<D, kCache, kWindow>(std::max<int64_t>(1, static_cast<int64_t>(B) * Hkv * hchunks),
                                                 static_cast<int64_t>(B) * Hq, G, nblk, &cs, &bpc);
         if (e != cudaSuccess) return e;
     } else {
