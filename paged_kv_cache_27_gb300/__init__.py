@@ -1131,27 +1131,34 @@ def kv_block_tables(lens_before: Optional[torch.Tensor], lens_after: torch.Tenso
     int32 [1]; cu_tokens int32 [B + 1]; slot_mapping int64 [num_slots], -1 behind the last token; positions int32
     [num_slots].  With a window (and sinks) a sequence's blocks are used in turn, see include/kvc.h.
     prepare=True returns a PreparedCall instead of launching."""
-    if block_table.dim() != 2:
+    tshape = block_table.shape
+    if len(tshape) != 2:
         raise ValueError("block_table must be [B][max_blocks]")
-    B, max_blocks = block_table.shape
-    num_slots = slot_mapping.numel()
-    if lens_after.numel() != B or (lens_before is not None and lens_before.numel() != B) or cu_tokens.numel() != B + 1:
-        raise ValueError("lens_before and lens_after must have B entries and cu_tokens B + 1")
-    if placed.numel() != 1 or new_placed.numel() != 1:
-        raise ValueError("placed and new_placed must have one entry")
-    if positions is not None and positions.numel() != num_slots:
-        raise ValueError("positions must have slot_mapping's size")
+    B, max_blocks = tshape
+    num_slots = slot_mapping.nbytes >> 3
     keep = (block_table, lens_before, lens_after, free_blocks, placed, new_placed, cu_tokens, slot_mapping, positions)
     dev = block_table.get_device()
+    # the common case in one expression (bytes cost a tensor less than its number of elements); the checks below only
+    # name the failure
     if not (dev >= 0 and dev == _current_device()
             and _ready(dev, _I32, block_table, lens_before, lens_after, free_blocks, placed, new_placed, cu_tokens,
-                       positions) and _ready(dev, _I64, slot_mapping)):
+                       positions) and _ready(dev, _I64, slot_mapping)
+            and lens_after.nbytes == 4 * B and cu_tokens.nbytes == 4 * B + 4 and placed.nbytes == 4
+            and new_placed.nbytes == 4 and (lens_before is None or lens_before.nbytes == 4 * B)
+            and (positions is None or positions.nbytes == 4 * num_slots)):
+        num_slots = slot_mapping.numel()
+        if lens_after.numel() != B or (lens_before is not None and lens_before.numel() != B) or cu_tokens.numel() != B + 1:
+            raise ValueError("lens_before and lens_after must have B entries and cu_tokens B + 1")
+        if placed.numel() != 1 or new_placed.numel() != 1:
+            raise ValueError("placed and new_placed must have one entry")
+        if positions is not None and positions.numel() != num_slots:
+            raise ValueError("positions must have slot_mapping's size")
         _check_all(keep, (block_table, _I32, "block_table"), (lens_before, _I32, "lens_before"),
                    (lens_after, _I32, "lens_after"), (free_blocks, _I32, "free_blocks"), (placed, _I32, "placed"),
                    (new_placed, _I32, "new_placed"), (cu_tokens, _I32, "cu_tokens"),
                    (slot_mapping, _I64, "slot_mapping"), (positions, _I32, "positions"))
     args = (0 if lens_before is None else lens_before.data_ptr(), lens_after.data_ptr(), B, free_blocks.data_ptr(),
-            free_blocks.numel(), placed.data_ptr(), int(window), int(sinks), block_table.data_ptr(), max_blocks,
+            free_blocks.nbytes >> 2, placed.data_ptr(), int(window), int(sinks), block_table.data_ptr(), max_blocks,
             int(block_size), new_placed.data_ptr(), cu_tokens.data_ptr(), slot_mapping.data_ptr(),
             0 if positions is None else positions.data_ptr(), num_slots)
     return _run(_BLOCK_TABLES, args, stream, prepare, dev, keep)
@@ -1166,9 +1173,10 @@ def _code_dtype(codes: torch.Tensor):
 
 def _code_shape(codes: torch.Tensor, scales: torch.Tensor, D: int):
     """(NB, Hkv, bs) of a block-scaled cache layer."""
-    if codes.dim() != 5:
+    shape = codes.shape
+    if len(shape) != 5:
         raise ValueError("codes must be [NB][Hkv][2][bs][D]")
-    NB, Hkv, two, bs, Dk = codes.shape
+    NB, Hkv, two, bs, Dk = shape
     if two != 2 or Dk != D or scales.shape != (NB, Hkv, 2):
         raise ValueError("codes must be [NB][Hkv][2][bs][D] and scales [NB][Hkv][2]")
     return NB, Hkv, bs
@@ -1185,15 +1193,17 @@ def kv_append_fp8_block(k_new: torch.Tensor, v_new: torch.Tensor, slot_mapping: 
         raise ValueError("k_new and v_new must be [n][Hkv][D]")
     n, Hkv, D = kshape
     NB, Hc, bs = _code_shape(codes, scales, D)
-    if Hc != Hkv or slot_mapping.numel() != n:
-        raise ValueError("codes do not match k_new, or slot_mapping has not n entries")
+    if Hc != Hkv:
+        raise ValueError("codes do not match k_new")
     dt = _code_dtype(codes)
     keep = (k_new, v_new, slot_mapping, codes, scales)
     dev = k_new.get_device()
     kst, vst = k_new.stride(), v_new.stride()
     if not (dev >= 0 and dev == _current_device() == v_new.get_device() and k_new.dtype is _F16 and v_new.dtype is _F16
             and kst[2] == vst[2] == 1 and kst[1] == vst[1] == D and _ready(dev, _I64, slot_mapping)
-            and _ready(dev, dt, codes) and _ready(dev, _F32, scales)):
+            and slot_mapping.nbytes == 8 * n and _ready(dev, dt, codes) and _ready(dev, _F32, scales)):
+        if slot_mapping.numel() != n:
+            raise ValueError("slot_mapping must have n entries")
         kst, vst = ((_token_stride(t, nm),) for t, nm in ((k_new, "k_new"), (v_new, "v_new")))
         _check_all(keep, (slot_mapping, _I64, "slot_mapping"), (codes, dt, "codes"), (scales, _F32, "scales"))
     if n == 1:  # a single token's stride means nothing
@@ -1212,16 +1222,18 @@ def paged_decode_fp8_block_plan(B: int, Hq: int, Hkv: int, head_dim: int, max_co
     return ws.value
 
 
-def _decode_shapes(q, block_table, context_lens, out):
-    """Output type of a decode call whose q, tables, lengths and out agree."""
-    if out.shape != q.shape:
+def _decode_shapes(qshape, block_table, context_lens, out):
+    """max_blocks and the output type of a decode call whose q, tables, lengths and out agree."""
+    if out.shape != qshape:
         raise ValueError("out must have q's shape")
-    if block_table.dim() != 2 or block_table.shape[0] != q.shape[0] or context_lens.numel() != q.shape[0]:
+    tshape = block_table.shape
+    if len(tshape) != 2 or tshape[0] != qshape[0] or context_lens.numel() != qshape[0]:
         raise ValueError("block_table / context_lens do not match B")
-    od = KVC_F16 if out.dtype is _F16 else KVC_F32 if out.dtype is _F32 else None
+    odt = out.dtype
+    od = KVC_F16 if odt is _F16 else KVC_F32 if odt is _F32 else None
     if od is None:
         raise TypeError("out must be float16 or float32")
-    return od
+    return tshape[1], od, odt
 
 
 def paged_decode_attention_fp8_block(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
@@ -1231,22 +1243,23 @@ def paged_decode_attention_fp8_block(q: torch.Tensor, codes: torch.Tensor, scale
     """paged_decode_attention over a block-scaled cache layer (codes and scales as kv_append_fp8_block writes them), of
     all of a context (window 0) or of its newest `window` and first `sinks` positions; workspace:
     paged_decode_fp8_block_plan bytes.  prepare=True returns a PreparedCall instead of launching."""
-    B, Hq, D = q.shape
+    qshape = q.shape
+    B, Hq, D = qshape
     NB, Hkv, bs = _code_shape(codes, scales, D)
-    od = _decode_shapes(q, block_table, context_lens, out)
+    max_blocks, od, odt = _decode_shapes(qshape, block_table, context_lens, out)
     dt = _code_dtype(codes)
     keep = (q, codes, scales, block_table, context_lens, out, workspace)
     dev = q.get_device()
     if not (dev >= 0 and dev == _current_device() and _ready(dev, _F16, q) and _ready(dev, dt, codes)
             and _ready(dev, _F32, scales) and _ready(dev, _I32, block_table, context_lens)
-            and _ready(dev, out.dtype, out) and (workspace is None or _ready(dev, workspace.dtype, workspace))):
+            and _ready(dev, odt, out) and (workspace is None or _ready(dev, workspace.dtype, workspace))):
         _check_all(keep, (q, _F16, "q"), (codes, dt, "codes"), (scales, _F32, "scales"),
                    (block_table, _I32, "block_table"), (context_lens, _I32, "context_lens"), (out, None, "out"),
                    (workspace, None, "workspace"))
-    args = (q.data_ptr(), codes.data_ptr(), scales.data_ptr(), NB, block_table.data_ptr(), block_table.shape[1],
+    args = (q.data_ptr(), codes.data_ptr(), scales.data_ptr(), NB, block_table.data_ptr(), max_blocks,
             context_lens.data_ptr(), int(window), int(sinks), B, Hq, Hkv, D, bs, int(max_context_len), float(scale),
             out.data_ptr(), od, 0 if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel() * workspace.element_size())
+            0 if workspace is None else workspace.nbytes)
     return _run(_ATTENTION_FP8_BLOCK, args, stream, prepare, dev, keep)
 
 
@@ -1268,11 +1281,12 @@ def paged_decode_window_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cach
     k_new / v_new ([B][Hkv][D] fp16) these are appended at position ctx-1 first, in the same kernel.  Blocks in which
     nothing is visible are not read, nor their table entries; workspace: paged_decode_window_plan bytes.
     prepare=True returns a PreparedCall instead of launching."""
-    B, Hq, D = q.shape
-    NB, Hkv, bs, Dk = k_cache.shape
-    if Dk != D or v_cache.shape != k_cache.shape:
+    qshape, cshape = q.shape, k_cache.shape
+    B, Hq, D = qshape
+    NB, Hkv, bs, Dk = cshape
+    if Dk != D or v_cache.shape != cshape:
         raise ValueError("cache shapes do not match q")
-    od = _decode_shapes(q, block_table, context_lens, out)
+    max_blocks, od, odt = _decode_shapes(qshape, block_table, context_lens, out)
     if (k_new is None) != (v_new is None):
         raise ValueError("k_new and v_new: both or neither")
     if k_new is not None and (k_new.shape != (B, Hkv, D) or v_new.shape != (B, Hkv, D)):
@@ -1280,16 +1294,16 @@ def paged_decode_window_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cach
     keep = (q, k_cache, v_cache, block_table, context_lens, out, workspace, k_new, v_new)
     dev = q.get_device()
     if not (dev >= 0 and dev == _current_device() and _ready(dev, _F16, q, k_cache, v_cache, k_new, v_new)
-            and _ready(dev, _I32, block_table, context_lens) and _ready(dev, out.dtype, out)
+            and _ready(dev, _I32, block_table, context_lens) and _ready(dev, odt, out)
             and (workspace is None or _ready(dev, workspace.dtype, workspace))):
         _check_all(keep, (q, _F16, "q"), (k_cache, _F16, "k_cache"), (v_cache, _F16, "v_cache"),
                    (k_new, _F16, "k_new"), (v_new, _F16, "v_new"), (block_table, _I32, "block_table"),
                    (context_lens, _I32, "context_lens"), (out, None, "out"), (workspace, None, "workspace"))
     args = (q.data_ptr(), 0 if k_new is None else k_new.data_ptr(), 0 if v_new is None else v_new.data_ptr(),
-            k_cache.data_ptr(), v_cache.data_ptr(), NB, block_table.data_ptr(), block_table.shape[1],
+            k_cache.data_ptr(), v_cache.data_ptr(), NB, block_table.data_ptr(), max_blocks,
             context_lens.data_ptr(), int(window), int(sinks), B, Hq, Hkv, D, bs, int(max_context_len), float(scale),
             out.data_ptr(), od, 0 if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel() * workspace.element_size())
+            0 if workspace is None else workspace.nbytes)
     return _run(_WINDOW_ATTENTION, args, stream, prepare, dev, keep)
 
 
@@ -1299,10 +1313,11 @@ def prefill_window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     """Packed varlen prefill, causal, each row over the newest `window` rows of its segment and the first `sinks`:
     q [T][Hq][D], k/v [T][Hkv][D] fp16, cu_seqlens int32 [nseq+1] -> out [T][Hq][D] fp16 or fp32.  precise as in
     prefill_attention.  prepare=True returns a PreparedCall instead of launching."""
-    T, Hq, D = q.shape
-    Hkv = k.shape[1]
-    if k.shape != (T, Hkv, D) or v.shape != k.shape or out.shape != q.shape:
+    qshape, kshape = q.shape, k.shape
+    T, Hq, D = qshape
+    if len(kshape) != 3 or kshape[0] != T or kshape[2] != D or v.shape != kshape or out.shape != qshape:
         raise ValueError("shape mismatch")
+    Hkv = kshape[1]
     od = KVC_F16 if out.dtype is _F16 else KVC_F32 if out.dtype is _F32 else None
     if od is None:
         raise TypeError("out must be float16 or float32")

@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "lib")
 LIB = os.path.join(OUT_DIR, "libkvc.so")
 SOURCES = ["api.cu", "append.cu", "append_fp8_block.cu", "append_rope.cu", "block_tables.cu", "decode.cu", "group.cu", "group_tc.cu",
-           "multi_tc.cu", "prefill.cu", "prefill_1t.cu", "tree_attention.cu", "tree_commit.cu", "tree_verify.cu"]
+           "multi_tc.cu", "prefill.cu", "prefill_1t.cu", "prefill_window.cu", "tree_attention.cu", "tree_commit.cu", "tree_verify.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-Wall", "-cudart", "shared"]

@@ -323,6 +323,8 @@ struct PrefillArgs {
     unsigned* err;
 };
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);
+// with a window (prefill_window.cu)
+cudaError_t launch_prefill_window(const PrefillArgs& a, cudaStream_t stream);
 // head dim 64: one 128-row query tile per CTA, S double-buffered in TMEM (prefill_1t.cu)
 cudaError_t launch_prefill_1t(const PrefillArgs& a, cudaStream_t stream);
 

@@ -758,6 +758,9 @@ static cudaError_t launch_prefill_d(const PrefillArgs& a, cudaStream_t stream) {
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
     if (a.nseq <= 0 || a.total_tokens <= 0 || a.max_seqlen <= 0) return cudaSuccess;
     if (a.window > 0) {
+#ifndef KVC_W_OLD
+        if (a.D == 128 || static_cast<int64_t>(a.total_tokens) * a.Hq >= KVC_PREFILL_D64_TWO_TILE_WORK) return launch_prefill_window(a, stream);
+#endif
         if (a.D == 64) {
             if (static_cast<int64_t>(a.total_tokens) * a.Hq < KVC_PREFILL_D64_TWO_TILE_WORK)
                 return launch_prefill_1t(a, stream);
