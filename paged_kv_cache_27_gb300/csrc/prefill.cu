@@ -24,20 +24,13 @@
 // so it waits for the commit of P_X V(j); while one group of row warps runs its softmax, the tensor cores work
 // on the other group's products.  K and V have rings of their own.  Every wait is bounded; a timeout sets an
 // error bit and drains the CTA.
-//
-// kWindow (causal): row i sees the newest `window` rows of its segment and the first `sinks`.  The key tiles of a CTA
-// are a list: the tile at the far end of A's window that B's no longer reaches (`lead`, 0 or 1 of them), the sinks'
-// tiles, then from B's window to the diagonal; A takes the list without its end, B without its beginning, so that
-// either works on a run of it and no tile is read that neither sees.
 #include <algorithm>
 #include <cmath>
 #include <cudaTypedefs.h>
 #include <mutex>
 
 #include "../../include/kvc.h"
-#include "decode_common.cuh"
 #include "kvc_internal.h"
-#include "prefill_window.cuh"
 #include "ptx.cuh"
 #include "tcgen05.cuh"
 
@@ -85,11 +78,6 @@ struct PrefillKernelParams {
     unsigned* err;
     int nseq, total_tokens, tiles_per_seq, Hq, Hkv, G, causal, out_f32;
     float scale_log2;
-    // kWindow
-    int window, sinks;
-    const __half* q;
-    const __half* k;
-    const __half* v;
 };
 
 // byte offset of 16-byte chunk c (0..7) of row `row` in a 1024-byte aligned tile of 128-byte rows, 128-byte
@@ -178,7 +166,7 @@ __device__ __forceinline__ int pf_key_tiles(int rx, int len, int causal) {
 #define KVC_PREFILL_SOFTMAX_ST32 1
 #endif
 
-template <int D, bool kSplitP, bool kWindow = false>
+template <int D, bool kSplitP>
 __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_constant__ CUtensorMap tmQ,
                                                                 const __grid_constant__ CUtensorMap tmK,
                                                                 const __grid_constant__ CUtensorMap tmV,
@@ -207,7 +195,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
     const int seg = static_cast<int>(blockIdx.x % per_block) / p.Hq, h = static_cast<int>(blockIdx.x % per_block) % p.Hq;
     const int hk = h / p.G;
 
-    if constexpr (kWindow) grid_dependency_wait();  // nothing is read before the kernel in front is done
     const int beg = p.cu_seqlens[seg], end = p.cu_seqlens[seg + 1];
     const int len = end - beg;
     if (beg < 0 || len < 0 || end > p.total_tokens) {
@@ -218,23 +205,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
         atomicOr(p.err, KVC_DEVERR_SEQLENS);  // rows past max_seqlen are not computed
     const int r0 = tile * kPfCtaRows;
     if (r0 >= len) return;
-    int nt0 = pf_key_tiles(r0, len, p.causal), nt1 = pf_key_tiles(r0 + kPfRows, len, p.causal);
+    const int nt0 = pf_key_tiles(r0, len, p.causal), nt1 = pf_key_tiles(r0 + kPfRows, len, p.causal);
     const int nq = nt1 > 0 ? 2 : 1;       // query tiles with rows in the segment
-    // kWindow: the list of key tiles; A works on entries [0, nt0) and B on [lead, nt1)
-    int lead = 0, sink_tiles = 0, far0 = 0, near0 = 0;
-    if constexpr (kWindow) {
-        // (tile A's keys end at nt0, and no window begins behind it: far0 <= near0 <= nt0)
-        sink_tiles = min((p.sinks + kPfKeys - 1) / kPfKeys, nt0);
-        far0 = max(max(0, r0 - p.window + 1) / kPfKeys, sink_tiles);
-        near0 = nq == 2 ? max(max(0, r0 + kPfRows - p.window + 1) / kPfKeys, sink_tiles) : far0;
-        lead = near0 - far0;
-        nt0 = lead + sink_tiles + nt0 - near0;
-        nt1 = nq == 2 ? lead + sink_tiles + nt1 - near0 : 0;
-    }
-    auto key_tile = [&](int j) {  // the key tile of entry j
-        if constexpr (!kWindow) return j;
-        return j < lead ? far0 + j : j < lead + sink_tiles ? j - lead : near0 + j - lead - sink_tiles;
-    };
     const int ntiles = max(nt0, nt1);     // key tiles of the CTA (tile B reads at least as many as A)
 
     auto qs = [&](int x) { return smem + Geo::kQOff + x * Geo::kQBytes; };
@@ -277,14 +249,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
                 mbar_arrive_expect_tx(bar, Geo::kKVBytes);
 #pragma unroll
                 for (int c = 0; c < Geo::kChunks; ++c)
-                    tma_load_3d(kst(t % KS) + c * Geo::kKVChunk, &tmK, bar, c * 64, hk, beg + key_tile(t) * kPfKeys);
+                    tma_load_3d(kst(t % KS) + c * Geo::kKVChunk, &tmK, bar, c * 64, hk, beg + t * kPfKeys);
             };
             auto load_v = [&](int t) {
                 uint64_t* bar = &v_full[t % VS];
                 mbar_arrive_expect_tx(bar, Geo::kKVBytes);
 #pragma unroll
                 for (int c = 0; c < Geo::kChunks; ++c)
-                    tma_load_3d(vst(t % VS) + c * Geo::kKVChunk, &tmV, bar, c * 64, hk, beg + key_tile(t) * kPfKeys);
+                    tma_load_3d(vst(t % VS) + c * Geo::kKVChunk, &tmV, bar, c * 64, hk, beg + t * kPfKeys);
             };
             prefetch_tensormap(&tmQ);
             prefetch_tensormap(&tmK);
@@ -354,8 +326,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
             bool ok = pf_wait(q_full, 0, s_abort) && pf_wait(&k_full[0], 0, s_abort);
             if (ok) {
                 tc_fence_after();
-                for (int x = 0; x < nq; ++x)
-                    if (x == 0 || lead == 0) mma_s(x, 0);
+                for (int x = 0; x < nq; ++x) mma_s(x, 0);
                 umma_commit(&k_empty[0]);
             }
             for (int j = 0; ok && j < ntiles; ++j) {
@@ -364,19 +335,17 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
                 // per query tile: P_X(j) V(j) once P_X(j) is in TMEM; then S_X(j + 1) into the same columns
                 // once that product has read P_X(j)
                 for (int x = 0; ok && x < nq; ++x) {
-                    const int ntx = x == 0 ? nt0 : nt1, j0 = x == 0 ? 0 : lead;
+                    const int ntx = x == 0 ? nt0 : nt1;
                     if (j >= ntx) continue;
-                    if (j >= j0) {
-                        if (!(ok = pf_wait(&p_full[x], (j - j0) & 1, s_abort))) break;
-                        tc_fence_after();
-                        mma_pv(x, j % VS, j == j0);
-                    }
-                    if (j + 1 < ntx) {  // (lead is 0 or 1: a tile that does not begin here begins with the next)
+                    if (!(ok = pf_wait(&p_full[x], j & 1, s_abort))) break;
+                    tc_fence_after();
+                    mma_pv(x, j % VS, j == 0);
+                    if (j + 1 < ntx) {
                         if (!k_next) {
                             if (!(ok = pf_wait(&k_full[(j + 1) % KS], ((j + 1) / KS) & 1, s_abort))) break;
                             k_next = true;
                         }
-                        if (j >= j0 && !(ok = pf_wait(&o_full[x], (j - j0) & 1, s_abort))) break;
+                        if (!(ok = pf_wait(&o_full[x], j & 1, s_abort))) break;
                         tc_fence_after();
                         mma_s(x, (j + 1) % KS);
                     }
@@ -396,7 +365,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
         const int rx = r0 + x * kPfRows;        // first row of this query tile
         const int row = wq * 32 + lane;
         const int qi = rx + row;                // row of the segment
-        const int nt = x == 0 ? nt0 : nt1, j0 = x == 0 ? 0 : lead;
+        const int nt = x == 0 ? nt0 : nt1;
         const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
         const uint32_t tS = tmem + x * kPfKeys + lane_base, tO = tmem + Geo::kTmemO + x * D + lane_base;
         const float sl2 = p.scale_log2;
@@ -404,16 +373,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
         const float fill = neg_scale ? INFINITY : -INFINITY;
         float m_used = -INFINITY, l = 0.f;
         bool ok = true;
-        for (int j = j0; j < nt; ++j) {
+        for (int j = 0; j < nt; ++j) {
             // S_X(j) complete also means P_X(j-1) V(j-1) complete: it was issued before S_X(j)
-            ok = __all_sync(0xffffffffu, pf_wait(&s_full[x], (j - j0) & 1, s_abort));
+            ok = __all_sync(0xffffffffu, pf_wait(&s_full[x], j & 1, s_abort));
             if (!ok) break;
             tc_fence_after();
-            const int k0 = key_tile(j) * kPfKeys;
+            const int k0 = j * kPfKeys;
             // a tile that crosses the causal diagonal or the segment end needs the mask; the others do not
-            // (kWindow: nor does one that every row sees, or that holds sinks alone)
-            const bool masked = k0 + kPfKeys > len || (p.causal && k0 + kPfKeys - 1 > rx) ||
-                                (kWindow && k0 <= rx + kPfRows - 1 - p.window && k0 + kPfKeys > p.sinks);
+            const bool masked = k0 + kPfKeys > len || (p.causal && k0 + kPfKeys - 1 > rx);
             float alpha = 1.f;       // rescale of O and of the l of earlier tiles
             float lsum[2] = {0.f, 0.f};  // per 64-key half: sum of the weights written
             // One pass per 64-key half: the half's extreme score, the lazy running max (it moves only when the
@@ -422,25 +389,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
             // residual in column 32 + i).  l sums the fp16 weights written (split form: P in fp32).
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
-                uint32_t bits[2] = {~0u, ~0u};
-                if (kWindow && masked) {
-                    bits[0] = window_bits(qi, k0 + hh * 64, len, p.window, p.sinks);
-                    bits[1] = window_bits(qi, k0 + hh * 64 + 32, len, p.window, p.sinks);
-                    // nothing of it for these 32 rows (half of the far tile, of the diagonal's, and of a tile of a few
-                    // sinks; giving the products fewer keys of such a tile too made the issuing thread, for which the
-                    // rest waits, 2 to 6 % slower over every tile)
-                    if (!__any_sync(0xffffffffu, (bits[0] | bits[1]) != 0)) {
-                        float zero[32] = {};
-                        tmem_st32(tS + hh * 64, zero);
-                        if constexpr (kSplitP) tmem_st32(tS + hh * 64 + 32, zero);
-                        continue;
-                    }
-                }
                 float s[64];
                 tmem_ld64(tS + hh * 64, s);
                 float e[4];
-                if (kWindow && masked) mask_scores(s, bits, fill);
-                if (!kWindow && masked) {
+                if (masked) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) e[i] = fill;
 #pragma unroll
@@ -505,11 +457,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
                     if constexpr (kSplitP) tmem_st32(tS + 32, r);
                     if (a_h != 1.f) lsum[0] = s0;
                     tmem_ld64(tS + 64, s);
-                    if (kWindow && masked) mask_scores(s, bits, fill);
                 }
                 alpha *= a_h;
                 const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
-                if (!kWindow && masked) {
+                if (masked) {
 #pragma unroll
                     for (int c = 0; c < 64; ++c) {
                         const int kj = k0 + hh * 64 + c;
@@ -585,7 +536,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
             }
             l = l * alpha + (lsum[0] + lsum[1]);
             // O_X is idle here (P_X(j-1) V(j-1) is complete, P_X(j) V(j) not issued): rescale it in place
-            if (j > j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     float o[32];
@@ -615,7 +566,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[x]);
         }
-        if (ok) ok = __all_sync(0xffffffffu, pf_wait(&o_full[x], (nt - 1 - j0) & 1, s_abort));
+        if (ok) ok = __all_sync(0xffffffffu, pf_wait(&o_full[x], (nt - 1) & 1, s_abort));
         if (ok) {
             tc_fence_after();
             const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -639,23 +590,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
                                                 pack_half2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
                                                 pack_half2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
                                                 pack_half2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
-                    }
-                }
-                if constexpr (kWindow) {
-                    float t = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) t = fmaf(o[i], 0.f, t);  // NaN if any is infinite or NaN
-                    unsigned again = __ballot_sync(0xffffffffu, qi < len && !(t == 0.f && l < INFINITY));
-                    for (; again != 0; again &= again - 1) {
-                        const int i = rx + wq * 32 + __ffs(again) - 1;
-                        const int64_t kv_stride = static_cast<int64_t>(p.Hkv) * D, kv0 = beg * kv_stride + hk * D;
-                        const int64_t at = (static_cast<int64_t>(beg + i) * p.Hq + h) * D;
-                        const float r = window_row_again<D>(p.q + at, p.k + kv0, p.v + kv0, kv_stride, i, p.window, p.sinks, sl2, c);
-                        __syncwarp();
-                        if (p.out_f32)
-                            static_cast<float*>(p.out)[at + c + lane] = r;
-                        else
-                            static_cast<__half*>(p.out)[at + c + lane] = __float2half_rn(r);
                     }
                 }
             }
@@ -700,14 +634,14 @@ static cudaError_t make_packed_map(CUtensorMap* map, const void* base, int D, in
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int D, bool kSplitP, bool kWindow = false>
+template <int D, bool kSplitP>
 static cudaError_t launch_prefill_d(const PrefillArgs& a, cudaStream_t stream) {
     using Geo = PfGeom<D>;
     static std::once_flag attr_once;
     static cudaError_t attr_err = cudaSuccess;
     std::call_once(attr_once, [] {
-        attr_err = cudaFuncSetAttribute(prefill_kernel<D, kSplitP, kWindow>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize, Geo::kSmemBytes);
+        attr_err = cudaFuncSetAttribute(prefill_kernel<D, kSplitP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        Geo::kSmemBytes);
     });
     if (attr_err != cudaSuccess) return attr_err;
     CUtensorMap tq, tk, tv;
@@ -728,21 +662,10 @@ static cudaError_t launch_prefill_d(const PrefillArgs& a, cudaStream_t stream) {
     p.causal = a.causal;
     p.out_f32 = a.out_f32;
     p.scale_log2 = a.scale * kPfLog2e;
-    if (kWindow && std::fabs(p.scale_log2) < kMinWindowScaleLog2) p.scale_log2 = kMinWindowScaleLog2;
     const int64_t nblocks = static_cast<int64_t>(p.tiles_per_seq) * a.nseq * a.Hq;
     if (nblocks > 2147483647LL) return cudaErrorInvalidConfiguration;
-    p.window = a.window;
-    p.sinks = a.sinks;
-    p.q = a.q;
-    p.k = a.k;
-    p.v = a.v;
-    if constexpr (kWindow) {
-        return launch(prefill_kernel<D, kSplitP, true>, dim3(static_cast<unsigned>(nblocks)), dim3(kPfThreads),
-                      Geo::kSmemBytes, stream, true, 1u, tq, tk, tv, p);
-    } else {
-        prefill_kernel<D, kSplitP><<<static_cast<unsigned>(nblocks), kPfThreads, Geo::kSmemBytes, stream>>>(tq, tk, tv, p);
-        return cudaGetLastError();
-    }
+    prefill_kernel<D, kSplitP><<<static_cast<unsigned>(nblocks), kPfThreads, Geo::kSmemBytes, stream>>>(tq, tk, tv, p);
+    return cudaGetLastError();
 }
 
 // Head dim 64: batches of at least this many (token, query head) pairs take this file's kernel (two query tiles
@@ -757,18 +680,7 @@ static cudaError_t launch_prefill_d(const PrefillArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
     if (a.nseq <= 0 || a.total_tokens <= 0 || a.max_seqlen <= 0) return cudaSuccess;
-    if (a.window > 0) {
-#ifndef KVC_W_OLD
-        if (a.D == 128 || static_cast<int64_t>(a.total_tokens) * a.Hq >= KVC_PREFILL_D64_TWO_TILE_WORK) return launch_prefill_window(a, stream);
-#endif
-        if (a.D == 64) {
-            if (static_cast<int64_t>(a.total_tokens) * a.Hq < KVC_PREFILL_D64_TWO_TILE_WORK)
-                return launch_prefill_1t(a, stream);
-            return a.split_p ? launch_prefill_d<64, true, true>(a, stream) : launch_prefill_d<64, false, true>(a, stream);
-        }
-        if (a.D != 128) return cudaErrorInvalidValue;
-        return a.split_p ? launch_prefill_d<128, true, true>(a, stream) : launch_prefill_d<128, false, true>(a, stream);
-    }
+    if (a.window > 0) return launch_prefill_window(a, stream);
     if (a.D == 64) {
         if (static_cast<int64_t>(a.total_tokens) * a.Hq < KVC_PREFILL_D64_TWO_TILE_WORK)
             return launch_prefill_1t(a, stream);  // one query tile per CTA (prefill_1t.cu)

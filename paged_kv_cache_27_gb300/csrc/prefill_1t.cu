@@ -17,16 +17,13 @@
 // buffer j % 2 as soon as P(j) V has read P(j) there.  K and V have rings of their own.  With D = 64 this
 // beats two query tiles per CTA (more CTAs, shorter chains); with D = 128 two query tiles sharing each K/V
 // tile win (prefill.cu).  Every wait is bounded; a timeout sets an error bit and drains the CTA.
-// kWindow (causal): the key tiles are those of the sinks, then from the window's first to the diagonal.
 #include <algorithm>
 #include <cmath>
 #include <cudaTypedefs.h>
 #include <mutex>
 
 #include "../../include/kvc.h"
-#include "decode_common.cuh"
 #include "kvc_internal.h"
-#include "prefill_window.cuh"
 #include "ptx.cuh"
 #include "tcgen05.cuh"
 
@@ -84,11 +81,6 @@ struct PrefillKernelParams {
     unsigned* err;
     int nseq, total_tokens, tiles_per_seq, Hq, Hkv, G, causal, out_f32;
     float scale_log2;
-    // kWindow
-    int window, sinks;
-    const __half* q;
-    const __half* k;
-    const __half* v;
 };
 
 // byte offset of 16-byte chunk c (0..7) of row `row` in a 1024-byte aligned tile of 128-byte rows, 128-byte
@@ -153,7 +145,7 @@ __device__ __forceinline__ bool pf_wait(uint64_t* bar, uint32_t parity, volatile
     }
 }
 
-template <int D, bool kSplitP, bool kWindow = false>
+template <int D, bool kSplitP>
 __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_constant__ CUtensorMap tmQ,
                                                                 const __grid_constant__ CUtensorMap tmK,
                                                                 const __grid_constant__ CUtensorMap tmV,
@@ -185,7 +177,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
     const int seg = static_cast<int>(blockIdx.x % per_block) / p.Hq, h = static_cast<int>(blockIdx.x % per_block) % p.Hq;
     const int hk = h / p.G;
 
-    if constexpr (kWindow) grid_dependency_wait();  // nothing is read before the kernel in front is done
     const int beg = p.cu_seqlens[seg], end = p.cu_seqlens[seg + 1];
     const int len = end - beg;
     if (beg < 0 || len < 0 || end > p.total_tokens) {
@@ -196,14 +187,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
         atomicOr(p.err, KVC_DEVERR_SEQLENS);  // rows past max_seqlen are not computed
     const int r0 = tile * kPfCtaRows;
     if (r0 >= len) return;
-    int nt = ((p.causal ? min(len, r0 + kPfRows) : len) + kPfKeys - 1) / kPfKeys;  // key tiles
-    int sink_tiles = 0, skipped = 0;  // kWindow: between the sinks and the window
-    if constexpr (kWindow) {
-        sink_tiles = min((p.sinks + kPfKeys - 1) / kPfKeys, nt);
-        skipped = max(max(0, r0 - p.window + 1) / kPfKeys - sink_tiles, 0);
-        nt -= skipped;
-    }
-    auto key_tile = [&](int j) { return kWindow && j >= sink_tiles ? j + skipped : j; };
+    const int nt = ((p.causal ? min(len, r0 + kPfRows) : len) + kPfKeys - 1) / kPfKeys;  // key tiles
 
     uint8_t* qs = smem + Geo::kQOff;
     auto kst = [&](int st) { return smem + Geo::kKOff + st * Geo::kKVBytes; };
@@ -247,14 +231,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
                 mbar_arrive_expect_tx(bar, Geo::kKVBytes);
 #pragma unroll
                 for (int c = 0; c < Geo::kChunks; ++c)
-                    tma_load_3d(kst(t % KS) + c * Geo::kKVChunk, &tmK, bar, c * 64, hk, beg + key_tile(t) * kPfKeys);
+                    tma_load_3d(kst(t % KS) + c * Geo::kKVChunk, &tmK, bar, c * 64, hk, beg + t * kPfKeys);
             };
             auto load_v = [&](int t) {
                 uint64_t* bar = &v_full[t % VS];
                 mbar_arrive_expect_tx(bar, Geo::kKVBytes);
 #pragma unroll
                 for (int c = 0; c < Geo::kChunks; ++c)
-                    tma_load_3d(vst(t % VS) + c * Geo::kKVChunk, &tmV, bar, c * 64, hk, beg + key_tile(t) * kPfKeys);
+                    tma_load_3d(vst(t % VS) + c * Geo::kKVChunk, &tmV, bar, c * 64, hk, beg + t * kPfKeys);
             };
             prefetch_tensormap(&tmQ);
             prefetch_tensormap(&tmK);
@@ -374,17 +358,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
             const uint32_t tS = tSp + (j & 1) * kPfKeys;
             float s[kPfPartKeys];
             tmem_ld32(tS, s);
-            const int k0 = key_tile(j) * kPfKeys + kp * kPfPartKeys;  // first key of this part
+            const int k0 = j * kPfKeys + kp * kPfPartKeys;  // first key of this part
             // a part that crosses the causal diagonal or the segment end needs the mask; the others do not
-            // (kWindow: nor does one that every row sees, or that holds sinks alone)
-            const bool masked = k0 + kPfPartKeys > len || (p.causal && k0 + kPfPartKeys - 1 > r0) ||
-                                (kWindow && k0 <= r0 + kPfRows - 1 - p.window && k0 + kPfPartKeys > p.sinks);
+            const bool masked = k0 + kPfPartKeys > len || (p.causal && k0 + kPfPartKeys - 1 > r0);
             float e[4];
-            if (kWindow && masked) {
-                const uint32_t bits = window_bits(qi, k0, len, p.window, p.sinks);
-                mask_scores(s, &bits, fill);
-            }
-            if (!kWindow && masked) {
+            if (masked) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) e[i] = fill;
 #pragma unroll
@@ -439,7 +417,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
             // P = 2^(s * scale * log2 e - m) written over this part's S columns in fp16, keys (2i, 2i + 1) in
             // column i (split form: the high part there, the residual in column 16 + i).  l sums the fp16
             // weights written (split form: P in fp32).
-            if (!kWindow && masked) {
+            if (masked) {
 #pragma unroll
                 for (int c = 0; c < kPfPartKeys; ++c) {
                     const int kj = k0 + c;
@@ -493,7 +471,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
             }
             // the segment's last key tile: V rows past its end (the next segment's tokens) are zeroed, so that
             // whatever they hold cannot reach this segment's output through a zero weight
-            const int vrem = len - key_tile(j) * kPfKeys;
+            const int vrem = len - j * kPfKeys;
             if (vrem < kPfKeys && warp == 0) {
                 ok = __all_sync(0xffffffffu, pf_wait(&v_full[j % VS], (j / VS) & 1, s_abort));
                 if (!ok) break;
@@ -547,23 +525,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_kernel(const __grid_con
                                             pack_half2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
                 }
             }
-            if constexpr (kWindow) {
-                float t = 0.f;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) t = fmaf(o[i], 0.f, t);  // NaN if any is infinite or NaN
-                unsigned again = __ballot_sync(0xffffffffu, qi < len && !(t == 0.f && l < INFINITY));
-                for (; again != 0; again &= again - 1) {
-                    const int i = r0 + wq * 32 + __ffs(again) - 1;
-                    const int64_t kv_stride = static_cast<int64_t>(p.Hkv) * D, kv0 = beg * kv_stride + hk * D;
-                    const int64_t at = (static_cast<int64_t>(beg + i) * p.Hq + h) * D;
-                    const float r = window_row_again<D>(p.q + at, p.k + kv0, p.v + kv0, kv_stride, i, p.window, p.sinks, sl2, kp * 32);
-                    __syncwarp();
-                    if (p.out_f32)
-                        static_cast<float*>(p.out)[at + kp * 32 + lane] = r;
-                    else
-                        static_cast<__half*>(p.out)[at + kp * 32 + lane] = __float2half_rn(r);
-                }
-            }
         }
     }
     // every TMEM access of the CTA is complete; the allocating warp frees it
@@ -605,14 +566,14 @@ static cudaError_t make_packed_map(CUtensorMap* map, const void* base, int D, in
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int D, bool kSplitP, bool kWindow = false>
+template <int D, bool kSplitP>
 static cudaError_t launch_prefill_d(const PrefillArgs& a, cudaStream_t stream) {
     using Geo = PfGeom<D>;
     static std::once_flag attr_once;
     static cudaError_t attr_err = cudaSuccess;
     std::call_once(attr_once, [] {
-        attr_err = cudaFuncSetAttribute(prefill_kernel<D, kSplitP, kWindow>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize, Geo::kSmemBytes);
+        attr_err = cudaFuncSetAttribute(prefill_kernel<D, kSplitP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        Geo::kSmemBytes);
     });
     if (attr_err != cudaSuccess) return attr_err;
     CUtensorMap tq, tk, tv;
@@ -633,21 +594,10 @@ static cudaError_t launch_prefill_d(const PrefillArgs& a, cudaStream_t stream) {
     p.causal = a.causal;
     p.out_f32 = a.out_f32;
     p.scale_log2 = a.scale * kPfLog2e;
-    if (kWindow && std::fabs(p.scale_log2) < kMinWindowScaleLog2) p.scale_log2 = kMinWindowScaleLog2;
     const int64_t nblocks = static_cast<int64_t>(p.tiles_per_seq) * a.nseq * a.Hq;
     if (nblocks > 2147483647LL) return cudaErrorInvalidConfiguration;
-    p.window = a.window;
-    p.sinks = a.sinks;
-    p.q = a.q;
-    p.k = a.k;
-    p.v = a.v;
-    if constexpr (kWindow) {
-        return launch(prefill_kernel<D, kSplitP, true>, dim3(static_cast<unsigned>(nblocks)), dim3(kPfThreads),
-                      Geo::kSmemBytes, stream, true, 1u, tq, tk, tv, p);
-    } else {
-        prefill_kernel<D, kSplitP><<<static_cast<unsigned>(nblocks), kPfThreads, Geo::kSmemBytes, stream>>>(tq, tk, tv, p);
-        return cudaGetLastError();
-    }
+    prefill_kernel<D, kSplitP><<<static_cast<unsigned>(nblocks), kPfThreads, Geo::kSmemBytes, stream>>>(tq, tk, tv, p);
+    return cudaGetLastError();
 }
 
 }  // namespace pf1
@@ -656,8 +606,6 @@ cudaError_t launch_prefill_1t(const PrefillArgs& a, cudaStream_t stream) {
     using namespace pf1;
     if (a.nseq <= 0 || a.total_tokens <= 0 || a.max_seqlen <= 0) return cudaSuccess;
     if (a.D != 64) return cudaErrorInvalidValue;
-    if (a.window > 0)
-        return a.split_p ? launch_prefill_d<64, true, true>(a, stream) : launch_prefill_d<64, false, true>(a, stream);
     return a.split_p ? launch_prefill_d<64, true>(a, stream) : launch_prefill_d<64, false>(a, stream);
 }
 

@@ -20,8 +20,13 @@
 // weights are carried 2^11 times as large, so that fp16's 11 bits last down to 2^-25 of a row's largest one.
 // Hidden values.  A masked key's weight is 0, and 0 times an infinity or NaN in its V row would be NaN: a row that comes
 // out infinite or NaN is computed again from its visible keys alone.
-// A CTA takes items until there are none left (every gridDim.x-th); copies and products of the next one start under the
-// end of this one.  Every wait is bounded; a timeout sets an error bit and drains the CTA.
+// Items.  The grid has a CTA for every item that max_seqlen allows, the last row blocks of all segments first (their key
+// lists are the longest), but a CTA that runs takes over those that have not started (cluster launch control): one warp
+// asks for them, passes over the row blocks that a segment does not have, and hands a description of the next one to the
+// rest when the last one's copies are out (asked for earlier, few items pile up on some CTAs: five uneven prompts of 5841
+// tokens in all, window 512, 8 heads, D = 64, 35 us so and 23.6 now; a CTA for every item 28).  Copies and products of
+// the next item start under the end of this one (window 128 of 4 x 4096 tokens, 32 / 8 heads, D = 128: 165 us with a CTA
+// per item, 124 now).  Every wait is bounded; a timeout sets an error bit and drains the CTA.
 #include <algorithm>
 #include <cmath>
 #include <cudaTypedefs.h>
@@ -46,7 +51,9 @@ constexpr int kSWarp = kRowWarps;       // S products of stream A, of stream B
 constexpr int kPvWarp = kRowWarps + 2;  // P V products of stream A, of stream B
 constexpr int kLoadKWarp = kRowWarps + 4;
 constexpr int kLoadVWarp = kRowWarps + 5;
-constexpr int kThreads = (kRowWarps + 6) * 32;
+constexpr int kItemWarp = kRowWarps + 6;  // hands out the items to the other warps
+constexpr int kThreads = (kRowWarps + 7) * 32;
+constexpr int kSlots = 2;  // items described at a time
 constexpr uint64_t kWaitNs = 1000000000ull;
 // (as in the tree attention: weights carried 2^11 times as large; the max moves when a score is 2^15 above it; beyond
 // kFar a step of a score's exponent is no longer small against fp16's range)
@@ -65,7 +72,8 @@ struct Geom {
     static constexpr int kVOff = kQOff + 2 * kTileBytes;
     static constexpr int kKOff = kVOff + kVStages * kTileBytes;
     static constexpr int kBarOff = kKOff + kKStages * kTileBytes;
-    static constexpr int kSmemBytes = kBarOff + 512 + 1024;  // barriers, TMEM address, flag; alignment
+    static constexpr int kItemOff = kBarOff + 512;  // barriers, TMEM address, flag; then the items
+    static constexpr int kSmemBytes = kItemOff + 256 + 1024;  // alignment
     static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
     // TMEM columns: two buffers of S / P per stream, A [0, 128) and B [128, 256), then O_A and O_B, D columns each
     static constexpr int kTmemO = 4 * kHalf;
@@ -80,7 +88,6 @@ struct Params {
     void* out;
     unsigned* err;
     int nseq, total_tokens, tiles_per_seq, Hq, Hkv, G, out_f32, window, sinks;
-    unsigned items;
     int negate;        // the scale is negative
     float scale_log2;  // |scale| * log2 e, at least kMinWindowScaleLog2
 };
@@ -155,16 +162,16 @@ struct Item {
     int beg, len, h, hk, r0;
     int lead, sink_tiles, far0, near0, end[2], entries;
     int narrow;  // the entry of which the first unit alone holds visible keys, or -1
-    bool any;
+    int any;     // 0: the last one was before this
     __device__ __forceinline__ int key_tile(int j) const {
         return j < lead ? far0 + j : j < lead + sink_tiles ? j - lead : near0 + j - lead - sink_tiles;
     }
     __device__ __forceinline__ int begin(int x) const { return x == 0 ? 0 : lead; }
     __device__ __forceinline__ int units(int j) const { return j == narrow ? 1 : 2; }
 };
-__device__ __forceinline__ Item make_item(const Params& p, unsigned index, bool report) {
+static_assert(sizeof(Item) <= 64, "items in shared memory");
+__device__ __forceinline__ Item make_item(const Params& p, unsigned index) {
     Item it;
-    // heaviest row blocks first: index = ((last row block - row block) * nseq + segment) * Hq + head
     const unsigned per_block = static_cast<unsigned>(p.nseq) * p.Hq, of_block = index / per_block;
     const int block = static_cast<int>(of_block), rest = static_cast<int>(index - of_block * per_block);
     const int tile = p.tiles_per_seq - 1 - block, seg = rest / p.Hq;
@@ -175,7 +182,7 @@ __device__ __forceinline__ Item make_item(const Params& p, unsigned index, bool 
     it.len = end - it.beg;
     it.r0 = tile * 2 * kRows;
     const bool bad = it.beg < 0 || it.len < 0 || end > p.total_tokens;
-    if (report && tile == 0 && it.h == 0 && (bad || it.len > p.tiles_per_seq * 2 * kRows))
+    if (tile == 0 && it.h == 0 && (bad || it.len > p.tiles_per_seq * 2 * kRows))
         atomicOr(p.err, KVC_DEVERR_SEQLENS);  // (rows past max_seqlen are not computed)
     it.any = !bad && it.r0 < it.len;
     if (!it.any) return it;
@@ -193,6 +200,29 @@ __device__ __forceinline__ Item make_item(const Params& p, unsigned index, bool 
     const int k0 = (it.sink_tiles - 1) * kKeys;
     it.narrow = it.sink_tiles > 0 && k0 + kKeys - 1 <= it.r0 - p.window && p.sinks <= k0 + kHalf ? it.lead + it.sink_tiles - 1 : -1;
     return it;
+}
+
+// Ask for a CTA of this grid that has not started (16 bytes to `answer`, counted on the barrier); whether there was one,
+// and its index.
+__device__ __forceinline__ void ask_for_cta(void* answer, uint64_t* bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_u32(answer)),
+                 "r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ bool got_cta(const void* answer, unsigned& index) {
+    uint32_t yes, x;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 h, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+        : "=r"(yes), "=r"(x)
+        : "r"(smem_u32(answer))
+        : "memory");
+    index = x;
+    return yes != 0;
 }
 
 template <int D, bool kSplitP>
@@ -216,9 +246,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
     uint64_t* o_full = p_full + 4;      // [2][2] P V of the buffer done
     uint64_t* fin = o_full + 4;         // [4] every product that a product warp issued is done
     uint64_t* v_land = fin + 4;         // a V tile that reaches past its segment landed (then mended)
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(v_land + 1);
+    uint64_t* item_full = v_land + 1;             // [kSlots] the slot's item is described
+    uint64_t* item_empty = item_full + kSlots;    // [kSlots] the other warps are done with it
+    uint64_t* cta_full = item_empty + kSlots;     // the answer is there
+    uint64_t* wanted = cta_full + 1;              // the last item's copies are all out
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(wanted + 1);
     volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
-    static_assert((2 + 2 * KS + 2 * VS + 17) * 8 + 8 <= 512, "barrier area");
+    static_assert((2 + 2 * KS + 2 * VS + 17 + 2 * kSlots + 2) * 8 + 8 <= 512, "barrier area");
+    Item* const s_item = reinterpret_cast<Item*>(smem + Geo::kItemOff);            // [kSlots], 64 bytes each
+    void* const s_answer = smem + Geo::kItemOff + kSlots * 64;
+    auto slot_item = [&](uint32_t slot) -> const Item& {
+        return *reinterpret_cast<const Item*>(reinterpret_cast<const uint8_t*>(s_item) + slot * 64);
+    };
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     auto qs = [&](int x) { return smem + Geo::kQOff + x * Geo::kTileBytes; };
@@ -243,6 +282,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
             mbar_init(&fin[i], 1);
         }
         mbar_init(v_land, 1);
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(&item_full[i], 1);
+            mbar_init(&item_empty[i], kItemWarp);
+        }
+        mbar_init(cta_full, 1);
+        mbar_init(wanted, 1);
         *s_abort = 0;
         fence_barrier_init();
     }
@@ -257,7 +302,42 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
     grid_dependency_wait();  // nothing is read or written before the kernel in front is done
 
     bool ok = true;
-    if (warp >= kLoadKWarp) {
+    uint32_t turn = 0;  // items so far: the next one is in slot turn % kSlots
+    auto next_item = [&]() { return __all_sync(0xffffffffu, wait(&item_full[turn % kSlots], turn / kSlots & 1, s_abort)); };
+    auto item_done = [&]() {  // the warp has read what it needs of the item
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&item_empty[turn % kSlots]);
+        ++turn;
+    };
+    if (warp == kItemWarp) {
+        // ================= items (one thread) =================
+        if (lane == 0) {
+            unsigned index = blockIdx.x;
+            bool more = true;
+            for (int answers = 0; ok; ++answers) {
+                Item it;
+                it.any = 0;
+                if (more) it = make_item(p, index);
+                if (it.any || !more) {
+                    if (turn >= kSlots) ok = wait(&item_empty[turn % kSlots], (turn / kSlots - 1) & 1, s_abort);
+                    if (!ok) break;
+                    *reinterpret_cast<Item*>(reinterpret_cast<uint8_t*>(s_item) + turn % kSlots * 64) = it;
+                    mbar_arrive(&item_full[turn % kSlots]);
+                    // no item is taken over before the last one's copies are all out: others may have nothing left
+                    if (more) ok = wait(wanted, turn & 1, s_abort);
+                    ++turn;
+                }
+                if (!more || !ok) break;
+                mbar_arrive_expect_tx(cta_full, 16);
+                ask_for_cta(s_answer, cta_full);
+                const bool there = mbar_wait_bounded(cta_full, answers & 1, kWaitNs);
+                more = there && got_cta(s_answer, index);
+                if (!there) *s_abort = 1;
+                fence_proxy_async_smem();  // the answer is read before the next one is written
+            }
+        }
+        __syncwarp();
+    } else if (warp >= kLoadKWarp) {
         // ================= copies: Q and K by one warp, V by the other, as far ahead as the rings allow =================
         const bool is_v = warp == kLoadVWarp;
         uint64_t* const full = is_v ? v_full : k_full;
@@ -270,9 +350,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
             if (!is_v) prefetch_tensormap(&tmQ);
             prefetch_tensormap(map);
         }
-        for (unsigned index = blockIdx.x; ok && index < p.items; index += gridDim.x) {
-            const Item it = make_item(p, index, !is_v && lane == 0);
-            if (!it.any) continue;
+        for (;; item_done()) {
+            ok = ok && next_item();
+            if (!ok) break;
+            const Item& it = slot_item(turn % kSlots);
+            if (!it.any) break;
             if (!is_v) {
                 if (done > 0) ok = __all_sync(0xffffffffu, wait(q_empty, (done - 1) & 1, s_abort));
                 if (!ok) break;
@@ -322,6 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
                     ++ph;
                 }
             }
+            if (!is_v && lane == 0) mbar_arrive(wanted);
         }
         // copies still in flight land before the shared memory is released (immediate unless aborted: the products
         // consumed every tile)
@@ -342,9 +425,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
             constexpr uint32_t idS = umma_idesc_f16(kRows, kHalf, 0, 0);
             const uint64_t dQ = umma_smem_desc(smem_u32(qs(x)), 16, 1024);
             const uint64_t dK = umma_smem_desc(smem_u32(kst(0)), 16, 1024);
-            for (unsigned index = blockIdx.x; ok && index < p.items; index += gridDim.x) {
-                const Item it = make_item(p, index, false);
-                if (!it.any) continue;
+            for (;; item_done()) {
+                ok = ok && next_item();
+                if (!ok) break;
+                const Item& it = slot_item(turn % kSlots);
+                if (!it.any) break;
                 ok = wait_all(q_full, done & 1, s_abort);
                 if (!ok) break;
                 ++done;
@@ -394,9 +479,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
             constexpr uint32_t idPV = umma_idesc_f16(kRows, D, 0, 1);
             const uint64_t dV = umma_smem_desc(smem_u32(vst(0)), Geo::kChunkBytes, 1024);
             const uint32_t tO = tmem + Geo::kTmemO + x * D;
-            for (unsigned index = blockIdx.x; ok && index < p.items; index += gridDim.x) {
-                const Item it = make_item(p, index, false);
-                if (!it.any) continue;
+            for (;; item_done()) {
+                ok = ok && next_item();
+                if (!ok) break;
+                const Item& it = slot_item(turn % kSlots);
+                if (!it.any) break;
                 const int first = it.begin(x), end = it.end[x];
                 for (int j = 0; j < it.entries; ++j) {
                     ok = wait_all(&v_full[st], ph & 1, s_abort);
@@ -448,9 +535,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
         const float sl2 = p.scale_log2;
         const uint64_t sc2 = pack_f32x2(sl2, sl2);
         int uc = 0;  // units so far
-        for (unsigned index = blockIdx.x; ok && index < p.items; index += gridDim.x) {
-            const Item it = make_item(p, index, false);
-            if (!it.any || it.end[x] == 0) continue;
+        for (;; item_done()) {
+            ok = ok && next_item();
+            if (!ok) break;
+            const Item& it = slot_item(turn % kSlots);
+            if (!it.any) break;
+            if (it.end[x] == 0) continue;
             const int rx = it.r0 + x * kRows;           // first row of the row tile
             const int qi = rx + wq * 32 + lane;         // row of the segment
             const int first = it.begin(x), end = it.end[x];
@@ -665,12 +755,7 @@ static cudaError_t launch_d(const PrefillArgs& a, cudaStream_t stream) {
     p.scale_log2 = std::max(std::min(std::fabs(a.scale) * kLog2e, 3.4e38f), kMinWindowScaleLog2);
     const int64_t items = static_cast<int64_t>(p.tiles_per_seq) * a.nseq * a.Hq;
     if (items > 2147483647LL) return cudaErrorInvalidConfiguration;
-    p.items = static_cast<unsigned>(items);
-#ifndef KVC_PFW_PERSIST
-#define KVC_PFW_PERSIST 1
-#endif
-    const int grid = static_cast<int>(KVC_PFW_PERSIST ? std::min<int64_t>(items, sm_count()) : items);
-    return launch(prefill_window_kernel<D, kSplitP>, dim3(grid), dim3(kThreads), Geo::kSmemBytes, stream, true, 1u, tq, tk,
+    return launch(prefill_window_kernel<D, kSplitP>, dim3(static_cast<unsigned>(items)), dim3(kThreads), Geo::kSmemBytes, stream, true, 1u, tq, tk,
                   tv, p);
 }
 

@@ -1,5 +1,4 @@
-// What the two prefill kernels share where a row sees a sliding window and sinks: which keys a row sees, and rows
-// computed again from these alone.
+// What a row sees through a sliding window and sinks, and rows computed again from that alone (prefill_window.cu).
 #pragma once
 #include <cuda_fp16.h>
 #include <stdint.h>

@@ -623,6 +623,18 @@ def test_prefill_of_long_prompts(heads, lens, window, sinks, scale):
     assert kvc.kvc_device_error_flags(clear=True) == 0
 
 
+@pytest.mark.parametrize("nseq", [255, 256, 257, 700])
+@pytest.mark.parametrize("heads", [(2, 1, 64), (3, 3, 128)])
+def test_prefill_of_many_prompts(nseq, heads):
+    """Listed segments (up to 256) and more than that; empty ones among them."""
+    lens = list(np.random.default_rng(nseq).integers(0, 40, nseq))
+    lens[3], lens[nseq - 2], lens[nseq - 1] = 300, 600, 0
+    q, k, v, cu = packed(lens, heads, 13)
+    ref = prefill_reference(q, k, v, lens, 0.2, 33, 5)
+    check_prefill(run_prefill(q, k, v, cu, 0.2, 33, 5, torch.float32), ref, q, k, v, 0.2, 40, False)
+    assert kvc.kvc_device_error_flags(clear=True) == 0
+
+
 def test_prefill_reference_is_the_oracles():
     lens = [9, 40]
     q, k, v, cu = packed(lens, (4, 2, 64), 8)
