@@ -71,12 +71,17 @@ struct Geom {
     static constexpr int kQOff = 0;  // Q_A, Q_B
     static constexpr int kVOff = kQOff + 2 * kTileBytes;
     static constexpr int kKOff = kVOff + kVStages * kTileBytes;
-    static constexpr int kBarOff = kKOff + kKStages * kTileBytes;
+    // D = 64 (TMEM has the columns for it): row sums come from a product too, with a tile of 64 keys of ones
+    static constexpr bool kSumProduct = D == 64;
+    static constexpr int kOnesOff = kKOff + kKStages * kTileBytes;
+    static constexpr int kOnesBytes = kSumProduct ? kHalf * 128 : 0;
+    static constexpr int kBarOff = kOnesOff + kOnesBytes;
     static constexpr int kItemOff = kBarOff + 512;  // barriers, TMEM address, flag; then the items
     static constexpr int kSmemBytes = kItemOff + 256 + 1024;  // alignment
     static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
     // TMEM columns: two buffers of S / P per stream, A [0, 128) and B [128, 256), then O_A and O_B, D columns each
     static constexpr int kTmemO = 4 * kHalf;
+    static constexpr int kTmemL = kTmemO + 2 * D;  // row sums of A and B, 64 equal columns each
     static constexpr uint32_t kTmemCols = 512;
 };
 
@@ -295,6 +300,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
         tmem_alloc(s_tmem, Geo::kTmemCols);
         tmem_relinquish();
     }
+    if constexpr (Geo::kSumProduct) {
+        for (int e = threadIdx.x; e < Geo::kOnesBytes / 16; e += kThreads)
+            reinterpret_cast<uint4*>(smem + Geo::kOnesOff)[e] = make_uint4(0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u);
+        fence_proxy_async_smem();  // visible to the tensor cores (async proxy)
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -478,7 +488,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
             // operand: 8-key groups 1024 bytes apart, 64-dim atoms one chunk apart
             constexpr uint32_t idPV = umma_idesc_f16(kRows, D, 0, 1);
             const uint64_t dV = umma_smem_desc(smem_u32(vst(0)), Geo::kChunkBytes, 1024);
-            const uint32_t tO = tmem + Geo::kTmemO + x * D;
+            const uint32_t tO = tmem + Geo::kTmemO + x * D, tL = tmem + Geo::kTmemL + x * 64;
+            const uint64_t dOnes = umma_smem_desc(smem_u32(smem + Geo::kOnesOff), Geo::kChunkBytes, 1024);
             for (;; item_done()) {
                 ok = ok && next_item();
                 if (!ok) break;
@@ -504,6 +515,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
                                     const uint64_t bd = v0 + ((kk * 2048) >> 4);
                                     umma_f16_ts(tO, tP + kk * 8, bd, idPV, (more || kk > 0) ? 1u : 0u);
                                     if constexpr (kSplitP) umma_f16_ts(tO, tP + kHalf / 2 + kk * 8, bd, idPV, 1u);
+                                }
+                                if constexpr (Geo::kSumProduct) {
+#pragma unroll
+                                    for (int kk = 0; kk < kHalf / 16; ++kk) {
+                                        const uint64_t bd = dOnes + ((kk * 2048) >> 4);
+                                        umma_f16_ts(tL, tP + kk * 8, bd, idPV, (more || kk > 0) ? 1u : 0u);
+                                        if constexpr (kSplitP) umma_f16_ts(tL, tP + kHalf / 2 + kk * 8, bd, idPV, 1u);
+                                    }
                                 }
                                 umma_commit(&o_full[buf]);
                                 if (half == units - 1) umma_commit(&v_empty[st]);
@@ -531,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
         // ================= row warps: softmax and output; thread = query row = TMEM lane =================
         const int x = warp / 4, wq = warp & 3;
         const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
-        const uint32_t tO = tmem + Geo::kTmemO + x * D + lane_base;
+        const uint32_t tO = tmem + Geo::kTmemO + x * D + lane_base, tL = tmem + Geo::kTmemL + x * 64 + lane_base;
         const float sl2 = p.scale_log2;
         const uint64_t sc2 = pack_f32x2(sl2, sl2);
         int uc = 0;  // units so far
@@ -607,6 +626,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
                                     for (int i = 0; i < 32; ++i) o[i] *= alpha;
                                     tmem_st32(tO + c, o);
                                 }
+                                if constexpr (Geo::kSumProduct) {  // (the one column that is read)
+                                    float sum[4];
+                                    tmem_ld4(tL, sum);
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) sum[i] *= alpha;
+                                    tmem_st4(tL, sum);
+                                }
                             }
                         }
                         const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
@@ -635,15 +661,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
                                 if constexpr (kSplitP) {
                                     const float2 f = unpack_half2(hv[i]);
                                     lv[i] = pack_half2(x0 - f.x, x1 - f.y);
-                                    ls[i & 3] += x0 + x1;
-                                } else {
+                                    if (!Geo::kSumProduct) ls[i & 3] += x0 + x1;
+                                } else if (!Geo::kSumProduct) {
                                     ls[i & 3] = add_halves(hv[i], ls[i & 3]);
                                 }
                             }
                             tmem_st16(tS + hh * 16, hv);
                             if constexpr (kSplitP) tmem_st16(tS + kHalf / 2 + hh * 16, lv);
                         }
-                        l = l * alpha + ((ls[0] + ls[1]) + (ls[2] + ls[3]));
+                        if (!Geo::kSumProduct) l = l * alpha + ((ls[0] + ls[1]) + (ls[2] + ls[3]));
                     }
                     tmem_wait_st();
                     tc_fence_before();
@@ -654,6 +680,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
             if (ok) ok = __all_sync(0xffffffffu, wait(&o_full[2 * x + ((uc - 1) & 1)], ((uc - 1) >> 1) & 1, s_abort));
             if (!ok) break;
             tc_fence_after();
+            if constexpr (Geo::kSumProduct) {
+                float sum[4];
+                tmem_ld4(tL, sum);
+                l = sum[0];
+            }
             const float inv = l > 0.f ? 1.f / l : 0.f;
             const int64_t row0 = (static_cast<int64_t>(it.beg + qi) * p.Hq + it.h) * D;
 #pragma unroll 1
