@@ -20,13 +20,14 @@
 // weights are carried 2^11 times as large, so that fp16's 11 bits last down to 2^-25 of a row's largest one.
 // Hidden values.  A masked key's weight is 0, and 0 times an infinity or NaN in its V row would be NaN: a row that comes
 // out infinite or NaN is computed again from its visible keys alone.
-// Items.  The grid has a CTA for every item that max_seqlen allows, the last row blocks of all segments first (their key
-// lists are the longest), but a CTA that runs takes over those that have not started (cluster launch control): one warp
-// asks for them, passes over the row blocks that a segment does not have, and hands a description of the next one to the
-// rest when the last one's copies are out (asked for earlier, few items pile up on some CTAs: five uneven prompts of 5841
-// tokens in all, window 512, 8 heads, D = 64, 35 us so and 23.6 now; a CTA for every item 28).  Copies and products of
+// Items.  The grid has a CTA for every item that total_tokens and max_seqlen leave possible; a CTA that runs takes over
+// those that have not started (cluster launch control).  One warp asks for them, finds the segment and row block that an
+// index stands for (sums of the segments' row blocks, 32 segments at a time), and hands a description of the next item to
+// the rest when the last one's copies are out (asked for earlier, few items pile up on some CTAs: five uneven prompts of
+// 5841 tokens in all, window 512, 8 heads, D = 64, 35 us so and 24 now; a CTA for every item 28).  Copies and products of
 // the next item start under the end of this one (window 128 of 4 x 4096 tokens, 32 / 8 heads, D = 128: 165 us with a CTA
-// per item, 124 now).  Every wait is bounded; a timeout sets an error bit and drains the CTA.
+// per item, 125 now).
+// Every wait is bounded; a timeout sets an error bit and drains the CTA.
 #include <algorithm>
 #include <cmath>
 #include <cudaTypedefs.h>
@@ -175,22 +176,57 @@ struct Item {
     __device__ __forceinline__ int units(int j) const { return j == narrow ? 1 : 2; }
 };
 static_assert(sizeof(Item) <= 64, "items in shared memory");
-__device__ __forceinline__ Item make_item(const Params& p, unsigned index) {
-    Item it;
-    const unsigned per_block = static_cast<unsigned>(p.nseq) * p.Hq, of_block = index / per_block;
-    const int block = static_cast<int>(of_block), rest = static_cast<int>(index - of_block * per_block);
-    const int tile = p.tiles_per_seq - 1 - block, seg = rest / p.Hq;
-    it.h = rest - seg * p.Hq;
-    it.hk = it.h / p.G;
-    it.beg = p.cu_seqlens[seg];
+// Row blocks of 256 rows that a segment has; its first row and its length.
+__device__ __forceinline__ int row_blocks(const Params& p, int seg, int& beg, int& len, bool& bad) {
+    beg = p.cu_seqlens[seg];
     const int end = p.cu_seqlens[seg + 1];
-    it.len = end - it.beg;
-    it.r0 = tile * 2 * kRows;
-    const bool bad = it.beg < 0 || it.len < 0 || end > p.total_tokens;
-    if (tile == 0 && it.h == 0 && (bad || it.len > p.tiles_per_seq * 2 * kRows))
-        atomicOr(p.err, KVC_DEVERR_SEQLENS);  // (rows past max_seqlen are not computed)
-    it.any = !bad && it.r0 < it.len;
+    len = end - beg;
+    if (beg < 0 || end < beg || end > p.total_tokens) {
+        bad = true;
+        return 0;
+    }
+    const int n = len / (2 * kRows) + (len % (2 * kRows) != 0);
+    if (n > p.tiles_per_seq) bad = true;  // (rows past max_seqlen are not computed)
+    return min(n, p.tiles_per_seq);
+}
+// The segments that the item warp is at: lane i has segment `first` + i's, and the row blocks up to its end.
+struct Segments {
+    int first = -32, beg, len, blocks, before, upto;  // before, upto: row blocks in front of these 32, and with them
+    int behind;                                       // row blocks up to this lane's segment, it included
+    __device__ __forceinline__ Segments() : before(0), upto(0) {}
+    __device__ __forceinline__ void next(const Params& p, int lane) {
+        first += 32;
+        before = upto;
+        const int seg = first + lane;
+        bool bad = false;
+        beg = len = 0;
+        blocks = seg < p.nseq ? row_blocks(p, seg, beg, len, bad) : 0;
+        if (bad) atomicOr(p.err, KVC_DEVERR_SEQLENS);
+        behind = blocks;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, behind, o);
+            if (lane >= o) behind += t;
+        }
+        behind += before;
+        upto = __shfl_sync(0xffffffffu, behind, 31);
+    }
+};
+// Item `index` (rising from one to the next, as CTAs are handed out; else the search begins anew): the head changes first, then the row block, from a segment's last one down
+// (its key list is the longest).  The whole warp; every lane gets it.
+__device__ __forceinline__ Item make_item(const Params& p, Segments& s, unsigned index, int lane) {
+    Item it;
+    const int block = static_cast<int>(index / static_cast<unsigned>(p.Hq));
+    it.h = static_cast<int>(index - static_cast<unsigned>(block) * p.Hq);
+    it.hk = it.h / p.G;
+    if (block < s.before) s = Segments();
+    while (block >= s.upto && s.first + 32 < p.nseq) s.next(p, lane);
+    it.any = block < s.upto;
     if (!it.any) return it;
+    const int who = __ffs(__ballot_sync(0xffffffffu, block < s.behind)) - 1;
+    it.beg = __shfl_sync(0xffffffffu, s.beg, who);
+    it.len = __shfl_sync(0xffffffffu, s.len, who);
+    it.r0 = (__shfl_sync(0xffffffffu, s.behind, who) - 1 - block) * 2 * kRows;
     const bool two = it.r0 + kRows < it.len;
     const int nt0 = (min(it.len, it.r0 + kRows) + kKeys - 1) / kKeys, nt1 = (min(it.len, it.r0 + 2 * kRows) + kKeys - 1) / kKeys;
     // (tile A's keys end at nt0, and no window begins behind it: far0 <= near0 <= nt0)
@@ -320,33 +356,41 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
         ++turn;
     };
     if (warp == kItemWarp) {
-        // ================= items (one thread) =================
-        if (lane == 0) {
-            unsigned index = blockIdx.x;
-            bool more = true;
-            for (int answers = 0; ok; ++answers) {
-                Item it;
-                it.any = 0;
-                if (more) it = make_item(p, index);
-                if (it.any || !more) {
-                    if (turn >= kSlots) ok = wait(&item_empty[turn % kSlots], (turn / kSlots - 1) & 1, s_abort);
-                    if (!ok) break;
+        // ================= items =================
+        Segments segments;
+        unsigned index = blockIdx.x;
+        bool more = true;
+        for (int answers = 0; ok; ++answers) {
+            Item it;
+            it.any = 0;
+            if (more) it = make_item(p, segments, index, lane);
+            if (it.any || !more) {
+                if (turn >= kSlots) ok = __all_sync(0xffffffffu, wait(&item_empty[turn % kSlots], (turn / kSlots - 1) & 1, s_abort));
+                if (!ok) break;
+                if (lane == 0) {
                     *reinterpret_cast<Item*>(reinterpret_cast<uint8_t*>(s_item) + turn % kSlots * 64) = it;
                     mbar_arrive(&item_full[turn % kSlots]);
-                    // no item is taken over before the last one's copies are all out: others may have nothing left
-                    if (more) ok = wait(wanted, turn & 1, s_abort);
-                    ++turn;
                 }
-                if (!more || !ok) break;
+                __syncwarp();
+                // no item is taken over before the last one's copies are all out: others may have nothing left
+                if (more) ok = __all_sync(0xffffffffu, wait(wanted, turn & 1, s_abort));
+                ++turn;
+            }
+            if (!more || !ok) break;
+            if (lane == 0) {
                 mbar_arrive_expect_tx(cta_full, 16);
                 ask_for_cta(s_answer, cta_full);
-                const bool there = mbar_wait_bounded(cta_full, answers & 1, kWaitNs);
-                more = there && got_cta(s_answer, index);
-                if (!there) *s_abort = 1;
-                fence_proxy_async_smem();  // the answer is read before the next one is written
             }
+            __syncwarp();
+            const bool there = __all_sync(0xffffffffu, mbar_wait_bounded(cta_full, answers & 1, kWaitNs));
+            more = there && got_cta(s_answer, index);
+            if (!there) *s_abort = 1;
+            fence_proxy_async_smem();  // the answer is read before the next one is written
+            __syncwarp();
         }
-        __syncwarp();
+        // the segments behind the last item are looked at too, for their errors, by one CTA
+        if (blockIdx.x == 0)
+            while (segments.first + 32 < p.nseq) segments.next(p, lane);
     } else if (warp >= kLoadKWarp) {
         // ================= copies: Q and K by one warp, V by the other, as far ahead as the rings allow =================
         const bool is_v = warp == kLoadVWarp;
@@ -784,7 +828,10 @@ static cudaError_t launch_d(const PrefillArgs& a, cudaStream_t stream) {
     p.sinks = a.sinks;
     p.negate = a.scale < 0.f;
     p.scale_log2 = std::max(std::min(std::fabs(a.scale) * kLog2e, 3.4e38f), kMinWindowScaleLog2);
-    const int64_t items = static_cast<int64_t>(p.tiles_per_seq) * a.nseq * a.Hq;
+    // no more row blocks than max_seqlen allows, nor than the tokens fill, one of each segment in part
+    const int64_t blocks = std::min<int64_t>(static_cast<int64_t>(p.tiles_per_seq) * a.nseq,
+                                             a.total_tokens / (2 * kRows) + static_cast<int64_t>(a.nseq));
+    const int64_t items = blocks * a.Hq;
     if (items > 2147483647LL) return cudaErrorInvalidConfiguration;
     return launch(prefill_window_kernel<D, kSplitP>, dim3(static_cast<unsigned>(items)), dim3(kThreads), Geo::kSmemBytes, stream, true, 1u, tq, tk,
                   tv, p);
