@@ -11,11 +11,13 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (KvcConfig, draft_tree_verify, kv_append, kv_append_rope, kv_block_alloc, kv_block_release,
-               kv_block_share, kv_cache_create, kv_cache_destroy, kv_copy_blocks, kv_rope_turns, kv_tree_commit,
-               kv_tree_masks, kvc_copy_async, kv_slot_mapping, kv_step_prepare, paged_decode_append_attention,
-               paged_decode_attention, paged_decode_plan, paged_decode_tree_attention, paged_decode_tree_plan,
-               paged_decode_workspace_init, prefill_attention)
+from . import (KvcConfig, draft_tree_verify, kv_append, kv_append_fp8_block, kv_append_rope, kv_block_alloc,
+               kv_block_release, kv_block_share, kv_block_tables, kv_cache_create, kv_cache_destroy, kv_copy_blocks,
+               kv_rope_turns, kv_tree_commit, kv_tree_masks, kvc_copy_async, kv_slot_mapping, kv_step_prepare,
+               paged_decode_append_attention, paged_decode_attention, paged_decode_attention_fp8_block,
+               paged_decode_fp8_block_plan, paged_decode_plan, paged_decode_tree_attention, paged_decode_tree_plan,
+               paged_decode_window_attention, paged_decode_window_plan, paged_decode_workspace_init, prefill_attention,
+               prefill_window_attention)
 
 F16_NAN = 0x7E00  # a quiet-NaN bit pattern used to poison cache slots nobody owns
 
@@ -283,6 +285,93 @@ class TreeSession:
             raise ValueError("the session's cache was destroyed")
         for call in self._calls:
             call(stream)
+
+    def close(self):
+        if self.h:
+            kv_cache_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class ServingSession:
+    """One layer of a serving loop whose request lengths stay on the GPU: prompts at once, then a token per sequence and
+    step, over an fp16 cache or (block8) a block-scaled 8-bit one, with a sliding window and sinks or without.
+
+    kv_block_tables places every step's tokens in blocks claimed from the library's pool (a windowed sequence goes
+    through its own in turn), so a step reads nothing on the host and can be captured into a graph: its inputs are q, k
+    and v, its output out."""
+
+    def __init__(self, B, Hq, Hkv, D, num_blocks, max_len, window=0, sinks=0, block8=False, device="cuda",
+                 out_dtype=torch.float16):
+        self.window, self.sinks, self.max_len, self.scale = window, sinks, max_len, D ** -0.5
+        f16, i32 = dict(dtype=torch.float16, device=device), dict(dtype=torch.int32, device=device)
+        cfg = KvcConfig(num_layers=1, num_blocks=num_blocks, num_kv_heads=Hkv, head_dim=D)
+        if block8:
+            self.codes = torch.full((num_blocks, Hkv, 2, 16, D), 0x7f, dtype=torch.uint8, device=device)
+            self.scales = torch.full((num_blocks, Hkv, 2), float("nan"), device=device)
+            self.h = kv_cache_create(cfg)  # the block pool alone
+        else:
+            self.codes = None
+            self.k_pool, self.v_pool = (poisoned_pool(cfg.pool_shape, device) for _ in range(2))
+            self.h = kv_cache_create(cfg, self.k_pool, self.v_pool)
+        self.free = torch.tensor([kv_block_alloc(self.h) for _ in range(num_blocks)], **i32)
+        self.placed, self.new_placed = torch.zeros(1, **i32), torch.zeros(1, **i32)
+        self.before, self.after = torch.zeros(B, **i32), torch.zeros(B, **i32)
+        self.table = torch.full((B, -(-max_len // 16)), -1, **i32)
+        self.cu, self.slots = torch.zeros(B + 1, **i32), torch.zeros(B, dtype=torch.int64, device=device)
+        self.q, self.k, self.v = torch.zeros(B, Hq, D, **f16), torch.zeros(B, Hkv, D, **f16), torch.zeros(B, Hkv, D, **f16)
+        self.out = torch.zeros(B, Hq, D, dtype=out_dtype, device=device)
+        plan = paged_decode_fp8_block_plan if block8 else paged_decode_window_plan
+        args = (B, Hq, Hkv, D, max_len)
+        ws = plan(*args, window=window, sinks=sinks) if block8 or window else paged_decode_plan(*args)[2]
+        self.workspace = torch.empty(max(ws, 16), dtype=torch.uint8, device=device)
+
+    def _append(self, k, v, slots):
+        if self.codes is not None:
+            kv_append_fp8_block(k, v, slots, self.codes, self.scales)
+        else:
+            kv_append(self.h, 0, k, v, slots)
+
+    def prompts(self, q, k, v, lens):
+        """Attention of every sequence's prompt (packed, lens rows each) and its rows in the cache."""
+        n = q.shape[0]
+        self.after.copy_(torch.as_tensor(np.asarray(lens, np.int32)))
+        slots = torch.zeros(n, dtype=torch.int64, device=q.device)
+        out = torch.zeros(q.shape, dtype=self.out.dtype, device=q.device)
+        kv_block_tables(None, self.after, self.free, self.placed, self.table, self.new_placed, self.cu, slots,
+                        window=self.window, sinks=self.sinks)
+        if self.window:
+            prefill_window_attention(q, k, v, self.cu, max(lens), self.window, self.sinks, self.scale, out)
+        else:
+            prefill_attention(q, k, v, self.cu, max(lens), self.scale, True, out)
+        self._append(k, v, slots)
+        self.placed.copy_(self.new_placed)
+        self.before.copy_(self.after)
+        return out
+
+    def step(self):
+        """One token of every sequence, from self.q, self.k and self.v to self.out (asynchronous)."""
+        torch.add(self.before, 1, out=self.after)
+        kv_block_tables(self.before, self.after, self.free, self.placed, self.table, self.new_placed, self.cu, self.slots,
+                        window=self.window, sinks=self.sinks)
+        if self.codes is not None:
+            self._append(self.k, self.v, self.slots)
+            paged_decode_attention_fp8_block(self.q, self.codes, self.scales, self.table, self.after, self.scale, self.out,
+                                             self.workspace, self.max_len, window=self.window, sinks=self.sinks)
+        elif self.window:
+            paged_decode_window_attention(self.q, self.k_pool[0], self.v_pool[0], self.table, self.after, self.window,
+                                          self.sinks, self.scale, self.out, self.workspace, self.max_len, k_new=self.k,
+                                          v_new=self.v)
+        else:
+            paged_decode_append_attention(self.q, self.k, self.v, self.k_pool[0], self.v_pool[0], self.table, self.after,
+                                          self.scale, self.out, self.workspace, self.max_len)
+        self.placed.copy_(self.new_placed)
+        self.before.copy_(self.after)
 
     def close(self):
         if self.h:

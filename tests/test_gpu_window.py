@@ -724,3 +724,102 @@ def test_prefill_captured_behind_the_tables():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+# ---------------------------------------------------------------- all of them together
+@pytest.mark.parametrize("block8", [False, True])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (20, 3), (33, 40)])
+@pytest.mark.parametrize("heads", [(14, 2, 64), (8, 2, 128)])
+def test_serving_prompts_and_steps(block8, window, sinks, heads):
+    """Prompts, then a captured step replayed 60 times: tables, cache contents and attention as the definitions have them,
+    step by step; a windowed sequence's blocks come round, and no more are taken."""
+    from paged_kv_cache_27_gb300.harness import ServingSession
+    Hq, Hkv, D = heads
+    lens, steps = [1, 70, 16, 47], 60
+    B, NB, most = len(lens), 64, 144
+    s = ServingSession(B, Hq, Hkv, D, NB, most, window, sinks, block8, out_dtype=torch.float32)
+    rng = np.random.default_rng(window + D)
+    free = s.free.cpu().numpy()
+    table, placed, before = np.full((B, most // BS), -1, np.int32), 0, None
+    codes, scales = np.full((NB, Hkv, 2, BS, D), 0x7f, np.uint8), np.full((NB, Hkv, 2), np.nan)
+    kv = np.full((NB, Hkv, 2, BS, D), np.nan)
+
+    def placed_rows(after, k, v):
+        nonlocal table, placed, before
+        table, placed, _, slots, _ = ow.block_tables(before, after, free, placed, table, window, sinks, len(k))
+        before = np.array(after)
+        if block8:
+            ow.append(k, v, slots, codes, scales)
+        for t, slot in enumerate(slots):
+            if slot >= 0:
+                kv[slot // BS, :, 0, slot % BS], kv[slot // BS, :, 1, slot % BS] = k[t], v[t]
+
+    def values(b, p):
+        x = kv if not block8 else ow.e4m3_values(codes) * scales[..., None, None]
+        x = x[table[b, p // BS], :, :, p % BS]
+        return x[:, :, 0], x[:, :, 1]
+
+    q, k, v, cu = packed(lens, heads, 31)
+    got = s.prompts(dev(q), dev(k), dev(v), lens)
+    ref = prefill_reference(q, k, v, lens, s.scale, window or 10 ** 6, sinks)
+    check_prefill(got, ref, q, k, v, s.scale, 100, False)
+    placed_rows(lens, k, v)
+    s.step()  # (a warm-up whose token stays)
+    zeros = [np.zeros((B, h, D), np.float16) for h in (Hkv, Hkv)]
+    placed_rows(before + 1, *zeros)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        s.step()
+    for step in range(steps):
+        q, k, v = (rng.standard_normal((B, h, D)).astype(np.float16) for h in (Hq, Hkv, Hkv))
+        for t, a in ((s.q, q), (s.k, k), (s.v, v)):
+            t.copy_(dev(a))
+        g.replay()
+        placed_rows(before + 1, k, v)
+        if step % 7 and step != steps - 1:
+            continue
+        np.testing.assert_array_equal(s.table.cpu().numpy(), table)
+        assert int(s.placed) == placed and np.array_equal(s.before.cpu().numpy(), before)
+        if block8:
+            used = ~np.isnan(scales)
+            np.testing.assert_array_equal(s.scales.cpu().numpy()[used], scales[used])
+            np.testing.assert_array_equal(s.codes.cpu().numpy()[used.any((1, 2))], codes[used.any((1, 2))])
+        values.ctx = before
+        ref = ow.decode(q, values, s.scale, window, sinks)
+        top = max(float(np.abs(q[b].astype(np.float64)).max(0) @ np.abs(values(b, ow.visible(int(before[b]), window, sinks))[0])
+                        .max((0, 1))) for b in range(B)) * s.scale
+        check(s.out, ref, min(top, 40.0), 6.0, most, D)
+    if window:
+        assert placed <= B * (ow.ring(window) + -(-sinks // BS))
+    assert kvc.kvc_device_error_flags(clear=True) == 0
+    s.close()
+
+
+def test_two_sessions_on_two_streams():
+    """Calls of both at once, each with its own tables, cache and workspace: as one after the other."""
+    from paged_kv_cache_27_gb300.harness import ServingSession
+    made = []
+    for block8, window in ((True, 0), (False, 50)):
+        def run(stream):
+            with torch.cuda.stream(stream):
+                s = ServingSession(3, 8, 2, 64, 200, 900, window, 4 if window else 0, block8)
+                q, k, v, cu = packed([800, 5, 300], (8, 2, 64), 41)
+                outs = [s.prompts(dev(q), dev(k), dev(v), [800, 5, 300])]
+                for i in range(20):
+                    for t, seed in ((s.q, 1), (s.k, 2), (s.v, 3)):
+                        t.copy_(dev(np.random.default_rng([i, seed]).standard_normal(t.shape).astype(np.float16)))
+                    s.step()
+                    outs.append(s.out.clone())
+            return s, outs
+        made.append(run)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    alone = []
+    for run, st in zip(made, streams):
+        alone.append(run(st)[1])
+        torch.cuda.synchronize()
+    together = [run(st) for run, st in zip(made, streams)]
+    torch.cuda.synchronize()
+    for a, (_, b) in zip(alone, together):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert kvc.kvc_device_error_flags(clear=True) == 0
