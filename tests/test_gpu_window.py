@@ -403,6 +403,55 @@ def test_offsets_beyond_32_bits():
         torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_largest_batch_and_group(fp8):
+    """65,535 sequences of one or two tokens in the same blocks; 64 query heads to a KV head."""
+    B, D = 65535, 64
+    rng = np.random.default_rng(61)
+    if fp8:
+        codes = rng.integers(0, 0x7e, (4, 1, 2, BS, D)).astype(np.uint8)
+        cache = dev(codes), torch.ones(4, 1, 2, device="cuda")
+        v = ow.e4m3_values(codes[:, 0, 1])
+    else:
+        kv = rng.standard_normal((2, 4, 1, BS, D)).astype(np.float16)
+        cache, v = (dev(kv[0]), dev(kv[1])), kv[1, :, 0].astype(np.float64)
+    table = rng.integers(0, 4, (B, 1)).astype(np.int32)
+    ctx = rng.integers(1, 3, B).astype(np.int32)
+    q, out = torch.zeros(B, 1, D, dtype=torch.float16, device="cuda"), torch.full((B, 1, D), 9.0, device="cuda")
+    args = (q, *cache, dev(table), dev(ctx))
+    if fp8:
+        assert kvc.paged_decode_fp8_block_plan(B, 1, 1, D, 16) == 0
+        kvc.paged_decode_attention_fp8_block(*args, 1.0, out, None, 16)
+    else:
+        assert kvc.paged_decode_window_plan(B, 1, 1, D, 16, 1) == 0
+        kvc.paged_decode_window_attention(*args, 1, 0, 1.0, out, None, 16)
+    t, n = table[:, 0], ctx[:, None]
+    want = np.where(n == 1, v[t, 0], (v[t, 0] + v[t, 1]) / 2 if fp8 else v[t, 1])
+    np.testing.assert_allclose(out[:, 0].cpu().numpy(), want, rtol=1e-6, atol=1e-6)
+    c = Case([100, 1, 33], (64, 1, 128), 40, 3, fp8, seed=62)
+    top, vmax = c.limits(0.1)
+    out = c.out()
+    c.run(0.1, out)
+    check(out, c.reference(0.1), top, vmax, 100, 128)
+    assert kvc.kvc_device_error_flags(clear=True) == 0
+
+
+def test_scales_that_no_append_writes():
+    """Scales of zero and of any positive value are taken as they are."""
+    c = Case([150, 40], (4, 2, 64), 0, 0, True, seed=63)
+    rng = np.random.default_rng(63)
+    scales = rng.uniform(0.001, 0.02, c.scales.shape).astype(np.float32)
+    scales[rng.random(scales.shape) < 0.2] = 0
+    c.values = ow.e4m3_values(c.codes) * scales.astype(np.float64)[..., None, None]
+    c.cache = c.cache[0], dev(np.where(np.isnan(c.cache[1].cpu().numpy()), np.nan, scales).astype(np.float32))
+    top, vmax = c.limits(0.3)
+    out = c.out()
+    c.run(0.3, out)
+    # (a scale that is no power of two: its product with the reference's reciprocal, and a rescaled accumulator, are
+    # rounded, 2^-24 each and at most once a pair of blocks)
+    check(out, c.reference(0.3), top, vmax, 150, 64, 2.0 ** -18)
+
+
 # ---------------------------------------------------------------- the block-scaled append
 def runs(lens, firsts, rng, blocks, skip=()):
     """Slots of runs of tokens, each from an offset `first` of a block of its own on; -1 between some."""
