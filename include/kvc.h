@@ -734,8 +734,8 @@ kvc_status kv_append_fp8_block(const void* k_new, int64_t k_stride, const void* 
  * paged_decode_fp8_block_plan's bytes for the same window and sinks.  Codes are
  * multiplied as they are: the K scale goes into the scores and the V scale into
  * the weights and, where scales of a context differ by more than 2^6, the
- * accumulators (exactly, for scales that are powers of two; others are taken
- * too).  Otherwise as paged_decode_window_attention. */
+ * accumulators (exactly, for scales that are powers of two).  A scale is 0 or
+ * from 2^-32 to 2^32.  Otherwise as paged_decode_window_attention. */
 kvc_status paged_decode_fp8_block_plan(int B, int Hq, int Hkv, int head_dim, int block_size, int max_context_len,
                                        int window, int sinks, size_t* workspace_bytes);
 kvc_status paged_decode_attention_fp8_block(const void* q, const void* codes, const float* scales, int num_blocks,
@@ -756,8 +756,8 @@ kvc_status prefill_window_attention(const void* q, const void* k, const void* v,
                                     int window, int sinks, int p_precision, void* out, int out_dtype, void* stream);
 
 /* The launching calls of this section and the one before with their arguments
- * as an array of 64-bit words, for bindings that pay per argument (a call from Python's
- * ctypes: 2.1 us for kv_append_rope's 26 arguments, 0.6 us this way).  words:
+ * as an array of 64-bit words, for bindings that pay per argument (a call from
+ * Python's ctypes: 2.1 us for kv_append_rope's 26 arguments, 0.6 us this way).  words:
  * the named call's `count` arguments in order without the stream, pointers and
  * integers as integers, a float as a double (addresses are taken as they are,
  * as in the named call itself).  KVC_ERR_INVALID for an unknown

@@ -1591,8 +1591,9 @@ kvc_status prefill_window_attention(const void* q, const void* k, const void* v,
                           {{q, qn * 2}, {k, kn * 2}, {v, kn * 2}, {cu_seqlens, (nseq + int64_t(1)) * 4}});
         if (s != KVC_OK) return s;
     }
-    return prefill_common(q, k, v, cu_seqlens, nseq, total_tokens, max_seqlen, Hq, Hkv, head_dim, scale, 1, window, sinks,
-                          p_precision, out, out_dtype, "prefill_window_attention launch", stream);
+    // (no segment is longer than all of the tokens, whatever max_seqlen says)
+    return prefill_common(q, k, v, cu_seqlens, nseq, total_tokens, std::min(max_seqlen, total_tokens), Hq, Hkv, head_dim,
+                          scale, 1, window, sinks, p_precision, out, out_dtype, "prefill_window_attention launch", stream);
 }
 
 kvc_status prefill_attention(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int nseq,

@@ -212,8 +212,9 @@ struct Segments {
         upto = __shfl_sync(0xffffffffu, behind, 31);
     }
 };
-// Item `index` (rising from one to the next, as CTAs are handed out; else the search begins anew): the head changes first, then the row block, from a segment's last one down
-// (its key list is the longest).  The whole warp; every lane gets it.
+// Item `index` (rising from one to the next, as CTAs are handed out; else the search begins anew): the head changes
+// first, then the row block, from a segment's last one down (its key list is the longest).  The whole warp; every lane
+// gets it.
 __device__ __forceinline__ Item make_item(const Params& p, Segments& s, unsigned index, int lane) {
     Item it;
     const int block = static_cast<int>(index / static_cast<unsigned>(p.Hq));

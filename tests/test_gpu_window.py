@@ -751,6 +751,17 @@ def test_prefill_bad_segments_are_flagged():
         kvc.kvc_set_checked_mode(False)
 
 
+def test_prefill_of_any_max_seqlen():
+    """max_seqlen may be as large as its type: no segment is longer than all tokens."""
+    q, k, v, cu = packed([60, 300], (2, 1, 64), 13)
+    want = run_prefill(q, k, v, cu, 0.125, 20, 2, torch.float32)
+    for most in (2 ** 31 - 1, 2 ** 31 - 200, 2 ** 30):
+        out = torch.zeros_like(want)
+        kvc.prefill_window_attention(dev(q), dev(k), dev(v), dev(cu), most, 20, 2, 0.125, out)
+        assert torch.equal(out, want)
+    assert kvc.kvc_device_error_flags(clear=True) == 0
+
+
 def test_prefill_captured_behind_the_tables():
     """cu_tokens of kv_block_tables are prefill's cu_seqlens; both captured into one graph."""
     lens = [130, 1, 260]
