@@ -361,6 +361,10 @@ class ServingSession:
                         window=self.window, sinks=self.sinks)
         if self.codes is not None:
             self._append(self.k, self.v, self.slots)
+        # (the copies also lie between the tables or the append and an attention launched with overlap)
+        self.placed.copy_(self.new_placed)
+        self.before.copy_(self.after)
+        if self.codes is not None:
             paged_decode_attention_fp8_block(self.q, self.codes, self.scales, self.table, self.after, self.scale, self.out,
                                              self.workspace, self.max_len, window=self.window, sinks=self.sinks)
         elif self.window:
@@ -370,8 +374,6 @@ class ServingSession:
         else:
             paged_decode_append_attention(self.q, self.k, self.v, self.k_pool[0], self.v_pool[0], self.table, self.after,
                                           self.scale, self.out, self.workspace, self.max_len)
-        self.placed.copy_(self.new_placed)
-        self.before.copy_(self.after)
 
     def close(self):
         if self.h:

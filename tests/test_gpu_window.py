@@ -856,6 +856,31 @@ def test_serving_prompts_and_steps(block8, window, sinks, heads):
     s.close()
 
 
+@pytest.mark.parametrize("block8,window", [(False, 0), (False, 50), (True, 0), (True, 50)])
+def test_session_with_launch_overlap(block8, window):
+    """With launch overlap on, a session's steps read what its tables and appends wrote."""
+    from paged_kv_cache_27_gb300.harness import ServingSession
+    lens, results = [400, 5, 300], []
+    q, k, v, cu = packed(lens, (8, 2, 64), 42)
+    try:
+        for on in (False, True):
+            kvc.kvc_set_launch_overlap(on)
+            s = ServingSession(3, 8, 2, 64, 120, 600, window, 4 if window else 0, block8)
+            outs = [s.prompts(dev(q), dev(k), dev(v), lens)]
+            for i in range(40):
+                for t, seed in ((s.q, 1), (s.k, 2), (s.v, 3)):
+                    t.copy_(dev(np.random.default_rng([i, seed]).standard_normal(t.shape).astype(np.float16)))
+                s.step()
+                outs.append(s.out.clone())
+            results.append(outs)
+            torch.cuda.synchronize()
+            s.close()
+    finally:
+        kvc.kvc_set_launch_overlap(False)
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    assert kvc.kvc_device_error_flags(clear=True) == 0
+
+
 def test_two_sessions_on_two_streams():
     """Calls of both at once, each with its own tables, cache and workspace: as one after the other."""
     from paged_kv_cache_27_gb300.harness import ServingSession
