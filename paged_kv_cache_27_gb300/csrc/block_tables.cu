@@ -12,7 +12,9 @@
 // Every CTA forms the prefix sums of tokens and blocks over all sequences by itself (a thread some consecutive ones,
 // then a scan over the threads) and knows from the totals whether the step fits, so that one launch without any
 // exchange is all or nothing; then it takes a share of the tokens, finds each one's sequence by bisection, and writes
-// its slot and position, and the token that starts a block also the table's entry.
+// its slot and position, and the token that starts a block also the table's entry.  Bound by launch and dependent loads,
+// not by bytes: 256 sequences' next tokens take 2.7 us, 128 prompts of up to 8192 tokens 6.5 (where their slots and
+// entries alone would be 1.1): the sums, then a bisection and three loads that follow one another for each token.
 #include "../../include/kvc.h"
 #include "decode_common.cuh"
 #include "kvc_internal.h"
