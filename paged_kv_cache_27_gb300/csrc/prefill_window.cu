@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
         for (;; item_done()) {
             ok = ok && next_item();
             if (!ok) break;
-            const Item& it = slot_item(turn % kSlots);
+            const Item it = slot_item(turn % kSlots);
             if (!it.any) break;
             if (!is_v) {
                 if (done > 0) ok = __all_sync(0xffffffffu, wait(q_empty, (done - 1) & 1, s_abort));
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
             for (;; item_done()) {
                 ok = ok && next_item();
                 if (!ok) break;
-                const Item& it = slot_item(turn % kSlots);
+                const Item it = slot_item(turn % kSlots);
                 if (!it.any) break;
                 ok = wait_all(q_full, done & 1, s_abort);
                 if (!ok) break;
@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
             for (;; item_done()) {
                 ok = ok && next_item();
                 if (!ok) break;
-                const Item& it = slot_item(turn % kSlots);
+                const Item it = slot_item(turn % kSlots);
                 if (!it.any) break;
                 const int first = it.begin(x), end = it.end[x];
                 for (int j = 0; j < it.entries; ++j) {
@@ -607,120 +607,131 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
             if (it.end[x] == 0) continue;
             const int rx = it.r0 + x * kRows;           // first row of the row tile
             const int qi = rx + wq * 32 + lane;         // row of the segment
-            const int first = it.begin(x), end = it.end[x];
+            const int keys_end = min(qi + 1, it.len);  // of this row
             float m_used = -INFINITY, l = 0.f;
             bool far = false;  // some row of the warp has its m beyond kFar
-            for (int j = first; ok && j < end; ++j) {
-                const int units = it.units(j), tile0 = it.key_tile(j) * kKeys;
-                for (int half = 0; half < units; ++half, ++uc) {
-                    const int buf = 2 * x + (uc & 1);
-                    const uint32_t tS = tmem + buf * kHalf + lane_base;
-                    const int k0 = tile0 + half * kHalf;  // the unit's first key
-                    // units that every row of the tile sees need no mask
-                    const bool masked = k0 + kHalf - 1 > rx || k0 + kHalf > it.len ||
-                                        (k0 <= rx + kRows - 1 - p.window && k0 + kHalf > p.sinks);
-                    uint32_t bits[2] = {~0u, ~0u};
-                    if (masked) {
-                        bits[0] = window_bits(qi, k0, it.len, p.window, p.sinks);
-                        bits[1] = window_bits(qi, k0 + 32, it.len, p.window, p.sinks);
-                    }
-                    ok = __all_sync(0xffffffffu, wait(&s_full[buf], (uc >> 1) & 1, s_abort));
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (masked && !__any_sync(0xffffffffu, (bits[0] | bits[1]) != 0)) {  // nothing for these 32 rows
-                        float zero[32] = {};
-                        tmem_st32(tS, zero);
-                        if constexpr (kSplitP) tmem_st32(tS + 32, zero);
-                    } else {
-                        float s[kHalf];
-                        tmem_ld64(tS, s);
-                        if (p.negate) {
-#pragma unroll
-                            for (int c = 0; c < kHalf; ++c) s[c] = -s[c];
-                        }
-                        if (masked) mask_scores(s, bits, -INFINITY);
-                        float e[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) e[i] = max3f(s[i], s[4 + i], s[8 + i]);
-#pragma unroll
-                        for (int c = 12; c + 8 <= kHalf; c += 8)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) e[i] = max3f(e[i], s[c + i], s[c + 4 + i]);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) e[i] = fmaxf(e[i], s[kHalf - 4 + i]);
-                        const float mx = __fmul_rd(max3f(e[0], e[1], fmaxf(e[2], e[3])), sl2);  // -inf: nothing seen
-                        float alpha = 1.f;
-                        if (mx > m_used + kRescaleLog2) {  // includes the first finite max (m_used = -inf)
-                            const float m_new = __fsub_rd(mx, kWeightLog2);
-                            alpha = m_used == -INFINITY ? 0.f : ex2(m_used - m_new);
-                            m_used = m_new;
-                        }
-                        if (__any_sync(0xffffffffu, alpha != 1.f)) {
-                            if constexpr (kSplitP) far = __any_sync(0xffffffffu, fabsf(m_used) >= kFar && m_used != -INFINITY);
-                            // rescale O_X, which idles once the stream's previous product is complete (this unit's P is
-                            // not there yet)
-                            if (j > first || half > 0) {
-                                ok = __all_sync(0xffffffffu, wait(&o_full[buf ^ 1], ((uc - 1) >> 1) & 1, s_abort));
-                                if (!ok) break;
-                                tc_fence_after();
-#pragma unroll 1
-                                for (int c = 0; c < D; c += 32) {
-                                    float o[32];
-                                    tmem_ld32(tO + c, o);
-#pragma unroll
-                                    for (int i = 0; i < 32; ++i) o[i] *= alpha;
-                                    tmem_st32(tO + c, o);
-                                }
-                                if constexpr (Geo::kSumProduct) {  // (the one column that is read)
-                                    float sum[4];
-                                    tmem_ld4(tL, sum);
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) sum[i] *= alpha;
-                                    tmem_st4(tL, sum);
-                                }
-                            }
-                        }
-                        const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
-                        float ls[4] = {0.f, 0.f, 0.f, 0.f};
-                        uint64_t by2 = sc2, nm2 = pack_f32x2(neg_m, neg_m);
-                        if (kSplitP && far) {
-#pragma unroll
-                            for (int c = 0; c < kHalf; ++c) {
-                                const float d = fmaf(s[c], sl2, neg_m);
-                                s[c] = d > kRescaleLog2 ? kRescaleLog2 : d;
-                            }
-                            by2 = pack_f32x2(1.f, 1.f);
-                            nm2 = 0;
-                        }
-#pragma unroll
-                        for (int hh = 0; hh < 2; ++hh) {  // 32 keys at a time
-                            uint32_t hv[16], lv[16];
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const int c = hh * 32 + 2 * i;
-                                float x0, x1;
-                                unpack_f32x2(fma_f32x2(pack_f32x2(s[c], s[c + 1]), by2, nm2), x0, x1);
-                                x0 = ex2(x0);
-                                x1 = ex2(x1);
-                                hv[i] = kSplitP ? pack_half2(x0, x1) : pack_half2_finite(x0, x1);
-                                if constexpr (kSplitP) {
-                                    const float2 f = unpack_half2(hv[i]);
-                                    lv[i] = pack_half2(x0 - f.x, x1 - f.y);
-                                    if (!Geo::kSumProduct) ls[i & 3] += x0 + x1;
-                                } else if (!Geo::kSumProduct) {
-                                    ls[i & 3] = add_halves(hv[i], ls[i & 3]);
-                                }
-                            }
-                            tmem_st16(tS + hh * 16, hv);
-                            if constexpr (kSplitP) tmem_st16(tS + kHalf / 2 + hh * 16, lv);
-                        }
-                        if (!Geo::kSumProduct) l = l * alpha + ((ls[0] + ls[1]) + (ls[2] + ls[3]));
-                    }
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_full[buf]);
+            // The list's three stretches of keys, a unit at a time; what an item says is read where one ends, not for
+            // every unit (a unit's loads from shared memory and what hung on them were 300 of its 1600 clocks)
+            const int uc0 = uc;
+            int part = x == 0 ? -1 : 0, k0 = 0, stop = 0;  // the unit's first key
+            auto next_part = [&]() {
+                while (k0 == stop && ++part < 3) {
+                    const int sinks_end = it.sink_tiles * kKeys - (it.narrow >= 0 ? kHalf : 0);
+                    k0 = part == 0 ? it.far0 * kKeys : part == 1 ? 0 : it.near0 * kKeys;
+                    stop = part == 0   ? (it.far0 + it.lead) * kKeys
+                           : part == 1 ? sinks_end
+                                       : (it.near0 + it.end[x] - it.lead - it.sink_tiles) * kKeys;
                 }
+                return k0 != stop;
+            };
+            for (bool left = next_part(); left; ++uc) {
+                const int buf = 2 * x + (uc & 1);
+                const uint32_t tS = tmem + buf * kHalf + lane_base;
+                // units that every row of the tile sees need no mask
+                const bool masked = k0 + kHalf - 1 > rx || (k0 <= rx + kRows - 1 - p.window && k0 + kHalf > p.sinks);
+                uint32_t bits[2] = {~0u, ~0u};
+                if (masked) {
+                    bits[0] = window_bits(qi, k0, keys_end, p.window, p.sinks);
+                    bits[1] = window_bits(qi, k0 + 32, keys_end, p.window, p.sinks);
+                }
+                ok = __all_sync(0xffffffffu, wait(&s_full[buf], (uc >> 1) & 1, s_abort));
+                if (!ok) break;
+                tc_fence_after();
+                if (masked && !__any_sync(0xffffffffu, (bits[0] | bits[1]) != 0)) {  // nothing for these 32 rows
+                    float zero[32] = {};
+                    tmem_st32(tS, zero);
+                    if constexpr (kSplitP) tmem_st32(tS + 32, zero);
+                } else {
+                    float s[kHalf];
+                    tmem_ld64(tS, s);
+                    if (p.negate) {
+#pragma unroll
+                        for (int c = 0; c < kHalf; ++c) s[c] = -s[c];
+                    }
+                    if (masked) mask_scores(s, bits, -INFINITY);
+                    float e[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) e[i] = max3f(s[i], s[4 + i], s[8 + i]);
+#pragma unroll
+                    for (int c = 12; c + 8 <= kHalf; c += 8)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) e[i] = max3f(e[i], s[c + i], s[c + 4 + i]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) e[i] = fmaxf(e[i], s[kHalf - 4 + i]);
+                    const float mx = __fmul_rd(max3f(e[0], e[1], fmaxf(e[2], e[3])), sl2);  // -inf: nothing seen
+                    float alpha = 1.f;
+                    if (mx > m_used + kRescaleLog2) {  // includes the first finite max (m_used = -inf)
+                        const float m_new = __fsub_rd(mx, kWeightLog2);
+                        alpha = m_used == -INFINITY ? 0.f : ex2(m_used - m_new);
+                        m_used = m_new;
+                    }
+                    if (__any_sync(0xffffffffu, alpha != 1.f)) {
+                        if constexpr (kSplitP) far = __any_sync(0xffffffffu, fabsf(m_used) >= kFar && m_used != -INFINITY);
+                        // rescale O_X, which idles once the stream's previous product is complete (this unit's P is
+                        // not there yet)
+                        if (uc != uc0) {
+                            ok = __all_sync(0xffffffffu, wait(&o_full[buf ^ 1], ((uc - 1) >> 1) & 1, s_abort));
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 32) {
+                                float o[32];
+                                tmem_ld32(tO + c, o);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) o[i] *= alpha;
+                                tmem_st32(tO + c, o);
+                            }
+                            if constexpr (Geo::kSumProduct) {  // (the one column that is read)
+                                float sum[4];
+                                tmem_ld4(tL, sum);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) sum[i] *= alpha;
+                                tmem_st4(tL, sum);
+                            }
+                        }
+                    }
+                    const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
+                    float ls[4] = {0.f, 0.f, 0.f, 0.f};
+                    uint64_t by2 = sc2, nm2 = pack_f32x2(neg_m, neg_m);
+                    if (kSplitP && far) {
+#pragma unroll
+                        for (int c = 0; c < kHalf; ++c) {
+                            const float d = fmaf(s[c], sl2, neg_m);
+                            s[c] = d > kRescaleLog2 ? kRescaleLog2 : d;
+                        }
+                        by2 = pack_f32x2(1.f, 1.f);
+                        nm2 = 0;
+                    }
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {  // 32 keys at a time
+                        uint32_t hv[16], lv[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int c = hh * 32 + 2 * i;
+                            float x0, x1;
+                            unpack_f32x2(fma_f32x2(pack_f32x2(s[c], s[c + 1]), by2, nm2), x0, x1);
+                            x0 = ex2(x0);
+                            x1 = ex2(x1);
+                            hv[i] = kSplitP ? pack_half2(x0, x1) : pack_half2_finite(x0, x1);
+                            if constexpr (kSplitP) {
+                                const float2 f = unpack_half2(hv[i]);
+                                lv[i] = pack_half2(x0 - f.x, x1 - f.y);
+                                if (!Geo::kSumProduct) ls[i & 3] += x0 + x1;
+                            } else if (!Geo::kSumProduct) {
+                                ls[i & 3] = add_halves(hv[i], ls[i & 3]);
+                            }
+                        }
+                        tmem_st16(tS + hh * 16, hv);
+                        if constexpr (kSplitP) tmem_st16(tS + kHalf / 2 + hh * 16, lv);
+                    }
+                    if (!Geo::kSumProduct) l = l * alpha + ((ls[0] + ls[1]) + (ls[2] + ls[3]));
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[buf]);
+                k0 += kHalf;
+                left = k0 != stop || next_part();
             }
             if (ok) ok = __all_sync(0xffffffffu, wait(&o_full[2 * x + ((uc - 1) & 1)], ((uc - 1) >> 1) & 1, s_abort));
             if (!ok) break;

@@ -10,9 +10,8 @@ namespace kvc {
 // The n lowest of 32 bits.
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
 
-// Bit i: key k0 + i is visible to row qi of a segment of len rows.
-__device__ __forceinline__ uint32_t window_bits(int qi, int k0, int len, int window, int sinks) {
-    const int end = min(qi + 1, len);
+// Bit i: key k0 + i is visible to row qi, whose keys end at `end` (behind its own, or at its segment's end).
+__device__ __forceinline__ uint32_t window_bits(int qi, int k0, int end, int window, int sinks) {
     return (low_bits(end - k0) & ~low_bits(qi - window + 1 - k0)) | low_bits(min(sinks, end) - k0);
 }
 
