@@ -146,6 +146,11 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
         }
     }
 }
+// The same for a whole warp: one vote and one branch where the phase is over already.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, wait(bar, parity, abort_flag));
+}
 // The same for a whole warp whose waits sit between two products: without the hint of a long sleep.  (Polling took issue
 // slots from the row warps: 266 against 257 us at 4 x 4096 tokens, window 1024, 32 / 8 heads, D = 128.)
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
@@ -634,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
                     bits[0] = window_bits(qi, k0, keys_end, p.window, p.sinks);
                     bits[1] = window_bits(qi, k0 + 32, keys_end, p.window, p.sinks);
                 }
-                ok = __all_sync(0xffffffffu, wait(&s_full[buf], (uc >> 1) & 1, s_abort));
+                ok = wait_warp(&s_full[buf], (uc >> 1) & 1, s_abort);
                 if (!ok) break;
                 tc_fence_after();
                 if (masked && !__any_sync(0xffffffffu, (bits[0] | bits[1]) != 0)) {  // nothing for these 32 rows
@@ -644,11 +649,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
                 } else {
                     float s[kHalf];
                     tmem_ld64(tS, s);
-                    if (p.negate) {
+                    if (masked || p.negate) {
+                        if (p.negate) {
 #pragma unroll
-                        for (int c = 0; c < kHalf; ++c) s[c] = -s[c];
+                            for (int c = 0; c < kHalf; ++c) s[c] = -s[c];
+                        }
+                        mask_scores(s, bits, -INFINITY);
                     }
-                    if (masked) mask_scores(s, bits, -INFINITY);
                     float e[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) e[i] = max3f(s[i], s[4 + i], s[8 + i]);
@@ -659,13 +666,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
 #pragma unroll
                     for (int i = 0; i < 4; ++i) e[i] = fmaxf(e[i], s[kHalf - 4 + i]);
                     const float mx = __fmul_rd(max3f(e[0], e[1], fmaxf(e[2], e[3])), sl2);  // -inf: nothing seen
-                    float alpha = 1.f;
-                    if (mx > m_used + kRescaleLog2) {  // includes the first finite max (m_used = -inf)
-                        const float m_new = __fsub_rd(mx, kWeightLog2);
-                        alpha = m_used == -INFINITY ? 0.f : ex2(m_used - m_new);
+                    const bool moves = mx > m_used + kRescaleLog2;  // includes the first finite max (m_used = -inf)
+                    if (__any_sync(0xffffffffu, moves)) {
+                        const float m_new = moves ? __fsub_rd(mx, kWeightLog2) : m_used;
+                        const float alpha = !moves ? 1.f : m_used == -INFINITY ? 0.f : ex2(m_used - m_new);
                         m_used = m_new;
-                    }
-                    if (__any_sync(0xffffffffu, alpha != 1.f)) {
+                        l *= alpha;
                         if constexpr (kSplitP) far = __any_sync(0xffffffffu, fabsf(m_used) >= kFar && m_used != -INFINITY);
                         // rescale O_X, which idles once the stream's previous product is complete (this unit's P is
                         // not there yet)
@@ -724,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
                         tmem_st16(tS + hh * 16, hv);
                         if constexpr (kSplitP) tmem_st16(tS + kHalf / 2 + hh * 16, lv);
                     }
-                    if (!Geo::kSumProduct) l = l * alpha + ((ls[0] + ls[1]) + (ls[2] + ls[3]));
+                    if (!Geo::kSumProduct) l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
                 }
                 tmem_wait_st();
                 tc_fence_before();
