@@ -78,7 +78,7 @@ struct Geom {
     static constexpr int kOnesBytes = kSumProduct ? kHalf * 128 : 0;
     static constexpr int kBarOff = kOnesOff + kOnesBytes;
     static constexpr int kItemOff = kBarOff + 512;  // barriers, TMEM address, flag; then the items
-    static constexpr int kSmemBytes = kItemOff + 256 + 1024;  // alignment
+    static constexpr int kSmemBytes = kItemOff + 384 + 1024;  // alignment
     static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
     // TMEM columns: two buffers of S / P per stream, A [0, 128) and B [128, 256), then O_A and O_B, D columns each
     static constexpr int kTmemO = 4 * kHalf;
@@ -95,6 +95,7 @@ struct Params {
     unsigned* err;
     int nseq, total_tokens, tiles_per_seq, Hq, Hkv, G, out_f32, window, sinks;
     int negate;        // the scale is negative
+    int out_wide;      // out is aligned to 32 bytes
     float scale_log2;  // |scale| * log2 e, at least kMinWindowScaleLog2
 };
 
@@ -107,6 +108,18 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* m
         " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
         : "memory");
+}
+// 32 bytes of a row of the output, at once where they are aligned to it (a row per lane: an instruction takes as long for
+// 16 bytes of each)
+__device__ __forceinline__ void store_32(void* at, const uint32_t (&w)[8], bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        static_cast<uint4*>(at)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4*>(at)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
 }
 // acc + the two fp16 halves of h (each converted exactly), as two rounded fp32 additions
 __device__ __forceinline__ float add_halves(uint32_t h, float acc) {
@@ -174,13 +187,15 @@ struct Item {
     int lead, sink_tiles, far0, near0, end[2], entries;
     int narrow;  // the entry of which the first unit alone holds visible keys, or -1
     int any;     // 0: the last one was before this
+    int2 part[2][3];  // the same list in keys, for either stream: from, to
     __device__ __forceinline__ int key_tile(int j) const {
         return j < lead ? far0 + j : j < lead + sink_tiles ? j - lead : near0 + j - lead - sink_tiles;
     }
     __device__ __forceinline__ int begin(int x) const { return x == 0 ? 0 : lead; }
     __device__ __forceinline__ int units(int j) const { return j == narrow ? 1 : 2; }
 };
-static_assert(sizeof(Item) <= 64, "items in shared memory");
+constexpr int kItemBytes = 128;
+static_assert(sizeof(Item) <= kItemBytes, "items in shared memory");
 // Row blocks of 256 rows that a segment has; its first row and its length.
 __device__ __forceinline__ int row_blocks(const Params& p, int seg, int& beg, int& len, bool& bad) {
     beg = p.cu_seqlens[seg];
@@ -246,6 +261,12 @@ __device__ __forceinline__ Item make_item(const Params& p, Segments& s, unsigned
     // the sinks' last tile: no row has its window begin in it, and its second half holds no sink
     const int k0 = (it.sink_tiles - 1) * kKeys;
     it.narrow = it.sink_tiles > 0 && k0 + kKeys - 1 <= it.r0 - p.window && p.sinks <= k0 + kHalf ? it.lead + it.sink_tiles - 1 : -1;
+    const int2 sinks = make_int2(0, it.sink_tiles * kKeys - (it.narrow >= 0 ? kHalf : 0));
+    it.part[0][0] = make_int2(it.far0 * kKeys, it.near0 * kKeys);
+    it.part[0][1] = it.part[1][1] = sinks;
+    it.part[0][2] = make_int2(it.near0 * kKeys, nt0 * kKeys);
+    it.part[1][0] = make_int2(0, 0);
+    it.part[1][2] = make_int2(it.near0 * kKeys, two ? nt1 * kKeys : it.near0 * kKeys);
     return it;
 }
 
@@ -300,10 +321,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(wanted + 1);
     volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
     static_assert((2 + 2 * KS + 2 * VS + 17 + 2 * kSlots + 2) * 8 + 8 <= 512, "barrier area");
-    Item* const s_item = reinterpret_cast<Item*>(smem + Geo::kItemOff);            // [kSlots], 64 bytes each
-    void* const s_answer = smem + Geo::kItemOff + kSlots * 64;
+    Item* const s_item = reinterpret_cast<Item*>(smem + Geo::kItemOff);            // [kSlots], kItemBytes each
+    void* const s_answer = smem + Geo::kItemOff + kSlots * kItemBytes;
     auto slot_item = [&](uint32_t slot) -> const Item& {
-        return *reinterpret_cast<const Item*>(reinterpret_cast<const uint8_t*>(s_item) + slot * 64);
+        return *reinterpret_cast<const Item*>(reinterpret_cast<const uint8_t*>(s_item) + slot * kItemBytes);
     };
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
@@ -374,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
                 if (turn >= kSlots) ok = __all_sync(0xffffffffu, wait(&item_empty[turn % kSlots], (turn / kSlots - 1) & 1, s_abort));
                 if (!ok) break;
                 if (lane == 0) {
-                    *reinterpret_cast<Item*>(reinterpret_cast<uint8_t*>(s_item) + turn % kSlots * 64) = it;
+                    *reinterpret_cast<Item*>(reinterpret_cast<uint8_t*>(s_item) + turn % kSlots * kItemBytes) = it;
                     mbar_arrive(&item_full[turn % kSlots]);
                 }
                 __syncwarp();
@@ -618,14 +639,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
             // The list's three stretches of keys, a unit at a time; what an item says is read where one ends, not for
             // every unit (a unit's loads from shared memory and what hung on them were 300 of its 1600 clocks)
             const int uc0 = uc;
-            int part = x == 0 ? -1 : 0, k0 = 0, stop = 0;  // the unit's first key
+            int part = x, k0 = 0, stop = 0;  // k0: the unit's first key
             auto next_part = [&]() {
-                while (k0 == stop && ++part < 3) {
-                    const int sinks_end = it.sink_tiles * kKeys - (it.narrow >= 0 ? kHalf : 0);
-                    k0 = part == 0 ? it.far0 * kKeys : part == 1 ? 0 : it.near0 * kKeys;
-                    stop = part == 0   ? (it.far0 + it.lead) * kKeys
-                           : part == 1 ? sinks_end
-                                       : (it.near0 + it.end[x] - it.lead - it.sink_tiles) * kKeys;
+                while (k0 == stop && part < 3) {
+                    const int2 keys = it.part[x][part++];
+                    k0 = keys.x;
+                    stop = keys.y;
                 }
                 return k0 != stop;
             };
@@ -755,18 +774,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
                 tmem_ld32(tO + c, o);
                 if (qi < it.len) {
                     if (p.out_f32) {
-                        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + row0 + c);
+                        float* dst = static_cast<float*>(p.out) + row0 + c;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            dst[i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(o[8 * i + k] * inv);
+                            store_32(dst + 8 * i, w, p.out_wide);
+                        }
                     } else {
-                        uint4* dst = reinterpret_cast<uint4*>(static_cast<__half*>(p.out) + row0 + c);
+                        __half* dst = static_cast<__half*>(p.out) + row0 + c;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            dst[i] = make_uint4(pack_half2(o[8 * i] * inv, o[8 * i + 1] * inv),
-                                                pack_half2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                                pack_half2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                                pack_half2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) w[k] = pack_half2(o[16 * i + 2 * k] * inv, o[16 * i + 2 * k + 1] * inv);
+                            store_32(dst + 16 * i, w, p.out_wide);
+                        }
                     }
                 }
                 float t = 0.f;
@@ -845,6 +869,7 @@ static cudaError_t launch_d(const PrefillArgs& a, cudaStream_t stream) {
     p.window = a.window;
     p.sinks = a.sinks;
     p.negate = a.scale < 0.f;
+    p.out_wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
     p.scale_log2 = std::max(std::min(std::fabs(a.scale) * kLog2e, 3.4e38f), kMinWindowScaleLog2);
     // no more row blocks than max_seqlen allows, nor than the tokens fill, one of each segment in part
     const int64_t blocks = std::min<int64_t>(static_cast<int64_t>(p.tiles_per_seq) * a.nseq,

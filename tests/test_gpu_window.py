@@ -751,6 +751,22 @@ def test_prefill_bad_segments_are_flagged():
         kvc.kvc_set_checked_mode(False)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefill_outputs_aligned_to_16_bytes(D, dtype):
+    """An output that begins 16 bytes behind a 32-byte boundary, or on one: the same values, nothing beside them."""
+    q, k, v, cu = packed([60, 300], (2, 1, D), 14)
+    want = run_prefill(q, k, v, cu, 0.125, 20, 2, dtype)
+    step = 16 // want.element_size()
+    for shift in (0, step, 2 * step, 3 * step):
+        room = torch.full((want.numel() + 4 * step,), 5.0, dtype=dtype, device="cuda")
+        out = room[shift:shift + want.numel()].view(want.shape)
+        kvc.prefill_window_attention(dev(q), dev(k), dev(v), dev(cu), 300, 20, 2, 0.125, out)
+        assert torch.equal(out, want)
+        assert (room[:shift] == 5).all() and (room[shift + want.numel():] == 5).all()
+    assert kvc.kvc_device_error_flags(clear=True) == 0
+
+
 def test_prefill_of_any_max_seqlen():
     """max_seqlen may be as large as its type: no segment is longer than all tokens."""
     q, k, v, cu = packed([60, 300], (2, 1, 64), 13)
