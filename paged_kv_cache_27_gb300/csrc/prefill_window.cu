@@ -688,13 +688,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
                     const bool moves = mx > m_used + kRescaleLog2;  // includes the first finite max (m_used = -inf)
                     if (__any_sync(0xffffffffu, moves)) {
                         const float m_new = moves ? __fsub_rd(mx, kWeightLog2) : m_used;
-                        const float alpha = !moves ? 1.f : m_used == -INFINITY ? 0.f : ex2(m_used - m_new);
+                        // (a row that had seen nothing has no weights in O and its sum)
+                        const bool grows = moves && m_used != -INFINITY;
+                        const float alpha = grows ? ex2(m_used - m_new) : 1.f;
                         m_used = m_new;
                         l *= alpha;
                         if constexpr (kSplitP) far = __any_sync(0xffffffffu, fabsf(m_used) >= kFar && m_used != -INFINITY);
-                        // rescale O_X, which idles once the stream's previous product is complete (this unit's P is
-                        // not there yet)
-                        if (uc != uc0) {
+                        // rescale O_X, which idles once the stream's previous product is complete (this unit's P is not
+                        // there yet)
+                        if (uc != uc0 && __any_sync(0xffffffffu, grows)) {
                             ok = __all_sync(0xffffffffu, wait(&o_full[buf ^ 1], ((uc - 1) >> 1) & 1, s_abort));
                             if (!ok) break;
                             tc_fence_after();
