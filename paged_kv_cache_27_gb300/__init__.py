@@ -807,6 +807,7 @@ def kv_rope_turns(inv_freq) -> np.ndarray:
 
 
 _F16, _F32, _I32, _I64 = torch.float16, torch.float32, torch.int32, torch.int64
+_U8, _E4M3 = torch.uint8, torch.float8_e4m3fn
 # the current device's index (the underscored form skips a wrapper, 0.1 µs a call)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
@@ -1166,7 +1167,7 @@ def kv_block_tables(lens_before: Optional[torch.Tensor], lens_after: torch.Tenso
 
 def _code_dtype(codes: torch.Tensor):
     """Codes come as torch.float8_e4m3fn or as their bytes."""
-    if not isinstance(codes, torch.Tensor) or codes.dtype not in (torch.float8_e4m3fn, torch.uint8):
+    if not isinstance(codes, torch.Tensor) or codes.dtype not in (_E4M3, _U8):
         raise TypeError("codes must be a torch.float8_e4m3fn or torch.uint8 tensor")
     return codes.dtype
 
@@ -1222,18 +1223,15 @@ def paged_decode_fp8_block_plan(B: int, Hq: int, Hkv: int, head_dim: int, max_co
     return ws.value
 
 
-def _decode_shapes(qshape, block_table, context_lens, out):
-    """max_blocks and the output type of a decode call whose q, tables, lengths and out agree."""
-    if out.shape != qshape:
+def _check_decode_shapes(q, block_table, context_lens, out) -> None:
+    """q, tables, lengths and out of a decode call agree."""
+    if out.shape != q.shape:
         raise ValueError("out must have q's shape")
     tshape = block_table.shape
-    if len(tshape) != 2 or tshape[0] != qshape[0] or context_lens.numel() != qshape[0]:
+    if len(tshape) != 2 or tshape[0] != q.shape[0] or context_lens.numel() != q.shape[0]:
         raise ValueError("block_table / context_lens do not match B")
-    odt = out.dtype
-    od = KVC_F16 if odt is _F16 else KVC_F32 if odt is _F32 else None
-    if od is None:
+    if out.dtype not in (_F16, _F32):
         raise TypeError("out must be float16 or float32")
-    return tshape[1], od, odt
 
 
 def paged_decode_attention_fp8_block(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
@@ -1243,22 +1241,32 @@ def paged_decode_attention_fp8_block(q: torch.Tensor, codes: torch.Tensor, scale
     """paged_decode_attention over a block-scaled cache layer (codes and scales as kv_append_fp8_block writes them), of
     all of a context (window 0) or of its newest `window` and first `sinks` positions; workspace:
     paged_decode_fp8_block_plan bytes.  prepare=True returns a PreparedCall instead of launching."""
-    qshape = q.shape
+    qshape, cshape, tshape = q.shape, codes.shape, block_table.shape
     B, Hq, D = qshape
-    NB, Hkv, bs = _code_shape(codes, scales, D)
-    max_blocks, od, odt = _decode_shapes(qshape, block_table, context_lens, out)
-    dt = _code_dtype(codes)
+    dt, odt = codes.dtype, out.dtype
     keep = (q, codes, scales, block_table, context_lens, out, workspace)
     dev = q.get_device()
-    if not (dev >= 0 and dev == _current_device() and _ready(dev, _F16, q) and _ready(dev, dt, codes)
-            and _ready(dev, _F32, scales) and _ready(dev, _I32, block_table, context_lens)
-            and _ready(dev, odt, out) and (workspace is None or _ready(dev, workspace.dtype, workspace))):
+    # the common case in one expression, written out (a call per tensor takes half as long again); the checks below only
+    # name the failure
+    if not (len(cshape) == 5 and len(tshape) == 2 and cshape[2] == 2 and cshape[4] == D and tshape[0] == B
+            and scales.shape == (cshape[0], cshape[1], 2) and out.shape == qshape and context_lens.nbytes == 4 * B
+            and dev >= 0 and dev == _current_device() and q.dtype is _F16 and (dt is _E4M3 or dt is _U8)
+            and scales.dtype is _F32 and block_table.dtype is _I32 and context_lens.dtype is _I32
+            and (odt is _F16 or odt is _F32)
+            and dev == codes.get_device() == scales.get_device() == block_table.get_device()
+            == context_lens.get_device() == out.get_device()
+            and q.is_contiguous() and codes.is_contiguous() and scales.is_contiguous() and block_table.is_contiguous()
+            and context_lens.is_contiguous() and out.is_contiguous()
+            and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous()))):
+        _code_shape(codes, scales, D)
+        _check_decode_shapes(q, block_table, context_lens, out)
+        dt = _code_dtype(codes)
         _check_all(keep, (q, _F16, "q"), (codes, dt, "codes"), (scales, _F32, "scales"),
                    (block_table, _I32, "block_table"), (context_lens, _I32, "context_lens"), (out, None, "out"),
                    (workspace, None, "workspace"))
-    args = (q.data_ptr(), codes.data_ptr(), scales.data_ptr(), NB, block_table.data_ptr(), max_blocks,
-            context_lens.data_ptr(), int(window), int(sinks), B, Hq, Hkv, D, bs, int(max_context_len), float(scale),
-            out.data_ptr(), od, 0 if workspace is None else workspace.data_ptr(),
+    args = (q.data_ptr(), codes.data_ptr(), scales.data_ptr(), cshape[0], block_table.data_ptr(), tshape[1],
+            context_lens.data_ptr(), int(window), int(sinks), B, Hq, cshape[1], D, cshape[3], int(max_context_len),
+            float(scale), out.data_ptr(), KVC_F16 if odt is _F16 else KVC_F32, 0 if workspace is None else workspace.data_ptr(),
             0 if workspace is None else workspace.nbytes)
     return _run(_ATTENTION_FP8_BLOCK, args, stream, prepare, dev, keep)
 
@@ -1281,28 +1289,36 @@ def paged_decode_window_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cach
     k_new / v_new ([B][Hkv][D] fp16) these are appended at position ctx-1 first, in the same kernel.  Blocks in which
     nothing is visible are not read, nor their table entries; workspace: paged_decode_window_plan bytes.
     prepare=True returns a PreparedCall instead of launching."""
-    qshape, cshape = q.shape, k_cache.shape
+    qshape, cshape, tshape = q.shape, k_cache.shape, block_table.shape
     B, Hq, D = qshape
     NB, Hkv, bs, Dk = cshape
     if Dk != D or v_cache.shape != cshape:
         raise ValueError("cache shapes do not match q")
-    max_blocks, od, odt = _decode_shapes(qshape, block_table, context_lens, out)
+    odt = out.dtype
     if (k_new is None) != (v_new is None):
         raise ValueError("k_new and v_new: both or neither")
     if k_new is not None and (k_new.shape != (B, Hkv, D) or v_new.shape != (B, Hkv, D)):
         raise ValueError("k_new/v_new must be [B][Hkv][D]")
     keep = (q, k_cache, v_cache, block_table, context_lens, out, workspace, k_new, v_new)
     dev = q.get_device()
-    if not (dev >= 0 and dev == _current_device() and _ready(dev, _F16, q, k_cache, v_cache, k_new, v_new)
-            and _ready(dev, _I32, block_table, context_lens) and _ready(dev, odt, out)
-            and (workspace is None or _ready(dev, workspace.dtype, workspace))):
+    # (as in paged_decode_attention_fp8_block)
+    if not (len(tshape) == 2 and tshape[0] == B and out.shape == qshape and context_lens.nbytes == 4 * B
+            and dev >= 0 and dev == _current_device() and q.dtype is k_cache.dtype is v_cache.dtype is _F16
+            and block_table.dtype is _I32 and context_lens.dtype is _I32 and (odt is _F16 or odt is _F32)
+            and dev == k_cache.get_device() == v_cache.get_device() == block_table.get_device()
+            == context_lens.get_device() == out.get_device()
+            and q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous() and block_table.is_contiguous()
+            and context_lens.is_contiguous() and out.is_contiguous()
+            and (k_new is None or _ready(dev, _F16, k_new, v_new))
+            and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous()))):
+        _check_decode_shapes(q, block_table, context_lens, out)
         _check_all(keep, (q, _F16, "q"), (k_cache, _F16, "k_cache"), (v_cache, _F16, "v_cache"),
                    (k_new, _F16, "k_new"), (v_new, _F16, "v_new"), (block_table, _I32, "block_table"),
                    (context_lens, _I32, "context_lens"), (out, None, "out"), (workspace, None, "workspace"))
     args = (q.data_ptr(), 0 if k_new is None else k_new.data_ptr(), 0 if v_new is None else v_new.data_ptr(),
-            k_cache.data_ptr(), v_cache.data_ptr(), NB, block_table.data_ptr(), max_blocks,
+            k_cache.data_ptr(), v_cache.data_ptr(), NB, block_table.data_ptr(), tshape[1],
             context_lens.data_ptr(), int(window), int(sinks), B, Hq, Hkv, D, bs, int(max_context_len), float(scale),
-            out.data_ptr(), od, 0 if workspace is None else workspace.data_ptr(),
+            out.data_ptr(), KVC_F16 if odt is _F16 else KVC_F32, 0 if workspace is None else workspace.data_ptr(),
             0 if workspace is None else workspace.nbytes)
     return _run(_WINDOW_ATTENTION, args, stream, prepare, dev, keep)
 
