@@ -10,8 +10,9 @@
 // of one KV head of a run: it holds the up to 16 rows in registers, reduces the largest magnitude, compares it with the
 // old scale where the block held rows before (slots are filled in order: the run's first offset says how many), recodes
 // those if the scale grows, and writes codes and scale.  One pass over everything, 3 bytes per value: memory bounds the
-// long appends (16,384 tokens, 8 heads, D = 128: 16.7 us, 90 % of the measured copy rate; 65,536 tokens, 2 heads, D = 64:
-// 8.0, 95 %), launch and three dependent loads the short ones (32 tokens, 2 heads, D = 64: 2.0).
+// long appends (16,384 tokens, 8 heads, D = 128: 17.5 us where nothing is in L2, 86 % of the measured copy rate, 14.4
+// where rows are; 65,536 tokens, 2 heads, D = 64: 11.5 and 8.0), launch and three dependent loads the short ones (32
+// tokens, 2 heads, D = 64: 2.0).
 #include "../../include/kvc.h"
 #include "decode_common.cuh"
 #include "kvc_internal.h"
@@ -19,7 +20,7 @@
 namespace kvc {
 namespace append8 {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 
 struct Params {
     const __half* k;
@@ -75,8 +76,12 @@ __device__ __forceinline__ uint32_t recode(uint32_t four, float ratio) {
            static_cast<uint32_t>(float2_to_e4m3x2(b.x * ratio, b.y * ratio)) << 16;
 }
 
+// Registers for 32 warps on an SM (40 at D = 64), CTAs of four: the loads of a warp follow one another, so what is in
+// flight is warps times rows (16,384 tokens of 8 heads, D = 128, 24 warps in CTAs of eight 19.5 us, 32 of eight 18.0, 32 of
+// four 17.5, 40 of four 18.3; 65,536 of 2 heads, D = 64, 12.5, 12.4 with 32 and 11.5 with 40).  Tried and slower: rows asked
+// for along with the slots (19.2).
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32) kv_append_fp8_block_kernel(const Params p) {
+__global__ void __launch_bounds__(kWarps * 32, D == 64 ? 10 : 8) kv_append_fp8_block_kernel(const Params p) {
     constexpr int kLanes = D / 8;         // lanes of a row, 8 values each
     constexpr int kRows = 32 / kLanes;    // rows of a pass
     constexpr int kPasses = kBlockSize / kRows;
@@ -168,10 +173,11 @@ cudaError_t launch_append_fp8_block(const AppendFp8BlockArgs& a, cudaStream_t st
     p.num_slots = static_cast<int64_t>(a.num_blocks) * kBlockSize;
     p.Hkv = a.Hkv;
     // Tokens of a warp: one where there are few, so that the runs of a decode step (a token each) are all worked on at
-    // once; else 16, so that the warps of a prompt's runs are not one in many.  16,384 prompt tokens, 8 heads, D = 128:
-    // 71 us with 1, 42 with 2, 28 with 4, 20 with 8, 16.7 with 16; at 1024 tokens of 8 heads a prompt takes 5.5 us with 1
-    // and 3.3 with 16, a step of 1024 sequences 9.5 and 14.5.
-    p.tile = a.n * 2 * a.Hkv <= 16384 ? 1 : 16;
+    // once; 16 where there are many, so that the warps of a prompt's runs are not one in many; 4 between.  8 heads,
+    // D = 128, in us with 1 / 4 / 16: 16,384 tokens of prompts 55 / 22 / 14.4, 1024 of a prompt 4.6 / 3.1 / 3.0; steps of
+    // 256 sequences 3.1 / 4.6 / 13.6, of 1024 8.5 / 8.0 / 14.4, of 2048 15.5 / 13.9 / 17.9.
+    const int64_t units = a.n * 2 * a.Hkv;
+    p.tile = units <= 4096 ? 1 : units <= 65536 ? 4 : 16;
     const int64_t items = (p.n + p.tile - 1) / p.tile * 2 * p.Hkv, grid = (items + append8::kWarps - 1) / append8::kWarps;
     if (grid > 2147483647LL) return cudaErrorInvalidConfiguration;
     const dim3 g(static_cast<unsigned>(grid)), block(append8::kWarps * 32);
