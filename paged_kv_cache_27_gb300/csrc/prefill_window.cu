@@ -159,10 +159,13 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
         }
     }
 }
-// The same for a whole warp: one vote and one branch where the phase is over already.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+// The same for a whole warp: one vote and one branch where the phase is over already, the rest out of the way.
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
     return __all_sync(0xffffffffu, wait(bar, parity, abort_flag));
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    if (__builtin_expect(__all_sync(0xffffffffu, mbar_try_wait(bar, parity)), 1)) return true;
+    return wait_on(bar, parity, abort_flag);
 }
 // The same for a whole warp whose waits sit between two products: without the hint of a long sleep.  (Polling took issue
 // slots from the row warps: 266 against 257 us at 4 x 4096 tokens, window 1024, 32 / 8 heads, D = 128.)
