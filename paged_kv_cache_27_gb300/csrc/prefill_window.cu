@@ -29,8 +29,8 @@
 // with a CTA per item, 125 so).
 // Bound by a row warp's chain through a unit, some 1350 clocks at D = 64 for products of 370: 500 in the exponentials (256
 // at their pipe's rate, shared with the other stream's), 230 in the load and the maximum, 140 in the wait for S, the rest
-// in votes, branches and the handing over.  Now 4 x 4096 tokens, 32 / 8 heads, D = 128: 368 us with window 4096 (1490
-// TFLOP/s, 75 % of the measured rate), 232 with 1024, 115 with 128; 32,768 tokens, window 4096, 14 / 2 heads, D = 64: 512;
+// in votes, branches and the handing over.  Now 4 x 4096 tokens, 32 / 8 heads, D = 128: 358 to 370 us with window 4096 (1490
+// to 1536 TFLOP/s, 75 % of the measured rate), 232 with 1024, 106 to 117 with 128; 32,768 tokens, window 4096, 14 / 2 heads, D = 64: 512;
 // the five uneven prompts 20.8.  Tried and slower: sixteen row warps, a set for each buffer that hands its maxima to the
 // other (641 against 554: with twice the warps everything in them takes twice as long), a warp of its own for Q (window 128
 // 117 -> 110, but 516 -> 520 at D = 64).
