@@ -13,17 +13,15 @@
 // then a scan over the threads) and knows from the totals whether the step fits, so that one launch without any
 // exchange is all or nothing; then it takes a share of the tokens, finds each one's sequence by bisection, and writes
 // its slot and position, and the token that starts a block also the table's entry.  Bound by launch and dependent loads,
-// not by bytes: 256 sequences' next tokens take 2.7 us, 128 prompts of up to 8192 tokens 6.5 (where their slots and
-// entries alone would be 1.1): the sums, then a bisection and three loads that follow one another for each token.
+// not by bytes: 256 sequences' next tokens take 2.3 us, 128 prompts of up to 8192 tokens 5.4 (where their slots and
+// entries alone would be 1.1): the sums, then for each token a bisection and two loads that follow one another (its
+// sequence's lengths are kept with the sums: read again they were 0.35 us more).
 #include "../../include/kvc.h"
 #include "decode_common.cuh"
 #include "kvc_internal.h"
 
 namespace kvc {
 namespace tables {
-
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 
 struct Params {
     const int32_t* before;  // null: zeros
@@ -46,15 +44,11 @@ struct Seq {
     int had, need;      // distinct blocks before, and how many the step adds
 };
 
-__device__ __forceinline__ Seq load_seq(const Params& p, int b, bool* bad) {
+__device__ __forceinline__ Seq make_seq(const Params& p, int before, int count) {
+    const int after = before + count;
     Seq s;
-    s.before = p.before != nullptr ? p.before[b] : 0;
-    int after = p.after[b];
-    if (s.before < 0 || after < s.before || after > p.max_blocks * kBlockSize) {  // (max_blocks * 16 is below 2^31)
-        *bad = true;
-        s.before = after = 0;
-    }
-    s.count = after - s.before;
+    s.before = before;
+    s.count = count;
     s.nb0 = (s.before + kBlockSize - 1) / kBlockSize;
     s.nb1 = (after + kBlockSize - 1) / kBlockSize;
     const int most = p.ring > 0 ? p.first + p.ring : p.max_blocks;
@@ -62,10 +56,24 @@ __device__ __forceinline__ Seq load_seq(const Params& p, int b, bool* bad) {
     s.need = min(s.nb1, most) - s.had;
     return s;
 }
+__device__ __forceinline__ Seq load_seq(const Params& p, int b, bool* bad) {
+    int before = p.before != nullptr ? p.before[b] : 0, after = p.after[b];
+    if (before < 0 || after < before || after > p.max_blocks * kBlockSize) {  // (max_blocks * 16 is below 2^31)
+        *bad = true;
+        before = after = 0;
+    }
+    return make_seq(p, before, after - before);
+}
 
+// The sums of many sequences want many threads, for few a CTA of fewer starts sooner: with 128 / 512 threads, in us, 256
+// sequences' next tokens 2.3 / 2.7, 128 prompts of up to 8192 tokens 5.4 / 6.2, the next tokens of 1024 sequences 3.5 /
+// 3.3, of 4096 17.9 / 6.7.
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads) kv_block_tables_kernel(const Params p) {
+    constexpr int kWarps = kThreads / 32;
     __shared__ int s_tok[kThreads], s_need[kThreads];  // sums before each thread's sequences
     __shared__ int64_t s_warp[2][kWarps];
+    __shared__ int2 s_lens[kThreads];  // lengths of each thread's first sequence, before and new
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dependency_wait();  // nothing is read or written before the kernel in front is done
     const int placed = *p.placed;
@@ -76,6 +84,7 @@ __global__ void __launch_bounds__(kThreads) kv_block_tables_kernel(const Params 
         const Seq s = load_seq(p, b, &bad);
         tok += s.count;
         need += s.need;
+        if (b == b0) s_lens[tid] = make_int2(s.before, s.count);
     }
     int64_t tok_in = tok, need_in = need;  // inclusive sums
 #pragma unroll
@@ -131,7 +140,7 @@ __global__ void __launch_bounds__(kThreads) kv_block_tables_kernel(const Params 
             for (int step = kThreads / 2; step > 0; step >>= 1)
                 if (s_tok[lo + step] <= t) lo += step;
             int b = lo * p.per, from = s_tok[lo], taken = s_need[lo];
-            Seq s = load_seq(p, b, &bad);
+            Seq s = make_seq(p, s_lens[lo].x, s_lens[lo].y);
             while (from + s.count <= t) {
                 from += s.count;
                 taken += s.need;
@@ -158,11 +167,19 @@ __global__ void __launch_bounds__(kThreads) kv_block_tables_kernel(const Params 
     }
 }
 
+// (1024 threads on an SM: with 512 a token's dependent loads show, with 1536 the sums that every CTA forms do)
+template <int kThreads>
+static cudaError_t launch_threads(Params& p, cudaStream_t stream) {
+    p.per = std::max(1, (p.B + kThreads - 1) / kThreads);
+    const int64_t want = (static_cast<int64_t>(p.num_slots) + kThreads - 1) / kThreads;
+    const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(want, 1024 / kThreads * sm_count())));
+    return launch(kv_block_tables_kernel<kThreads>, dim3(grid), dim3(kThreads), 0, stream, true, 1u, p);
+}
+
 }  // namespace tables
 
 cudaError_t launch_block_tables(const BlockTableArgs& a, cudaStream_t stream) {
-    const int sms = sm_count();
-    if (sms <= 0) return cudaErrorNoDevice;
+    if (sm_count() <= 0) return cudaErrorNoDevice;
     tables::Params p;
     p.before = a.lens_before;
     p.after = a.lens_after;
@@ -178,12 +195,9 @@ cudaError_t launch_block_tables(const BlockTableArgs& a, cudaStream_t stream) {
     p.num_free = a.num_free;
     p.max_blocks = a.max_blocks;
     p.num_slots = a.num_slots;
-    p.per = std::max(1, (a.B + tables::kThreads - 1) / tables::kThreads);
     p.first = a.window > 0 ? (a.sinks + kBlockSize - 1) / kBlockSize : 0;
     p.ring = a.window > 0 ? (a.window + 2 * kBlockSize - 2) / kBlockSize : 0;
-    const int64_t want = (static_cast<int64_t>(a.num_slots) + tables::kThreads - 1) / tables::kThreads;
-    const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(want, 2 * sms)));
-    return launch(tables::kv_block_tables_kernel, dim3(grid), dim3(tables::kThreads), 0, stream, true, 1u, p);
+    return a.B <= 512 ? tables::launch_threads<128>(p, stream) : tables::launch_threads<512>(p, stream);
 }
 
 }  // namespace kvc
