@@ -497,6 +497,12 @@ def test_append_fp8_block(Hkv, D, lens, firsts):
     assert kvc.kvc_device_error_flags(clear=True) == 0
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_append_fp8_block_of_long_prompts(D):
+    """Prompts of thousands of tokens and many heads: 16 tokens to a warp, runs that end inside its tokens and past them."""
+    test_append_fp8_block(8, D, [6001, 3, 700, 1, 90], [7, 13, 0, 4, 15])
+
+
 def test_append_fp8_block_edges():
     """Largest and smallest values, ties, infinities and NaN, float8 tensors, slots out of range."""
     D = 64
